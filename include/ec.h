@@ -184,8 +184,9 @@ typedef struct {
     int32_t reserved;
 } ec_fp8_params;
 
-/* Output dtypes of ec_decode_as. */
-enum { EC_DTYPE_BF16 = 0, EC_DTYPE_FP8_E4M3 = 1, EC_DTYPE_INT8 = 2 };
+/* Element types: the first three are outputs of ec_decode_as, BF16, FP16 and FP32 are
+ * what the cache calls (ec_kv_*) read and write. */
+enum { EC_DTYPE_BF16 = 0, EC_DTYPE_FP8_E4M3 = 1, EC_DTYPE_INT8 = 2, EC_DTYPE_FP16 = 3, EC_DTYPE_FP32 = 4 };
 
 /* Sizes and rates of one encoded matrix (ec_stats). */
 typedef struct {
@@ -418,6 +419,163 @@ void ec_free(ec_matrix* W);
 
 /* Human-readable text for an EC_* code. */
 const char* ec_strerror(int code);
+
+/* ------------------------------------------------------------------------------
+ * A paged key/value cache in microscaled 4-bit floating point, and the attention
+ * that reads it.
+ *
+ * Values.  32 consecutive channels of one token and head form a block (OCP
+ * Microscaling): a scale 2^(e - 127) held as the byte e, and 32 FP4 E2M1 elements
+ * (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives).  ec_kv_append takes the smallest
+ * power of two for which no element exceeds 6 and rounds to nearest, ties to the even
+ * code.  e = 0 stands for a block of zeros, e = 255 (a block that held an infinity or a
+ * NaN) reads as NaN; blocks whose largest element is below 6 * 2^-126 take e = 1.
+ *
+ * Pool.  Device memory of the caller, ec_kv_pool_bytes() large, 16-byte aligned:
+ * [page][layer][head][page_tokens / 16] units of 17 * head_dim bytes, each 16
+ * consecutive tokens of one head.  D = head_dim, lane = 4 g + c with g = 0..7, c =
+ * 0..3; a word is 4 bytes, element i of a word its nibble i (low first):
+ *   key codes, 8 D bytes: word i of lane (i = 0..D/16-1) at (i/4)*512 + lane*16 +
+ *     (i%4)*4: token g + 8 (i%2), channels 32 (i/2) + 8 c + 0..7;
+ *   value codes, 8 D bytes: same places; byte r + 2 p of word i holds channel
+ *     16 i + 8 r + g of tokens 2c + 8p (low nibble) and 2c + 8p + 1;
+ *   key scales, D/2 bytes: [token][block];
+ *   value scales, D/2 bytes: [c][block][p][n]: token 8 p + 2 c + n.
+ * (The words are the operands of the attention's matrix instructions.)
+ *
+ * Sequences.  An ec_kv_seqs names n_seqs sequences: lens[s] tokens each (device), token
+ * t in page table[s * table_stride + t / page_tokens] (device).  A call on "new" tokens
+ * takes `starts` (device, n_seqs + 1): rows starts[s] .. starts[s+1]-1 of its dense
+ * arguments belong to the LAST starts[s+1] - starts[s] tokens of sequence s, which are
+ * counted in lens[s] already (ec_kv_fork makes the room).  starts = NULL: one new token
+ * per sequence, row s.  lens <= 0 is an empty sequence.
+ *
+ * Dense arguments are [rows, heads, head_dim] of EC_DTYPE_BF16, FP16 or FP32 with
+ * strides in elements between rows and heads (any, multiples of 1; head_dim is
+ * contiguous); pointers need the alignment of one element, and 16-byte alignment of
+ * pointer and strides takes the wide loads and stores.
+ *
+ * All calls are asynchronous on `stream`, allocate nothing and can be captured in a
+ * graph.  Device-side inconsistencies (a page number outside the pool, rows outside
+ * `starts`, more tokens than the table row can hold) set the status word (ec_status:
+ * EC_ERR_CORRUPT) and are read as page 0 or left out: no access leaves the pool. */
+#define EC_KV_MAX_SEQS 1024
+
+typedef struct ec_kv ec_kv; /* opaque: the geometry and the caller's pool */
+
+/*  n_layers       layers that share the page numbering, 1..1024
+ *  n_kv_heads     key/value heads, 1..1024
+ *  head_dim       64, 128, 192 or 256 (EC_ERR_UNSUPPORTED otherwise)
+ *  page_tokens    tokens per page: 16, 32, 64, 128 or 256 (EC_ERR_UNSUPPORTED otherwise)
+ *  n_pages        pages in the pool, 1..2^30 */
+typedef struct {
+    int32_t n_layers;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t page_tokens;
+    int64_t n_pages;
+} ec_kv_params;
+
+typedef struct {
+    int32_t* table;        /* device, [n_seqs, table_stride] page numbers */
+    int64_t table_stride;  /* pages a row can hold */
+    int32_t* lens;         /* device, [n_seqs] */
+    int32_t n_seqs;        /* 0..EC_KV_MAX_SEQS */
+} ec_kv_seqs;
+
+/* Dense rows: data + row * row_stride + head * head_stride (elements). */
+typedef struct {
+    void* data;
+    int64_t row_stride;
+    int64_t head_stride;
+    int32_t dtype;
+} ec_kv_rows;
+
+/* Attention parameters.
+ *  n_q_heads   query heads, a multiple of n_kv_heads; query head j reads key/value head
+ *              j / (n_q_heads / n_kv_heads)
+ *  window      0: a query at position t sees tokens 0..t; w > 0: the last w of them, t
+ *              itself among them, and
+ *  sinks       the first `sinks` tokens of the sequence (window > 0 only)
+ *  scale       factor of the scores (0: 1 / sqrt(head_dim)) */
+typedef struct {
+    int32_t n_q_heads;
+    int32_t window;
+    int32_t sinks;
+    float scale;
+} ec_kv_attn;
+
+/* Bytes of the pool for this geometry (host only). */
+int ec_kv_pool_bytes(const ec_kv_params* params, size_t* bytes);
+
+/* Describe a pool of at least ec_kv_pool_bytes() bytes on `device`.  The pool belongs to
+ * the caller, who keeps it alive; its contents are left as they are (pages need no
+ * clearing).  device < 0: no pool (geometry and argument checks only; every call that
+ * would launch returns EC_ERR_INVALID_ARG). */
+int ec_kv_create(const ec_kv_params* params, void* pool, size_t pool_bytes, int device, ec_kv** out);
+
+/* Free the descriptor (not the pool). NULL is ignored. */
+void ec_kv_free(ec_kv* C);
+
+/* Quantise the new tokens' keys and values into the cache (layer 0..n_layers-1).
+ * n_rows: rows of k and v; max_new: an upper bound of the new tokens of one sequence.
+ * Pages that receive tokens must not be shared with a sequence that reads those places
+ * (ec_kv_fork gives every sequence a partly filled page of its own). */
+int ec_kv_append(const ec_kv* C, int layer, const ec_kv_seqs* seqs, const int32_t* starts, int64_t n_rows,
+                 int max_new, const ec_kv_rows* k, const ec_kv_rows* v, cudaStream_t stream);
+
+/* The values that the cache holds of the last tokens of each sequence (same convention
+ * as ec_kv_append; k or v NULL leaves it out), rounded to the rows' type (BF16 holds
+ * every finite value of 2^-126 and above exactly).  Rows of tokens before a sequence's
+ * first are zeros. */
+int ec_kv_read(const ec_kv* C, int layer, const ec_kv_seqs* seqs, const int32_t* starts, int64_t n_rows,
+               int max_new, const ec_kv_rows* k, const ec_kv_rows* v, cudaStream_t stream);
+
+/* out[row, j] = sum_t p_t v_t, p = softmax_t(scale * q[row, j] . k_t) over the tokens t
+ * that the row sees; lse[row, j] (FP32, may be NULL) the natural logarithm of the sum of
+ * the exponentials.  Scores, sums and outputs are held in FP32; products are exact in
+ * the 4-bit values times FP16 parts of q (one for BF16 and FP16, two for FP32) and
+ * FP16 probabilities.  A row that sees nothing gives zeros and lse = -inf.
+ * max_new and max_len are upper bounds, over the sequences, of the new tokens and of
+ * lens (0: what a table row can hold).  work: device memory of the caller, 16-byte
+ * aligned, of at least ec_kv_attend_work_bytes(); its contents need no clearing, and
+ * two calls that may overlap need one each.  out: FP16, BF16 or FP32. */
+int ec_kv_attend(const ec_kv* C, int layer, const ec_kv_seqs* seqs, const int32_t* starts, int64_t n_rows,
+                 int max_new, int64_t max_len, const ec_kv_attn* attn, const ec_kv_rows* q, const ec_kv_rows* out,
+                 float* lse, void* work, size_t work_bytes, cudaStream_t stream);
+
+/* Work bytes of ec_kv_attend for these sizes on the current device (host only). */
+int ec_kv_attend_work_bytes(const ec_kv* C, int n_seqs, int64_t n_rows, int max_new, int64_t max_len,
+                            const ec_kv_attn* attn, size_t* bytes);
+
+/* Sequences that continue others, for all layers at once: sequence i of `to` gets the
+ * tokens of sequence parents[i] of `from` (parents device, [to->n_seqs], -1: an empty
+ * sequence; NULL: i) and room for grow[i] >= 0 more (device; NULL: none); its len is
+ * the parent's plus grow[i].  Whole pages are shared; a partly filled last page stays
+ * with the first child (lowest i), the others get copies of its used units.  Sequences
+ * of `from` without a child are dropped.  refs (device, [n_pages]): how many table
+ * entries name each page, here and in tables that are not in this call; refs_out is the
+ * same afterwards, and pages with refs_out = 0 are free.  New pages are the free ones of
+ * lowest number, taken in the order of the sequences (a copied page first).  A sequence
+ * for which no pages are left (or whose row would be longer than table_stride) gets
+ * lens = -1 and no pages.  Entries past a sequence's pages are -1.  `to` and refs_out
+ * must not overlap `from` and refs.  Freeing = a fork without the ended sequences;
+ * a decoding step = a fork with parents = NULL and grow = 1. */
+int ec_kv_fork(const ec_kv* C, const ec_kv_seqs* from, const int32_t* refs, const int32_t* parents,
+               const int32_t* grow, const ec_kv_seqs* to, int32_t* refs_out, void* work, size_t work_bytes,
+               cudaStream_t stream);
+
+/* Move the n pages in use (refs > 0) to the numbers 0..n-1, for all layers: a page below
+ * n stays, the others, in ascending order, fill the free numbers below n in ascending
+ * order.  to: the same sequences with the new numbers (entries outside 0..n_pages-1 stay
+ * as they are; lens are copied); map (device, [n_pages], may be NULL): old number -> new,
+ * -1 for a free page, for tables that are not in this call.  `to`, refs_out and map must
+ * not overlap `from` and refs. */
+int ec_kv_compact(const ec_kv* C, const ec_kv_seqs* from, const int32_t* refs, const ec_kv_seqs* to,
+                  int32_t* refs_out, int32_t* map, void* work, size_t work_bytes, cudaStream_t stream);
+
+/* Work bytes of ec_kv_fork (n_from and n_to sequences) and ec_kv_compact (host only). */
+int ec_kv_pages_work_bytes(const ec_kv* C, int n_from, int n_to, size_t* bytes);
 
 #ifdef __cplusplus
 }

@@ -7,7 +7,8 @@ built the access raises ImportError (there is no fallback path).
 """
 _API = ("EC_KIND_E8", "EC_KIND_HUFFMAN_BF16", "EC_KIND_RANS_FP8", "EC_KIND_RANS_EXP", "EC_KIND_RANS_INT4", "EC_MAX_BATCH", "EC_MAX_GROUP", "EcError", "Matrix",
         "bf16_gemm", "bf16_gemv", "decode", "decode_as", "decode_batch", "deserialize", "encode_bf16", "encode_bf16_exp", "encode_e8", "encode_fp8", "encode_rans", "gemm", "gemm_group", "gemm_group_work_bytes", "gemm_work_bytes", "gemv", "gemv_group", "gemv_path", "gemv_static", "lib",
-        "status", "strerror", "LIB_PATH", "EXPORTS")
+        "EC_KV_MAX_SEQS", "KvCache", "KvSeqs", "kv_append", "kv_attend", "kv_attend_work_bytes", "kv_cache", "kv_compact",
+        "kv_fork", "kv_pages_work_bytes", "kv_pool_bytes", "kv_read", "kv_seqs", "status", "strerror", "LIB_PATH", "EXPORTS")
 
 __all__ = list(_API)
 

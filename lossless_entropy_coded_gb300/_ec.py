@@ -41,7 +41,8 @@ EXPORTS = ["ec_encode_bf16", "ec_encode_rans", "ec_decode", "ec_decode_batch", "
            "ec_bf16_gemv", "ec_stats", "ec_code_lengths", "ec_serialize", "ec_deserialize", "ec_status", "ec_free",
            "ec_strerror", "ec_gemv_static", "ec_gemv_path", "ec_encode_e8", "ec_decode_as", "ec_encode_fp8",
            "ec_gemm", "ec_gemm_work_bytes", "ec_bf16_gemm", "ec_encode_bf16_exp", "ec_gemm_group",
-           "ec_gemm_group_work_bytes"]
+           "ec_gemm_group_work_bytes", "ec_kv_pool_bytes", "ec_kv_create", "ec_kv_free", "ec_kv_append", "ec_kv_read",
+           "ec_kv_attend", "ec_kv_attend_work_bytes", "ec_kv_fork", "ec_kv_compact", "ec_kv_pages_work_bytes"]
 
 
 class HuffParams(ctypes.Structure):
@@ -83,6 +84,26 @@ class Stats(ctypes.Structure):
         return {k: getattr(self, k) for k, _ in self._fields_}
 
 
+class KvParams(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("n_pages", ctypes.c_int64)]
+
+
+class KvSeqsStruct(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("lens", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int32)]
+
+
+class KvRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
+
+
+class KvAttn(ctypes.Structure):
+    _fields_ = [("n_q_heads", ctypes.c_int32), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
 _sig = {
     "ec_encode_bf16": ([_vp, _i64, _i64, ctypes.POINTER(HuffParams), _i32, ctypes.POINTER(_vp)], _i32),
@@ -104,6 +125,16 @@ _sig = {
     "ec_bf16_gemm": ([_vp, _i64, _i64, _vp, _vp, _i32, _vp, ctypes.c_size_t, _vp], _i32),
     "ec_gemv_static": ([_vp, _vp, _vp, _i32, _vp], _i32),
     "ec_gemv_path": ([_vp, _i32, _i32], _i32),
+    "ec_kv_pool_bytes": ([_vp, _vp], _i32),
+    "ec_kv_create": ([_vp, _vp, ctypes.c_size_t, _i32, _vp], _i32),
+    "ec_kv_free": ([_vp], None),
+    "ec_kv_append": ([_vp, _i32, _vp, _vp, _i64, _i32, _vp, _vp, _vp], _i32),
+    "ec_kv_read": ([_vp, _i32, _vp, _vp, _i64, _i32, _vp, _vp, _vp], _i32),
+    "ec_kv_attend": ([_vp, _i32, _vp, _vp, _i64, _i32, _i64, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp], _i32),
+    "ec_kv_attend_work_bytes": ([_vp, _i32, _i64, _i32, _i64, _vp, _vp], _i32),
+    "ec_kv_fork": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp], _i32),
+    "ec_kv_compact": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp], _i32),
+    "ec_kv_pages_work_bytes": ([_vp, _i32, _i32, _vp], _i32),
     "ec_stats": ([_vp, ctypes.POINTER(Stats)], _i32),
     "ec_code_lengths": ([_vp, _vp], _i32),
     "ec_serialize": ([_vp, _vp, _i64, ctypes.POINTER(_i64)], _i32),
@@ -383,3 +414,206 @@ def bf16_gemm(w, x, y, batch: int, work=None, stream=None) -> None:
 def status(stream=None) -> int:
     """Synchronise the stream and return (and clear) the device status word."""
     return int(lib.ec_status(_stream_ptr(stream)))
+
+
+# ---------------------------------------------------------------- key/value cache
+EC_DTYPE_FP16, EC_DTYPE_FP32 = 3, 4
+EC_KV_MAX_SEQS = 1024
+_ROW_DTYPES = {"torch.bfloat16": EC_DTYPE_BF16, "torch.float16": EC_DTYPE_FP16, "torch.float32": EC_DTYPE_FP32}
+
+
+class KvCache:
+    """A paged 4-bit key/value cache over a pool tensor (kept alive here)."""
+
+    def __init__(self, handle: int, params: KvParams, pool, device: int):
+        self.handle = ctypes.c_void_p(handle)
+        self.params, self.pool, self.device = params, pool, device
+
+    def free(self) -> None:
+        if self.handle:
+            lib.ec_kv_free(self.handle)
+            self.handle = ctypes.c_void_p(0)
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+def _on_gpu(t, what: str, device=None):
+    """The address of a device tensor (on the cache's device)."""
+    if not t.is_cuda or (device is not None and t.device.index != device):
+        raise EcError(EC_ERR_INVALID_ARG, what + ": tensors on the cache's device")
+    return t.data_ptr()
+
+
+class KvSeqs:
+    """Sequences of a cache: int32 device tensors table [n, pages] and lens [n] (kept alive here)."""
+
+    def __init__(self, table, lens):
+        for t, dims in ((table, 2), (lens, 1)):
+            if str(t.dtype) != "torch.int32" or t.dim() != dims or not t.is_contiguous():
+                raise EcError(EC_ERR_INVALID_ARG, "kv_seqs: contiguous int32 tensors [n, pages] and [n]")
+        if table.shape[0] != lens.shape[0]:
+            raise EcError(EC_ERR_SHAPE, "kv_seqs")
+        _on_gpu(table, "kv_seqs"), _on_gpu(lens, "kv_seqs", table.device.index)
+        self.table, self.lens = table, lens
+        self.n, self.pages = int(table.shape[0]), int(table.shape[1])
+        self.struct = KvSeqsStruct(table.data_ptr(), self.pages, lens.data_ptr(), self.n)
+        self.ref = ctypes.addressof(self.struct)
+
+
+def kv_pool_bytes(n_layers: int, n_pages: int, n_kv_heads: int, head_dim: int, page_tokens: int = 64) -> int:
+    """ec_kv_pool_bytes: the pool's size."""
+    n = ctypes.c_size_t(0)
+    p = KvParams(n_layers, n_kv_heads, head_dim, page_tokens, n_pages)
+    _check(lib.ec_kv_pool_bytes(ctypes.byref(p), ctypes.byref(n)), "ec_kv_pool_bytes")
+    return int(n.value)
+
+
+def kv_cache(n_layers: int, n_pages: int, n_kv_heads: int, head_dim: int, page_tokens: int = 64, pool=None,
+             device: int = 0) -> KvCache:
+    """ec_kv_create over `pool` (a contiguous device tensor of at least kv_pool_bytes;
+    None allocates one).  device < 0: no pool."""
+    p = KvParams(n_layers, n_kv_heads, head_dim, page_tokens, n_pages)
+    nbytes = kv_pool_bytes(n_layers, n_pages, n_kv_heads, head_dim, page_tokens)
+    if device >= 0 and pool is None:
+        import torch
+        pool = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{device}")
+    if pool is not None:
+        if not pool.is_contiguous():
+            raise EcError(EC_ERR_INVALID_ARG, "kv_cache: a contiguous pool")
+        nbytes = pool.numel() * pool.element_size()
+        if device >= 0:
+            _on_gpu(pool, "kv_cache", device)
+    h = ctypes.c_void_p()
+    _check(lib.ec_kv_create(ctypes.byref(p), _dev_ptr(pool), nbytes, device, ctypes.byref(h)), "ec_kv_create")
+    return KvCache(h.value, p, pool, device)
+
+
+def kv_seqs(table, lens) -> KvSeqs:
+    return KvSeqs(table, lens)
+
+
+def _kv_rows(t, cache, heads: int, what: str) -> KvRows:
+    """[rows, heads, dim] with any strides between rows and heads."""
+    dtype = _ROW_DTYPES.get(str(t.dtype))
+    if dtype is None or t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise EcError(EC_ERR_INVALID_ARG, what + ": bfloat16, float16 or float32 [rows, heads, head_dim], contiguous in head_dim")
+    if t.shape[1] != heads or t.shape[2] != cache.params.head_dim:
+        raise EcError(EC_ERR_SHAPE, what)
+    return KvRows(_on_gpu(t, what, cache.device), t.stride(0), t.stride(1), dtype)
+
+
+def _starts_ptr(starts, cache, n: int, what: str) -> int:
+    if starts is None:
+        return 0
+    if str(starts.dtype) != "torch.int32" or not starts.is_contiguous():
+        raise EcError(EC_ERR_INVALID_ARG, what + ": starts is a contiguous int32 device tensor")
+    if starts.numel() != n + 1:
+        raise EcError(EC_ERR_SHAPE, what + ": starts has n_seqs + 1 entries")
+    return _on_gpu(starts, what, cache.device)
+
+
+def kv_append(cache: KvCache, layer: int, seqs: KvSeqs, k, v, starts=None, max_new: int = 1, stream=None) -> None:
+    """ec_kv_append: quantise the new tokens' k and v [rows, n_kv_heads, head_dim] into the cache."""
+    p = cache.params
+    kr, vr = (_kv_rows(t, cache, p.n_kv_heads, "ec_kv_append") for t in (k, v))
+    if k.shape[0] != v.shape[0]:
+        raise EcError(EC_ERR_SHAPE, "ec_kv_append")
+    _check(lib.ec_kv_append(cache.handle, layer, seqs.ref, _starts_ptr(starts, cache, seqs.n, "ec_kv_append"), k.shape[0],
+                            max_new, ctypes.addressof(kr), ctypes.addressof(vr), _stream_ptr(stream)), "ec_kv_append")
+
+
+def kv_read(cache: KvCache, layer: int, seqs: KvSeqs, k=None, v=None, starts=None, max_new: int = 1,
+            stream=None) -> None:
+    """ec_kv_read: the cached values of the sequences' last tokens into k and / or v."""
+    p = cache.params
+    kr, vr = (None if t is None else _kv_rows(t, cache, p.n_kv_heads, "ec_kv_read") for t in (k, v))
+    if k is not None and v is not None and k.shape[0] != v.shape[0]:
+        raise EcError(EC_ERR_SHAPE, "ec_kv_read")
+    rows = next((t.shape[0] for t in (k, v) if t is not None), 0)
+    _check(lib.ec_kv_read(cache.handle, layer, seqs.ref, _starts_ptr(starts, cache, seqs.n, "ec_kv_read"), rows, max_new,
+                          0 if kr is None else ctypes.addressof(kr), 0 if vr is None else ctypes.addressof(vr),
+                          _stream_ptr(stream)), "ec_kv_read")
+
+
+def kv_attend_work_bytes(cache: KvCache, n_seqs: int, n_rows: int, n_q_heads: int, max_new: int = 1,
+                         max_len: int = 0, window: int = 0, sinks: int = 0) -> int:
+    """ec_kv_attend_work_bytes: the work buffer of kv_attend for these sizes."""
+    n = ctypes.c_size_t(0)
+    at = KvAttn(n_q_heads, window, sinks, 0.0)
+    _check(lib.ec_kv_attend_work_bytes(cache.handle, n_seqs, n_rows, max_new, max_len, ctypes.byref(at),
+                                       ctypes.byref(n)), "ec_kv_attend_work_bytes")
+    return int(n.value)
+
+
+def kv_attend(cache: KvCache, layer: int, seqs: KvSeqs, q, out, starts=None, max_new: int = 1, max_len: int = 0,
+              scale: float = 0.0, window: int = 0, sinks: int = 0, lse=None, work=None, stream=None) -> None:
+    """ec_kv_attend: out [rows, n_q_heads, head_dim] = attention of the new tokens' q over
+    the cache; lse float32 [rows, n_q_heads] (optional).  max_len 0: what the table can
+    hold.  work: a device tensor of kv_attend_work_bytes; None allocates one."""
+    p = cache.params
+    heads = int(q.shape[1]) if q.dim() == 3 else 0
+    qr, orr = (_kv_rows(t, cache, heads, "ec_kv_attend") for t in (q, out))
+    if out.shape[0] != q.shape[0]:
+        raise EcError(EC_ERR_SHAPE, "ec_kv_attend")
+    if lse is not None and (str(lse.dtype) != "torch.float32" or not lse.is_contiguous() or lse.numel() != q.shape[0] * heads):
+        raise EcError(EC_ERR_INVALID_ARG, "ec_kv_attend: lse is a contiguous float32 tensor [rows, n_q_heads]")
+    at = KvAttn(heads, window, sinks, scale)
+    if work is None:
+        import torch
+        work = torch.empty(kv_attend_work_bytes(cache, seqs.n, q.shape[0], heads, max_new,
+                                                max_len or seqs.pages * p.page_tokens, window, sinks),
+                           dtype=torch.uint8, device=q.device)
+    _check(lib.ec_kv_attend(cache.handle, layer, seqs.ref, _starts_ptr(starts, cache, seqs.n, "ec_kv_attend"), q.shape[0],
+                            max_new, max_len, ctypes.addressof(at), ctypes.addressof(qr), ctypes.addressof(orr),
+                            0 if lse is None else _on_gpu(lse, "ec_kv_attend", cache.device),
+                            _on_gpu(work, "ec_kv_attend", cache.device), work.numel() * work.element_size(),
+                            _stream_ptr(stream)), "ec_kv_attend")
+
+
+def kv_pages_work_bytes(cache: KvCache, n_from: int, n_to: int) -> int:
+    """ec_kv_pages_work_bytes: the work buffer of kv_fork and kv_compact."""
+    n = ctypes.c_size_t(0)
+    _check(lib.ec_kv_pages_work_bytes(cache.handle, n_from, n_to, ctypes.byref(n)), "ec_kv_pages_work_bytes")
+    return int(n.value)
+
+
+def _int32_ptr(t, cache, n: int, what: str) -> int:
+    if t is None:
+        return 0
+    if str(t.dtype) != "torch.int32" or not t.is_contiguous():
+        raise EcError(EC_ERR_INVALID_ARG, what + ": contiguous int32 device tensors")
+    if t.numel() != n:
+        raise EcError(EC_ERR_SHAPE, what)
+    return _on_gpu(t, what, cache.device)
+
+
+def _pages_work(cache, a: KvSeqs, b: KvSeqs, work):
+    if work is None:
+        import torch
+        work = torch.empty(kv_pages_work_bytes(cache, a.n, b.n), dtype=torch.uint8, device=a.lens.device)
+    return work
+
+
+def kv_fork(cache: KvCache, seqs: KvSeqs, refs, to: KvSeqs, refs_out, parents=None, grow=None, work=None,
+            stream=None) -> None:
+    """ec_kv_fork: sequences `to` continue seqs[parents] with room for `grow` more tokens."""
+    n = cache.params.n_pages
+    work = _pages_work(cache, seqs, to, work)
+    _check(lib.ec_kv_fork(cache.handle, seqs.ref, _int32_ptr(refs, cache, n, "ec_kv_fork"), _int32_ptr(parents, cache, to.n, "ec_kv_fork"),
+                          _int32_ptr(grow, cache, to.n, "ec_kv_fork"), to.ref, _int32_ptr(refs_out, cache, n, "ec_kv_fork"),
+                          _on_gpu(work, "ec_kv_fork", cache.device), work.numel() * work.element_size(),
+                          _stream_ptr(stream)), "ec_kv_fork")
+
+
+def kv_compact(cache: KvCache, seqs: KvSeqs, refs, to: KvSeqs, refs_out, page_map=None, work=None, stream=None) -> None:
+    """ec_kv_compact: the pages in use move to the lowest numbers; page_map: old number -> new."""
+    n = cache.params.n_pages
+    work = _pages_work(cache, seqs, to, work)
+    _check(lib.ec_kv_compact(cache.handle, seqs.ref, _int32_ptr(refs, cache, n, "ec_kv_compact"), to.ref,
+                             _int32_ptr(refs_out, cache, n, "ec_kv_compact"), _int32_ptr(page_map, cache, n, "ec_kv_compact"),
+                             _on_gpu(work, "ec_kv_compact", cache.device), work.numel() * work.element_size(),
+                             _stream_ptr(stream)), "ec_kv_compact")

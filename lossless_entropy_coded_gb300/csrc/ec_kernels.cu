@@ -4202,6 +4202,13 @@ extern "C" int ec_bf16_gemm(const uint16_t* w, int64_t n_rows, int64_t k_cols, c
     return gemm_run(w, n_rows, k_cols, k_cols, x, k_cols, batch, y, n_rows, 0, (float*)work, work ? work_bytes : 0,
                     stream, d);
 }
+
+int ec_internal_status_ptr(int device, int** out) {
+    DeviceInfo* d = nullptr;
+    const int rc = device_info(device, &d);
+    if (rc == EC_OK) *out = d->status;
+    return rc;
+}
 /* ---- not in the Huffman GEMV: end ---- */
 
 extern "C" int ec_decode(const ec_matrix* W, uint16_t* out, cudaStream_t stream) {

@@ -1,0 +1,845 @@
+/*
+ * ec_kv.cu -- the paged 4-bit key/value cache: its descriptor, quantising new tokens
+ * into pages (ec_kv_append), reading values back (ec_kv_read), and the page operations
+ * (ec_kv_fork, ec_kv_compact).  The format and the contracts are in ec.h.
+ */
+#include <cstdlib>
+#include <cstring>
+#include <mutex>
+#include <new>
+#include <vector>
+
+#include "ec_kv_internal.h"
+
+namespace kv {
+
+/* ============================================================ host helpers */
+bool use_pdl() {
+    static const bool on = [] {
+        const char* e = std::getenv("EC_NO_PDL");
+        return !(e && e[0] == '1');
+    }();
+    return on;
+}
+
+int device_of(const ec_kv* C, Device* out) {
+    if (!C->pool) return EC_ERR_INVALID_ARG;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return EC_ERR_CUDA;
+    if (dev != C->device) return EC_ERR_INVALID_ARG;
+    static std::mutex mu;
+    static std::vector<int> sms;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if ((int)sms.size() <= dev) sms.resize(dev + 1, 0);
+        if (!sms[dev] && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+            sms[dev] = 0;
+            return EC_ERR_CUDA;
+        }
+        out->sms = sms[dev];
+    }
+    return ec_internal_status_ptr(dev, &out->status);
+}
+
+static int log2_of(int v) {
+    int s = 0;
+    while ((1 << s) < v) ++s;
+    return s;
+}
+
+bool pool_view(const ec_kv* C, int layer, Pool* o) {
+    const ec_kv_params& p = C->p;
+    if (layer < 0 || layer >= p.n_layers) return false;
+    o->base = C->pool;
+    o->dim = p.head_dim;
+    o->n_heads = p.n_kv_heads;
+    o->n_pages = (int32_t)p.n_pages;
+    o->page_shift = log2_of(p.page_tokens);
+    o->unit_bytes = 17 * p.head_dim;
+    o->head_bytes = (int64_t)o->unit_bytes * (p.page_tokens / kUnit);
+    o->layer_off = o->head_bytes * p.n_kv_heads * layer;
+    o->page_bytes = o->head_bytes * p.n_kv_heads * p.n_layers;
+    return true;
+}
+
+int check_seqs(const ec_kv_seqs* S) {
+    if (!S) return EC_ERR_INVALID_ARG;
+    if (S->n_seqs < 0 || S->table_stride < 0) return EC_ERR_SHAPE;
+    if (S->n_seqs > EC_KV_MAX_SEQS) return EC_ERR_UNSUPPORTED;
+    if (S->table_stride > (int64_t(1) << 26)) return EC_ERR_UNSUPPORTED;
+    if (S->n_seqs > 0 && (!S->lens || (S->table_stride > 0 && !S->table))) return EC_ERR_INVALID_ARG;
+    return EC_OK;
+}
+
+int check_rows(const ec_kv* C, const ec_kv_rows* r, int heads, int64_t n_rows, Rows* o) {
+    if (!r) return EC_ERR_INVALID_ARG;
+    int size = 0;
+    if (r->dtype == EC_DTYPE_FP32) size = 4;
+    else if (r->dtype == EC_DTYPE_BF16 || r->dtype == EC_DTYPE_FP16) size = 2;
+    else return EC_ERR_INVALID_ARG;
+    if (n_rows < 0) return EC_ERR_SHAPE;
+    if (r->row_stride < 0 || r->head_stride < 0) return EC_ERR_SHAPE;
+    /* the last element's offset in bytes fits 62 bits */
+    const int64_t lim = int64_t(1) << 60;
+    if (n_rows > 1 && r->row_stride > lim / (n_rows - 1)) return EC_ERR_OVERFLOW;
+    if (heads > 1 && r->head_stride > lim / (heads - 1)) return EC_ERR_OVERFLOW;
+    if (n_rows > 0 && (!r->data || (uintptr_t)r->data % size)) return EC_ERR_INVALID_ARG;
+    o->data = r->data;
+    o->row = r->row_stride;
+    o->head = r->head_stride;
+    o->dtype = r->dtype;
+    o->wide = ((uintptr_t)r->data % 16 == 0 && r->row_stride * size % 16 == 0 && r->head_stride * size % 16 == 0) ? 1 : 0;
+    (void)C;
+    return EC_OK;
+}
+
+/* The checks that every call on new tokens makes; *go = false when there is nothing to do. */
+static int check_call(const ec_kv* C, int layer, const ec_kv_seqs* seqs, const int32_t* starts, int64_t n_rows,
+                      int max_new, Pool* P, Seqs* S, bool* go) {
+    if (!C) return EC_ERR_INVALID_ARG;
+    int rc = check_seqs(seqs);
+    if (rc != EC_OK) return rc;
+    if (!pool_view(C, layer, P)) return EC_ERR_INVALID_ARG;
+    if (n_rows < 0 || max_new < 0) return EC_ERR_SHAPE;
+    if (max_new > (1 << 24)) return EC_ERR_UNSUPPORTED;
+    if (!starts && n_rows < seqs->n_seqs) return EC_ERR_SHAPE;
+    S->table = seqs->table;
+    S->lens = seqs->lens;
+    S->starts = starts;
+    S->table_stride = seqs->table_stride;
+    S->n_rows = n_rows;
+    S->n_seqs = seqs->n_seqs;
+    *go = seqs->n_seqs > 0 && n_rows > 0 && max_new > 0;
+    return EC_OK;
+}
+
+/* ============================================================ append and read */
+/* One warp owns one unit of 16 tokens of one head: the unit is put together in shared
+ * memory (an existing unit that keeps older tokens is brought in first) and written with
+ * 16-byte stores, so nothing else writes its bytes and a token's nibbles can share bytes
+ * with its neighbour's.  Lane 4 g + c reads channels 32 b + 8 c + 0..7 of tokens g and
+ * g + 8: a quad of lanes holds a block, whose largest magnitude takes two shuffles. */
+constexpr int kIoWarps = 4;
+
+struct AppendArgs {
+    Pool P;
+    Seqs S;
+    Rows k, v;
+    int32_t units;       /* units that max_new tokens can touch */
+    int32_t max_new;
+    int* status;
+};
+
+/* 8 consecutive elements of a row */
+__device__ __forceinline__ void load8(const Rows& R, int64_t off, float (&x)[8]) {
+    if (R.wide) {
+        if (R.dtype == EC_DTYPE_FP32) {
+            const float4 a = *(const float4*)((const float*)R.data + off), b = *(const float4*)((const float*)R.data + off + 4);
+            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+        } else {
+            const uint4 w = *(const uint4*)((const uint16_t*)R.data + off);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float2 f;
+                if (R.dtype == EC_DTYPE_FP16) f = __half22float2(*(const __half2*)&u[i]);
+                else f = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
+                x[2 * i] = f.x;
+                x[2 * i + 1] = f.y;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = load_elem(R, off + i);
+    }
+}
+
+__device__ __forceinline__ void store8(const Rows& R, int64_t off, const float (&x)[8]) {
+    if (R.wide) {
+        if (R.dtype == EC_DTYPE_FP32) {
+            *(float4*)((float*)R.data + off) = make_float4(x[0], x[1], x[2], x[3]);
+            *(float4*)((float*)R.data + off + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+            uint32_t u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (R.dtype == EC_DTYPE_FP16) {
+                    const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+                    u[i] = *(const uint32_t*)&h;
+                } else {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                    u[i] = *(const uint32_t*)&h;
+                }
+            }
+            *(uint4*)((uint16_t*)R.data + off) = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) store_elem(R, off + i, x[i]);
+    }
+}
+
+/* Eight channels of one token -> their word and the block's scale byte (the quad's four
+ * lanes take part). */
+__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], int& e) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu); /* NaN and infinity are the largest */
+    top = max(top, __shfl_xor_sync(kAll, top, 1));
+    top = max(top, __shfl_xor_sync(kAll, top, 2));
+    e = scale_byte(top);
+    if (e == 0 || e == 255) return 0u;
+    const float s = inv_scale(e);
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w |= f32x2_e2m1x2(x[2 * i + 1] * s, x[2 * i] * s) << (8 * i);
+    return w;
+}
+
+/* Which unit of which head a warp works on. */
+struct UnitJob {
+    int b, h, unit, tok0;  /* sequence, head, unit of the sequence, token of its first place */
+    int64_t row0;          /* dense row of token tok0 (may lie before the first) */
+    int lo, hi;            /* places of the unit that the call covers */
+    bool any;
+    Seq q;
+};
+
+__device__ __forceinline__ UnitJob unit_job(const Pool& P, const Seqs& S, int units, int max_new, int* status) {
+    UnitJob j;
+    const int64_t item = (int64_t)blockIdx.x * kIoWarps + (threadIdx.x >> 5);
+    j.h = (int)(item % P.n_heads);
+    const int64_t r = item / P.n_heads;
+    const int u = (int)(r % units);
+    j.b = (int)(r / units);
+    j.any = false;
+    if (j.b >= S.n_seqs) return j;
+    j.q = seq_of(S, P.page_shift, j.b);
+    if ((j.q.bad || j.q.m > max_new) && u == 0 && j.h == 0 && (threadIdx.x & 31) == 0) flag_corrupt(status);
+    const int first = j.q.len - j.q.m; /* position of the first new token; < 0: rows without a token */
+    const int f = first < 0 ? 0 : first;
+    j.unit = f / kUnit + u;
+    j.tok0 = j.unit * kUnit;
+    j.lo = f - j.tok0 > 0 ? f - j.tok0 : 0;
+    j.hi = j.q.len - j.tok0 < kUnit ? j.q.len - j.tok0 : kUnit;
+    j.row0 = j.q.row0 + (j.tok0 - first);
+    j.any = j.hi > j.lo;
+    return j;
+}
+
+__device__ __forceinline__ uint8_t* unit_ptr(const Pool& P, const Seqs& S, const UnitJob& j, int* status) {
+    const int slot = j.tok0 >> P.page_shift;
+    const int page = S.table[(int64_t)j.b * S.table_stride + slot];
+    if (page < 0 || page >= P.n_pages) {
+        if ((threadIdx.x & 31) == 0) flag_corrupt(status);
+        return nullptr;
+    }
+    return (uint8_t*)page_ptr(P, page, j.h, (j.tok0 & ((1 << P.page_shift) - 1)) / kUnit);
+}
+
+__global__ void __launch_bounds__(kIoWarps * 32) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+    extern __shared__ __align__(16) uint8_t io_smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const int D = a.P.dim, nb = D / 32;
+    uint8_t* buf = io_smem + warp * a.P.unit_bytes;
+    grid_dep_launch();
+    grid_dep_wait();
+    const UnitJob j = unit_job(a.P, a.S, a.units, a.max_new, a.status);
+    if (!j.any) return;
+    uint8_t* dst = unit_ptr(a.P, a.S, j, a.status);
+    if (!dst) return;
+    const int n16 = a.P.unit_bytes / 16;
+    if (j.lo > 0 || j.hi < kUnit) {
+        /* older tokens stay; places past the sequence's end are zeros */
+        for (int i = lane; i < n16; i += 32) ((uint4*)buf)[i] = j.lo > 0 ? ((const uint4*)dst)[i] : make_uint4(0, 0, 0, 0);
+    }
+    __syncwarp();
+    for (int b = 0; b < nb; ++b) {
+        /* keys */
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int t = g + 8 * r;
+            const bool on = t >= j.lo && t < j.hi;
+            float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (on) load8(a.k, (j.row0 + t) * a.k.row + (int64_t)j.h * a.k.head + 32 * b + 8 * c, x);
+            int e;
+            const uint32_t w = quantise8(x, e);
+            if (on) {
+                const int i = 2 * b + r;
+                *(uint32_t*)(buf + (i >> 2) * 512 + lane * 16 + (i & 3) * 4) = w;
+                if (c == 0) buf[16 * D + t * nb + b] = (uint8_t)e;
+            }
+        }
+        /* values: a byte holds a channel of tokens 2m and 2m + 1, lanes 4 apart */
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int t = g + 8 * r;
+            const bool on = t >= j.lo && t < j.hi;
+            float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (on) load8(a.v, (j.row0 + t) * a.v.row + (int64_t)j.h * a.v.head + 32 * b + 8 * c, x);
+            int e;
+            const uint32_t own = quantise8(x, e), other = __shfl_xor_sync(kAll, own, 4);
+            const int p = r, cc = (t >> 1) & 3; /* the pair's place: token 8 p + 2 cc (+1) */
+            if (on && c == 0) buf[16 * D + D / 2 + ((cc * nb + b) * 2 + p) * 2 + (t & 1)] = (uint8_t)e;
+            /* the even token's lane writes channels 0..3 of the eight, the odd one's 4..7 */
+            const bool odd = g & 1;
+            const bool on_even = (t & ~1) >= j.lo && (t & ~1) < j.hi, on_odd = (t | 1) >= j.lo && (t | 1) < j.hi;
+            const uint32_t ev = (odd ? other : own) >> (odd ? 16 : 0), od = (odd ? own : other) >> (odd ? 16 : 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int d = 32 * b + 8 * c + (odd ? 4 : 0) + k; /* channel */
+                const int i = d >> 4;
+                uint8_t* at = buf + 8 * D + (i >> 2) * 512 + ((d & 7) * 4 + cc) * 16 + (i & 3) * 4 + ((d >> 3) & 1) + 2 * p;
+                const uint32_t lo = (ev >> (4 * k)) & 15u, hi = (od >> (4 * k)) & 15u;
+                if (on_even && on_odd) *at = (uint8_t)(lo | hi << 4);
+                else if (on_even) *at = (uint8_t)((*at & 0xF0u) | lo);
+                else if (on_odd) *at = (uint8_t)((*at & 0x0Fu) | hi << 4);
+            }
+        }
+    }
+    __syncwarp();
+    for (int i = lane; i < n16; i += 32) ((uint4*)dst)[i] = ((const uint4*)buf)[i];
+}
+
+struct ReadArgs {
+    Pool P;
+    Seqs S;
+    Rows k, v;
+    int32_t has_k, has_v;
+    int32_t units, max_new;
+    int* status;
+};
+
+__device__ __forceinline__ float nib_value(uint32_t code, float s) {
+    const __half2 h = [&] {
+        const uint32_t r = e2m1x2_f16x2(code & 15u);
+        return *(const __half2*)&r;
+    }();
+    return __low2float(h) * s;
+}
+
+/* 2^(e - 127), NaN for 255 (e = 0: blocks of zeros). */
+__device__ __forceinline__ float scale_value(int e) {
+    return e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)e << 23);
+}
+
+__global__ void __launch_bounds__(kIoWarps * 32) kv_read_kernel(const __grid_constant__ ReadArgs a) {
+    extern __shared__ __align__(16) uint8_t io_smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const int D = a.P.dim, nb = D / 32;
+    uint8_t* buf = io_smem + warp * a.P.unit_bytes;
+    grid_dep_launch();
+    grid_dep_wait();
+    UnitJob j = unit_job(a.P, a.S, a.units, a.max_new, a.status);
+    const int64_t item = (int64_t)blockIdx.x * kIoWarps + warp;
+    const int u = (int)(item / a.P.n_heads % a.units);
+    if (j.b < a.S.n_seqs) {
+        /* rows of tokens before the sequence's first: zeros, 16 at a time */
+        const int none = j.q.m - j.q.len;
+        const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int r0 = u * kUnit; r0 < none; r0 += a.units * kUnit)
+            for (int r = r0; r < min(none, r0 + kUnit); ++r)
+                for (int d = 8 * lane; d < D; d += 256) {
+                    if (a.has_k) store8(a.k, (j.q.row0 + r) * a.k.row + (int64_t)j.h * a.k.head + d, z);
+                    if (a.has_v) store8(a.v, (j.q.row0 + r) * a.v.row + (int64_t)j.h * a.v.head + d, z);
+                }
+    }
+    if (!j.any) return;
+    const uint8_t* src = unit_ptr(a.P, a.S, j, a.status);
+    if (!src) return;
+    for (int i = lane; i < a.P.unit_bytes / 16; i += 32) ((uint4*)buf)[i] = ((const uint4*)src)[i];
+    __syncwarp();
+    for (int b = 0; b < nb; ++b)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int t = g + 8 * r;
+            if (t < j.lo || t >= j.hi) continue;
+            float x[8];
+            if (a.has_k) {
+                const int i = 2 * b + r;
+                const uint32_t w = *(const uint32_t*)(buf + (i >> 2) * 512 + lane * 16 + (i & 3) * 4);
+                const float s = scale_value(buf[16 * D + t * nb + b]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = nib_value(w >> (4 * k), s);
+                store8(a.k, (j.row0 + t) * a.k.row + (int64_t)j.h * a.k.head + 32 * b + 8 * c, x);
+            }
+            if (a.has_v) {
+                const int cc = (t >> 1) & 3;
+                const float s = scale_value(buf[16 * D + D / 2 + ((cc * nb + b) * 2 + r) * 2 + (t & 1)]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int d = 32 * b + 8 * c + k, i = d >> 4;
+                    const uint32_t y = buf[8 * D + (i >> 2) * 512 + ((d & 7) * 4 + cc) * 16 + (i & 3) * 4 + ((d >> 3) & 1) + 2 * r];
+                    x[k] = nib_value(y >> (4 * (t & 1)), s);
+                }
+                store8(a.v, (j.row0 + t) * a.v.row + (int64_t)j.h * a.v.head + 32 * b + 8 * c, x);
+            }
+        }
+}
+
+/* units that n consecutive tokens can touch */
+static int units_of(int n) { return (n + 14) / kUnit + 1; }
+
+/* ============================================================ page operations */
+/* What a plan leaves in `work` for the copy kernel: the number of copies, then
+ * (source page, destination page, units per head) triples.  A fork has at most one copy
+ * per sequence, a compaction at most n_pages / 2. */
+struct PlanArgs {
+    Pool P;
+    const int32_t *table, *lens, *refs, *parents, *grow;
+    int32_t *table_out, *lens_out, *refs_out, *map;
+    int64_t in_stride, out_stride;
+    int32_t n_in, n_out;
+    int32_t* count;     /* [1] */
+    int32_t* copies;    /* [.][3] */
+    int32_t *first;     /* [n_in] lowest child, or n_out */
+    int32_t *kept, *need, *begin; /* [n_out] pages shared, pages in all, first new page's rank */
+    int* status;
+};
+
+constexpr int kPlanThreads = 1024;
+
+/* Exclusive scan of one value per thread over the CTA; *total gets the sum. */
+__device__ __forceinline__ int block_scan(int v, int* total, int* tmp /* [33] */) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kAll, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) tmp[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int y = tmp[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int z = __shfl_up_sync(kAll, y, o);
+            if (lane >= o) y += z;
+        }
+        tmp[lane] = y;
+        if (lane == 31) tmp[32] = y;
+    }
+    __syncthreads();
+    *total = tmp[32];
+    return x - v + (warp ? tmp[warp - 1] : 0);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const __grid_constant__ PlanArgs a) {
+    __shared__ int tmp[33];
+    __shared__ int free_total, n_copies;
+    const int tid = threadIdx.x, T = 1 << a.P.page_shift;
+    const int64_t in_cap = a.in_stride << a.P.page_shift;
+    grid_dep_launch();
+    grid_dep_wait();
+    for (int i = tid; i < a.P.n_pages; i += kPlanThreads) a.refs_out[i] = a.refs[i];
+    for (int i = tid; i < a.n_in; i += kPlanThreads) a.first[i] = a.n_out;
+    if (tid == 0) n_copies = 0;
+    __syncthreads();
+    auto len_in = [&](int s) {
+        const int64_t n = a.lens[s];
+        return (int)(n < 0 ? 0 : n > in_cap ? in_cap : n);
+    };
+    auto parent_of = [&](int i) {
+        const int p = a.parents ? a.parents[i] : i;
+        return p < 0 || p >= a.n_in ? -1 : p;
+    };
+    auto page_in = [&](int s, int k) {
+        const int p = a.table[(int64_t)s * a.in_stride + k];
+        return p < 0 || p >= a.P.n_pages ? -1 : p;
+    };
+    for (int i = tid; i < a.n_out; i += kPlanThreads) {
+        const int p = parent_of(i);
+        if (p >= 0) atomicMin(&a.first[p], i);
+        else if (a.parents && (a.parents[i] < -1 || a.parents[i] >= a.n_in)) flag_corrupt(a.status);
+    }
+    __syncthreads();
+    /* pages shared and wanted */
+    int at = 0;
+    for (int base = 0; base < a.n_out; base += kPlanThreads) {
+        const int i = base + tid;
+        int want = 0;
+        if (i < a.n_out) {
+            const int p = parent_of(i);
+            int kept = 0, need = 0;
+            if (p >= 0) {
+                const int len = len_in(p);
+                const int64_t g = a.grow ? max(a.grow[i], 0) : 0;
+                const int64_t now = len + g;
+                kept = len / T + (len % T && a.first[p] == i ? 1 : 0);
+                const int64_t n = (now + T - 1) / T;
+                need = n > a.out_stride || now > 0x7FFFFFFF ? -1 : (int)n;
+                want = need < 0 ? 0 : need - kept;
+            }
+            a.kept[i] = kept;
+            a.need[i] = need;
+        }
+        int total;
+        const int x = block_scan(want, &total, tmp);
+        if (i < a.n_out) a.begin[i] = at + x;
+        at += total;
+    }
+    __syncthreads();
+    /* reference counts: sequences without a child give their pages up; children past the
+     * first add theirs (a first child takes its parent's place in every count) */
+    for (int s = tid >> 5; s < a.n_in; s += kPlanThreads / 32)
+        if (a.first[s] == a.n_out)
+            for (int k = tid & 31; k < (len_in(s) + T - 1) / T; k += 32) {
+                const int p = page_in(s, k);
+                if (p >= 0) atomicSub(&a.refs_out[p], 1);
+                else flag_corrupt(a.status);
+            }
+    for (int i = tid >> 5; i < a.n_out; i += kPlanThreads / 32) {
+        const int s = parent_of(i);
+        if (s < 0) continue;
+        for (int k = tid & 31; k < a.kept[i]; k += 32) {
+            const int p = page_in(s, k);
+            if (p < 0) flag_corrupt(a.status);
+            else if (a.first[s] != i) atomicAdd(&a.refs_out[p], 1);
+        }
+    }
+    __syncthreads();
+    /* how many pages are free; which sequences fit */
+    int mine = 0;
+    for (int i = tid; i < a.P.n_pages; i += kPlanThreads) mine += a.refs_out[i] == 0;
+    {
+        int total;
+        block_scan(mine, &total, tmp);
+        if (tid == 0) free_total = total;
+    }
+    __syncthreads();
+    const int F = free_total;
+    auto fits = [&](int i) { return a.need[i] >= 0 && (a.need[i] == a.kept[i] || a.begin[i] + (a.need[i] - a.kept[i]) <= F); };
+    /* the free pages in ascending order go to the ranks begin[i] .. */
+    int rank0 = 0;
+    for (int base = 0; base < a.P.n_pages && rank0 < at; base += kPlanThreads) {
+        const int page = base + tid;
+        const int is = page < a.P.n_pages && a.refs_out[page] == 0 ? 1 : 0;
+        int total;
+        const int r = rank0 + block_scan(is, &total, tmp);
+        if (is && r < at) {
+            int lo = 0, hi = a.n_out - 1; /* the last sequence that begins at r or before and wants something */
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (a.begin[mid] <= r) lo = mid;
+                else hi = mid - 1;
+            }
+            if (fits(lo)) {
+                a.table_out[(int64_t)lo * a.out_stride + a.kept[lo] + (r - a.begin[lo])] = page;
+                a.refs_out[page] = 1;
+            }
+        }
+        rank0 += total;
+        __syncthreads();
+    }
+    __syncthreads();
+    /* rows, lengths, copies */
+    for (int i = tid >> 5; i < a.n_out; i += kPlanThreads / 32) {
+        const int lane = tid & 31, s = parent_of(i);
+        const bool ok = fits(i);
+        int32_t* row = a.table_out + (int64_t)i * a.out_stride;
+        const int kept = a.kept[i], need = a.need[i];
+        for (int64_t k = lane; k < a.out_stride; k += 32) {
+            if (ok && k < kept) row[k] = a.table[(int64_t)s * a.in_stride + k];
+            else if (!ok || k >= need) row[k] = -1;
+        }
+        if (!ok)
+            for (int k = lane; k < kept; k += 32) {
+                const int p = page_in(s, k);
+                if (p >= 0) atomicSub(&a.refs_out[p], 1);
+            }
+        __syncwarp();
+        if (lane == 0) {
+            const int len = s >= 0 ? len_in(s) : 0;
+            a.lens_out[i] = !ok ? -1 : s < 0 ? 0 : len + (a.grow ? max(a.grow[i], 0) : 0);
+            if (ok && s >= 0 && len % T && a.first[s] != i) {
+                const int from = page_in(s, len / T);
+                if (from >= 0) {
+                    const int n = atomicAdd(&n_copies, 1);
+                    a.copies[3 * n] = from;
+                    a.copies[3 * n + 1] = row[kept];
+                    a.copies[3 * n + 2] = (len % T + kUnit - 1) / kUnit;
+                } else flag_corrupt(a.status);
+            }
+        }
+    }
+    __syncthreads();
+    if (tid == 0) *a.count = n_copies;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const __grid_constant__ PlanArgs a) {
+    __shared__ int tmp[33];
+    __shared__ int live_total;
+    const int tid = threadIdx.x, N = a.P.n_pages;
+    grid_dep_launch();
+    grid_dep_wait();
+    int mine = 0;
+    for (int i = tid; i < N; i += kPlanThreads) mine += a.refs[i] > 0;
+    {
+        int total;
+        block_scan(mine, &total, tmp);
+        if (tid == 0) live_total = total;
+    }
+    __syncthreads();
+    const int n = live_total;
+    int holes = 0, movers = 0;
+    for (int base = 0; base < N; base += kPlanThreads) {
+        const int i = base + tid;
+        const int ref = i < N ? a.refs[i] : 0;
+        const bool live = ref > 0, hole = i < n && !live, mover = live && i >= n;
+        int total;
+        const int x = block_scan((hole ? 1 : 0) | (mover ? 1 << 16 : 0), &total, tmp);
+        if (hole) a.copies[3 * (holes + (x & 0xFFFF)) + 1] = i;
+        if (mover) a.copies[3 * (movers + (x >> 16))] = i;
+        holes += total & 0xFFFF;
+        movers += total >> 16;
+        if (i < N) {
+            a.refs_out[i] = live && i < n ? ref : 0;
+            a.map[i] = live && i < n ? i : -1;
+        }
+    }
+    __syncthreads();
+    for (int k = tid; k < movers; k += kPlanThreads) {
+        const int src = a.copies[3 * k], dst = a.copies[3 * k + 1];
+        a.copies[3 * k + 2] = 1 << (a.P.page_shift - 4);
+        a.map[src] = dst;
+        a.refs_out[dst] = a.refs[src];
+    }
+    __syncthreads();
+    if (tid == 0) *a.count = movers;
+    for (int s = tid; s < a.n_in; s += kPlanThreads) a.lens_out[s] = a.lens[s];
+    const int64_t cells = (int64_t)a.n_in * a.out_stride;
+    for (int64_t k = tid; k < cells; k += kPlanThreads) {
+        const int64_t s = k / a.out_stride, col = k % a.out_stride;
+        const int p = col < a.in_stride ? a.table[s * a.in_stride + col] : -1;
+        a.table_out[k] = p >= 0 && p < N ? a.map[p] : p;
+    }
+}
+
+struct CopyArgs {
+    Pool P;
+    const int32_t* count;
+    const int32_t* copies;
+    int32_t heads;   /* heads of all layers */
+};
+
+/* A copy moves the first `units` units of every head of every layer of a page: runs of
+ * units * 17 D contiguous bytes, one CTA per (copy, head) run at a time. */
+constexpr int kCopyThreads = 256;
+__global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_constant__ CopyArgs a) {
+    grid_dep_launch();
+    grid_dep_wait();
+    const int64_t items = (int64_t)*a.count * a.heads;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const int64_t c = it / a.heads, h = it % a.heads;
+        const int64_t src = a.copies[3 * c], dst = a.copies[3 * c + 1];
+        const int n = a.copies[3 * c + 2] * (a.P.unit_bytes / 16);
+        const uint4* s = (const uint4*)(a.P.base + src * a.P.page_bytes + h * a.P.head_bytes);
+        uint4* d = (uint4*)(a.P.base + dst * a.P.page_bytes + h * a.P.head_bytes);
+        for (int i = threadIdx.x; i < n; i += 4 * kCopyThreads) {
+            uint4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i + k * kCopyThreads < n) v[k] = s[i + k * kCopyThreads];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i + k * kCopyThreads < n) d[i + k * kCopyThreads] = v[k];
+        }
+    }
+}
+
+static size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+/* work: count (16 bytes) | copies | first, kept, need, begin (fork) or map (compact) */
+static size_t pages_work(const ec_kv* C, int64_t n_in, int64_t n_out) {
+    const size_t fork = 16 + align16(12 * (size_t)n_out) + align16(4 * (size_t)n_in) + 3 * align16(4 * (size_t)n_out);
+    const size_t compact = 16 + align16(12 * ((size_t)C->p.n_pages / 2 + 1)) + align16(4 * (size_t)C->p.n_pages);
+    return fork > compact ? fork : compact;
+}
+
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    return a && b && na && nb && (const uint8_t*)a < (const uint8_t*)b + nb && (const uint8_t*)b < (const uint8_t*)a + na;
+}
+
+static int check_pages(const ec_kv* C, const ec_kv_seqs* from, const int32_t* refs, const ec_kv_seqs* to,
+                       const int32_t* refs_out, const void* work, size_t work_bytes) {
+    if (!C) return EC_ERR_INVALID_ARG;
+    int rc = check_seqs(from);
+    if (rc == EC_OK) rc = check_seqs(to);
+    if (rc != EC_OK) return rc;
+    if (!refs || !refs_out || !work || (uintptr_t)work % 16) return EC_ERR_INVALID_ARG;
+    if (work_bytes < pages_work(C, from->n_seqs, to->n_seqs)) return EC_ERR_INVALID_ARG;
+    const size_t in = sizeof(int32_t) * (size_t)(from->n_seqs * from->table_stride), nr = sizeof(int32_t) * (size_t)C->p.n_pages,
+                 out = sizeof(int32_t) * (size_t)(to->n_seqs * to->table_stride);
+    if (overlap(from->table, in, to->table, out) || overlap(refs, nr, refs_out, nr) ||
+        overlap(from->lens, sizeof(int32_t) * (size_t)from->n_seqs, to->lens, sizeof(int32_t) * (size_t)to->n_seqs))
+        return EC_ERR_INVALID_ARG;
+    return EC_OK;
+}
+
+static int run_copies(const ec_kv* C, const PlanArgs& a, int64_t most, const Device& d, cudaStream_t stream) {
+    CopyArgs c{};
+    c.P = a.P;
+    c.count = a.count;
+    c.copies = a.copies;
+    c.heads = C->p.n_layers * C->p.n_kv_heads;
+    const int64_t items = most * c.heads;
+    const int64_t full = (int64_t)d.sms * 8;
+    const int grid = (int)(items < 1 ? 1 : items < full ? items : full);
+    return launch(kv_copy_kernel, dim3(grid), kCopyThreads, 0, stream, c);
+}
+
+}  // namespace kv
+
+using namespace kv;
+
+/* ============================================================ C ABI */
+static int check_params(const ec_kv_params* p, size_t* bytes) {
+    if (!p) return EC_ERR_INVALID_ARG;
+    if (p->n_layers < 1 || p->n_kv_heads < 1 || p->head_dim < 1 || p->page_tokens < 1 || p->n_pages < 1) return EC_ERR_SHAPE;
+    if (p->n_layers > 1024 || p->n_kv_heads > 1024 || p->n_pages > (int64_t(1) << 30)) return EC_ERR_UNSUPPORTED;
+    if (p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 192 && p->head_dim != 256) return EC_ERR_UNSUPPORTED;
+    if (p->page_tokens != 16 && p->page_tokens != 32 && p->page_tokens != 64 && p->page_tokens != 128 && p->page_tokens != 256)
+        return EC_ERR_UNSUPPORTED;
+    /* at most 1024 * 1024 * 16 * 4352 < 2^37 bytes per page, 2^30 pages: checked before the product */
+    const int64_t page = (int64_t)p->n_layers * p->n_kv_heads * (p->page_tokens / kUnit) * 17 * p->head_dim;
+    if (p->n_pages > (int64_t(1) << 62) / page) return EC_ERR_OVERFLOW;
+    *bytes = (size_t)(page * p->n_pages);
+    return EC_OK;
+}
+
+extern "C" int ec_kv_pool_bytes(const ec_kv_params* params, size_t* bytes) {
+    if (!bytes) return EC_ERR_INVALID_ARG;
+    return check_params(params, bytes);
+}
+
+extern "C" int ec_kv_create(const ec_kv_params* params, void* pool, size_t pool_bytes, int device, ec_kv** out) {
+    if (!out) return EC_ERR_INVALID_ARG;
+    *out = nullptr;
+    size_t need = 0;
+    const int rc = check_params(params, &need);
+    if (rc != EC_OK) return rc;
+    if (device >= 0) {
+        if (!pool || (uintptr_t)pool % 16 || pool_bytes < need) return EC_ERR_INVALID_ARG;
+        int n = 0;
+        if (cudaGetDeviceCount(&n) != cudaSuccess) return EC_ERR_CUDA;
+        if (device >= n) return EC_ERR_INVALID_ARG;
+    }
+    ec_kv* C = new (std::nothrow) ec_kv;
+    if (!C) return EC_ERR_OOM;
+    C->p = *params;
+    C->pool = device >= 0 ? (uint8_t*)pool : nullptr;
+    C->device = device;
+    *out = C;
+    return EC_OK;
+}
+
+extern "C" void ec_kv_free(ec_kv* C) { delete C; }
+
+extern "C" int ec_kv_append(const ec_kv* C, int layer, const ec_kv_seqs* seqs, const int32_t* starts, int64_t n_rows,
+                            int max_new, const ec_kv_rows* k, const ec_kv_rows* v, cudaStream_t stream) {
+    AppendArgs a{};
+    bool go = false;
+    int rc = check_call(C, layer, seqs, starts, n_rows, max_new, &a.P, &a.S, &go);
+    if (rc == EC_OK) rc = check_rows(C, k, a.P.n_heads, n_rows, &a.k);
+    if (rc == EC_OK) rc = check_rows(C, v, a.P.n_heads, n_rows, &a.v);
+    if (rc != EC_OK) return rc;
+    Device d;
+    if ((rc = device_of(C, &d)) != EC_OK) return rc;
+    if (!go) return EC_OK;
+    a.units = units_of(max_new);
+    a.max_new = max_new;
+    a.status = d.status;
+    const int64_t items = (int64_t)a.S.n_seqs * a.units * a.P.n_heads, grid = (items + kIoWarps - 1) / kIoWarps;
+    if (grid > 0x7FFFFFFF) return EC_ERR_UNSUPPORTED;
+    return launch(kv_append_kernel, dim3((unsigned)grid), kIoWarps * 32, (size_t)kIoWarps * a.P.unit_bytes, stream, a);
+}
+
+extern "C" int ec_kv_read(const ec_kv* C, int layer, const ec_kv_seqs* seqs, const int32_t* starts, int64_t n_rows,
+                          int max_new, const ec_kv_rows* k, const ec_kv_rows* v, cudaStream_t stream) {
+    ReadArgs a{};
+    bool go = false;
+    int rc = check_call(C, layer, seqs, starts, n_rows, max_new, &a.P, &a.S, &go);
+    if (rc == EC_OK && !k && !v) rc = EC_ERR_INVALID_ARG;
+    if (rc == EC_OK && k) rc = check_rows(C, k, a.P.n_heads, n_rows, &a.k);
+    if (rc == EC_OK && v) rc = check_rows(C, v, a.P.n_heads, n_rows, &a.v);
+    if (rc != EC_OK) return rc;
+    Device d;
+    if ((rc = device_of(C, &d)) != EC_OK) return rc;
+    if (!go) return EC_OK;
+    a.has_k = k != nullptr;
+    a.has_v = v != nullptr;
+    a.units = units_of(max_new);
+    a.max_new = max_new;
+    a.status = d.status;
+    const int64_t items = (int64_t)a.S.n_seqs * a.units * a.P.n_heads, grid = (items + kIoWarps - 1) / kIoWarps;
+    if (grid > 0x7FFFFFFF) return EC_ERR_UNSUPPORTED;
+    return launch(kv_read_kernel, dim3((unsigned)grid), kIoWarps * 32, (size_t)kIoWarps * a.P.unit_bytes, stream, a);
+}
+
+extern "C" int ec_kv_pages_work_bytes(const ec_kv* C, int n_from, int n_to, size_t* bytes) {
+    if (!C || !bytes) return EC_ERR_INVALID_ARG;
+    if (n_from < 0 || n_to < 0) return EC_ERR_SHAPE;
+    if (n_from > EC_KV_MAX_SEQS || n_to > EC_KV_MAX_SEQS) return EC_ERR_UNSUPPORTED;
+    *bytes = pages_work(C, n_from, n_to);
+    return EC_OK;
+}
+
+extern "C" int ec_kv_fork(const ec_kv* C, const ec_kv_seqs* from, const int32_t* refs, const int32_t* parents,
+                          const int32_t* grow, const ec_kv_seqs* to, int32_t* refs_out, void* work, size_t work_bytes,
+                          cudaStream_t stream) {
+    int rc = check_pages(C, from, refs, to, refs_out, work, work_bytes);
+    if (rc != EC_OK) return rc;
+    if (!parents && to->n_seqs > 0 && from->n_seqs != to->n_seqs) return EC_ERR_SHAPE;
+    PlanArgs a{};
+    if (!pool_view(C, 0, &a.P)) return EC_ERR_INVALID_ARG;
+    Device d;
+    if ((rc = device_of(C, &d)) != EC_OK) return rc;
+    a.table = from->table, a.lens = from->lens, a.refs = refs, a.parents = parents, a.grow = grow;
+    a.table_out = to->table, a.lens_out = to->lens, a.refs_out = refs_out;
+    a.in_stride = from->table_stride, a.out_stride = to->table_stride;
+    a.n_in = from->n_seqs, a.n_out = to->n_seqs;
+    uint8_t* w = (uint8_t*)work;
+    a.count = (int32_t*)w;
+    w += 16;
+    a.copies = (int32_t*)w;
+    w += align16(12 * (size_t)a.n_out);
+    a.first = (int32_t*)w;
+    w += align16(4 * (size_t)a.n_in);
+    a.kept = (int32_t*)w;
+    w += align16(4 * (size_t)a.n_out);
+    a.need = (int32_t*)w;
+    w += align16(4 * (size_t)a.n_out);
+    a.begin = (int32_t*)w;
+    a.status = d.status;
+    if ((rc = launch(kv_fork_plan_kernel, dim3(1), kPlanThreads, 0, stream, a)) != EC_OK) return rc;
+    return run_copies(C, a, a.n_out, d, stream);
+}
+
+extern "C" int ec_kv_compact(const ec_kv* C, const ec_kv_seqs* from, const int32_t* refs, const ec_kv_seqs* to,
+                             int32_t* refs_out, int32_t* map, void* work, size_t work_bytes, cudaStream_t stream) {
+    int rc = check_pages(C, from, refs, to, refs_out, work, work_bytes);
+    if (rc != EC_OK) return rc;
+    if (from->n_seqs != to->n_seqs) return EC_ERR_SHAPE;
+    if (to->table_stride < from->table_stride) return EC_ERR_SHAPE;
+    const size_t nr = sizeof(int32_t) * (size_t)C->p.n_pages;
+    if (overlap(map, nr, refs, nr) || overlap(map, nr, refs_out, nr)) return EC_ERR_INVALID_ARG;
+    PlanArgs a{};
+    if (!pool_view(C, 0, &a.P)) return EC_ERR_INVALID_ARG;
+    Device d;
+    if ((rc = device_of(C, &d)) != EC_OK) return rc;
+    a.table = from->table, a.lens = from->lens, a.refs = refs;
+    a.table_out = to->table, a.lens_out = to->lens, a.refs_out = refs_out;
+    a.in_stride = from->table_stride, a.out_stride = to->table_stride;
+    a.n_in = from->n_seqs, a.n_out = to->n_seqs;
+    uint8_t* w = (uint8_t*)work;
+    a.count = (int32_t*)w;
+    w += 16;
+    a.copies = (int32_t*)w;
+    w += align16(12 * ((size_t)C->p.n_pages / 2 + 1));
+    a.map = map ? map : (int32_t*)w;
+    a.status = d.status;
+    if ((rc = launch(kv_compact_plan_kernel, dim3(1), kPlanThreads, 0, stream, a)) != EC_OK) return rc;
+    return run_copies(C, a, C->p.n_pages / 2 + 1, d, stream);
+}

@@ -1,0 +1,720 @@
+/*
+ * ec_kv_attn.cu -- attention of new tokens over the 4-bit cache (ec_kv_attend).
+ *
+ * For a query row q, head by head: s_t = scale q . k_t over the visible tokens, p = exp
+ * (s - m), o = sum p v / sum p.  All rows of a key/value head's query group, times a few
+ * new tokens, form the 8 or 16 columns of the products S^T = K Q^T and O^T = V^T P^T, so
+ * each 4-bit key or value is read from memory and expanded once for all of them.
+ */
+#include <float.h>
+
+#include "ec_kv_internal.h"
+
+namespace kv {
+
+constexpr int kWarps = 8;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct AttnArgs {
+    Pool P;
+    Seqs S;
+    Rows q, out;
+    float* lse;       /* [n_rows, n_q_heads] or NULL */
+    float* part;
+    int32_t n_q_heads, group;   /* query heads, per key/value head */
+    int32_t window, sinks;
+    float scale;
+    int32_t max_new;
+    int32_t solo;     /* one CTA per tile, no partial results */
+    int* status;
+};
+
+/* The keys that a sequence's new rows see, in units of 16 tokens: the sinks' units, then
+ * lo_u .. ceil(len / 16) - 1. */
+struct Span {
+    int len, m, row_tiles;
+    int sink_u, lo_u, units;   /* units >= 1 (one empty step where there is no token) */
+    int64_t row0;
+};
+
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int b, int rows_per_tile) {
+    const Seq q = seq_of(a.S, a.P.page_shift, b);
+    Span s;
+    s.len = q.len;
+    s.m = q.m;
+    s.row0 = q.row0;
+    s.row_tiles = (int)(((int64_t)q.m * a.group + rows_per_tile - 1) / rows_per_tile);
+    const int first = q.len - q.m; /* position of row 0; may be negative */
+    const int64_t lo = a.window ? (int64_t)first - a.window + 1 : 0;
+    s.lo_u = lo > 0 ? (int)min(lo / kUnit, (int64_t)((q.len + kUnit - 1) / kUnit)) : 0;
+    s.sink_u = min((a.sinks + kUnit - 1) / kUnit, s.lo_u);
+    s.units = max(1, s.sink_u + (q.len + kUnit - 1) / kUnit - s.lo_u);
+    return s;
+}
+
+/* Work in front of each sequence, in shared memory: pre[b] = units of all tiles of the
+ * sequences before b.  Every thread of the CTA takes part; one warp scans. */
+__device__ __forceinline__ void scan_seqs(const AttnArgs& a, int rows_per_tile, int64_t* pre, bool flag) {
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x < 32) {
+        int64_t at = 0;
+        for (int base = 0; base < a.S.n_seqs; base += 32) {
+            const int b = base + lane;
+            int64_t n = 0;
+            if (b < a.S.n_seqs) {
+                const Span s = span_of(a, b, rows_per_tile);
+                if (flag && (s.m > a.max_new || seq_of(a.S, a.P.page_shift, b).bad)) flag_corrupt(a.status);
+                n = (int64_t)s.row_tiles * a.P.n_heads * (a.solo ? 1 : s.units);
+            }
+            int64_t x = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(kAll, x, o);
+                if (lane >= o) x += y;
+            }
+            if (b < a.S.n_seqs) pre[b] = at + x - n;
+            at += __shfl_sync(kAll, x, 31);
+        }
+        if (lane == 0) pre[a.S.n_seqs] = at;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ int find_seq(const int64_t* pre, int n, int64_t x) {
+    int lo = 0, hi = n - 1; /* the last sequence whose work begins at x or before, and has some */
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (pre[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *(const uint32_t*)&h;
+}
+
+/* Bits of the probabilities: p is held as 2^kBias p in FP16, the running reference of a
+ * row moves only when a score passes it by more than kSlack (powers of two), and value
+ * scales lie up to 2^7 above their block's reference: 2^(6 + 2 + 7) < 65504. */
+constexpr float kBias = 6.f, kSlack = 2.f;
+
+template <int NB>
+__host__ __device__ constexpr int stages_of() { return NB == 2 ? 6 : NB == 8 ? 3 : 4; }
+template <int NB>
+__host__ __device__ constexpr size_t attn_smem(int n_seqs) {
+    return (size_t)kWarps * stages_of<NB>() * 17 * 32 * NB + (size_t)kWarps * stages_of<NB>() * 8 + 8 * ((size_t)n_seqs + 1);
+}
+
+template <int NB>
+__device__ __forceinline__ void key_scales(uint32_t row, uint32_t (&w)[(NB + 3) / 4]) {
+    if constexpr (NB % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < NB / 4; ++i) w[i] = lds32(row + 4 * i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) {
+            unsigned short v;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(row + 2 * i) : "memory");
+            if (i % 2 == 0) w[i / 2] = v;
+            else w[i / 2] |= (uint32_t)v << 16;
+        }
+    }
+}
+
+/* One CTA per share of the work (or per tile): see the launch.  Per unit and warp: S^T
+ * tile by tile of 32 channels (each with its own scale, applied to the FP32 products),
+ * softmax weights against a lazily moved reference, O^T with the value scales folded into
+ * the FP16 weights. */
+template <int NB, int NT, int QT>
+__global__ void __launch_bounds__(kWarps * 32, NB <= 6 && NB * NT <= 8 ? 2 : 1) kv_attn_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int D = 32 * NB, RB = 8 * NT, S = stages_of<NB>(), UB = 17 * D, LD = D + 4;
+    extern __shared__ __align__(128) uint8_t at_smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const uint32_t ring = smem_u32(at_smem) + warp * (S * UB);
+    const uint32_t bars = smem_u32(at_smem) + kWarps * S * UB + warp * S * 8;
+    int64_t* pre = (int64_t*)(at_smem + kWarps * S * UB + kWarps * S * 8);
+    float* merge = (float*)at_smem; /* per warp [RB][LD], m[RB], l[RB], in the ring's place */
+    constexpr int MW = S * UB / 4;
+    static_assert(RB * LD + 2 * RB <= MW, "the merge area lies in the ring");
+    if (lane == 0) {
+        for (int s = 0; s < S; ++s) mbar_init(bars + 8 * s, 1);
+        mbar_fence_init();
+    }
+    grid_dep_launch();
+    grid_dep_wait();
+    scan_seqs(a, RB, pre, blockIdx.x == 0);
+    const int64_t X = pre[a.S.n_seqs];
+    int64_t share = 1;
+    if (!a.solo) {
+        share = (X + gridDim.x - 1) / gridDim.x;
+        if (share < kWarps) share = kWarps;
+    }
+    int64_t x = blockIdx.x * share;
+    const int64_t x_end = min(X, x + share);
+    uint32_t phase = 0; /* one bit per stage */
+    bool live = true;
+
+    while (x < x_end) {
+        const int b = find_seq(pre, a.S.n_seqs, x);
+        const Span sp = span_of(a, b, RB);
+        const int64_t local = x - pre[b];
+        const int tile = (int)(a.solo ? local : local / sp.units);
+        const int u0 = a.solo ? 0 : (int)(local % sp.units);
+        const int u1 = a.solo ? sp.units : (int)min((int64_t)sp.units, u0 + (x_end - x));
+        x += a.solo ? 1 : u1 - u0;
+        const int h = tile % a.P.n_heads, r0 = tile / a.P.n_heads * RB;
+        const int R = sp.m * a.group, first = sp.len - sp.m;
+        const int real_units = sp.len > 0 ? sp.units : 0;
+        const int n = max(0, min(u1, real_units) - u0 - warp + kWarps - 1) / kWarps; /* this warp's units */
+
+        /* the copies of the first units start before the queries are read */
+        int page_of = 0; /* lane l: page of this warp's unit 32 j + l */
+        auto unit_at = [&](int k) {
+            const int u = u0 + warp + k * kWarps;
+            return u < sp.sink_u ? u : u - sp.sink_u + sp.lo_u;
+        };
+        auto issue = [&](int k) {
+            if ((k & 31) == 0) {
+                const int kk = k + lane;
+                page_of = 0;
+                if (kk < n) {
+                    page_of = a.S.table[(int64_t)b * a.S.table_stride + (unit_at(kk) >> (a.P.page_shift - 4))];
+                    if (page_of < 0 || page_of >= a.P.n_pages) {
+                        page_of = 0;
+                        flag_corrupt(a.status);
+                    }
+                }
+            }
+            const int page = __shfl_sync(kAll, page_of, k & 31);
+            if (lane == 0) {
+                const int s = k % S;
+                mbar_arrive_tx(bars + 8 * s, UB);
+                bulk_g2s(ring + s * UB, page_ptr(a.P, page, h, unit_at(k) & ((1 << (a.P.page_shift - 4)) - 1)), UB, bars + 8 * s);
+            }
+        };
+        for (int k = 0; k < min(n, S); ++k) issue(k);
+
+        /* queries: lane 4 g + c holds row g's channels 32 b + 8 c + 0..7, scaled by a power
+         * of two so that the row's largest lies in [2^14, 2^15): BF16 and FP16 rows are
+         * exact in one FP16 part but for elements 2^-28 of the row's largest, FP32 rows
+         * take two parts (22 bits) */
+        uint32_t qf[NT][QT][NB][4];
+        float fac[NT][2];
+        int pos[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int r = r0 + 8 * t + g;
+            const bool on = r < R;
+            const int64_t off = on ? (sp.row0 + r / a.group) * a.q.row + (int64_t)(h * a.group + r % a.group) * a.q.head : 0;
+            float xq[NB][8];
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) xq[k][i] = 0.f;
+                if (on) {
+                    if (a.q.wide && a.q.dtype == EC_DTYPE_FP32) {
+                        const float4* p = (const float4*)((const float*)a.q.data + off + 32 * k + 8 * c);
+                        const float4 u = p[0], v = p[1];
+                        xq[k][0] = u.x, xq[k][1] = u.y, xq[k][2] = u.z, xq[k][3] = u.w;
+                        xq[k][4] = v.x, xq[k][5] = v.y, xq[k][6] = v.z, xq[k][7] = v.w;
+                    } else if (a.q.wide) {
+                        const uint4 w = *(const uint4*)((const uint16_t*)a.q.data + off + 32 * k + 8 * c);
+                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (a.q.dtype == EC_DTYPE_FP16) {
+                                const float2 f = __half22float2(*(const __half2*)&u[i]);
+                                xq[k][2 * i] = f.x, xq[k][2 * i + 1] = f.y;
+                            } else {
+                                xq[k][2 * i] = __uint_as_float(u[i] << 16);
+                                xq[k][2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) xq[k][i] = load_elem(a.q, off + 32 * k + 8 * c + i);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(xq[k][i]) & 0x7FFFFFFFu);
+            }
+            top = max(top, __shfl_xor_sync(kAll, top, 1));
+            top = max(top, __shfl_xor_sync(kAll, top, 2));
+            const int E = (int)(top >> 23);
+            const int up = E == 255 ? 127 : min(253, 268 - E);
+            const float s = __uint_as_float((uint32_t)up << 23);
+            const float inv = __uint_as_float((uint32_t)(254 - up) << 23) * a.scale * kLog2e;
+#pragma unroll
+            for (int k = 0; k < NB; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float y0 = xq[k][2 * i] * s, y1 = xq[k][2 * i + 1] * s;
+                    qf[t][0][k][i] = pack_f16(y0, y1);
+                    if constexpr (QT == 2) {
+                        const float2 hi = __half22float2(*(const __half2*)&qf[t][0][k][i]);
+                        qf[t][QT - 1][k][i] = pack_f16(y0 - hi.x, y1 - hi.y);
+                    }
+                }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                fac[t][j] = __shfl_sync(kAll, inv, 8 * c + 4 * j);
+                pos[t][j] = first + min(r0 + 8 * t + 2 * c + j, R - 1) / a.group;
+            }
+        }
+        const int pos_lo = first + min(r0, R - 1) / a.group, pos_hi = first + min(r0 + RB - 1, R - 1) / a.group;
+
+        float o[NT][2 * NB][4];
+        float m[NT][2], l[NT][2];
+        int ref[NB];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[t][i][j] = 0.f;
+            m[t][0] = m[t][1] = -FLT_MAX;
+            l[t][0] = l[t][1] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < NB; ++k) ref[k] = -8; /* any scale passes it: the first unit sets it */
+
+        for (int k = 0; k < n; ++k) {
+            const int st = k % S;
+            const uint32_t buf = ring + st * UB;
+            if (live && !mbar_wait(bars + 8 * st, (phase >> st) & 1u)) {
+                live = false;
+                if (lane == 0) flag_corrupt(a.status);
+            }
+            phase ^= 1u << st;
+            const int tok = unit_at(k) * kUnit;
+
+            /* S^T: rows = tokens g, g + 8, columns = query rows 2c, 2c + 1 */
+            float s[NT][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[t][j] = 0.f;
+            uint32_t ka[(NB + 3) / 4], kb[(NB + 3) / 4];
+            key_scales<NB>(buf + 16 * D + g * NB, ka);
+            key_scales<NB>(buf + 16 * D + (g + 8) * NB, kb);
+#pragma unroll
+            for (int i4 = 0; i4 < NB / 2; ++i4) {
+                const uint4 w = lds128(buf + i4 * 512 + lane * 16);
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int bb = 0; bb < 2; ++bb) {
+                    const int blk = 2 * i4 + bb;
+                    uint32_t ra[4], rb[4];
+                    e2m1x8_f16(ww[2 * bb], ra);
+                    e2m1x8_f16(ww[2 * bb + 1], rb);
+                    const float sa = __uint_as_float(((ka[blk / 4] >> (8 * (blk % 4))) & 0xFFu) << 23);
+                    const float sb = __uint_as_float(((kb[blk / 4] >> (8 * (blk % 4))) & 0xFFu) << 23);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int q = 0; q < QT; ++q) {
+                            mma16816(d, ra[0], rb[0], ra[1], rb[1], qf[t][q][blk][0], qf[t][q][blk][1]);
+                            mma16816(d, ra[2], rb[2], ra[3], rb[3], qf[t][q][blk][2], qf[t][q][blk][3]);
+                        }
+                        s[t][0] = fmaf(d[0], sa, s[t][0]);
+                        s[t][1] = fmaf(d[1], sa, s[t][1]);
+                        s[t][2] = fmaf(d[2], sb, s[t][2]);
+                        s[t][3] = fmaf(d[3], sb, s[t][3]);
+                    }
+                }
+            }
+            const bool all = tok + kUnit - 1 <= pos_lo && (!a.window || tok > pos_hi - a.window || tok + kUnit - 1 < a.sinks);
+            uint32_t vmask = 0xFFFFFFFFu; /* bytes: tokens 2c, 2c + 1, 2c + 8, 2c + 9 that some row sees */
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[t][j] *= fac[t][j & 1];
+            if (!all) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int at = tok + g + 8 * (j >> 1), p = pos[t][j & 1];
+                        const bool see = at <= p && (!a.window || at > p - a.window || at < a.sinks);
+                        if (!see) s[t][j] = -INFINITY;
+                    }
+                vmask = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int at = tok + 2 * c + (j & 1) + 8 * (j >> 1);
+                    if (at <= pos_hi && (!a.window || at > pos_lo - a.window || at < a.sinks)) vmask |= 0xFFu << (8 * j);
+                }
+            }
+
+            /* the rows' references move when a score passes them by more than the slack */
+            bool move = false;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) move |= s[t][j] > m[t][j & 1] + kSlack;
+            if (__any_sync(kAll, move)) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float mx = fmaxf(s[t][j], s[t][j + 2]);
+#pragma unroll
+                        for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, w));
+                        const float nm = fmaxf(m[t][j], mx), al = ex2(m[t][j] - nm);
+                        m[t][j] = nm;
+                        l[t][j] *= al;
+#pragma unroll
+                        for (int i = 0; i < 2 * NB; ++i) {
+                            o[t][i][j] *= al;
+                            o[t][i][j + 2] *= al;
+                        }
+                    }
+            }
+            /* weights, and their transposition into the second product's operand */
+            uint32_t p0[NT], p1[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float p[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    p[j] = ex2(s[t][j] - (m[t][j & 1] - kBias));
+                    l[t][j & 1] += p[j];
+                }
+                p0[t] = transpose8x8(pack_f16(p[0], p[1]));
+                p1[t] = transpose8x8(pack_f16(p[2], p[3]));
+            }
+
+            /* value scales 2^(e - ref) as FP16 pairs: exponent field z - 9 = e - ref + 15,
+             * 0 where that is not positive; z >= 32 means more than 2^7 above the reference */
+            uint32_t vw[NB], z0[NB], z1[NB], over = 0;
+#pragma unroll
+            for (int i = 0; i < NB / 2; ++i) {
+                const uint32_t at = buf + 16 * D + D / 2 + (c * NB + 2 * i) * 4;
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vw[2 * i]), "=r"(vw[2 * i + 1]) : "r"(at) : "memory");
+            }
+#pragma unroll
+            for (int k2 = 0; k2 < NB; ++k2) {
+                vw[k2] &= vmask;
+                const uint32_t add = (uint32_t)(24 - ref[k2]) * 0x10001u; /* two halves; |24 - ref| < 2^15 */
+                const uint32_t add2 = ref[k2] > 24 ? add + 0x10000u : add; /* a negative low half borrows from the high one */
+                z0[k2] = __viaddmax_s16x2(__byte_perm(vw[k2], 0, 0x4140), add2, 0x00090009u);
+                z1[k2] = __viaddmax_s16x2(__byte_perm(vw[k2], 0, 0x4342), add2, 0x00090009u);
+                over |= z0[k2] | z1[k2];
+            }
+            bool bad = false;
+            if (__any_sync(kAll, (over & 0xFFE0FFE0u) != 0)) {
+#pragma unroll
+                for (int k2 = 0; k2 < NB; ++k2) {
+                    int mx = -8;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int e = (vw[k2] >> (8 * j)) & 0xFF;
+                        if (e != 255 && ((vmask >> (8 * j)) & 1u)) mx = max(mx, e);
+                        bad |= e == 255;
+                    }
+                    mx = __reduce_max_sync(kAll, mx);
+                    if (mx > ref[k2]) {
+                        const float f = ref[k2] < 0 ? 0.f : ex2((float)(ref[k2] - mx));
+                        ref[k2] = mx;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                o[t][2 * k2][j] *= f;
+                                o[t][2 * k2 + 1][j] *= f;
+                            }
+                    }
+                    const int r = 24 - ref[k2];
+                    z0[k2] = z1[k2] = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int e = (vw[k2] >> (8 * j)) & 0xFF;
+                        const uint32_t z = e == 255 ? 9u : (uint32_t)max(e + r, 9);
+                        if (j < 2) z0[k2] |= z << (16 * j);
+                        else z1[k2] |= z << (16 * (j - 2));
+                    }
+                }
+                bad = __any_sync(kAll, bad);
+            }
+
+            /* O^T: rows = channels, columns = query rows */
+#pragma unroll
+            for (int i4 = 0; i4 < NB / 2; ++i4) {
+                const uint4 w = lds128(buf + 8 * D + i4 * 512 + lane * 16);
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int bb = 0; bb < 2; ++bb) {
+                    const int blk = 2 * i4 + bb;
+                    uint32_t s0 = z0[blk] * 1024u - 0x24002400u, s1 = z1[blk] * 1024u - 0x24002400u;
+                    uint32_t b0[NT], b1[NT];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        b0[t] = hmul2(p0[t], s0);
+                        b1[t] = hmul2(p1[t], s1);
+                    }
+                    if (bad) { /* a block of NaN makes its channels NaN for every row that sees the token */
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                if (((vw[blk] >> (8 * j)) & 0xFFu) != 255u) continue;
+                                const int at = tok + 2 * c + (j & 1) + 8 * (j >> 1);
+                                const int p = first + min(r0 + 8 * t + g, R - 1) / a.group;
+                                if (at > p || (a.window && at <= p - a.window && at >= a.sinks)) continue;
+                                (j < 2 ? b0[t] : b1[t]) |= 0x7FFFu << (16 * (j & 1));
+                            }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t ra[4];
+                        e2m1x8_f16(ww[2 * bb + j], ra);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) mma16816(o[t][2 * blk + j], ra[0], ra[1], ra[2], ra[3], b0[t], b1[t]);
+                    }
+                }
+            }
+            __syncwarp(); /* every lane has read the stage */
+            if (k + S < n) issue(k + S);
+        }
+
+        /* merge the warps */
+        __syncthreads();
+        float* mine = merge + warp * MW;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float ls = l[t][j];
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) ls += __shfl_xor_sync(kAll, ls, w);
+                const int r = 8 * t + 2 * c + j;
+                if (g == 0) {
+                    mine[RB * LD + r] = m[t][j];
+                    mine[RB * LD + RB + r] = ls;
+                }
+#pragma unroll
+                for (int i = 0; i < 2 * NB; ++i) {
+                    const float f = ref[i / 2] > 0 ? __uint_as_float((uint32_t)ref[i / 2] << 23) : 0.f;
+                    /* ref = 0 or -8: nothing but blocks of zeros so far (a NaN there stays one) */
+                    mine[r * LD + 16 * i + g] = o[t][i][j] * f;
+                    mine[r * LD + 16 * i + 8 + g] = o[t][i][j + 2] * f;
+                }
+            }
+        __syncthreads();
+        const bool whole = u0 == 0 && u1 == sp.units;
+        const int slot = u0 == 0 ? 1 : 0;
+        float* part = a.part + ((int64_t)blockIdx.x * 2 + slot) * (RB * (D + 2));
+        for (int e = threadIdx.x; e < RB * (D / 4); e += kWarps * 32) {
+            const int r = e / (D / 4), d = 4 * (e % (D / 4));
+            float M = -FLT_MAX;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, merge[w * MW + RB * LD + r]);
+            float L = 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = ex2(merge[w * MW + RB * LD + r] - M);
+                L = fmaf(merge[w * MW + RB * LD + RB + r], f, L);
+                const float4 y = *(const float4*)&merge[w * MW + r * LD + d];
+                v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
+            }
+            if (whole) {
+                if (r0 + r < R) {
+                    const int64_t row = sp.row0 + (r0 + r) / a.group;
+                    const int head = h * a.group + (r0 + r) % a.group;
+                    const float inv = L == 0.f ? 0.f : 1.f / L;
+                    const int64_t off = row * a.out.row + (int64_t)head * a.out.head + d;
+                    store_elem(a.out, off, v.x * inv);
+                    store_elem(a.out, off + 1, v.y * inv);
+                    store_elem(a.out, off + 2, v.z * inv);
+                    store_elem(a.out, off + 3, v.w * inv);
+                    if (d == 0 && a.lse) a.lse[row * a.n_q_heads + head] = L == 0.f ? -INFINITY : (M - kBias + log2f(L)) * kLn2;
+                }
+            } else {
+                *(float4*)&part[r * D + d] = v;
+                if (d == 0) {
+                    part[RB * D + r] = M;
+                    part[RB * D + RB + r] = L;
+                }
+            }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); /* the ring's next copies follow these accesses */
+        __syncthreads();
+    }
+}
+
+/* Join the partial results of a tile that several shares cover: CTA i looks at the tile
+ * in which share i ends; if it begins there, the CTA adds the shares' parts in order. */
+template <int NB, int NT>
+__global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ AttnArgs a, int grid) {
+    constexpr int D = 32 * NB, RB = 8 * NT, PS = RB * (D + 2);
+    extern __shared__ __align__(128) uint8_t at_smem[];
+    int64_t* pre = (int64_t*)at_smem;
+    grid_dep_launch();
+    grid_dep_wait();
+    scan_seqs(a, RB, pre, false);
+    const int64_t X = pre[a.S.n_seqs];
+    int64_t share = (X + grid - 1) / grid;
+    if (share < kWarps) share = kWarps;
+    const int64_t x0 = blockIdx.x * share, x1 = min(X, x0 + share);
+    if (x0 >= x1) return;
+    const int b = find_seq(pre, a.S.n_seqs, x1 - 1);
+    const Span sp = span_of(a, b, RB);
+    const int tile = (int)((x1 - 1 - pre[b]) / sp.units);
+    const int64_t t0 = pre[b] + (int64_t)tile * sp.units, t1 = t0 + sp.units;
+    if (t0 < x0 || t1 <= x1) return;
+    const int n = (int)((t1 - 1) / share) - (int)blockIdx.x + 1;
+    const int h = tile % a.P.n_heads, r0 = tile / a.P.n_heads * RB, R = sp.m * a.group;
+    const float* p0 = a.part + ((int64_t)blockIdx.x * 2 + 1) * PS;  /* the first share's part */
+    const float* p1 = a.part + ((int64_t)blockIdx.x * 2) * PS;      /* share i's: p1 + 2 i PS */
+    for (int e = threadIdx.x; e < RB * (D / 4); e += 256) {
+        const int r = e / (D / 4), d = 4 * (e % (D / 4));
+        if (r0 + r >= R) continue;
+        float M = p0[RB * D + r];
+        for (int i = 1; i < n; ++i) M = fmaxf(M, p1[(int64_t)2 * i * PS + RB * D + r]);
+        float L = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < n; ++i) {
+            const float* p = i ? p1 + (int64_t)2 * i * PS : p0;
+            const float f = ex2(p[RB * D + r] - M);
+            L = fmaf(p[RB * D + RB + r], f, L);
+            const float4 y = *(const float4*)&p[r * D + d];
+            v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
+        }
+        const int64_t row = sp.row0 + (r0 + r) / a.group;
+        const int head = h * a.group + (r0 + r) % a.group;
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const int64_t off = row * a.out.row + (int64_t)head * a.out.head + d;
+        store_elem(a.out, off, v.x * inv);
+        store_elem(a.out, off + 1, v.y * inv);
+        store_elem(a.out, off + 2, v.z * inv);
+        store_elem(a.out, off + 3, v.w * inv);
+        if (d == 0 && a.lse) a.lse[row * a.n_q_heads + head] = L == 0.f ? -INFINITY : (M - kBias + log2f(L)) * kLn2;
+    }
+}
+
+/* ------------------------------------------------------------ launch */
+struct Plan {
+    int nt, grid, solo;
+    size_t work;
+};
+
+static Plan plan_of(const ec_kv* C, int sms, int n_seqs, int max_new, int64_t max_len, const ec_kv_attn* at) {
+    Plan p;
+    const int group = at->n_q_heads / C->p.n_kv_heads, D = C->p.head_dim;
+    const int64_t rows = (int64_t)group * max_new;
+    p.nt = rows > 8 && D <= 128 ? 2 : 1;
+    int64_t units = (max_len + kUnit - 1) / kUnit;
+    if (at->window) {
+        const int64_t w = ((int64_t)at->window + max_new + kUnit) / kUnit + 1 + (at->sinks + kUnit - 1) / kUnit;
+        if (w < units) units = w;
+    }
+    /* up to 4 units per warp there is nothing to gain from splitting a tile */
+    p.solo = units <= 4 * kWarps;
+    const int64_t tiles = (int64_t)n_seqs * C->p.n_kv_heads * ((rows + 8 * p.nt - 1) / (8 * p.nt));
+    p.grid = p.solo ? (int)(tiles < 0x7FFFFFFF ? tiles : 0x7FFFFFFF) : sms * (D <= 128 ? 2 : D <= 192 ? 2 : 1);
+    p.work = p.solo ? 0 : (size_t)p.grid * 2 * (8 * p.nt) * (D + 2) * sizeof(float);
+    return p;
+}
+
+template <int NB, int NT, int QT>
+static int run_attn(const AttnArgs& a, const Plan& p, cudaStream_t stream) {
+    static SmemOnce once;
+    int rc = once.set(kv_attn_kernel<NB, NT, QT>, attn_smem<NB>(EC_KV_MAX_SEQS));
+    if (rc != EC_OK) return rc;
+    rc = launch(kv_attn_kernel<NB, NT, QT>, dim3(p.grid), kWarps * 32, attn_smem<NB>(a.S.n_seqs), stream, a);
+    if (rc == EC_OK && !p.solo) rc = launch(kv_join_kernel<NB, NT>, dim3(p.grid), 256, 8 * ((size_t)a.S.n_seqs + 1), stream, a, p.grid);
+    return rc;
+}
+
+template <int NB, int NT>
+static int run_terms(const AttnArgs& a, const Plan& p, cudaStream_t stream) {
+    return a.q.dtype == EC_DTYPE_FP32 ? run_attn<NB, NT, 2>(a, p, stream) : run_attn<NB, NT, 1>(a, p, stream);
+}
+
+static int check_attn(const ec_kv* C, int n_seqs, int64_t n_rows, int max_new, int64_t max_len, const ec_kv_attn* at) {
+    if (!C || !at) return EC_ERR_INVALID_ARG;
+    if (n_seqs < 0 || n_rows < 0 || max_new < 0 || max_len < 0) return EC_ERR_SHAPE;
+    if (n_seqs > EC_KV_MAX_SEQS || max_new > (1 << 24) || at->n_q_heads > 65536) return EC_ERR_UNSUPPORTED;
+    if (at->n_q_heads < 1 || at->n_q_heads % C->p.n_kv_heads) return EC_ERR_SHAPE;
+    if (at->window < 0 || at->sinks < 0 || (at->sinks > 0 && at->window == 0)) return EC_ERR_INVALID_ARG;
+    if (!(at->scale >= 0.f) || at->scale > FLT_MAX) return EC_ERR_INVALID_ARG;
+    return EC_OK;
+}
+
+}  // namespace kv
+
+using namespace kv;
+
+extern "C" int ec_kv_attend_work_bytes(const ec_kv* C, int n_seqs, int64_t n_rows, int max_new, int64_t max_len,
+                                       const ec_kv_attn* attn, size_t* bytes) {
+    if (!bytes) return EC_ERR_INVALID_ARG;
+    int rc = check_attn(C, n_seqs, n_rows, max_new, max_len, attn);
+    if (rc != EC_OK) return rc;
+    int sms = 0, dev = 0;
+    if (C->pool) {
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return EC_ERR_CUDA;
+    } else sms = 152;
+    *bytes = plan_of(C, sms, n_seqs, max_new, max_len, attn).work;
+    return EC_OK;
+}
+
+extern "C" int ec_kv_attend(const ec_kv* C, int layer, const ec_kv_seqs* seqs, const int32_t* starts, int64_t n_rows,
+                            int max_new, int64_t max_len, const ec_kv_attn* attn, const ec_kv_rows* q, const ec_kv_rows* out,
+                            float* lse, void* work, size_t work_bytes, cudaStream_t stream) {
+    if (!C || !attn) return EC_ERR_INVALID_ARG;
+    int rc = check_seqs(seqs);
+    if (rc != EC_OK) return rc;
+    if (max_len == 0) max_len = seqs->table_stride * C->p.page_tokens;
+    if ((rc = check_attn(C, seqs->n_seqs, n_rows, max_new, max_len, attn)) != EC_OK) return rc;
+    if (!starts && n_rows < seqs->n_seqs) return EC_ERR_SHAPE;
+    AttnArgs a{};
+    if (!pool_view(C, layer, &a.P)) return EC_ERR_INVALID_ARG;
+    if ((rc = check_rows(C, q, attn->n_q_heads, n_rows, &a.q)) != EC_OK) return rc;
+    if ((rc = check_rows(C, out, attn->n_q_heads, n_rows, &a.out)) != EC_OK) return rc;
+    if (lse && (uintptr_t)lse % 4) return EC_ERR_INVALID_ARG;
+    Device d;
+    if ((rc = device_of(C, &d)) != EC_OK) return rc;
+    if (seqs->n_seqs == 0 || n_rows == 0 || max_new == 0) return EC_OK;
+    const Plan p = plan_of(C, d.sms, seqs->n_seqs, max_new, max_len, attn);
+    if (p.work && (!work || (uintptr_t)work % 16 || work_bytes < p.work)) return EC_ERR_INVALID_ARG;
+    a.S = Seqs{seqs->table, seqs->lens, starts, seqs->table_stride, n_rows, seqs->n_seqs};
+    a.lse = lse;
+    a.part = (float*)work;
+    a.n_q_heads = attn->n_q_heads;
+    a.group = attn->n_q_heads / C->p.n_kv_heads;
+    a.window = attn->window;
+    a.sinks = attn->sinks;
+    a.scale = attn->scale > 0.f ? attn->scale : 1.f / sqrtf((float)C->p.head_dim);
+    a.max_new = max_new;
+    a.solo = p.solo;
+    a.status = d.status;
+    switch (C->p.head_dim / 32) {
+        case 2: return p.nt == 1 ? run_terms<2, 1>(a, p, stream) : run_terms<2, 2>(a, p, stream);
+        case 4: return p.nt == 1 ? run_terms<4, 1>(a, p, stream) : run_terms<4, 2>(a, p, stream);
+        case 6: return run_terms<6, 1>(a, p, stream);
+        default: return run_terms<8, 1>(a, p, stream);
+    }
+}
