@@ -12,7 +12,6 @@
 
 namespace kv {
 
-constexpr int kWarps = 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttnArgs {
@@ -24,37 +23,35 @@ struct AttnArgs {
     int32_t n_q_heads, group;   /* query heads, per key/value head */
     int32_t window, sinks;
     float scale;
-    int32_t max_new;
-    int32_t solo;     /* one CTA per tile, no partial results */
+    int32_t max_new, max_len;
+    int32_t solo;     /* > 0: one CTA per tile, this many places of work each; 0: even shares */
     int* status;
 };
 
-/* The keys that a sequence's new rows see, in units of 16 tokens: the sinks' units, then
- * lo_u .. ceil(len / 16) - 1. */
-struct Span {
-    int len, m, row_tiles;
-    int sink_u, lo_u, units;   /* units >= 1 (one empty step where there is no token) */
-    int64_t row0;
-};
+/* Work is counted in units of 16 tokens of one tile (the rows of one key/value head's
+ * group, 8 or 16 at a time), plus kTileCost for a tile's queries and outputs. */
+constexpr int kTileCost = 6;
 
-__device__ __forceinline__ Span span_of(const AttnArgs& a, int b, int rows_per_tile) {
-    const Seq q = seq_of(a.S, a.P.page_shift, b);
+/* The keys that a sequence's new rows see, in units: the sinks' units, then lo_u ..
+ * ceil(len / 16) - 1. */
+struct Span {
+    int sink_u, lo_u, units;   /* units >= 1 (one empty step where there is no token) */
+};
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int len, int m) {
     Span s;
-    s.len = q.len;
-    s.m = q.m;
-    s.row0 = q.row0;
-    s.row_tiles = (int)(((int64_t)q.m * a.group + rows_per_tile - 1) / rows_per_tile);
-    const int first = q.len - q.m; /* position of row 0; may be negative */
-    const int64_t lo = a.window ? (int64_t)first - a.window + 1 : 0;
-    s.lo_u = lo > 0 ? (int)min(lo / kUnit, (int64_t)((q.len + kUnit - 1) / kUnit)) : 0;
+    const int all = (len + kUnit - 1) / kUnit;
+    const int64_t lo = a.window ? (int64_t)(len - m) - a.window + 1 : 0; /* first token of row 0's window */
+    s.lo_u = lo > 0 ? (int)min(lo / kUnit, (int64_t)all) : 0;
     s.sink_u = min((a.sinks + kUnit - 1) / kUnit, s.lo_u);
-    s.units = max(1, s.sink_u + (q.len + kUnit - 1) / kUnit - s.lo_u);
+    s.units = max(1, s.sink_u + all - s.lo_u);
     return s;
 }
+__device__ __forceinline__ int tile_cost(const AttnArgs& a, int units) { return a.solo ? a.solo : units + kTileCost; }
 
-/* Work in front of each sequence, in shared memory: pre[b] = units of all tiles of the
- * sequences before b.  Every thread of the CTA takes part; one warp scans. */
-__device__ __forceinline__ void scan_seqs(const AttnArgs& a, int rows_per_tile, int64_t* pre, bool flag) {
+/* Per sequence, in shared memory: pre[b], the work in front of it (pre[n_seqs]: all work),
+ * and {len, new tokens, first row, units}.  Every thread of the CTA takes part; one warp
+ * scans. */
+__device__ __forceinline__ void scan_seqs(const AttnArgs& a, int rows_per_tile, int64_t* pre, int4* info, bool flag) {
     const int lane = threadIdx.x & 31;
     if (threadIdx.x < 32) {
         int64_t at = 0;
@@ -62,9 +59,19 @@ __device__ __forceinline__ void scan_seqs(const AttnArgs& a, int rows_per_tile, 
             const int b = base + lane;
             int64_t n = 0;
             if (b < a.S.n_seqs) {
-                const Span s = span_of(a, b, rows_per_tile);
-                if (flag && (s.m > a.max_new || seq_of(a.S, a.P.page_shift, b).bad)) flag_corrupt(a.status);
-                n = (int64_t)s.row_tiles * a.P.n_heads * (a.solo ? 1 : s.units);
+                Seq q = seq_of(a.S, a.P.page_shift, b);
+                if (q.len > a.max_len) {
+                    q.len = a.max_len;
+                    q.bad = true;
+                }
+                if (q.m > a.max_new) {
+                    q.m = a.max_new;
+                    q.bad = true;
+                }
+                if (flag && q.bad) flag_corrupt(a.status);
+                const int units = span_of(a, q.len, q.m).units;
+                info[b] = make_int4(q.len, q.m, (int)q.row0, units);
+                n = (int64_t)((q.m * a.group + rows_per_tile - 1) / rows_per_tile) * a.P.n_heads * tile_cost(a, units);
             }
             int64_t x = n;
 #pragma unroll
@@ -80,14 +87,37 @@ __device__ __forceinline__ void scan_seqs(const AttnArgs& a, int rows_per_tile, 
     __syncthreads();
 }
 
-__device__ __forceinline__ int find_seq(const int64_t* pre, int n, int64_t x) {
-    int lo = 0, hi = n - 1; /* the last sequence whose work begins at x or before, and has some */
+/* Where a place of work lies: sequence, head, first row of the tile, units u0 .. u1 - 1 up
+ * to the place `end`, and the place of the tile's first unit (its name). */
+struct Seg {
+    int b, h, r0, u0, u1, units;
+    int64_t tile, next;
+};
+__device__ __forceinline__ Seg seg_at(const AttnArgs& a, const int64_t* pre, const int4* info, int rows_per_tile, int64_t x, int64_t end) {
+    int lo = 0, hi = a.S.n_seqs - 1; /* the last sequence whose work begins at x or before (those without any come before it) */
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
         if (pre[mid] <= x) lo = mid;
         else hi = mid - 1;
     }
-    return lo;
+    Seg s;
+    s.b = lo;
+    s.units = info[lo].w;
+    const uint32_t per = (uint32_t)tile_cost(a, s.units), local = (uint32_t)(x - pre[lo]), tile = local / per, off = local - tile * per;
+    s.tile = x - off;
+    s.next = min(s.tile + per, end);
+    s.u0 = min((int)off, s.units);
+    s.u1 = (int)min((int64_t)s.units, s.next - s.tile);
+    s.h = (int)(tile % (uint32_t)a.P.n_heads);
+    s.r0 = (int)(tile / (uint32_t)a.P.n_heads) * rows_per_tile;
+    return s;
+}
+
+/* The share of CTA i of n: places i * share .. . */
+__device__ __forceinline__ int64_t share_of(const AttnArgs& a, int64_t X, int n, int warps) {
+    if (a.solo) return a.solo;
+    const int64_t s = (X + n - 1) / n;
+    return max((s + warps - 1) / warps, (int64_t)4) * warps;
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -116,12 +146,21 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
  * scales lie up to 2^7 above their block's reference: 2^(6 + 2 + 7) < 65504. */
 constexpr float kBias = 6.f, kSlack = 2.f;
 
-template <int NB>
-__host__ __device__ constexpr int stages_of() { return NB == 2 ? 6 : NB == 8 ? 3 : 4; }
-template <int NB>
-__host__ __device__ constexpr size_t attn_smem(int n_seqs) {
-    return (size_t)kWarps * stages_of<NB>() * 17 * 32 * NB + (size_t)kWarps * stages_of<NB>() * 8 + 8 * ((size_t)n_seqs + 1);
-}
+/* Warps per CTA, CTAs per SM and stages of a warp's ring by the tile's registers; `keep`
+ * floats hold a warp's partial result of a tile: [rows][LD], maxima, sums. */
+template <int NB, int NT>
+struct Shape {
+    static constexpr int D = 32 * NB, RB = 8 * NT, LD = D + 4, UB = 17 * D;
+    static constexpr int W = NB <= 4 && NT == 1 ? 8 : 4;
+    static constexpr int CTAS = NT == 2 ? 3 : 2;
+    static constexpr int S = NB == 2 ? 6 : NB == 8 ? 3 : 4;
+    static constexpr int KEEP = RB * LD + 2 * RB;
+    static constexpr int WARP_BYTES = S * UB + KEEP * 4;
+    static_assert(KEEP * 4 <= S * UB, "a second partial result fits the ring");
+    static constexpr size_t smem(int n_seqs) {
+        return (size_t)W * WARP_BYTES + W * S * 8 + 2 * W * 8 + 2 * W * 4 + 16 * (size_t)n_seqs + 8 * ((size_t)n_seqs + 1) + 16;
+    }
+};
 
 template <int NB>
 __device__ __forceinline__ void key_scales(uint32_t row, uint32_t (&w)[(NB + 3) / 4]) {
@@ -139,78 +178,108 @@ __device__ __forceinline__ void key_scales(uint32_t row, uint32_t (&w)[(NB + 3) 
     }
 }
 
-/* One CTA per share of the work (or per tile): see the launch.  Per unit and warp: S^T
- * tile by tile of 32 channels (each with its own scale, applied to the FP32 products),
- * softmax weights against a lazily moved reference, O^T with the value scales folded into
- * the FP16 weights. */
+/* Four channels of a tile's row r from its unnormalised sums v, L relative to M. */
+__device__ __forceinline__ void write_row(const AttnArgs& a, int row0, int h, int r, int d, const float4& v, float M, float L) {
+    const int64_t row = row0 + r / a.group;
+    const int head = h * a.group + r % a.group;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int64_t off = row * a.out.row + (int64_t)head * a.out.head + d;
+    store_elem(a.out, off, v.x * inv);
+    store_elem(a.out, off + 1, v.y * inv);
+    store_elem(a.out, off + 2, v.z * inv);
+    store_elem(a.out, off + 3, v.w * inv);
+    if (d == 0 && a.lse) a.lse[row * a.n_q_heads + head] = L == 0.f ? -INFINITY : (M - kBias + log2f(L)) * kLn2;
+}
+
+/* Each CTA takes a share of the work (or one tile), each of its warps an even part of
+ * that: a run of units, which may cover the end of a tile, whole tiles and the begin of
+ * another.  Per unit: S^T, 32 channels at a time (each block with its own scale, applied
+ * to the FP32 products), weights against a lazily moved reference, O^T with the value
+ * scales folded into the FP16 weights.  A warp writes tiles that it has seen whole; parts
+ * meet in shared memory at the end, and what the CTA has not seen whole goes to `part`.
+ * Units come by bulk copies through a ring of the warp's own, several ahead and across
+ * tiles. */
 template <int NB, int NT, int QT>
-__global__ void __launch_bounds__(kWarps * 32, NB <= 6 && NB * NT <= 8 ? 2 : 1) kv_attn_kernel(const __grid_constant__ AttnArgs a) {
-    constexpr int D = 32 * NB, RB = 8 * NT, S = stages_of<NB>(), UB = 17 * D, LD = D + 4;
+__global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv_attn_kernel(const __grid_constant__ AttnArgs a) {
+    using H = Shape<NB, NT>;
+    constexpr int D = H::D, RB = H::RB, S = H::S, UB = H::UB, LD = H::LD, W = H::W;
     extern __shared__ __align__(128) uint8_t at_smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    const uint32_t ring = smem_u32(at_smem) + warp * (S * UB);
-    const uint32_t bars = smem_u32(at_smem) + kWarps * S * UB + warp * S * 8;
-    int64_t* pre = (int64_t*)(at_smem + kWarps * S * UB + kWarps * S * 8);
-    float* merge = (float*)at_smem; /* per warp [RB][LD], m[RB], l[RB], in the ring's place */
-    constexpr int MW = S * UB / 4;
-    static_assert(RB * LD + 2 * RB <= MW, "the merge area lies in the ring");
+    const uint32_t ring = smem_u32(at_smem) + warp * H::WARP_BYTES;
+    uint8_t* tail = at_smem + W * H::WARP_BYTES;
+    const uint32_t bars = smem_u32(tail) + warp * S * 8;
+    int64_t* slot_tile = (int64_t*)(tail + W * S * 8);   /* [2 W]: a warp's first and last partial tile, -1: none */
+    int32_t* slot_flags = (int32_t*)(slot_tile + 2 * W); /* bit 0: the tile's first unit is in, bit 1: its last */
+    int4* info = (int4*)(slot_flags + 2 * W);
+    int64_t* pre = (int64_t*)(info + a.S.n_seqs);
+    static_assert((W * S * 8 + 2 * W * 8 + 2 * W * 4) % 16 == 0, "info is 16-byte aligned");
     if (lane == 0) {
         for (int s = 0; s < S; ++s) mbar_init(bars + 8 * s, 1);
         mbar_fence_init();
+        slot_tile[2 * warp] = slot_tile[2 * warp + 1] = -1;
     }
     grid_dep_launch();
     grid_dep_wait();
-    scan_seqs(a, RB, pre, blockIdx.x == 0);
+    scan_seqs(a, RB, pre, info, blockIdx.x == 0);
     const int64_t X = pre[a.S.n_seqs];
-    int64_t share = 1;
-    if (!a.solo) {
-        share = (X + gridDim.x - 1) / gridDim.x;
-        if (share < kWarps) share = kWarps;
-    }
-    int64_t x = blockIdx.x * share;
-    const int64_t x_end = min(X, x + share);
-    uint32_t phase = 0; /* one bit per stage */
-    bool live = true;
+    const int64_t share = share_of(a, X, gridDim.x, W);
+    const int64_t x0 = min(X, blockIdx.x * share), x1 = min(X, x0 + share);
+    if (x0 >= x1) return;
+    int64_t x = min(x1, x0 + warp * (share / W));
+    const int64_t x_end = min(x1, x + share / W);
+    const int unit_mask = (1 << (a.P.page_shift - 4)) - 1;
 
-    while (x < x_end) {
-        const int b = find_seq(pre, a.S.n_seqs, x);
-        const Span sp = span_of(a, b, RB);
-        const int64_t local = x - pre[b];
-        const int tile = (int)(a.solo ? local : local / sp.units);
-        const int u0 = a.solo ? 0 : (int)(local % sp.units);
-        const int u1 = a.solo ? sp.units : (int)min((int64_t)sp.units, u0 + (x_end - x));
-        x += a.solo ? 1 : u1 - u0;
-        const int h = tile % a.P.n_heads, r0 = tile / a.P.n_heads * RB;
-        const int R = sp.m * a.group, first = sp.len - sp.m;
-        const int real_units = sp.len > 0 ? sp.units : 0;
-        const int n = max(0, min(u1, real_units) - u0 - warp + kWarps - 1) / kWarps; /* this warp's units */
-
-        /* the copies of the first units start before the queries are read */
-        int page_of = 0; /* lane l: page of this warp's unit 32 j + l */
-        auto unit_at = [&](int k) {
-            const int u = u0 + warp + k * kWarps;
-            return u < sp.sink_u ? u : u - sp.sink_u + sp.lo_u;
-        };
-        auto issue = [&](int k) {
-            if ((k & 31) == 0) {
-                const int kk = k + lane;
-                page_of = 0;
-                if (kk < n) {
-                    page_of = a.S.table[(int64_t)b * a.S.table_stride + (unit_at(kk) >> (a.P.page_shift - 4))];
-                    if (page_of < 0 || page_of >= a.P.n_pages) {
-                        page_of = 0;
-                        flag_corrupt(a.status);
-                    }
+    /* the ring's filling side: a cursor of its own over the warp's segments */
+    int64_t px = x;
+    int pu = 0, pu_end = 0, pu_base = 0, p_sink = 0, p_lo = 0, p_h = 0, p_stage = 0, page_of = 0;
+    const int32_t* p_table = nullptr;
+    auto fill = [&]() {
+        while (pu >= pu_end) {
+            if (px >= x_end) return;
+            const Seg s = seg_at(a, pre, info, RB, px, x_end);
+            const int4 f = info[s.b];
+            const Span sp = span_of(a, f.x, f.y);
+            px = s.next;
+            pu = s.u0;
+            pu_end = f.x > 0 ? s.u1 : 0;
+            pu_base = pu - 32;
+            p_sink = sp.sink_u, p_lo = sp.lo_u - sp.sink_u, p_h = s.h;
+            p_table = a.S.table + (int64_t)s.b * a.S.table_stride;
+        }
+        if (pu - pu_base >= 32) { /* lane l: the page of unit pu_base + l */
+            pu_base = pu;
+            const int u = pu + lane;
+            page_of = 0;
+            if (u < pu_end) {
+                page_of = p_table[(u < p_sink ? u : u + p_lo) >> (a.P.page_shift - 4)];
+                if (page_of < 0 || page_of >= a.P.n_pages) {
+                    page_of = 0;
+                    flag_corrupt(a.status);
                 }
             }
-            const int page = __shfl_sync(kAll, page_of, k & 31);
-            if (lane == 0) {
-                const int s = k % S;
-                mbar_arrive_tx(bars + 8 * s, UB);
-                bulk_g2s(ring + s * UB, page_ptr(a.P, page, h, unit_at(k) & ((1 << (a.P.page_shift - 4)) - 1)), UB, bars + 8 * s);
-            }
-        };
-        for (int k = 0; k < min(n, S); ++k) issue(k);
+        }
+        const int page = __shfl_sync(kAll, page_of, pu - pu_base);
+        if (lane == 0) {
+            const int u = pu < p_sink ? pu : pu + p_lo;
+            mbar_arrive_tx(bars + 8 * p_stage, UB);
+            bulk_g2s(ring + p_stage * UB, page_ptr(a.P, page, p_h, u & unit_mask), UB, bars + 8 * p_stage);
+        }
+        ++pu;
+        p_stage = p_stage + 1 == S ? 0 : p_stage + 1;
+    };
+#pragma unroll 1
+    for (int k = 0; k < S; ++k) fill();
+
+    int st = 0;
+    uint32_t phase = 0; /* one bit per stage */
+    bool live = true;
+    while (x < x_end) {
+        const Seg sg = seg_at(a, pre, info, RB, x, x_end);
+        x = sg.next;
+        if (sg.u0 >= sg.u1) continue;
+        const int4 f = info[sg.b];
+        const Span sp = span_of(a, f.x, f.y);
+        const int h = sg.h, r0 = sg.r0, len = f.x, R = f.y * a.group, first = len - f.y, u1 = len > 0 ? sg.u1 : 0;
 
         /* queries: lane 4 g + c holds row g's channels 32 b + 8 c + 0..7, scaled by a power
          * of two so that the row's largest lies in [2^14, 2^15): BF16 and FP16 rows are
@@ -223,7 +292,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 6 && NB * NT <= 8 ? 2 : 1) 
         for (int t = 0; t < NT; ++t) {
             const int r = r0 + 8 * t + g;
             const bool on = r < R;
-            const int64_t off = on ? (sp.row0 + r / a.group) * a.q.row + (int64_t)(h * a.group + r % a.group) * a.q.head : 0;
+            const int64_t off = on ? (int64_t)(f.z + r / a.group) * a.q.row + (int64_t)(h * a.group + r % a.group) * a.q.head : 0;
             float xq[NB][8];
             uint32_t top = 0;
 #pragma unroll
@@ -297,15 +366,16 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 6 && NB * NT <= 8 ? 2 : 1) 
 #pragma unroll
         for (int k = 0; k < NB; ++k) ref[k] = -8; /* any scale passes it: the first unit sets it */
 
-        for (int k = 0; k < n; ++k) {
-            const int st = k % S;
+#pragma unroll 1
+        for (int u = sg.u0; u < u1; ++u) {
             const uint32_t buf = ring + st * UB;
             if (live && !mbar_wait(bars + 8 * st, (phase >> st) & 1u)) {
                 live = false;
                 if (lane == 0) flag_corrupt(a.status);
             }
             phase ^= 1u << st;
-            const int tok = unit_at(k) * kUnit;
+            st = st + 1 == S ? 0 : st + 1;
+            const int tok = (u < sp.sink_u ? u : u - sp.sink_u + sp.lo_u) * kUnit;
 
             /* S^T: rows = tokens g, g + 8, columns = query rows 2c, 2c + 1 */
             float s[NT][4];
@@ -494,63 +564,133 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 6 && NB * NT <= 8 ? 2 : 1) 
                 }
             }
             __syncwarp(); /* every lane has read the stage */
-            if (k + S < n) issue(k + S);
+            fill();
         }
 
-        /* merge the warps */
-        __syncthreads();
-        float* mine = merge + warp * MW;
+        /* the lanes' sums; values are held relative to 2^(ref - 127) per block (ref = 0 or
+         * -8: nothing but blocks of zeros so far, a NaN there stays one) */
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float ls = l[t][j];
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int w = 4; w < 32; w <<= 1) ls += __shfl_xor_sync(kAll, ls, w);
-                const int r = 8 * t + 2 * c + j;
-                if (g == 0) {
-                    mine[RB * LD + r] = m[t][j];
-                    mine[RB * LD + RB + r] = ls;
+                for (int w = 4; w < 32; w <<= 1) l[t][j] += __shfl_xor_sync(kAll, l[t][j], w);
+        float back[NB];
+#pragma unroll
+        for (int k = 0; k < NB; ++k) back[k] = ref[k] > 0 ? __uint_as_float((uint32_t)ref[k] << 23) : 0.f;
+        if (sg.u0 == 0 && sg.u1 == sg.units) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float inv[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    inv[j] = l[t][j] == 0.f ? 0.f : 1.f / l[t][j];
+                    const int r = r0 + 8 * t + 2 * c + j;
+                    if (a.lse && g == 0 && r < R)
+                        a.lse[(int64_t)(f.z + r / a.group) * a.n_q_heads + h * a.group + r % a.group] =
+                            l[t][j] == 0.f ? -INFINITY : (m[t][j] - kBias + log2f(l[t][j])) * kLn2;
                 }
+                /* 8 x 8 transpositions turn channels g of rows 2c, 2c + 1 into channels 2c,
+                 * 2c + 1 of row g (FP32 rows are stored as they lie) */
+                if (a.out.dtype != EC_DTYPE_FP32) {
+                    const int r = r0 + 8 * t + g;
+                    const int64_t off = (int64_t)(f.z + r / a.group) * a.out.row + (int64_t)(h * a.group + r % a.group) * a.out.head + 2 * c;
 #pragma unroll
-                for (int i = 0; i < 2 * NB; ++i) {
-                    const float f = ref[i / 2] > 0 ? __uint_as_float((uint32_t)ref[i / 2] << 23) : 0.f;
-                    /* ref = 0 or -8: nothing but blocks of zeros so far (a NaN there stays one) */
-                    mine[r * LD + 16 * i + g] = o[t][i][j] * f;
-                    mine[r * LD + 16 * i + 8 + g] = o[t][i][j + 2] * f;
+                    for (int i = 0; i < 2 * NB; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float v0 = o[t][i][2 * j] * back[i / 2] * inv[0], v1 = o[t][i][2 * j + 1] * back[i / 2] * inv[1];
+                            uint32_t w;
+                            if (a.out.dtype == EC_DTYPE_FP16) w = pack_f16(v0, v1);
+                            else {
+                                const __nv_bfloat162 y = __floats2bfloat162_rn(v0, v1);
+                                w = *(const uint32_t*)&y;
+                            }
+                            w = transpose8x8(w);
+                            if (r < R) {
+                                uint16_t* at = (uint16_t*)a.out.data + off + 16 * i + 8 * j;
+                                if (a.out.wide) *(uint32_t*)at = w;
+                                else {
+                                    at[0] = (uint16_t)w;
+                                    at[1] = (uint16_t)(w >> 16);
+                                }
+                            }
+                        }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int r = r0 + 8 * t + 2 * c + j;
+                        if (r >= R) continue;
+                        float* at = (float*)a.out.data + (int64_t)(f.z + r / a.group) * a.out.row + (int64_t)(h * a.group + r % a.group) * a.out.head + g;
+#pragma unroll
+                        for (int i = 0; i < 2 * NB; ++i) {
+                            at[16 * i] = o[t][i][j] * back[i / 2] * inv[j];
+                            at[16 * i + 8] = o[t][i][j + 2] * back[i / 2] * inv[j];
+                        }
+                    }
                 }
             }
-        __syncthreads();
-        const bool whole = u0 == 0 && u1 == sp.units;
-        const int slot = u0 == 0 ? 1 : 0;
-        float* part = a.part + ((int64_t)blockIdx.x * 2 + slot) * (RB * (D + 2));
-        for (int e = threadIdx.x; e < RB * (D / 4); e += kWarps * 32) {
+        } else {
+            /* the end of a tile is the warp's first segment, the begin of another its last,
+             * when the ring is empty */
+            const int slot = sg.u0 == 0 ? 1 : 0;
+            float* mine = (float*)(at_smem + warp * H::WARP_BYTES + (slot ? 0 : S * UB));
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int r = 8 * t + 2 * c + j;
+                    if (g == 0) {
+                        mine[RB * LD + r] = m[t][j];
+                        mine[RB * LD + RB + r] = l[t][j];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2 * NB; ++i) {
+                        mine[r * LD + 16 * i + g] = o[t][i][j] * back[i / 2];
+                        mine[r * LD + 16 * i + 8 + g] = o[t][i][j + 2] * back[i / 2];
+                    }
+                }
+            if (lane == 0) {
+                slot_tile[2 * warp + slot] = sg.tile;
+                slot_flags[2 * warp + slot] = (sg.u0 == 0 ? 1 : 0) | (sg.u1 == sg.units ? 2 : 0);
+            }
+        }
+    }
+
+    /* join the warps' parts, tile by tile, in order */
+    __syncthreads();
+    for (int s0 = 0; s0 < 2 * W;) {
+        const int64_t tile = slot_tile[s0];
+        if (tile < 0) {
+            ++s0;
+            continue;
+        }
+        int s1 = s0, last = s0;
+        while (s1 < 2 * W && (slot_tile[s1] < 0 || slot_tile[s1] == tile)) {
+            if (slot_tile[s1] == tile) last = s1;
+            ++s1;
+        }
+        const bool whole = (slot_flags[s0] & 1) && (slot_flags[last] & 2);
+        const Seg sg = seg_at(a, pre, info, RB, tile, X);
+        const int4 f = info[sg.b];
+        const int R = f.y * a.group;
+        float* part = a.part + ((int64_t)blockIdx.x * 2 + (slot_flags[s0] & 1)) * (RB * (D + 2));
+        for (int e = threadIdx.x; e < RB * (D / 4); e += W * 32) {
             const int r = e / (D / 4), d = 4 * (e % (D / 4));
-            float M = -FLT_MAX;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, merge[w * MW + RB * LD + r]);
-            float L = 0.f;
+            if (sg.r0 + r >= R) continue;
+            float M = -FLT_MAX, L = 0.f;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2(merge[w * MW + RB * LD + r] - M);
-                L = fmaf(merge[w * MW + RB * LD + RB + r], f, L);
-                const float4 y = *(const float4*)&merge[w * MW + r * LD + d];
-                v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
+            for (int k = s0; k <= last; ++k) {
+                if (slot_tile[k] != tile) continue;
+                const float* p = (const float*)(at_smem + (k / 2) * H::WARP_BYTES + (k & 1 ? 0 : S * UB));
+                const float pm = p[RB * LD + r], nm = fmaxf(M, pm), fo = ex2(M - nm), fp = ex2(pm - nm);
+                const float4 y = *(const float4*)&p[r * LD + d];
+                M = nm;
+                L = L * fo + p[RB * LD + RB + r] * fp;
+                v.x = v.x * fo + y.x * fp, v.y = v.y * fo + y.y * fp, v.z = v.z * fo + y.z * fp, v.w = v.w * fo + y.w * fp;
             }
-            if (whole) {
-                if (r0 + r < R) {
-                    const int64_t row = sp.row0 + (r0 + r) / a.group;
-                    const int head = h * a.group + (r0 + r) % a.group;
-                    const float inv = L == 0.f ? 0.f : 1.f / L;
-                    const int64_t off = row * a.out.row + (int64_t)head * a.out.head + d;
-                    store_elem(a.out, off, v.x * inv);
-                    store_elem(a.out, off + 1, v.y * inv);
-                    store_elem(a.out, off + 2, v.z * inv);
-                    store_elem(a.out, off + 3, v.w * inv);
-                    if (d == 0 && a.lse) a.lse[row * a.n_q_heads + head] = L == 0.f ? -INFINITY : (M - kBias + log2f(L)) * kLn2;
-                }
-            } else {
+            if (whole) write_row(a, f.z, sg.h, sg.r0 + r, d, v, M, L);
+            else {
                 *(float4*)&part[r * D + d] = v;
                 if (d == 0) {
                     part[RB * D + r] = M;
@@ -558,8 +698,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 6 && NB * NT <= 8 ? 2 : 1) 
                 }
             }
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); /* the ring's next copies follow these accesses */
-        __syncthreads();
+        s0 = s1;
     }
 }
 
@@ -567,49 +706,42 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 6 && NB * NT <= 8 ? 2 : 1) 
  * in which share i ends; if it begins there, the CTA adds the shares' parts in order. */
 template <int NB, int NT>
 __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ AttnArgs a, int grid) {
-    constexpr int D = 32 * NB, RB = 8 * NT, PS = RB * (D + 2);
+    using H = Shape<NB, NT>;
+    constexpr int D = H::D, RB = H::RB, PS = RB * (D + 2);
     extern __shared__ __align__(128) uint8_t at_smem[];
-    int64_t* pre = (int64_t*)at_smem;
+    int4* info = (int4*)at_smem;
+    int64_t* pre = (int64_t*)(info + a.S.n_seqs);
     grid_dep_launch();
     grid_dep_wait();
-    scan_seqs(a, RB, pre, false);
+    scan_seqs(a, RB, pre, info, false);
     const int64_t X = pre[a.S.n_seqs];
-    int64_t share = (X + grid - 1) / grid;
-    if (share < kWarps) share = kWarps;
+    const int64_t share = share_of(a, X, grid, H::W);
     const int64_t x0 = blockIdx.x * share, x1 = min(X, x0 + share);
     if (x0 >= x1) return;
-    const int b = find_seq(pre, a.S.n_seqs, x1 - 1);
-    const Span sp = span_of(a, b, RB);
-    const int tile = (int)((x1 - 1 - pre[b]) / sp.units);
-    const int64_t t0 = pre[b] + (int64_t)tile * sp.units, t1 = t0 + sp.units;
-    if (t0 < x0 || t1 <= x1) return;
+    const Seg sg = seg_at(a, pre, info, RB, x1 - 1, X);
+    const int64_t t1 = sg.tile + sg.units; /* places past the units hold no work */
+    if (sg.tile < x0 || t1 <= x1) return;
     const int n = (int)((t1 - 1) / share) - (int)blockIdx.x + 1;
-    const int h = tile % a.P.n_heads, r0 = tile / a.P.n_heads * RB, R = sp.m * a.group;
+    const int4 f = info[sg.b];
+    const int R = f.y * a.group;
     const float* p0 = a.part + ((int64_t)blockIdx.x * 2 + 1) * PS;  /* the first share's part */
     const float* p1 = a.part + ((int64_t)blockIdx.x * 2) * PS;      /* share i's: p1 + 2 i PS */
     for (int e = threadIdx.x; e < RB * (D / 4); e += 256) {
         const int r = e / (D / 4), d = 4 * (e % (D / 4));
-        if (r0 + r >= R) continue;
+        if (sg.r0 + r >= R) continue;
         float M = p0[RB * D + r];
         for (int i = 1; i < n; ++i) M = fmaxf(M, p1[(int64_t)2 * i * PS + RB * D + r]);
         float L = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
         for (int i = 0; i < n; ++i) {
             const float* p = i ? p1 + (int64_t)2 * i * PS : p0;
-            const float f = ex2(p[RB * D + r] - M);
-            L = fmaf(p[RB * D + RB + r], f, L);
+            const float w = ex2(p[RB * D + r] - M);
+            L = fmaf(p[RB * D + RB + r], w, L);
             const float4 y = *(const float4*)&p[r * D + d];
-            v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
+            v.x = fmaf(y.x, w, v.x), v.y = fmaf(y.y, w, v.y), v.z = fmaf(y.z, w, v.z), v.w = fmaf(y.w, w, v.w);
         }
-        const int64_t row = sp.row0 + (r0 + r) / a.group;
-        const int head = h * a.group + (r0 + r) % a.group;
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        const int64_t off = row * a.out.row + (int64_t)head * a.out.head + d;
-        store_elem(a.out, off, v.x * inv);
-        store_elem(a.out, off + 1, v.y * inv);
-        store_elem(a.out, off + 2, v.z * inv);
-        store_elem(a.out, off + 3, v.w * inv);
-        if (d == 0 && a.lse) a.lse[row * a.n_q_heads + head] = L == 0.f ? -INFINITY : (M - kBias + log2f(L)) * kLn2;
+        write_row(a, f.z, sg.h, sg.r0 + r, d, v, M, L);
     }
 }
 
@@ -619,31 +751,44 @@ struct Plan {
     size_t work;
 };
 
-static Plan plan_of(const ec_kv* C, int sms, int n_seqs, int max_new, int64_t max_len, const ec_kv_attn* at) {
-    Plan p;
-    const int group = at->n_q_heads / C->p.n_kv_heads, D = C->p.head_dim;
+template <int NB, int NT>
+static void plan_shape(Plan* p, int sms, int64_t tiles, int64_t units) {
+    using H = Shape<NB, NT>;
+    /* up to 4 units per warp there is nothing to gain from splitting a tile, and one launch does */
+    p->solo = units <= 4 * H::W && tiles < 0x7FFFFFFF ? (int)((units + H::W - 1) / H::W) * H::W : 0;
+    p->grid = p->solo ? (int)tiles : sms * H::CTAS;
+    p->work = p->solo ? 0 : (size_t)p->grid * 2 * H::RB * (H::D + 2) * sizeof(float);
+}
+
+/* false: more work than the kernels count (one sequence's places fit 31 bits) */
+static bool plan_of(const ec_kv* C, int sms, int n_seqs, int max_new, int64_t max_len, const ec_kv_attn* at, Plan* p) {
+    const int group = at->n_q_heads / C->p.n_kv_heads, nb = C->p.head_dim / 32;
     const int64_t rows = (int64_t)group * max_new;
-    p.nt = rows > 8 && D <= 128 ? 2 : 1;
+    p->nt = rows > 8 && nb <= 4 ? 2 : 1;
     int64_t units = (max_len + kUnit - 1) / kUnit;
     if (at->window) {
         const int64_t w = ((int64_t)at->window + max_new + kUnit) / kUnit + 1 + (at->sinks + kUnit - 1) / kUnit;
         if (w < units) units = w;
     }
-    /* up to 4 units per warp there is nothing to gain from splitting a tile */
-    p.solo = units <= 4 * kWarps;
-    const int64_t tiles = (int64_t)n_seqs * C->p.n_kv_heads * ((rows + 8 * p.nt - 1) / (8 * p.nt));
-    p.grid = p.solo ? (int)(tiles < 0x7FFFFFFF ? tiles : 0x7FFFFFFF) : sms * (D <= 128 ? 2 : D <= 192 ? 2 : 1);
-    p.work = p.solo ? 0 : (size_t)p.grid * 2 * (8 * p.nt) * (D + 2) * sizeof(float);
-    return p;
+    if (units < 1) units = 1;
+    const int64_t row_tiles = (rows + 8 * p->nt - 1) / (8 * p->nt), per_seq = row_tiles * C->p.n_kv_heads, tiles = per_seq * n_seqs;
+    if (rows > 0x7FFFFFFF || per_seq > 0x7FFFFFFF / (units + kTileCost)) return false;
+    if (nb == 2) p->nt == 1 ? plan_shape<2, 1>(p, sms, tiles, units) : plan_shape<2, 2>(p, sms, tiles, units);
+    else if (nb == 4) p->nt == 1 ? plan_shape<4, 1>(p, sms, tiles, units) : plan_shape<4, 2>(p, sms, tiles, units);
+    else if (nb == 6) plan_shape<6, 1>(p, sms, tiles, units);
+    else plan_shape<8, 1>(p, sms, tiles, units);
+    return true;
 }
 
 template <int NB, int NT, int QT>
 static int run_attn(const AttnArgs& a, const Plan& p, cudaStream_t stream) {
+    using H = Shape<NB, NT>;
     static SmemOnce once;
-    int rc = once.set(kv_attn_kernel<NB, NT, QT>, attn_smem<NB>(EC_KV_MAX_SEQS));
+    int rc = once.set(kv_attn_kernel<NB, NT, QT>, H::smem(EC_KV_MAX_SEQS));
     if (rc != EC_OK) return rc;
-    rc = launch(kv_attn_kernel<NB, NT, QT>, dim3(p.grid), kWarps * 32, attn_smem<NB>(a.S.n_seqs), stream, a);
-    if (rc == EC_OK && !p.solo) rc = launch(kv_join_kernel<NB, NT>, dim3(p.grid), 256, 8 * ((size_t)a.S.n_seqs + 1), stream, a, p.grid);
+    rc = launch(kv_attn_kernel<NB, NT, QT>, dim3(p.grid), H::W * 32, H::smem(a.S.n_seqs), stream, a);
+    if (rc == EC_OK && !p.solo)
+        rc = launch(kv_join_kernel<NB, NT>, dim3(p.grid), 256, 16 * (size_t)a.S.n_seqs + 8 * ((size_t)a.S.n_seqs + 1), stream, a, p.grid);
     return rc;
 }
 
@@ -655,6 +800,7 @@ static int run_terms(const AttnArgs& a, const Plan& p, cudaStream_t stream) {
 static int check_attn(const ec_kv* C, int n_seqs, int64_t n_rows, int max_new, int64_t max_len, const ec_kv_attn* at) {
     if (!C || !at) return EC_ERR_INVALID_ARG;
     if (n_seqs < 0 || n_rows < 0 || max_new < 0 || max_len < 0) return EC_ERR_SHAPE;
+    if (max_len > 0x7FFFFFF0) return EC_ERR_UNSUPPORTED;
     if (n_seqs > EC_KV_MAX_SEQS || max_new > (1 << 24) || at->n_q_heads > 65536) return EC_ERR_UNSUPPORTED;
     if (at->n_q_heads < 1 || at->n_q_heads % C->p.n_kv_heads) return EC_ERR_SHAPE;
     if (at->window < 0 || at->sinks < 0 || (at->sinks > 0 && at->window == 0)) return EC_ERR_INVALID_ARG;
@@ -677,7 +823,9 @@ extern "C" int ec_kv_attend_work_bytes(const ec_kv* C, int n_seqs, int64_t n_row
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return EC_ERR_CUDA;
     } else sms = 152;
-    *bytes = plan_of(C, sms, n_seqs, max_new, max_len, attn).work;
+    Plan p;
+    if (!plan_of(C, sms, n_seqs, max_new, max_len, attn, &p)) return EC_ERR_UNSUPPORTED;
+    *bytes = p.work;
     return EC_OK;
 }
 
@@ -687,7 +835,10 @@ extern "C" int ec_kv_attend(const ec_kv* C, int layer, const ec_kv_seqs* seqs, c
     if (!C || !attn) return EC_ERR_INVALID_ARG;
     int rc = check_seqs(seqs);
     if (rc != EC_OK) return rc;
-    if (max_len == 0) max_len = seqs->table_stride * C->p.page_tokens;
+    if (max_len == 0) {
+        max_len = seqs->table_stride * C->p.page_tokens;
+        if (max_len > 0x7FFFFFF0) max_len = 0x7FFFFFF0; /* lens are 32-bit */
+    }
     if ((rc = check_attn(C, seqs->n_seqs, n_rows, max_new, max_len, attn)) != EC_OK) return rc;
     if (!starts && n_rows < seqs->n_seqs) return EC_ERR_SHAPE;
     AttnArgs a{};
@@ -698,7 +849,8 @@ extern "C" int ec_kv_attend(const ec_kv* C, int layer, const ec_kv_seqs* seqs, c
     Device d;
     if ((rc = device_of(C, &d)) != EC_OK) return rc;
     if (seqs->n_seqs == 0 || n_rows == 0 || max_new == 0) return EC_OK;
-    const Plan p = plan_of(C, d.sms, seqs->n_seqs, max_new, max_len, attn);
+    Plan p;
+    if (!plan_of(C, d.sms, seqs->n_seqs, max_new, max_len, attn, &p)) return EC_ERR_UNSUPPORTED;
     if (p.work && (!work || (uintptr_t)work % 16 || work_bytes < p.work)) return EC_ERR_INVALID_ARG;
     a.S = Seqs{seqs->table, seqs->lens, starts, seqs->table_stride, n_rows, seqs->n_seqs};
     a.lse = lse;
@@ -709,6 +861,7 @@ extern "C" int ec_kv_attend(const ec_kv* C, int layer, const ec_kv_seqs* seqs, c
     a.sinks = attn->sinks;
     a.scale = attn->scale > 0.f ? attn->scale : 1.f / sqrtf((float)C->p.head_dim);
     a.max_new = max_new;
+    a.max_len = (int32_t)max_len;
     a.solo = p.solo;
     a.status = d.status;
     switch (C->p.head_dim / 32) {
