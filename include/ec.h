@@ -517,62 +517,91 @@ int ec_kv_create(const ec_kv_params* params, void* pool, size_t pool_bytes, int 
 /* Free the descriptor (not the pool). NULL is ignored. */
 void ec_kv_free(ec_kv* C);
 
-/* Quantise the new tokens' keys and values into the cache (layer 0..n_layers-1).
- * n_rows: rows of k and v; max_new: an upper bound of the new tokens of one sequence.
+/* New tokens of some sequences and their dense keys and values.
+ *  n_rows    rows of k and v
+ *  max_new   an upper bound of the new tokens of one sequence */
+typedef struct {
+    ec_kv_seqs seqs;
+    const int32_t* starts;
+    int64_t n_rows;
+    int32_t layer;         /* 0..n_layers-1 */
+    int32_t max_new;
+    ec_kv_rows k, v;
+} ec_kv_tokens;
+
+/* Quantise the new tokens' keys and values into the cache.
  * Pages that receive tokens must not be shared with a sequence that reads those places
  * (ec_kv_fork gives every sequence a partly filled page of its own). */
-int ec_kv_append(const ec_kv* C, int layer, const ec_kv_seqs* seqs, const int32_t* starts, int64_t n_rows,
-                 int max_new, const ec_kv_rows* k, const ec_kv_rows* v, cudaStream_t stream);
+int ec_kv_append(const ec_kv* C, const ec_kv_tokens* a, cudaStream_t stream);
 
 /* The values that the cache holds of the last tokens of each sequence (same convention
- * as ec_kv_append; k or v NULL leaves it out), rounded to the rows' type (BF16 holds
- * every finite value of 2^-126 and above exactly).  Rows of tokens before a sequence's
- * first are zeros. */
-int ec_kv_read(const ec_kv* C, int layer, const ec_kv_seqs* seqs, const int32_t* starts, int64_t n_rows,
-               int max_new, const ec_kv_rows* k, const ec_kv_rows* v, cudaStream_t stream);
+ * as ec_kv_append; k or v with data = NULL is left out), rounded to the rows' type (BF16
+ * holds every finite value of 2^-126 and above exactly).  Rows of tokens before a
+ * sequence's first are zeros. */
+int ec_kv_read(const ec_kv* C, const ec_kv_tokens* a, cudaStream_t stream);
 
 /* out[row, j] = sum_t p_t v_t, p = softmax_t(scale * q[row, j] . k_t) over the tokens t
- * that the row sees; lse[row, j] (FP32, may be NULL) the natural logarithm of the sum of
- * the exponentials.  Scores, sums and outputs are held in FP32; products are exact in
- * the 4-bit values times FP16 parts of q (one for BF16 and FP16, two for FP32) and
- * FP16 probabilities.  A row that sees nothing gives zeros and lse = -inf.
+ * that the row sees; lse[row, j] (FP32 [n_rows, n_q_heads], may be NULL) the natural
+ * logarithm of the sum of the exponentials.  Scores, sums and outputs are held in FP32;
+ * products are those of the 4-bit values with FP16 parts of q (one for BF16 and FP16, two
+ * for FP32) and with FP16 probabilities.  A row that sees nothing gives zeros and lse =
+ * -inf; a block of NaN that a row sees makes its channels NaN.
  * max_new and max_len are upper bounds, over the sequences, of the new tokens and of
- * lens (0: what a table row can hold).  work: device memory of the caller, 16-byte
+ * lens (0: what a table row can hold); work: device memory of the caller, 16-byte
  * aligned, of at least ec_kv_attend_work_bytes(); its contents need no clearing, and
  * two calls that may overlap need one each.  out: FP16, BF16 or FP32. */
-int ec_kv_attend(const ec_kv* C, int layer, const ec_kv_seqs* seqs, const int32_t* starts, int64_t n_rows,
-                 int max_new, int64_t max_len, const ec_kv_attn* attn, const ec_kv_rows* q, const ec_kv_rows* out,
-                 float* lse, void* work, size_t work_bytes, cudaStream_t stream);
+typedef struct {
+    ec_kv_seqs seqs;
+    const int32_t* starts;
+    int64_t n_rows;
+    int32_t layer;
+    int32_t max_new;
+    int64_t max_len;
+    ec_kv_attn attn;
+    ec_kv_rows q, out;
+    float* lse;
+    void* work;
+    size_t work_bytes;
+} ec_kv_attention;
+int ec_kv_attend(const ec_kv* C, const ec_kv_attention* a, cudaStream_t stream);
 
 /* Work bytes of ec_kv_attend for these sizes on the current device (host only). */
 int ec_kv_attend_work_bytes(const ec_kv* C, int n_seqs, int64_t n_rows, int max_new, int64_t max_len,
                             const ec_kv_attn* attn, size_t* bytes);
 
+/* Arguments of the page operations: the sequences as they are (from) and as they will be
+ * (to), and how many table entries name each page (refs, device, [n_pages]), here and in
+ * tables that are not in the call, before and after (refs_out; pages with refs_out = 0 are
+ * free).  `to`, refs_out and map must not overlap `from` and refs. */
+typedef struct {
+    ec_kv_seqs from, to;
+    const int32_t* refs;
+    int32_t* refs_out;
+    const int32_t* parents;   /* fork */
+    const int32_t* grow;      /* fork */
+    int32_t* map;             /* compact */
+    void* work;               /* device, 16-byte aligned, ec_kv_pages_work_bytes() */
+    size_t work_bytes;
+} ec_kv_pages;
+
 /* Sequences that continue others, for all layers at once: sequence i of `to` gets the
- * tokens of sequence parents[i] of `from` (parents device, [to->n_seqs], -1: an empty
+ * tokens of sequence parents[i] of `from` (parents device, [to.n_seqs], -1: an empty
  * sequence; NULL: i) and room for grow[i] >= 0 more (device; NULL: none); its len is
  * the parent's plus grow[i].  Whole pages are shared; a partly filled last page stays
  * with the first child (lowest i), the others get copies of its used units.  Sequences
- * of `from` without a child are dropped.  refs (device, [n_pages]): how many table
- * entries name each page, here and in tables that are not in this call; refs_out is the
- * same afterwards, and pages with refs_out = 0 are free.  New pages are the free ones of
- * lowest number, taken in the order of the sequences (a copied page first).  A sequence
- * for which no pages are left (or whose row would be longer than table_stride) gets
- * lens = -1 and no pages.  Entries past a sequence's pages are -1.  `to` and refs_out
- * must not overlap `from` and refs.  Freeing = a fork without the ended sequences;
- * a decoding step = a fork with parents = NULL and grow = 1. */
-int ec_kv_fork(const ec_kv* C, const ec_kv_seqs* from, const int32_t* refs, const int32_t* parents,
-               const int32_t* grow, const ec_kv_seqs* to, int32_t* refs_out, void* work, size_t work_bytes,
-               cudaStream_t stream);
+ * of `from` without a child are dropped.  New pages are the free ones of lowest number,
+ * taken in the order of the sequences (a copied page first).  A sequence for which no
+ * pages are left (or whose row would be longer than table_stride) gets lens = -1 and no
+ * pages.  Entries past a sequence's pages are -1.  Freeing = a fork without the ended
+ * sequences; a decoding step = a fork with parents = NULL and grow = 1. */
+int ec_kv_fork(const ec_kv* C, const ec_kv_pages* a, cudaStream_t stream);
 
 /* Move the n pages in use (refs > 0) to the numbers 0..n-1, for all layers: a page below
  * n stays, the others, in ascending order, fill the free numbers below n in ascending
  * order.  to: the same sequences with the new numbers (entries outside 0..n_pages-1 stay
  * as they are; lens are copied); map (device, [n_pages], may be NULL): old number -> new,
- * -1 for a free page, for tables that are not in this call.  `to`, refs_out and map must
- * not overlap `from` and refs. */
-int ec_kv_compact(const ec_kv* C, const ec_kv_seqs* from, const int32_t* refs, const ec_kv_seqs* to,
-                  int32_t* refs_out, int32_t* map, void* work, size_t work_bytes, cudaStream_t stream);
+ * -1 for a free page, for tables that are not in this call. */
+int ec_kv_compact(const ec_kv* C, const ec_kv_pages* a, cudaStream_t stream);
 
 /* Work bytes of ec_kv_fork (n_from and n_to sequences) and ec_kv_compact (host only). */
 int ec_kv_pages_work_bytes(const ec_kv* C, int n_from, int n_to, size_t* bytes);

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -89,16 +90,6 @@ class KvParams(ctypes.Structure):
                 ("page_tokens", ctypes.c_int32), ("n_pages", ctypes.c_int64)]
 
 
-class KvSeqsStruct(ctypes.Structure):
-    _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("lens", ctypes.c_void_p),
-                ("n_seqs", ctypes.c_int32)]
-
-
-class KvRows(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
-                ("dtype", ctypes.c_int32)]
-
-
 class KvAttn(ctypes.Structure):
     _fields_ = [("n_q_heads", ctypes.c_int32), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
                 ("scale", ctypes.c_float)]
@@ -128,12 +119,12 @@ _sig = {
     "ec_kv_pool_bytes": ([_vp, _vp], _i32),
     "ec_kv_create": ([_vp, _vp, ctypes.c_size_t, _i32, _vp], _i32),
     "ec_kv_free": ([_vp], None),
-    "ec_kv_append": ([_vp, _i32, _vp, _vp, _i64, _i32, _vp, _vp, _vp], _i32),
-    "ec_kv_read": ([_vp, _i32, _vp, _vp, _i64, _i32, _vp, _vp, _vp], _i32),
-    "ec_kv_attend": ([_vp, _i32, _vp, _vp, _i64, _i32, _i64, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp], _i32),
+    "ec_kv_append": ([_vp, _vp, _vp], _i32),
+    "ec_kv_read": ([_vp, _vp, _vp], _i32),
+    "ec_kv_attend": ([_vp, _vp, _vp], _i32),
     "ec_kv_attend_work_bytes": ([_vp, _i32, _i64, _i32, _i64, _vp, _vp], _i32),
-    "ec_kv_fork": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp], _i32),
-    "ec_kv_compact": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp], _i32),
+    "ec_kv_fork": ([_vp, _vp, _vp], _i32),
+    "ec_kv_compact": ([_vp, _vp, _vp], _i32),
     "ec_kv_pages_work_bytes": ([_vp, _i32, _i32, _vp], _i32),
     "ec_stats": ([_vp, ctypes.POINTER(Stats)], _i32),
     "ec_code_lengths": ([_vp, _vp], _i32),
@@ -419,7 +410,30 @@ def status(stream=None) -> int:
 # ---------------------------------------------------------------- key/value cache
 EC_DTYPE_FP16, EC_DTYPE_FP32 = 3, 4
 EC_KV_MAX_SEQS = 1024
-_ROW_DTYPES = {"torch.bfloat16": EC_DTYPE_BF16, "torch.float16": EC_DTYPE_FP16, "torch.float32": EC_DTYPE_FP32}
+_ROW_DTYPES = {}   # torch dtype -> EC_DTYPE_*, filled on first use (torch is imported when needed)
+_I32 = [None]
+_RAW_STREAM = [None]
+# The argument structures of ec.h, field by field: ec_kv_seqs, ec_kv_rows, then the rest.
+_SEQS, _ROWS = struct.Struct("=qqqi4x"), struct.Struct("=qqqi4x")
+_TOKENS = struct.Struct("=32sqqii32s32s")
+_ATTENTION = struct.Struct("=32sqqiiqiiif32s32sqqq")
+_PAGES = struct.Struct("=32s32sqqqqqqq")
+_NO_ROWS = bytes(_ROWS.size)
+
+
+def _torch_types() -> None:
+    import torch
+    _I32[0] = torch.int32
+    _RAW_STREAM[0] = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _ROW_DTYPES.update({torch.bfloat16: EC_DTYPE_BF16, torch.float16: EC_DTYPE_FP16, torch.float32: EC_DTYPE_FP32})
+
+
+def _kv_stream(stream, cache) -> int:
+    """The stream's handle (None: the current stream of the cache's device, without building a Stream object)."""
+    if stream is not None:
+        return _stream_ptr(stream)
+    return _RAW_STREAM[0](cache.device) if cache.device >= 0 else 0
 
 
 class KvCache:
@@ -441,9 +455,9 @@ class KvCache:
             pass
 
 
-def _on_gpu(t, what: str, device=None):
-    """The address of a device tensor (on the cache's device)."""
-    if not t.is_cuda or (device is not None and t.device.index != device):
+def _at(t, cache, what: str) -> int:
+    """The address of a tensor on the cache's device."""
+    if t.get_device() != cache.device:
         raise EcError(EC_ERR_INVALID_ARG, what + ": tensors on the cache's device")
     return t.data_ptr()
 
@@ -452,16 +466,19 @@ class KvSeqs:
     """Sequences of a cache: int32 device tensors table [n, pages] and lens [n] (kept alive here)."""
 
     def __init__(self, table, lens):
+        if _I32[0] is None:
+            _torch_types()
         for t, dims in ((table, 2), (lens, 1)):
-            if str(t.dtype) != "torch.int32" or t.dim() != dims or not t.is_contiguous():
+            if t.dtype != _I32[0] or t.dim() != dims or not t.is_contiguous():
                 raise EcError(EC_ERR_INVALID_ARG, "kv_seqs: contiguous int32 tensors [n, pages] and [n]")
         if table.shape[0] != lens.shape[0]:
             raise EcError(EC_ERR_SHAPE, "kv_seqs")
-        _on_gpu(table, "kv_seqs"), _on_gpu(lens, "kv_seqs", table.device.index)
+        if not table.is_cuda or table.device != lens.device:
+            raise EcError(EC_ERR_INVALID_ARG, "kv_seqs: tensors on one GPU")
+        self.device = table.get_device()
         self.table, self.lens = table, lens
         self.n, self.pages = int(table.shape[0]), int(table.shape[1])
-        self.struct = KvSeqsStruct(table.data_ptr(), self.pages, lens.data_ptr(), self.n)
-        self.ref = ctypes.addressof(self.struct)
+        self.packed = _SEQS.pack(table.data_ptr(), self.pages, lens.data_ptr(), self.n)
 
 
 def kv_pool_bytes(n_layers: int, n_pages: int, n_kv_heads: int, head_dim: int, page_tokens: int = 64) -> int:
@@ -485,8 +502,8 @@ def kv_cache(n_layers: int, n_pages: int, n_kv_heads: int, head_dim: int, page_t
         if not pool.is_contiguous():
             raise EcError(EC_ERR_INVALID_ARG, "kv_cache: a contiguous pool")
         nbytes = pool.numel() * pool.element_size()
-        if device >= 0:
-            _on_gpu(pool, "kv_cache", device)
+        if device >= 0 and pool.get_device() != device:
+            raise EcError(EC_ERR_INVALID_ARG, "kv_cache: a pool on the cache's device")
     h = ctypes.c_void_p()
     _check(lib.ec_kv_create(ctypes.byref(p), _dev_ptr(pool), nbytes, device, ctypes.byref(h)), "ec_kv_create")
     return KvCache(h.value, p, pool, device)
@@ -496,47 +513,65 @@ def kv_seqs(table, lens) -> KvSeqs:
     return KvSeqs(table, lens)
 
 
-def _kv_rows(t, cache, heads: int, what: str) -> KvRows:
-    """[rows, heads, dim] with any strides between rows and heads."""
-    dtype = _ROW_DTYPES.get(str(t.dtype))
-    if dtype is None or t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
-        raise EcError(EC_ERR_INVALID_ARG, what + ": bfloat16, float16 or float32 [rows, heads, head_dim], contiguous in head_dim")
-    if t.shape[1] != heads or t.shape[2] != cache.params.head_dim:
+def _seqs(seqs, cache, what: str) -> bytes:
+    if seqs.device != cache.device:
+        raise EcError(EC_ERR_INVALID_ARG, what + ": sequences on the cache's device")
+    return seqs.packed
+
+
+def _kv_rows(t, cache, heads: int, what: str) -> bytes:
+    """ec_kv_rows of [rows, heads, head_dim] with any strides between rows and heads."""
+    if _I32[0] is None:
+        _torch_types()
+    dtype, shape, stride = _ROW_DTYPES.get(t.dtype), t.shape, t.stride()
+    if dtype is None or len(shape) != 3 or stride[2] != 1 or t.get_device() != cache.device:
+        raise EcError(EC_ERR_INVALID_ARG, what + ": bfloat16, float16 or float32 [rows, heads, head_dim], contiguous in "
+                                                 "head_dim, on the cache's device")
+    if shape[1] != heads or shape[2] != cache.params.head_dim:
         raise EcError(EC_ERR_SHAPE, what)
-    return KvRows(_on_gpu(t, what, cache.device), t.stride(0), t.stride(1), dtype)
+    return _ROWS.pack(t.data_ptr(), stride[0], stride[1], dtype)
 
 
-def _starts_ptr(starts, cache, n: int, what: str) -> int:
-    if starts is None:
+def _int32_ptr(t, cache, n: int, what: str) -> int:
+    if t is None:
         return 0
-    if str(starts.dtype) != "torch.int32" or not starts.is_contiguous():
-        raise EcError(EC_ERR_INVALID_ARG, what + ": starts is a contiguous int32 device tensor")
-    if starts.numel() != n + 1:
-        raise EcError(EC_ERR_SHAPE, what + ": starts has n_seqs + 1 entries")
-    return _on_gpu(starts, what, cache.device)
+    if t.dtype != _I32[0] or not t.is_contiguous():
+        raise EcError(EC_ERR_INVALID_ARG, what + ": contiguous int32 tensors")
+    if t.numel() != n:
+        raise EcError(EC_ERR_SHAPE, what)
+    return _at(t, cache, what)
 
 
 def kv_append(cache: KvCache, layer: int, seqs: KvSeqs, k, v, starts=None, max_new: int = 1, stream=None) -> None:
     """ec_kv_append: quantise the new tokens' k and v [rows, n_kv_heads, head_dim] into the cache."""
-    p = cache.params
-    kr, vr = (_kv_rows(t, cache, p.n_kv_heads, "ec_kv_append") for t in (k, v))
-    if k.shape[0] != v.shape[0]:
+    heads = cache.params.n_kv_heads
+    kr, vr = _kv_rows(k, cache, heads, "ec_kv_append"), _kv_rows(v, cache, heads, "ec_kv_append")
+    n = k.shape[0]
+    if n != v.shape[0]:
         raise EcError(EC_ERR_SHAPE, "ec_kv_append")
-    _check(lib.ec_kv_append(cache.handle, layer, seqs.ref, _starts_ptr(starts, cache, seqs.n, "ec_kv_append"), k.shape[0],
-                            max_new, ctypes.addressof(kr), ctypes.addressof(vr), _stream_ptr(stream)), "ec_kv_append")
+    args = _TOKENS.pack(_seqs(seqs, cache, "ec_kv_append"), _int32_ptr(starts, cache, seqs.n + 1, "ec_kv_append"), n, layer,
+                        max_new, kr, vr)
+    rc = lib.ec_kv_append(cache.handle, args, _kv_stream(stream, cache))
+    if rc:
+        raise EcError(rc, "ec_kv_append")
 
 
 def kv_read(cache: KvCache, layer: int, seqs: KvSeqs, k=None, v=None, starts=None, max_new: int = 1,
             stream=None) -> None:
     """ec_kv_read: the cached values of the sequences' last tokens into k and / or v."""
-    p = cache.params
-    kr, vr = (None if t is None else _kv_rows(t, cache, p.n_kv_heads, "ec_kv_read") for t in (k, v))
+    heads = cache.params.n_kv_heads
+    kr = _NO_ROWS if k is None else _kv_rows(k, cache, heads, "ec_kv_read")
+    vr = _NO_ROWS if v is None else _kv_rows(v, cache, heads, "ec_kv_read")
     if k is not None and v is not None and k.shape[0] != v.shape[0]:
         raise EcError(EC_ERR_SHAPE, "ec_kv_read")
-    rows = next((t.shape[0] for t in (k, v) if t is not None), 0)
-    _check(lib.ec_kv_read(cache.handle, layer, seqs.ref, _starts_ptr(starts, cache, seqs.n, "ec_kv_read"), rows, max_new,
-                          0 if kr is None else ctypes.addressof(kr), 0 if vr is None else ctypes.addressof(vr),
-                          _stream_ptr(stream)), "ec_kv_read")
+    if _I32[0] is None:
+        _torch_types()
+    n = k.shape[0] if k is not None else v.shape[0] if v is not None else 0
+    args = _TOKENS.pack(_seqs(seqs, cache, "ec_kv_read"), _int32_ptr(starts, cache, seqs.n + 1, "ec_kv_read"), n, layer,
+                        max_new, kr, vr)
+    rc = lib.ec_kv_read(cache.handle, args, _kv_stream(stream, cache))
+    if rc:
+        raise EcError(rc, "ec_kv_read")
 
 
 def kv_attend_work_bytes(cache: KvCache, n_seqs: int, n_rows: int, n_q_heads: int, max_new: int = 1,
@@ -554,24 +589,26 @@ def kv_attend(cache: KvCache, layer: int, seqs: KvSeqs, q, out, starts=None, max
     """ec_kv_attend: out [rows, n_q_heads, head_dim] = attention of the new tokens' q over
     the cache; lse float32 [rows, n_q_heads] (optional).  max_len 0: what the table can
     hold.  work: a device tensor of kv_attend_work_bytes; None allocates one."""
-    p = cache.params
-    heads = int(q.shape[1]) if q.dim() == 3 else 0
-    qr, orr = (_kv_rows(t, cache, heads, "ec_kv_attend") for t in (q, out))
-    if out.shape[0] != q.shape[0]:
+    shape = q.shape
+    heads = shape[1] if len(shape) == 3 else 0
+    qr, orr = _kv_rows(q, cache, heads, "ec_kv_attend"), _kv_rows(out, cache, heads, "ec_kv_attend")
+    n = shape[0]
+    if out.shape[0] != n:
         raise EcError(EC_ERR_SHAPE, "ec_kv_attend")
-    if lse is not None and (str(lse.dtype) != "torch.float32" or not lse.is_contiguous() or lse.numel() != q.shape[0] * heads):
+    if lse is not None and (lse.dtype not in _ROW_DTYPES or _ROW_DTYPES[lse.dtype] != EC_DTYPE_FP32
+                            or not lse.is_contiguous() or lse.numel() != n * heads):
         raise EcError(EC_ERR_INVALID_ARG, "ec_kv_attend: lse is a contiguous float32 tensor [rows, n_q_heads]")
-    at = KvAttn(heads, window, sinks, scale)
     if work is None:
         import torch
-        work = torch.empty(kv_attend_work_bytes(cache, seqs.n, q.shape[0], heads, max_new,
-                                                max_len or seqs.pages * p.page_tokens, window, sinks),
+        work = torch.empty(kv_attend_work_bytes(cache, seqs.n, n, heads, max_new,
+                                                max_len or seqs.pages * cache.params.page_tokens, window, sinks),
                            dtype=torch.uint8, device=q.device)
-    _check(lib.ec_kv_attend(cache.handle, layer, seqs.ref, _starts_ptr(starts, cache, seqs.n, "ec_kv_attend"), q.shape[0],
-                            max_new, max_len, ctypes.addressof(at), ctypes.addressof(qr), ctypes.addressof(orr),
-                            0 if lse is None else _on_gpu(lse, "ec_kv_attend", cache.device),
-                            _on_gpu(work, "ec_kv_attend", cache.device), work.numel() * work.element_size(),
-                            _stream_ptr(stream)), "ec_kv_attend")
+    args = _ATTENTION.pack(_seqs(seqs, cache, "ec_kv_attend"), _int32_ptr(starts, cache, seqs.n + 1, "ec_kv_attend"), n, layer,
+                           max_new, max_len, heads, window, sinks, scale, qr, orr,
+                           0 if lse is None else _at(lse, cache, "ec_kv_attend"), _at(work, cache, "ec_kv_attend"), work.nbytes)
+    rc = lib.ec_kv_attend(cache.handle, args, _kv_stream(stream, cache))
+    if rc:
+        raise EcError(rc, "ec_kv_attend")
 
 
 def kv_pages_work_bytes(cache: KvCache, n_from: int, n_to: int) -> int:
@@ -579,16 +616,6 @@ def kv_pages_work_bytes(cache: KvCache, n_from: int, n_to: int) -> int:
     n = ctypes.c_size_t(0)
     _check(lib.ec_kv_pages_work_bytes(cache.handle, n_from, n_to, ctypes.byref(n)), "ec_kv_pages_work_bytes")
     return int(n.value)
-
-
-def _int32_ptr(t, cache, n: int, what: str) -> int:
-    if t is None:
-        return 0
-    if str(t.dtype) != "torch.int32" or not t.is_contiguous():
-        raise EcError(EC_ERR_INVALID_ARG, what + ": contiguous int32 device tensors")
-    if t.numel() != n:
-        raise EcError(EC_ERR_SHAPE, what)
-    return _on_gpu(t, what, cache.device)
 
 
 def _pages_work(cache, a: KvSeqs, b: KvSeqs, work):
@@ -601,19 +628,23 @@ def _pages_work(cache, a: KvSeqs, b: KvSeqs, work):
 def kv_fork(cache: KvCache, seqs: KvSeqs, refs, to: KvSeqs, refs_out, parents=None, grow=None, work=None,
             stream=None) -> None:
     """ec_kv_fork: sequences `to` continue seqs[parents] with room for `grow` more tokens."""
-    n = cache.params.n_pages
+    n, what = cache.params.n_pages, "ec_kv_fork"
     work = _pages_work(cache, seqs, to, work)
-    _check(lib.ec_kv_fork(cache.handle, seqs.ref, _int32_ptr(refs, cache, n, "ec_kv_fork"), _int32_ptr(parents, cache, to.n, "ec_kv_fork"),
-                          _int32_ptr(grow, cache, to.n, "ec_kv_fork"), to.ref, _int32_ptr(refs_out, cache, n, "ec_kv_fork"),
-                          _on_gpu(work, "ec_kv_fork", cache.device), work.numel() * work.element_size(),
-                          _stream_ptr(stream)), "ec_kv_fork")
+    args = _PAGES.pack(_seqs(seqs, cache, what), _seqs(to, cache, what), _int32_ptr(refs, cache, n, what),
+                       _int32_ptr(refs_out, cache, n, what), _int32_ptr(parents, cache, to.n, what),
+                       _int32_ptr(grow, cache, to.n, what), 0, _at(work, cache, what), work.nbytes)
+    rc = lib.ec_kv_fork(cache.handle, args, _kv_stream(stream, cache))
+    if rc:
+        raise EcError(rc, what)
 
 
 def kv_compact(cache: KvCache, seqs: KvSeqs, refs, to: KvSeqs, refs_out, page_map=None, work=None, stream=None) -> None:
     """ec_kv_compact: the pages in use move to the lowest numbers; page_map: old number -> new."""
-    n = cache.params.n_pages
+    n, what = cache.params.n_pages, "ec_kv_compact"
     work = _pages_work(cache, seqs, to, work)
-    _check(lib.ec_kv_compact(cache.handle, seqs.ref, _int32_ptr(refs, cache, n, "ec_kv_compact"), to.ref,
-                             _int32_ptr(refs_out, cache, n, "ec_kv_compact"), _int32_ptr(page_map, cache, n, "ec_kv_compact"),
-                             _on_gpu(work, "ec_kv_compact", cache.device), work.numel() * work.element_size(),
-                             _stream_ptr(stream)), "ec_kv_compact")
+    args = _PAGES.pack(_seqs(seqs, cache, what), _seqs(to, cache, what), _int32_ptr(refs, cache, n, what),
+                       _int32_ptr(refs_out, cache, n, what), 0, 0, _int32_ptr(page_map, cache, n, what),
+                       _at(work, cache, what), work.nbytes)
+    rc = lib.ec_kv_compact(cache.handle, args, _kv_stream(stream, cache))
+    if rc:
+        raise EcError(rc, what)

@@ -63,7 +63,6 @@ bool pool_view(const ec_kv* C, int layer, Pool* o) {
 }
 
 int check_seqs(const ec_kv_seqs* S) {
-    if (!S) return EC_ERR_INVALID_ARG;
     if (S->n_seqs < 0 || S->table_stride < 0) return EC_ERR_SHAPE;
     if (S->n_seqs > EC_KV_MAX_SEQS) return EC_ERR_UNSUPPORTED;
     if (S->table_stride > (int64_t(1) << 26)) return EC_ERR_UNSUPPORTED;
@@ -71,8 +70,7 @@ int check_seqs(const ec_kv_seqs* S) {
     return EC_OK;
 }
 
-int check_rows(const ec_kv* C, const ec_kv_rows* r, int heads, int64_t n_rows, Rows* o) {
-    if (!r) return EC_ERR_INVALID_ARG;
+int check_rows(const ec_kv_rows* r, int heads, int64_t n_rows, Rows* o) {
     int size = 0;
     if (r->dtype == EC_DTYPE_FP32) size = 4;
     else if (r->dtype == EC_DTYPE_BF16 || r->dtype == EC_DTYPE_FP16) size = 2;
@@ -89,14 +87,12 @@ int check_rows(const ec_kv* C, const ec_kv_rows* r, int heads, int64_t n_rows, R
     o->head = r->head_stride;
     o->dtype = r->dtype;
     o->wide = ((uintptr_t)r->data % 16 == 0 && r->row_stride * size % 16 == 0 && r->head_stride * size % 16 == 0) ? 1 : 0;
-    (void)C;
     return EC_OK;
 }
 
 /* The checks that every call on new tokens makes; *go = false when there is nothing to do. */
 static int check_call(const ec_kv* C, int layer, const ec_kv_seqs* seqs, const int32_t* starts, int64_t n_rows,
                       int max_new, Pool* P, Seqs* S, bool* go) {
-    if (!C) return EC_ERR_INVALID_ARG;
     int rc = check_seqs(seqs);
     if (rc != EC_OK) return rc;
     if (!pool_view(C, layer, P)) return EC_ERR_INVALID_ARG;
@@ -662,18 +658,18 @@ static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     return a && b && na && nb && (const uint8_t*)a < (const uint8_t*)b + nb && (const uint8_t*)b < (const uint8_t*)a + na;
 }
 
-static int check_pages(const ec_kv* C, const ec_kv_seqs* from, const int32_t* refs, const ec_kv_seqs* to,
-                       const int32_t* refs_out, const void* work, size_t work_bytes) {
-    if (!C) return EC_ERR_INVALID_ARG;
-    int rc = check_seqs(from);
-    if (rc == EC_OK) rc = check_seqs(to);
+static int check_pages(const ec_kv* C, const ec_kv_pages* g) {
+    if (!C || !g) return EC_ERR_INVALID_ARG;
+    const ec_kv_seqs &from = g->from, &to = g->to;
+    int rc = check_seqs(&from);
+    if (rc == EC_OK) rc = check_seqs(&to);
     if (rc != EC_OK) return rc;
-    if (!refs || !refs_out || !work || (uintptr_t)work % 16) return EC_ERR_INVALID_ARG;
-    if (work_bytes < pages_work(C, from->n_seqs, to->n_seqs)) return EC_ERR_INVALID_ARG;
-    const size_t in = sizeof(int32_t) * (size_t)(from->n_seqs * from->table_stride), nr = sizeof(int32_t) * (size_t)C->p.n_pages,
-                 out = sizeof(int32_t) * (size_t)(to->n_seqs * to->table_stride);
-    if (overlap(from->table, in, to->table, out) || overlap(refs, nr, refs_out, nr) ||
-        overlap(from->lens, sizeof(int32_t) * (size_t)from->n_seqs, to->lens, sizeof(int32_t) * (size_t)to->n_seqs))
+    if (!g->refs || !g->refs_out || !g->work || (uintptr_t)g->work % 16) return EC_ERR_INVALID_ARG;
+    if (g->work_bytes < pages_work(C, from.n_seqs, to.n_seqs)) return EC_ERR_INVALID_ARG;
+    const size_t in = sizeof(int32_t) * (size_t)(from.n_seqs * from.table_stride), nr = sizeof(int32_t) * (size_t)C->p.n_pages,
+                 out = sizeof(int32_t) * (size_t)(to.n_seqs * to.table_stride);
+    if (overlap(from.table, in, to.table, out) || overlap(g->refs, nr, g->refs_out, nr) ||
+        overlap(from.lens, sizeof(int32_t) * (size_t)from.n_seqs, to.lens, sizeof(int32_t) * (size_t)to.n_seqs))
         return EC_ERR_INVALID_ARG;
     return EC_OK;
 }
@@ -737,41 +733,41 @@ extern "C" int ec_kv_create(const ec_kv_params* params, void* pool, size_t pool_
 
 extern "C" void ec_kv_free(ec_kv* C) { delete C; }
 
-extern "C" int ec_kv_append(const ec_kv* C, int layer, const ec_kv_seqs* seqs, const int32_t* starts, int64_t n_rows,
-                            int max_new, const ec_kv_rows* k, const ec_kv_rows* v, cudaStream_t stream) {
+extern "C" int ec_kv_append(const ec_kv* C, const ec_kv_tokens* t, cudaStream_t stream) {
+    if (!C || !t) return EC_ERR_INVALID_ARG;
     AppendArgs a{};
     bool go = false;
-    int rc = check_call(C, layer, seqs, starts, n_rows, max_new, &a.P, &a.S, &go);
-    if (rc == EC_OK) rc = check_rows(C, k, a.P.n_heads, n_rows, &a.k);
-    if (rc == EC_OK) rc = check_rows(C, v, a.P.n_heads, n_rows, &a.v);
+    int rc = check_call(C, t->layer, &t->seqs, t->starts, t->n_rows, t->max_new, &a.P, &a.S, &go);
+    if (rc == EC_OK) rc = check_rows(&t->k, a.P.n_heads, t->n_rows, &a.k);
+    if (rc == EC_OK) rc = check_rows(&t->v, a.P.n_heads, t->n_rows, &a.v);
     if (rc != EC_OK) return rc;
     Device d;
     if ((rc = device_of(C, &d)) != EC_OK) return rc;
     if (!go) return EC_OK;
-    a.units = units_of(max_new);
-    a.max_new = max_new;
+    a.units = units_of(t->max_new);
+    a.max_new = t->max_new;
     a.status = d.status;
     const int64_t items = (int64_t)a.S.n_seqs * a.units * a.P.n_heads, grid = (items + kIoWarps - 1) / kIoWarps;
     if (grid > 0x7FFFFFFF) return EC_ERR_UNSUPPORTED;
     return launch(kv_append_kernel, dim3((unsigned)grid), kIoWarps * 32, (size_t)kIoWarps * a.P.unit_bytes, stream, a);
 }
 
-extern "C" int ec_kv_read(const ec_kv* C, int layer, const ec_kv_seqs* seqs, const int32_t* starts, int64_t n_rows,
-                          int max_new, const ec_kv_rows* k, const ec_kv_rows* v, cudaStream_t stream) {
+extern "C" int ec_kv_read(const ec_kv* C, const ec_kv_tokens* t, cudaStream_t stream) {
+    if (!C || !t) return EC_ERR_INVALID_ARG;
     ReadArgs a{};
     bool go = false;
-    int rc = check_call(C, layer, seqs, starts, n_rows, max_new, &a.P, &a.S, &go);
-    if (rc == EC_OK && !k && !v) rc = EC_ERR_INVALID_ARG;
-    if (rc == EC_OK && k) rc = check_rows(C, k, a.P.n_heads, n_rows, &a.k);
-    if (rc == EC_OK && v) rc = check_rows(C, v, a.P.n_heads, n_rows, &a.v);
+    int rc = check_call(C, t->layer, &t->seqs, t->starts, t->n_rows, t->max_new, &a.P, &a.S, &go);
+    a.has_k = t->k.data != nullptr;
+    a.has_v = t->v.data != nullptr;
+    if (rc == EC_OK && t->n_rows > 0 && !a.has_k && !a.has_v) rc = EC_ERR_INVALID_ARG;
+    if (rc == EC_OK && a.has_k) rc = check_rows(&t->k, a.P.n_heads, t->n_rows, &a.k);
+    if (rc == EC_OK && a.has_v) rc = check_rows(&t->v, a.P.n_heads, t->n_rows, &a.v);
     if (rc != EC_OK) return rc;
     Device d;
     if ((rc = device_of(C, &d)) != EC_OK) return rc;
     if (!go) return EC_OK;
-    a.has_k = k != nullptr;
-    a.has_v = v != nullptr;
-    a.units = units_of(max_new);
-    a.max_new = max_new;
+    a.units = units_of(t->max_new);
+    a.max_new = t->max_new;
     a.status = d.status;
     const int64_t items = (int64_t)a.S.n_seqs * a.units * a.P.n_heads, grid = (items + kIoWarps - 1) / kIoWarps;
     if (grid > 0x7FFFFFFF) return EC_ERR_UNSUPPORTED;
@@ -786,21 +782,20 @@ extern "C" int ec_kv_pages_work_bytes(const ec_kv* C, int n_from, int n_to, size
     return EC_OK;
 }
 
-extern "C" int ec_kv_fork(const ec_kv* C, const ec_kv_seqs* from, const int32_t* refs, const int32_t* parents,
-                          const int32_t* grow, const ec_kv_seqs* to, int32_t* refs_out, void* work, size_t work_bytes,
-                          cudaStream_t stream) {
-    int rc = check_pages(C, from, refs, to, refs_out, work, work_bytes);
+extern "C" int ec_kv_fork(const ec_kv* C, const ec_kv_pages* g, cudaStream_t stream) {
+    int rc = check_pages(C, g);
     if (rc != EC_OK) return rc;
-    if (!parents && to->n_seqs > 0 && from->n_seqs != to->n_seqs) return EC_ERR_SHAPE;
+    const ec_kv_seqs *from = &g->from, *to = &g->to;
+    if (!g->parents && to->n_seqs > 0 && from->n_seqs != to->n_seqs) return EC_ERR_SHAPE;
     PlanArgs a{};
     if (!pool_view(C, 0, &a.P)) return EC_ERR_INVALID_ARG;
     Device d;
     if ((rc = device_of(C, &d)) != EC_OK) return rc;
-    a.table = from->table, a.lens = from->lens, a.refs = refs, a.parents = parents, a.grow = grow;
-    a.table_out = to->table, a.lens_out = to->lens, a.refs_out = refs_out;
+    a.table = from->table, a.lens = from->lens, a.refs = g->refs, a.parents = g->parents, a.grow = g->grow;
+    a.table_out = to->table, a.lens_out = to->lens, a.refs_out = g->refs_out;
     a.in_stride = from->table_stride, a.out_stride = to->table_stride;
     a.n_in = from->n_seqs, a.n_out = to->n_seqs;
-    uint8_t* w = (uint8_t*)work;
+    uint8_t* w = (uint8_t*)g->work;
     a.count = (int32_t*)w;
     w += 16;
     a.copies = (int32_t*)w;
@@ -817,28 +812,28 @@ extern "C" int ec_kv_fork(const ec_kv* C, const ec_kv_seqs* from, const int32_t*
     return run_copies(C, a, a.n_out, d, stream);
 }
 
-extern "C" int ec_kv_compact(const ec_kv* C, const ec_kv_seqs* from, const int32_t* refs, const ec_kv_seqs* to,
-                             int32_t* refs_out, int32_t* map, void* work, size_t work_bytes, cudaStream_t stream) {
-    int rc = check_pages(C, from, refs, to, refs_out, work, work_bytes);
+extern "C" int ec_kv_compact(const ec_kv* C, const ec_kv_pages* g, cudaStream_t stream) {
+    int rc = check_pages(C, g);
     if (rc != EC_OK) return rc;
+    const ec_kv_seqs *from = &g->from, *to = &g->to;
     if (from->n_seqs != to->n_seqs) return EC_ERR_SHAPE;
     if (to->table_stride < from->table_stride) return EC_ERR_SHAPE;
     const size_t nr = sizeof(int32_t) * (size_t)C->p.n_pages;
-    if (overlap(map, nr, refs, nr) || overlap(map, nr, refs_out, nr)) return EC_ERR_INVALID_ARG;
+    if (overlap(g->map, nr, g->refs, nr) || overlap(g->map, nr, g->refs_out, nr)) return EC_ERR_INVALID_ARG;
     PlanArgs a{};
     if (!pool_view(C, 0, &a.P)) return EC_ERR_INVALID_ARG;
     Device d;
     if ((rc = device_of(C, &d)) != EC_OK) return rc;
-    a.table = from->table, a.lens = from->lens, a.refs = refs;
-    a.table_out = to->table, a.lens_out = to->lens, a.refs_out = refs_out;
+    a.table = from->table, a.lens = from->lens, a.refs = g->refs;
+    a.table_out = to->table, a.lens_out = to->lens, a.refs_out = g->refs_out;
     a.in_stride = from->table_stride, a.out_stride = to->table_stride;
     a.n_in = from->n_seqs, a.n_out = to->n_seqs;
-    uint8_t* w = (uint8_t*)work;
+    uint8_t* w = (uint8_t*)g->work;
     a.count = (int32_t*)w;
     w += 16;
     a.copies = (int32_t*)w;
     w += align16(12 * ((size_t)C->p.n_pages / 2 + 1));
-    a.map = map ? map : (int32_t*)w;
+    a.map = g->map ? g->map : (int32_t*)w;
     a.status = d.status;
     if ((rc = launch(kv_compact_plan_kernel, dim3(1), kPlanThreads, 0, stream, a)) != EC_OK) return rc;
     return run_copies(C, a, C->p.n_pages / 2 + 1, d, stream);

@@ -829,38 +829,38 @@ extern "C" int ec_kv_attend_work_bytes(const ec_kv* C, int n_seqs, int64_t n_row
     return EC_OK;
 }
 
-extern "C" int ec_kv_attend(const ec_kv* C, int layer, const ec_kv_seqs* seqs, const int32_t* starts, int64_t n_rows,
-                            int max_new, int64_t max_len, const ec_kv_attn* attn, const ec_kv_rows* q, const ec_kv_rows* out,
-                            float* lse, void* work, size_t work_bytes, cudaStream_t stream) {
-    if (!C || !attn) return EC_ERR_INVALID_ARG;
-    int rc = check_seqs(seqs);
+extern "C" int ec_kv_attend(const ec_kv* C, const ec_kv_attention* t, cudaStream_t stream) {
+    if (!C || !t) return EC_ERR_INVALID_ARG;
+    int rc = check_seqs(&t->seqs);
     if (rc != EC_OK) return rc;
+    int64_t max_len = t->max_len;
     if (max_len == 0) {
-        max_len = seqs->table_stride * C->p.page_tokens;
+        max_len = t->seqs.table_stride * C->p.page_tokens;
         if (max_len > 0x7FFFFFF0) max_len = 0x7FFFFFF0; /* lens are 32-bit */
     }
-    if ((rc = check_attn(C, seqs->n_seqs, n_rows, max_new, max_len, attn)) != EC_OK) return rc;
-    if (!starts && n_rows < seqs->n_seqs) return EC_ERR_SHAPE;
+    const ec_kv_attn& at = t->attn;
+    if ((rc = check_attn(C, t->seqs.n_seqs, t->n_rows, t->max_new, max_len, &at)) != EC_OK) return rc;
+    if (!t->starts && t->n_rows < t->seqs.n_seqs) return EC_ERR_SHAPE;
     AttnArgs a{};
-    if (!pool_view(C, layer, &a.P)) return EC_ERR_INVALID_ARG;
-    if ((rc = check_rows(C, q, attn->n_q_heads, n_rows, &a.q)) != EC_OK) return rc;
-    if ((rc = check_rows(C, out, attn->n_q_heads, n_rows, &a.out)) != EC_OK) return rc;
-    if (lse && (uintptr_t)lse % 4) return EC_ERR_INVALID_ARG;
+    if (!pool_view(C, t->layer, &a.P)) return EC_ERR_INVALID_ARG;
+    if ((rc = check_rows(&t->q, at.n_q_heads, t->n_rows, &a.q)) != EC_OK) return rc;
+    if ((rc = check_rows(&t->out, at.n_q_heads, t->n_rows, &a.out)) != EC_OK) return rc;
+    if ((uintptr_t)t->lse % 4) return EC_ERR_INVALID_ARG;
     Device d;
     if ((rc = device_of(C, &d)) != EC_OK) return rc;
-    if (seqs->n_seqs == 0 || n_rows == 0 || max_new == 0) return EC_OK;
+    if (t->seqs.n_seqs == 0 || t->n_rows == 0 || t->max_new == 0) return EC_OK;
     Plan p;
-    if (!plan_of(C, d.sms, seqs->n_seqs, max_new, max_len, attn, &p)) return EC_ERR_UNSUPPORTED;
-    if (p.work && (!work || (uintptr_t)work % 16 || work_bytes < p.work)) return EC_ERR_INVALID_ARG;
-    a.S = Seqs{seqs->table, seqs->lens, starts, seqs->table_stride, n_rows, seqs->n_seqs};
-    a.lse = lse;
-    a.part = (float*)work;
-    a.n_q_heads = attn->n_q_heads;
-    a.group = attn->n_q_heads / C->p.n_kv_heads;
-    a.window = attn->window;
-    a.sinks = attn->sinks;
-    a.scale = attn->scale > 0.f ? attn->scale : 1.f / sqrtf((float)C->p.head_dim);
-    a.max_new = max_new;
+    if (!plan_of(C, d.sms, t->seqs.n_seqs, t->max_new, max_len, &at, &p)) return EC_ERR_UNSUPPORTED;
+    if (p.work && (!t->work || (uintptr_t)t->work % 16 || t->work_bytes < p.work)) return EC_ERR_INVALID_ARG;
+    a.S = Seqs{t->seqs.table, t->seqs.lens, t->starts, t->seqs.table_stride, t->n_rows, t->seqs.n_seqs};
+    a.lse = t->lse;
+    a.part = (float*)t->work;
+    a.n_q_heads = at.n_q_heads;
+    a.group = at.n_q_heads / C->p.n_kv_heads;
+    a.window = at.window;
+    a.sinks = at.sinks;
+    a.scale = at.scale > 0.f ? at.scale : 1.f / sqrtf((float)C->p.head_dim);
+    a.max_new = t->max_new;
     a.max_len = (int32_t)max_len;
     a.solo = p.solo;
     a.status = d.status;

@@ -207,7 +207,7 @@ struct Device {
 int device_of(const ec_kv* C, Device* out);              /* EC_ERR_* unless C's pool is on the current device */
 bool pool_view(const ec_kv* C, int layer, Pool* out);    /* false: layer out of range */
 int check_seqs(const ec_kv_seqs* S);
-int check_rows(const ec_kv* C, const ec_kv_rows* r, int heads, int64_t n_rows, Rows* out);
+int check_rows(const ec_kv_rows* r, int heads, int64_t n_rows, Rows* out);
 bool use_pdl();
 
 /* A kernel's dynamic shared-memory limit, raised before its first launch on a device. */

@@ -53,6 +53,39 @@ def test_create(ec, e):
     c.free()
 
 
+class Seqs(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("lens", ctypes.c_void_p), ("n_seqs", ctypes.c_int32)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class Attn(ctypes.Structure):
+    _fields_ = [("n_q_heads", ctypes.c_int32), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class Tokens(ctypes.Structure):
+    _fields_ = [("seqs", Seqs), ("starts", ctypes.c_void_p), ("n_rows", ctypes.c_int64), ("layer", ctypes.c_int32),
+                ("max_new", ctypes.c_int32), ("k", Rows), ("v", Rows)]
+
+
+class Attention(ctypes.Structure):
+    _fields_ = [("seqs", Seqs), ("starts", ctypes.c_void_p), ("n_rows", ctypes.c_int64), ("layer", ctypes.c_int32),
+                ("max_new", ctypes.c_int32), ("max_len", ctypes.c_int64), ("attn", Attn), ("q", Rows), ("out", Rows),
+                ("lse", ctypes.c_void_p), ("work", ctypes.c_void_p), ("work_bytes", ctypes.c_size_t)]
+
+
+class Pages(ctypes.Structure):
+    _fields_ = [("frm", Seqs), ("to", Seqs), ("refs", ctypes.c_void_p), ("refs_out", ctypes.c_void_p), ("parents", ctypes.c_void_p),
+                ("grow", ctypes.c_void_p), ("map", ctypes.c_void_p), ("work", ctypes.c_void_p), ("work_bytes", ctypes.c_size_t)]
+
+
+def test_packed_arguments_have_the_structures_sizes(e):
+    for a, b in ((e._SEQS, Seqs), (e._ROWS, Rows), (e._TOKENS, Tokens), (e._ATTENTION, Attention), (e._PAGES, Pages)):
+        assert a.size == ctypes.sizeof(b)
+
+
 class Host:
     """A cache without a device and arguments that are right otherwise (host addresses that
     no call gets as far as using)."""
@@ -62,22 +95,18 @@ class Host:
         self.cache = ec.kv_cache(2, 100, heads, dim, 64, device=-1)
         self.buf = np.zeros(1 << 16, np.int32)
         self.at = self.buf.ctypes.data & ~15
-        self.seqs = e.KvSeqsStruct(self.at, 10, self.at, 3)
-        self.rows = e.KvRows(self.at, heads * dim, dim, 0)
-        self.q = e.KvRows(self.at, 4 * heads * dim, dim, 4)
-        self.attn = e.KvAttn(4 * heads, 0, 0, 0.0)
+        self.seqs = (self.at, 10, self.at, 3)
+        self.rows = (self.at, heads * dim, dim, 0)
+        self.attn = (4 * heads, 0, 0, 0.0)
 
-    def append(self, fn="ec_kv_append", cache=None, layer=0, seqs=0, starts=0, n_rows=3, max_new=1, k=0, v=0):
-        a = ctypes.addressof
-        pick = lambda given, own: own if given == 0 else given
-        return getattr(self.lib, fn)(self.cache.handle if cache is None else cache, layer, pick(seqs, a(self.seqs)), starts,
-                                     n_rows, max_new, pick(k, a(self.rows)), pick(v, a(self.rows)), None)
+    def append(self, fn="ec_kv_append", cache=0, args=0, seqs=None, n_rows=3, layer=0, max_new=1, k=None, v=None):
+        t = Tokens(Seqs(*(seqs or self.seqs)), 0, n_rows, layer, max_new, Rows(*(k or self.rows)), Rows(*(v or self.rows)))
+        return getattr(self.lib, fn)(self.cache.handle if cache == 0 else cache, ctypes.addressof(t) if args == 0 else args, None)
 
-    def attend(self, layer=0, seqs=0, starts=0, n_rows=3, max_new=1, max_len=0, attn=0, q=0, out=0, lse=0, work=0, work_bytes=0):
-        a = ctypes.addressof
-        pick = lambda given, own: own if given == 0 else given
-        return self.lib.ec_kv_attend(self.cache.handle, layer, pick(seqs, a(self.seqs)), starts, n_rows, max_new, max_len,
-                                     pick(attn, a(self.attn)), pick(q, a(self.q)), pick(out, a(self.q)), lse, work, work_bytes, None)
+    def attend(self, cache=0, args=0, seqs=None, n_rows=3, layer=0, max_new=1, max_len=0, attn=None, q=None, out=None, lse=0, work=0, n=0):
+        t = Attention(Seqs(*(seqs or self.seqs)), 0, n_rows, layer, max_new, max_len, Attn(*(attn or self.attn)),
+                      Rows(*(q or self.rows)), Rows(*(out or self.rows)), lse, work, n)
+        return self.lib.ec_kv_attend(self.cache.handle if cache == 0 else cache, ctypes.addressof(t) if args == 0 else args, None)
 
 
 @pytest.fixture()
@@ -85,56 +114,49 @@ def host(ec, e):
     return Host(ec, e)
 
 
-def seqs_of(e, *v):
-    return e.KvSeqsStruct(*v)
-
-
 @pytest.mark.parametrize("fn", ["ec_kv_append", "ec_kv_read"])
 def test_append_and_read_refuse(host, e, fn):
-    a, at = ctypes.addressof, host.at
+    at = host.at
     assert host.append(fn) == e.EC_ERR_INVALID_ARG  # no pool: every check before that passed
-    assert host.append(fn, cache=ctypes.c_void_p(0)) == e.EC_ERR_INVALID_ARG
+    assert host.append(fn, cache=None) == e.EC_ERR_INVALID_ARG and host.append(fn, args=None) == e.EC_ERR_INVALID_ARG
     for layer in (-1, 2):
         assert host.append(fn, layer=layer) == e.EC_ERR_INVALID_ARG
-    assert host.append(fn, seqs=None) == e.EC_ERR_INVALID_ARG
     for s, code in (((0, 10, at, 3), e.EC_ERR_INVALID_ARG), ((at, 10, 0, 3), e.EC_ERR_INVALID_ARG), ((at, -1, at, 3), e.EC_ERR_SHAPE),
                     ((at, 10, at, -1), e.EC_ERR_SHAPE), ((at, 10, at, 1025), e.EC_ERR_UNSUPPORTED)):
-        x = seqs_of(e, *s)
-        assert host.append(fn, seqs=a(x), n_rows=2000) == code, s
+        assert host.append(fn, seqs=s, n_rows=2000) == code, s
     assert host.append(fn, n_rows=-1) == e.EC_ERR_SHAPE and host.append(fn, max_new=-1) == e.EC_ERR_SHAPE
     assert host.append(fn, n_rows=2) == e.EC_ERR_SHAPE  # fewer rows than sequences, one each
     assert host.append(fn, max_new=(1 << 24) + 1) == e.EC_ERR_UNSUPPORTED
-    for r, code in (((at, 512, 128, 1), e.EC_ERR_INVALID_ARG), ((at, 512, 128, 9), e.EC_ERR_INVALID_ARG), ((0, 512, 128, 0), e.EC_ERR_INVALID_ARG),
+    for r, code in (((at, 512, 128, 1), e.EC_ERR_INVALID_ARG), ((at, 512, 128, 9), e.EC_ERR_INVALID_ARG),
                     ((at + 1, 512, 128, 0), e.EC_ERR_INVALID_ARG), ((at + 2, 512, 128, 4), e.EC_ERR_INVALID_ARG),
                     ((at, -512, 128, 0), e.EC_ERR_SHAPE), ((at, 512, -128, 0), e.EC_ERR_SHAPE),
                     ((at, 1 << 60, 128, 0), e.EC_ERR_OVERFLOW), ((at, 512, 1 << 60, 0), e.EC_ERR_OVERFLOW)):
-        x = e.KvRows(*r)
-        assert host.append(fn, k=a(x)) == code, r
-        assert host.append(fn, v=a(x)) == code, r
-    if fn == "ec_kv_append":
-        assert host.append(fn, k=None) == e.EC_ERR_INVALID_ARG
+        assert host.append(fn, k=r) == code, r
+        assert host.append(fn, v=r) == code, r
+    none = (0, 512, 128, 0)
+    assert host.append(fn, k=none) == e.EC_ERR_INVALID_ARG and host.append(fn, k=none, v=none) == e.EC_ERR_INVALID_ARG
 
 
 def test_attend_refuses(host, e):
     a, at = ctypes.addressof, host.at
     assert host.attend() == e.EC_ERR_INVALID_ARG
-    assert host.attend(layer=2) == e.EC_ERR_INVALID_ARG and host.attend(attn=None) == e.EC_ERR_INVALID_ARG
+    assert host.attend(cache=None) == e.EC_ERR_INVALID_ARG and host.attend(args=None) == e.EC_ERR_INVALID_ARG
+    assert host.attend(layer=2) == e.EC_ERR_INVALID_ARG
     for t, code in (((15, 0, 0, 0), e.EC_ERR_SHAPE), ((0, 0, 0, 0), e.EC_ERR_SHAPE), ((16, -1, 0, 0), e.EC_ERR_INVALID_ARG),
                     ((16, 5, -1, 0), e.EC_ERR_INVALID_ARG), ((16, 0, 3, 0), e.EC_ERR_INVALID_ARG), ((16, 0, 0, -1.0), e.EC_ERR_INVALID_ARG),
                     ((16, 0, 0, float("nan")), e.EC_ERR_INVALID_ARG), ((16, 0, 0, float("inf")), e.EC_ERR_INVALID_ARG)):
-        x = e.KvAttn(*t)
-        assert host.attend(attn=a(x)) == code, t
+        assert host.attend(attn=t) == code, t
     assert host.attend(max_len=-1) == e.EC_ERR_SHAPE
     for r, code in (((0, 512, 128, 0), e.EC_ERR_INVALID_ARG), ((at, 512, 128, 2), e.EC_ERR_INVALID_ARG), ((at, -1, 128, 0), e.EC_ERR_SHAPE)):
-        x = e.KvRows(*r)
-        assert host.attend(q=a(x)) == code and host.attend(out=a(x)) == code
+        assert host.attend(q=r) == code and host.attend(out=r) == code
     assert host.attend(lse=at + 2) == e.EC_ERR_INVALID_ARG
-    n = ctypes.c_size_t()
+    assert host.attend(seqs=(at, 10, at, 1025), n_rows=2000) == e.EC_ERR_UNSUPPORTED and host.attend(n_rows=2) == e.EC_ERR_SHAPE
+    n, own = ctypes.c_size_t(), Attn(*host.attn)
     lib = host.lib
-    assert lib.ec_kv_attend_work_bytes(host.cache.handle, 3, 3, 1, 640, a(host.attn), None) == e.EC_ERR_INVALID_ARG
-    assert lib.ec_kv_attend_work_bytes(None, 3, 3, 1, 640, a(host.attn), a(n)) == e.EC_ERR_INVALID_ARG
-    assert lib.ec_kv_attend_work_bytes(host.cache.handle, -3, 3, 1, 640, a(host.attn), a(n)) == e.EC_ERR_SHAPE
-    assert lib.ec_kv_attend_work_bytes(host.cache.handle, 3, 3, 1, 640, a(host.attn), a(n)) == 0
+    assert lib.ec_kv_attend_work_bytes(host.cache.handle, 3, 3, 1, 640, a(own), None) == e.EC_ERR_INVALID_ARG
+    assert lib.ec_kv_attend_work_bytes(None, 3, 3, 1, 640, a(own), a(n)) == e.EC_ERR_INVALID_ARG
+    assert lib.ec_kv_attend_work_bytes(host.cache.handle, -3, 3, 1, 640, a(own), a(n)) == e.EC_ERR_SHAPE
+    assert lib.ec_kv_attend_work_bytes(host.cache.handle, 3, 3, 1, 640, a(own), a(n)) == 0
 
 
 def test_pages_refuse(host, e, ec):
@@ -142,23 +164,29 @@ def test_pages_refuse(host, e, ec):
     need = ec.kv_pages_work_bytes(host.cache, 3, 5)
     assert need > 0
     far = at + 40000
-    frm, to = e.KvSeqsStruct(at, 10, at + 4096, 3), e.KvSeqsStruct(far, 10, far + 4096, 3)
+    frm, to = (at, 10, at + 4096, 3), (far, 10, far + 4096, 3)
 
-    def fork(c=host.cache.handle, f=frm, r=at + 8192, p=0, g=0, t=to, o=far + 8192, w=at + 16384, n=1 << 20):
-        return lib.ec_kv_fork(c, None if f is None else a(f), r, p, g, None if t is None else a(t), o, w, n, None)
+    def call(name, c, f, r, t, o, m, w, n):
+        x = Pages(Seqs(*f), Seqs(*t), r, o, 0, 0, m, w, n)
+        return getattr(lib, name)(c, a(x), None)
+
+    def fork(c=host.cache.handle, f=frm, r=at + 8192, t=to, o=far + 8192, w=at + 16384, n=1 << 20):
+        return call("ec_kv_fork", c, f, r, t, o, 0, w, n)
 
     def compact(c=host.cache.handle, f=frm, r=at + 8192, t=to, o=far + 8192, m=0, w=at + 16384, n=1 << 20):
-        return lib.ec_kv_compact(c, None if f is None else a(f), r, None if t is None else a(t), o, m, w, n, None)
+        return call("ec_kv_compact", c, f, r, t, o, m, w, n)
 
+    assert lib.ec_kv_fork(host.cache.handle, None, None) == e.EC_ERR_INVALID_ARG
+    assert lib.ec_kv_compact(host.cache.handle, None, None) == e.EC_ERR_INVALID_ARG
     for fn in (fork, compact):
         assert fn() == e.EC_ERR_INVALID_ARG  # no pool
-        assert fn(c=None) == e.EC_ERR_INVALID_ARG and fn(f=None) == e.EC_ERR_INVALID_ARG and fn(t=None) == e.EC_ERR_INVALID_ARG
+        assert fn(c=None) == e.EC_ERR_INVALID_ARG
         assert fn(r=0) == e.EC_ERR_INVALID_ARG and fn(o=0) == e.EC_ERR_INVALID_ARG and fn(w=0) == e.EC_ERR_INVALID_ARG
         assert fn(w=at + 8) == e.EC_ERR_INVALID_ARG and fn(n=63) == e.EC_ERR_INVALID_ARG
         assert fn(o=at + 8192 + 16) == e.EC_ERR_INVALID_ARG  # overlaps refs
-        assert fn(t=e.KvSeqsStruct(at + 8, 10, far, 3)) == e.EC_ERR_INVALID_ARG
-        assert fn(t=e.KvSeqsStruct(far, 10, far + 4096, 2)) == e.EC_ERR_SHAPE
-    assert compact(t=e.KvSeqsStruct(far, 9, far + 4096, 3)) == e.EC_ERR_SHAPE
+        assert fn(t=(at + 8, 10, far, 3)) == e.EC_ERR_INVALID_ARG
+        assert fn(t=(far, 10, far + 4096, 2)) == e.EC_ERR_SHAPE
+    assert compact(t=(far, 9, far + 4096, 3)) == e.EC_ERR_SHAPE
     assert compact(m=at + 8192) == e.EC_ERR_INVALID_ARG
     with pytest.raises(ec.EcError):
         ec.kv_pages_work_bytes(host.cache, 1025, 1)
@@ -171,14 +199,14 @@ def test_binding_refuses_host_tensors_and_types(ec, e):
             ec.kv_seqs(t, n)
     cache = ec.kv_cache(1, 4, 2, 64, 16, device=-1)
 
-    class Seqs:
-        n, ref, pages = 2, 0, 3
+    class Some:
+        n, packed, pages, device = 2, bytes(32), 3, -1
     x = torch.zeros((2, 2, 64))
     for k in (x, x.double(), x[..., :32], x[:, :1], x.transpose(1, 2)):
         with pytest.raises(ec.EcError):
-            ec.kv_append(cache, 0, Seqs, k, k)
+            ec.kv_append(cache, 0, Some, k, k)
         with pytest.raises(ec.EcError):
-            ec.kv_attend(cache, 0, Seqs, k, k, work=x)
+            ec.kv_attend(cache, 0, Some, k, k, work=x)
     with pytest.raises(ec.EcError):
         ec.kv_cache(1, 4, 2, 64, 16, pool=torch.zeros(1 << 20, dtype=torch.uint8), device=0)
 
