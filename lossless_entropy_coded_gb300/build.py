@@ -16,7 +16,7 @@ OUT = os.path.join(HERE, "libec.so")
 BUILD = os.path.join(HERE, "_build")
 CUDA_HOME = os.environ.get("CUDA_HOME", "/usr/local/cuda")
 NVCC = os.path.join(CUDA_HOME, "bin", "nvcc") if os.path.exists(os.path.join(CUDA_HOME, "bin", "nvcc")) else "nvcc"
-KERNELS = ["ec_kernels", "ec_kv", "ec_kv_attn"]
+KERNELS = ["ec_kernels", "ec_kv", "ec_kv_attn", "ec_kv_prefill"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -150,31 +150,6 @@ __device__ __forceinline__ void load8(const Rows& R, int64_t off, float (&x)[8])
     }
 }
 
-__device__ __forceinline__ void store8(const Rows& R, int64_t off, const float (&x)[8]) {
-    if (R.wide) {
-        if (R.dtype == EC_DTYPE_FP32) {
-            *(float4*)((float*)R.data + off) = make_float4(x[0], x[1], x[2], x[3]);
-            *(float4*)((float*)R.data + off + 4) = make_float4(x[4], x[5], x[6], x[7]);
-        } else {
-            uint32_t u[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (R.dtype == EC_DTYPE_FP16) {
-                    const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-                    u[i] = *(const uint32_t*)&h;
-                } else {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-                    u[i] = *(const uint32_t*)&h;
-                }
-            }
-            *(uint4*)((uint16_t*)R.data + off) = make_uint4(u[0], u[1], u[2], u[3]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) store_elem(R, off + i, x[i]);
-    }
-}
-
 /* Eight channels of one token -> their word and the block's scale byte (the quad's four
  * lanes take part). */
 __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], int& e) {

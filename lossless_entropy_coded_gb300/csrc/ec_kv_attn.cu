@@ -8,25 +8,11 @@
  */
 #include <float.h>
 
-#include "ec_kv_internal.h"
+#include "ec_kv_attn.h"
 
 namespace kv {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-struct AttnArgs {
-    Pool P;
-    Seqs S;
-    Rows q, out;
-    float* lse;       /* [n_rows, n_q_heads] or NULL */
-    float* part;
-    int32_t n_q_heads, group;   /* query heads, per key/value head */
-    int32_t window, sinks;
-    float scale;
-    int32_t max_new, max_len;
-    int32_t solo;     /* > 0: one CTA per tile, this many places of work each; 0: even shares */
-    int* status;
-};
 
 /* Work is counted in units of 16 tokens of one tile (the rows of one key/value head's
  * group, 8 or 16 at a time), plus kTileCost for a tile's queries and outputs. */
@@ -749,6 +735,8 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ At
 struct Plan {
     int nt, grid, solo;
     size_t work;
+    bool many;         /* the tensor-memory form */
+    PrefillPlan pre;
 };
 
 template <int NB, int NT>
@@ -760,8 +748,12 @@ static void plan_shape(Plan* p, int sms, int64_t tiles, int64_t units) {
     p->work = p->solo ? 0 : (size_t)p->grid * 2 * H::RB * (H::D + 2) * sizeof(float);
 }
 
+/* Query rows per key/value head up to which the register form runs (it expands the tokens
+ * once per 8 or 16 rows, the tensor-memory form once per 128 or 256). */
+constexpr int64_t kFewRows = 16;
+
 /* false: more work than the kernels count (one sequence's places fit 31 bits) */
-static bool plan_of(const ec_kv* C, int sms, int n_seqs, int max_new, int64_t max_len, const ec_kv_attn* at, Plan* p) {
+static bool plan_of(const ec_kv* C, int sms, int n_seqs, int max_new, int64_t max_len, const ec_kv_attn* at, int dtype, Plan* p) {
     const int group = at->n_q_heads / C->p.n_kv_heads, nb = C->p.head_dim / 32;
     const int64_t rows = (int64_t)group * max_new;
     p->nt = rows > 8 && nb <= 4 ? 2 : 1;
@@ -771,6 +763,13 @@ static bool plan_of(const ec_kv* C, int sms, int n_seqs, int max_new, int64_t ma
         if (w < units) units = w;
     }
     if (units < 1) units = 1;
+    p->many = rows > kFewRows;
+    if (p->many) {
+        p->grid = p->solo = 0;
+        if (!plan_prefill(C, sms, n_seqs, max_new, units, group, dtype, &p->pre)) return false;
+        p->work = p->pre.work;
+        return true;
+    }
     const int64_t row_tiles = (rows + 8 * p->nt - 1) / (8 * p->nt), per_seq = row_tiles * C->p.n_kv_heads, tiles = per_seq * n_seqs;
     if (rows > 0x7FFFFFFF || per_seq > 0x7FFFFFFF / (units + kTileCost)) return false;
     if (nb == 2) p->nt == 1 ? plan_shape<2, 1>(p, sms, tiles, units) : plan_shape<2, 2>(p, sms, tiles, units);
@@ -823,9 +822,11 @@ extern "C" int ec_kv_attend_work_bytes(const ec_kv* C, int n_seqs, int64_t n_row
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return EC_ERR_CUDA;
     } else sms = 152;
-    Plan p;
-    if (!plan_of(C, sms, n_seqs, max_new, max_len, attn, &p)) return EC_ERR_UNSUPPORTED;
-    *bytes = p.work;
+    Plan p, f; /* FP32 queries take smaller row tiles */
+    if (!plan_of(C, sms, n_seqs, max_new, max_len, attn, EC_DTYPE_BF16, &p) ||
+        !plan_of(C, sms, n_seqs, max_new, max_len, attn, EC_DTYPE_FP32, &f))
+        return EC_ERR_UNSUPPORTED;
+    *bytes = p.work > f.work ? p.work : f.work;
     return EC_OK;
 }
 
@@ -850,7 +851,7 @@ extern "C" int ec_kv_attend(const ec_kv* C, const ec_kv_attention* t, cudaStream
     if ((rc = device_of(C, &d)) != EC_OK) return rc;
     if (t->seqs.n_seqs == 0 || t->n_rows == 0 || t->max_new == 0) return EC_OK;
     Plan p;
-    if (!plan_of(C, d.sms, t->seqs.n_seqs, t->max_new, max_len, &at, &p)) return EC_ERR_UNSUPPORTED;
+    if (!plan_of(C, d.sms, t->seqs.n_seqs, t->max_new, max_len, &at, t->q.dtype, &p)) return EC_ERR_UNSUPPORTED;
     if (p.work && (!t->work || (uintptr_t)t->work % 16 || t->work_bytes < p.work)) return EC_ERR_INVALID_ARG;
     a.S = Seqs{t->seqs.table, t->seqs.lens, t->starts, t->seqs.table_stride, t->n_rows, t->seqs.n_seqs};
     a.lse = t->lse;
@@ -864,6 +865,7 @@ extern "C" int ec_kv_attend(const ec_kv* C, const ec_kv_attention* t, cudaStream
     a.max_len = (int32_t)max_len;
     a.solo = p.solo;
     a.status = d.status;
+    if (p.many) return launch_prefill(a, p.pre, stream);
     switch (C->p.head_dim / 32) {
         case 2: return p.nt == 1 ? run_terms<2, 1>(a, p, stream) : run_terms<2, 2>(a, p, stream);
         case 4: return p.nt == 1 ? run_terms<4, 1>(a, p, stream) : run_terms<4, 2>(a, p, stream);

@@ -1,0 +1,774 @@
+/*
+ * ec_kv_prefill.cu -- attention of many new rows over the 4-bit cache on the tensor
+ * cores (tcgen05), the form of ec_kv_attend for more rows per key/value head than the
+ * register kernel holds at once.
+ *
+ * One CTA takes 128 NQ rows (row r of a sequence: new token r / group, query head r %
+ * group of one key/value head) and walks the tokens they see in tiles.  A tile is
+ * expanded from 4 bits once for all rows:
+ *   keys    FP16 k 2^(e - kref + 13), kref the tile's largest scale, so S = Q K^T comes
+ *           out times a power of two of the tile;
+ *   values  FP16 v 2^(e - vref), vref per 32 channels for the CTA's whole walk: it moves
+ *           (and the accumulators with it) only when a scale lies more than 2^13 above.
+ * S (FP32, in tensor memory) is read one row per thread, the weights 2^(s - m + 6) go
+ * back as FP16 in S's place and are the tensor-memory operand of O += P V.  The row's
+ * reference m moves, and O with it, only when a score passes it by 2^8.
+ *
+ * Warps: NQ groups of four for the softmax, four that expand tiles, one that issues the
+ * matrix instructions, one that copies units in.  Matrix instructions of the NQ row
+ * tiles alternate (P0 V, Q0 K', P1 V, Q1 K', ...), so that one tile's softmax runs under
+ * the other's products.
+ */
+#include <float.h>
+
+#include "ec_kv_attn.h"
+
+namespace kv {
+
+constexpr float kPBias = 6.f, kPSlack = 8.f;
+
+template <int NB, int NQ, int QT>
+struct PShape {
+    static constexpr int D = 32 * NB, UB = 17 * D;
+    static constexpr int TN = NB <= 4 ? 128 : 64;        /* tokens per tile */
+    static constexpr int UT = TN / kUnit;                /* units per tile */
+    static constexpr int QBYTES = 128 * D * 2;           /* one row tile, one part */
+    static constexpr int BUF = TN * D * 2;               /* one expanded tile */
+    static constexpr int RAW = UT * UB;                  /* one tile in 4 bits */
+    static constexpr int META = 32 + 32 + TN;            /* kfac, flags, vref[8], NaN masks */
+    static constexpr int RS = NB == 8 && QT == 2 ? 1 : 2; /* tiles in 4 bits */
+    static constexpr int FIXED = NQ * QT * QBYTES + RS * RAW + 1024;
+    static constexpr int ROOM = (232448 - 1024 - FIXED) / (BUF + META);
+    static constexpr int NBUF = ROOM > 4 ? 4 : ROOM;
+    static_assert(NBUF >= 2, "a key and a value tile fit");
+    static_assert(NQ * QT * QBYTES + NBUF * (BUF + META) + RS * RAW + 256 + 1024 <= 232448, "shared memory");
+    static constexpr int WARPS = 4 * NQ + 6;
+    static constexpr int SMEM = NQ * QT * QBYTES + NBUF * (BUF + META) + RS * RAW + 256 + 1024;
+    static constexpr int O_COL = NQ * TN;                /* accumulators behind the scores */
+    static constexpr uint32_t COLS = NQ * (TN + D) <= 256 ? 256 : 512;
+    static_assert(NQ * (TN + D) <= 512, "tensor memory");
+};
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+/* 32 lanes x 32 columns of 32 bits; the wait ties the registers, so nothing uses them before. */
+__device__ __forceinline__ void tc_ld32(uint32_t at, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                   "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]),
+                   "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
+                   "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t at, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
+        ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+          "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+          "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+          "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t at, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
+        ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+          "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(at)
+        : "memory");
+}
+/* Descriptor of a K-major operand in 128-byte-swizzled atoms of 64 FP16 columns, 8-row
+ * groups 1024 bytes apart: start address >> 4, stride 1024 B >> 4 at bit 32, version 1 at
+ * bit 46, swizzle mode 2 (128 B) at bit 61.  16 columns on: 32 bytes further. */
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t at) {
+    return (uint64_t)((at >> 4) & 0x3FFFu) | ((uint64_t)1u << 16) | ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1u << 46) |
+           ((uint64_t)2u << 61);
+}
+/* One matrix instruction by one elected lane of a converged warp: A from shared or from tensor memory. */
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t x) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory"); }
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t v;
+    asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u8 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t half_mul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t half_pack(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *(const uint32_t*)&h;
+}
+
+/* The largest of a word's four bytes that is not 255; *nan is set where one is 255. */
+__device__ __forceinline__ int byte_max(uint32_t w, bool* nan) {
+    int m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = (w >> (8 * i)) & 0xFF;
+        *nan |= e == 255;
+        m = max(m, e == 255 ? 0 : e);
+    }
+    return m;
+}
+
+/* What a CTA works on. */
+struct PJob {
+    int b, h, r0, R, len, first, group;
+    int sink_u, lo_u, units; /* units that its rows see */
+    int u0, u1;              /* this split's */
+    int64_t row0;
+};
+
+template <int NB, int NQ, int QT>
+__global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_kernel(const __grid_constant__ AttnArgs a) {
+    using H = PShape<NB, NQ, QT>;
+    constexpr int D = H::D, TN = H::TN, UT = H::UT, UB = H::UB, NBUF = H::NBUF;
+    extern __shared__ __align__(1024) uint8_t pf_smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const uint32_t base = (smem_u32(pf_smem) + 1023u) & ~1023u;
+    const uint32_t q_at = base, buf_at = q_at + NQ * QT * H::QBYTES, raw_at = buf_at + NBUF * H::BUF, meta_at = raw_at + H::RS * H::RAW,
+                   bars = meta_at + NBUF * H::META;
+    static_assert(H::META % 16 == 0 && H::RAW % 16 == 0, "sections stay aligned");
+    const uint32_t raw_full = bars, raw_empty = bars + 16, buf_full = bars + 32, buf_empty = buf_full + 8 * NBUF,
+                   s_full = buf_empty + 8 * NBUF, p_full = s_full + 8 * NQ, o_done = p_full + 8 * NQ, q_full = o_done + 8 * NQ,
+                   tslot = q_full + 8;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(raw_full + 8 * i, 1);
+            mbar_init(raw_empty + 8 * i, 4);
+        }
+        for (int i = 0; i < NBUF; ++i) {
+            mbar_init(buf_full + 8 * i, 4);
+            mbar_init(buf_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < NQ; ++i) {
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_full + 8 * i, 4);
+            mbar_init(o_done + 8 * i, 1);
+        }
+        mbar_init(q_full, 4 * NQ);
+        mbar_fence_init();
+    }
+    if (warp == 4 * NQ + 4) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tslot), "r"(H::COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = lds32(tslot);
+    grid_dep_launch();
+    grid_dep_wait();
+
+    /* late row tiles see the most tokens and come first */
+    PJob J;
+    {
+        int i = blockIdx.x;
+        const int sp = i % a.splits;
+        i /= a.splits;
+        J.h = i % a.P.n_heads;
+        i /= a.P.n_heads;
+        J.b = i % a.S.n_seqs;
+        const int rt = a.row_tiles - 1 - i / a.S.n_seqs;
+        Seq q = seq_of(a.S, a.P.page_shift, J.b);
+        if (q.len > a.max_len) q.len = a.max_len, q.bad = true;
+        if (q.m > a.max_new) q.m = a.max_new, q.bad = true;
+        if (q.bad && J.h == 0 && sp == 0 && rt == 0 && threadIdx.x == 0) flag_corrupt(a.status);
+        J.group = a.group;
+        J.len = q.len;
+        J.row0 = q.row0;
+        J.first = q.len - q.m;
+        J.R = q.m * a.group;
+        J.r0 = rt * (128 * NQ);
+        J.u0 = J.u1 = 0;
+        if (J.r0 < J.R) {
+            const int pos0 = J.first + J.r0 / a.group, pos1 = J.first + min(J.r0 + 128 * NQ - 1, J.R - 1) / a.group;
+            const int all = pos1 < 0 ? 0 : pos1 / kUnit + 1;
+            const int64_t lo = a.window ? (int64_t)pos0 - a.window + 1 : 0;
+            J.lo_u = lo > 0 ? (int)min(lo / kUnit, (int64_t)all) : 0;
+            J.sink_u = min((a.sinks + kUnit - 1) / kUnit, J.lo_u);
+            J.units = J.sink_u + all - J.lo_u;
+            const int tiles = (J.units + UT - 1) / UT, per = (tiles + a.splits - 1) / a.splits;
+            J.u0 = min(J.units, sp * per * UT);
+            J.u1 = min(J.units, (sp + 1) * per * UT);
+        }
+    }
+    const int T = (J.u1 - J.u0 + UT - 1) / UT;
+    bool live = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (live && !mbar_wait(bar, parity)) {
+            live = false;
+            flag_corrupt(a.status);
+        }
+        __syncwarp();
+    };
+    auto unit_of = [&](int u) { return u < J.sink_u ? u : u - J.sink_u + J.lo_u; };
+
+    if (J.r0 >= J.R) {
+        /* a row tile that this sequence does not have */
+    } else if (warp < 4 * NQ) {
+        /* ---------------------------------------------------------------- softmax */
+        const int t = warp >> 2, q4 = warp & 3, r = J.r0 + 128 * t + 32 * q4 + lane;
+        const bool on = r < J.R;
+        const uint32_t lanes = (uint32_t)(32 * q4) << 16;
+        const uint32_t s_at = tmem + lanes + t * TN, o_at = tmem + lanes + H::O_COL + t * D;
+        const int rr = min(r, J.R - 1), pos = J.first + rr / J.group, head = J.h * J.group + rr % J.group;
+        const int64_t row = J.row0 + rr / J.group;
+        float rowfac;
+        /* the row's query: a power of two brings its largest element to [2^14, 2^15) */
+        {
+            const int64_t off = row * a.q.row + (int64_t)head * a.q.head;
+            uint32_t top = 0;
+            auto get8 = [&](int d, float (&x)[8]) {
+                if (a.q.wide && a.q.dtype == EC_DTYPE_FP32) {
+                    const float4 u = *(const float4*)((const float*)a.q.data + off + d), v = *(const float4*)((const float*)a.q.data + off + d + 4);
+                    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+                } else if (a.q.wide) {
+                    const uint4 w = *(const uint4*)((const uint16_t*)a.q.data + off + d);
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (a.q.dtype == EC_DTYPE_FP16) {
+                            const float2 f = __half22float2(*(const __half2*)&u[i]);
+                            x[2 * i] = f.x, x[2 * i + 1] = f.y;
+                        } else x[2 * i] = __uint_as_float(u[i] << 16), x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = load_elem(a.q, off + d + i);
+                }
+                if (!on)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = 0.f;
+            };
+            for (int d = 0; d < D; d += 8) {
+                float x[8];
+                get8(d, x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+            }
+            const int E = (int)(top >> 23), up = E == 255 ? 127 : min(253, 268 - E);
+            const float s = __uint_as_float((uint32_t)up << 23);
+            rowfac = __uint_as_float((uint32_t)(254 - up) << 23) * a.scale * 1.4426950408889634f;
+            const int lr = 32 * q4 + lane;
+            for (int d = 0; d < D; d += 8) {
+                float x[8];
+                get8(d, x);
+                uint32_t w[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float y0 = x[2 * i] * s, y1 = x[2 * i + 1] * s;
+                    w[i] = half_pack(y0, y1);
+                    const float2 hi = __half22float2(*(const __half2*)&w[i]);
+                    lo[i] = half_pack(y0 - hi.x, y1 - hi.y);
+                }
+                const uint32_t at = q_at + t * QT * H::QBYTES + (d >> 6) * (128 * 128) + lr * 128 + ((((d >> 3) & 7) ^ (lr & 7)) << 4);
+                sts128(at, w[0], w[1], w[2], w[3]);
+                if constexpr (QT == 2) sts128(at + H::QBYTES, lo[0], lo[1], lo[2], lo[3]);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+        }
+
+        float m = 0.f, l = 0.f;
+        bool set = false; /* the row has seen a token: m is its reference */
+        int vref[NB];
+        uint32_t nan_blocks = 0;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) vref[k] = 0;
+        const int pos_lo = __shfl_sync(kAll, pos, 0), pos_hi = __shfl_sync(kAll, pos, 31);
+
+        for (int j = 0; j < T; ++j) {
+            const int vn = 2 * j + 1, vb = vn % NBUF;
+            const uint32_t meta = meta_at + vb * H::META;
+            wait(s_full + 8 * t, j & 1);
+            wait(buf_full + 8 * vb, (vn / NBUF) & 1);
+            tc_fence_after();
+            const float f = rowfac * __uint_as_float(lds32(meta));
+            const uint32_t flags = lds32(meta + 4);
+            const int ut = J.u0 + j * UT; /* the tile's first unit */
+            bool moved = false;
+            float vfac[NB];
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                const int nv = (int)lds32(meta + 32 + 4 * k);
+                vfac[k] = ex2((float)(vref[k] - nv));
+                moved |= nv != vref[k];
+                vref[k] = nv;
+            }
+            const int tok_a = unit_of(ut) * kUnit, tok_z = unit_of(min(ut + UT, J.u1) - 1) * kUnit + kUnit - 1;
+            const bool all = ut + UT <= J.u1 && tok_z <= pos_lo &&
+                             (!a.window || tok_a > pos_hi - a.window || tok_z < a.sinks);
+            uint32_t p[TN / 2];
+            float sum, tmax;
+            auto weights = [&](float mm) {
+                const float off = kPBias - mm;
+                float s0 = 0.f, s1 = 0.f, mx = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < TN / 32; ++k) {
+                    uint32_t v[32];
+                    tc_ld32(s_at + 32 * k, v);
+                    tc_wait_ld(v);
+                    if (!all) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int u = ut + 2 * k + (i >> 4), tok = unit_of(u) * kUnit + (i & 15);
+                            const bool see = u < J.u1 && tok <= pos && (!a.window || tok > pos - a.window || tok < a.sinks);
+                            v[i] = see ? v[i] : 0xFF800000u;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float x0 = __uint_as_float(v[i]), x1 = __uint_as_float(v[i + 1]);
+                        /* a masked score stays -inf whatever the factor's sign of zero */
+                        const float t0 = !all && v[i] == 0xFF800000u ? -INFINITY : fmaf(x0, f, off);
+                        const float t1 = !all && v[i + 1] == 0xFF800000u ? -INFINITY : fmaf(x1, f, off);
+                        mx = fmaxf(mx, fmaxf(t0, t1));
+                        const float p0 = ex2(t0), p1 = ex2(t1);
+                        s0 += p0;
+                        s1 += p1;
+                        p[16 * k + i / 2] = half_pack(p0, p1);
+                    }
+                }
+                sum = s0 + s1;
+                tmax = mx - off;
+            };
+            weights(m);
+            if (__any_sync(kAll, tmax > m + kPSlack || (!set && tmax > -INFINITY)) || moved) {
+                /* references move: the accumulators follow once the products before are done */
+                const float nm = set ? fmaxf(m, tmax) : tmax > -INFINITY ? tmax : 0.f, al = set ? ex2(m - nm) : 0.f;
+                set |= tmax > -INFINITY;
+                if (j > 0) {
+                    wait(o_done + 8 * t, (j - 1) & 1);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < NB; ++k) {
+                        uint32_t v[32];
+                        tc_ld32(o_at + 32 * k, v);
+                        tc_wait_ld(v);
+                        float fk = 1.f;
+#pragma unroll
+                        for (int k2 = 0; k2 < NB; ++k2) fk = k2 == k ? vfac[k2] : fk;
+                        fk *= al;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * fk);
+                        tc_st32(o_at + 32 * k, v);
+                    }
+                    tc_wait_st();
+                }
+                m = nm;
+                l *= al;
+                weights(m);
+            }
+            l += sum;
+#pragma unroll
+            for (int k = 0; k < TN / 32; ++k) tc_st16(s_at + 16 * k, &p[16 * k]);
+            tc_wait_st();
+            tc_fence_before();
+            if (flags & 1u) { /* tokens with NaN values: their blocks are NaN for the rows that see them */
+                for (int i = 0; i < TN; ++i) {
+                    const int u = ut + (i >> 4);
+                    if (u >= J.u1) break;
+                    const uint32_t w = lds8(meta + 64 + i);
+                    const int tok = unit_of(u) * kUnit + (i & 15);
+                    if (w && tok <= pos && (!a.window || tok > pos - a.window || tok < a.sinks)) nan_blocks |= w;
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full + 8 * t);
+        }
+
+        /* outputs */
+        if (T > 0) {
+            wait(o_done + 8 * t, (T - 1) & 1);
+            tc_fence_after();
+        }
+        const float inv = a.splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        float* part = a.part + ((int64_t)blockIdx.x * NQ + t) * (128 * (D + 2));
+#pragma unroll 1
+        for (int k = 0; k < NB; ++k) {
+            uint32_t v[32];
+            int vr = 0;
+#pragma unroll
+            for (int k2 = 0; k2 < NB; ++k2) vr = k2 == k ? vref[k2] : vr;
+            const float back = vr > 0 ? __uint_as_float((uint32_t)vr << 23) : 0.f;
+            if (T > 0) {
+                tc_ld32(o_at + 32 * k, v);
+                tc_wait_ld(v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0;
+            }
+            const bool nan = nan_blocks >> k & 1u;
+            float x[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = nan ? __uint_as_float(0x7FC00000u) : __uint_as_float(v[i]) * back * inv;
+            if (!on) continue;
+            if (a.splits > 1) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    *(float4*)&part[(32 * q4 + lane) * D + 32 * k + i] = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+            } else {
+                const int64_t off = row * a.out.row + (int64_t)head * a.out.head + 32 * k;
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    const float y[8] = {x[i], x[i + 1], x[i + 2], x[i + 3], x[i + 4], x[i + 5], x[i + 6], x[i + 7]};
+                    store8(a.out, off + i, y);
+                }
+            }
+        }
+        if (on) {
+            if (a.splits > 1) {
+                part[128 * D + 32 * q4 + lane] = set || !(l == 0.f) ? m : -FLT_MAX;
+                part[128 * D + 128 + 32 * q4 + lane] = l;
+            } else if (a.lse) a.lse[row * a.n_q_heads + head] = l == 0.f ? -INFINITY : (m - kPBias + log2f(l)) * 0.6931471805599453f;
+        }
+    } else if (warp < 4 * NQ + 4) {
+        /* ---------------------------------------------------------------- expansion */
+        const int w4 = warp - 4 * NQ;
+        int vref = 0; /* lane: of block lane % NB (0: unset) */
+        int n = 0;    /* tiles expanded: keys 2 j, values 2 j + 1 */
+        for (int j = 0; j < T; ++j) {
+            const uint32_t raw = raw_at + (j % H::RS) * H::RAW;
+            const int ut = J.u0 + j * UT, have = min(UT, J.u1 - ut);
+            wait(raw_full + 8 * (j % H::RS), (j / H::RS) & 1);
+            /* tokens that hold something: all but the last unit's end */
+            auto valid_in = [&](int u) { return u < have ? min(kUnit, J.len - unit_of(ut + u) * kUnit) : 0; };
+
+            /* the keys' largest scale: every warp looks at all of them, lane by lane a word
+             * of a token's scales (NB = 2, 6: two bytes at a time) */
+            int top = 0;
+            for (int i = lane; i < TN; i += 32) {
+                const int u = i >> 4, tk = i & 15;
+                if (tk < valid_in(u)) {
+                    const uint32_t at = raw + u * UB + 16 * D + tk * NB;
+                    bool nan = false;
+#pragma unroll
+                    for (int k = 0; k < NB; k += 2) {
+                        unsigned short x;
+                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at + k) : "memory");
+                        top = max(top, byte_max((uint32_t)x, &nan));
+                    }
+                }
+            }
+            const int kref = max(16, __reduce_max_sync(kAll, top));
+            {
+                const int buf = n % NBUF;
+                const uint32_t dst = buf_at + buf * H::BUF;
+                wait(buf_empty + 8 * buf, ((n / NBUF) & 1) ^ 1u);
+                for (int u = w4; u < UT; u += 4) {
+                    const uint32_t src = raw + u * UB;
+#pragma unroll
+                    for (int i4 = 0; i4 < NB / 2; ++i4) {
+                        const uint4 wv = lds128(src + i4 * 512 + lane * 16);
+                        const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int blk = 2 * i4 + (k >> 1), tk = g + 8 * (k & 1), rowt = u * kUnit + tk;
+                            const int e = (int)lds8(src + 16 * D + tk * NB + blk);
+                            /* 2^(e - kref + 13) twice, NaN for 255 */
+                            const uint32_t s = e == 255 ? 0x7E007E00u : (uint32_t)max(e - kref + 28, 0) * 0x04000400u;
+                            uint32_t h4[4];
+                            e2m1x8_f16(ww[k], h4);
+                            const int chunk = 4 * blk + c;
+                            sts128(dst + (chunk >> 3) * (TN * 128) + rowt * 128 + (((chunk & 7) ^ (rowt & 7)) << 4),
+                                   half_mul2(h4[0], s), half_mul2(h4[1], s), half_mul2(h4[2], s), half_mul2(h4[3], s));
+                        }
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(buf_full + 8 * buf);
+                ++n;
+            }
+
+            /* the values' largest scale per block: word 32 k + lane is of block lane % NB */
+            {
+                int vt = 0;
+                bool nan = false;
+                constexpr int WU = 4 * NB; /* words per unit */
+                for (int u = 0; u < have; ++u) {
+                    const int nv = valid_in(u);
+                    for (int i = lane; i < WU; i += 32) {
+                        uint32_t x = lds32(raw + u * UB + 16 * D + D / 2 + 4 * i);
+                        const int cc = i / NB;
+                        if (nv < kUnit) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (2 * cc + (k & 1) + 8 * (k >> 1) >= nv) x &= ~(0xFFu << (8 * k));
+                        }
+                        vt = max(vt, byte_max(x, &nan));
+                    }
+                }
+                /* lanes of one block: lane % NB equal (NB divides 32, or 24 of the lanes for NB = 6) */
+                int best = 0;
+#pragma unroll
+                for (int k = 0; k < (32 + NB - 1) / NB; ++k) {
+                    const int from = lane % NB + k * NB;
+                    const int y = __shfl_sync(kAll, vt, from & 31);
+                    if (from < 32) best = max(best, y);
+                }
+                if (vref == 0 || best > vref + 13) vref = max(vref, max(best, 1));
+                nan = __any_sync(kAll, nan);
+
+                const int buf = n % NBUF;
+                const uint32_t dst = buf_at + buf * H::BUF, meta = meta_at + buf * H::META;
+                wait(buf_empty + 8 * buf, ((n / NBUF) & 1) ^ 1u);
+                if (w4 == 0) {
+                    if (lane == 0) {
+                        sts32(meta, (uint32_t)(kref - 13) << 23); /* 2^(kref - 140) */
+                        sts32(meta + 4, nan ? 1u : 0u);
+                    }
+                    if (lane < NB) sts32(meta + 32 + 4 * lane, (uint32_t)vref);
+                }
+                if (nan && w4 == 0) {
+                    for (int i = lane; i < TN; i += 32) {
+                        const int u = i >> 4, tk = i & 15;
+                        uint32_t mask = 0;
+                        if (tk < valid_in(u))
+                            for (int k = 0; k < NB; ++k)
+                                if (lds8(raw + u * UB + 16 * D + D / 2 + ((((tk >> 1) & 3) * NB + k) * 2 + (tk >> 3)) * 2 + (tk & 1)) == 255u)
+                                    mask |= 1u << k;
+                        asm volatile("st.shared.u8 [%0], %1;" ::"r"(meta + 64 + i), "r"(mask) : "memory");
+                    }
+                }
+                for (int u = w4; u < UT; u += 4) {
+                    const uint32_t src = raw + u * UB;
+                    const int nv = valid_in(u);
+#pragma unroll
+                    for (int blk = 0; blk < NB; ++blk) {
+                        const int ref = __shfl_sync(kAll, vref, blk);
+                        const uint32_t x = lds32(src + 16 * D + D / 2 + (c * NB + blk) * 4);
+                        uint32_t s[2] = {0u, 0u};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int e = (x >> (8 * k)) & 0xFF, tk = 2 * c + (k & 1) + 8 * (k >> 1);
+                            const int z = e == 255 || tk >= nv ? 0 : min(max(e - ref + 15, 0), 30);
+                            s[k >> 1] |= (uint32_t)z << (10 + 16 * (k & 1));
+                        }
+                        uint32_t wv[2];
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(wv[0]), "=r"(wv[1])
+                                     : "r"(src + 8 * D + (blk >> 1) * 512 + lane * 16 + (blk & 1) * 8) : "memory");
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t h4[4];
+                            e2m1x8_f16(wv[i], h4);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) { /* byte r + 2 p */
+                                const int d = 32 * blk + 16 * i + 8 * (k & 1) + g, p = k >> 1;
+                                const int chunk = 2 * u + p;
+                                sts32(dst + (chunk >> 3) * (D * 128) + d * 128 + (((chunk & 7) ^ (d & 7)) << 4) + 4 * c, half_mul2(h4[k], s[p]));
+                            }
+                        }
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(buf_full + 8 * buf);
+                    mbar_arrive(raw_empty + 8 * (j % H::RS));
+                }
+                ++n;
+            }
+        }
+    } else if (warp == 4 * NQ + 4) {
+        /* ---------------------------------------------------------------- matrix instructions */
+        if (T > 0) {
+            /* kind::f16, FP32 accumulators, FP16 operands, both K-major: N / 8 at bit 17, M / 16 at bit 24 */
+            const uint32_t id_s = (1u << 4) | ((uint32_t)(TN / 8) << 17) | (8u << 24), id_o = (1u << 4) | ((uint32_t)(D / 8) << 17) | (8u << 24);
+            auto scores = [&](int t, int kb) {
+                const uint32_t qa = q_at + t * QT * H::QBYTES, ka = buf_at + kb * H::BUF;
+#pragma unroll
+                for (int x = 0; x < QT; ++x)
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        tc_mma_ss(tmem + t * TN, sw128_desc(qa + x * H::QBYTES + (k >> 2) * (128 * 128)) + 2 * (k & 3),
+                                  sw128_desc(ka + (k >> 2) * (TN * 128)) + 2 * (k & 3), id_s, x > 0 || k > 0);
+            };
+            auto values = [&](int t, int vb, bool acc) {
+                const uint32_t va = buf_at + vb * H::BUF;
+#pragma unroll
+                for (int k = 0; k < TN / 16; ++k)
+                    tc_mma_ts(tmem + H::O_COL + t * D, tmem + t * TN + 8 * k, sw128_desc(va + (k >> 2) * (D * 128)) + 2 * (k & 3), id_o,
+                              acc || k > 0);
+            };
+            wait(q_full, 0);
+            wait(buf_full, 0);
+            tc_fence_after();
+            for (int t = 0; t < NQ; ++t) {
+                scores(t, 0);
+                tc_commit(s_full + 8 * t);
+            }
+            tc_commit(buf_empty);
+            for (int j = 0; j < T; ++j) {
+                const int vn = 2 * j + 1, kn = 2 * j + 2, vb = vn % NBUF, kb = kn % NBUF;
+                wait(buf_full + 8 * vb, (vn / NBUF) & 1);
+                for (int t = 0; t < NQ; ++t) {
+                    wait(p_full + 8 * t, j & 1);
+                    tc_fence_after();
+                    values(t, vb, j > 0);
+                    tc_commit(o_done + 8 * t);
+                    if (t == NQ - 1) tc_commit(buf_empty + 8 * vb);
+                    if (j + 1 < T) {
+                        if (t == 0) {
+                            wait(buf_full + 8 * kb, (kn / NBUF) & 1);
+                            tc_fence_after();
+                        }
+                        scores(t, kb);
+                        tc_commit(s_full + 8 * t);
+                        if (t == NQ - 1) tc_commit(buf_empty + 8 * kb);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        /* ---------------------------------------------------------------- copies */
+        for (int j = 0; j < T; ++j) {
+            const int s = j % H::RS, ut = J.u0 + j * UT, have = min(UT, J.u1 - ut);
+            int page = 0, unit = 0;
+            if (lane < have) {
+                unit = unit_of(ut + lane);
+                page = a.S.table[(int64_t)J.b * a.S.table_stride + (unit >> (a.P.page_shift - 4))];
+                if (page < 0 || page >= a.P.n_pages) {
+                    page = 0;
+                    flag_corrupt(a.status);
+                }
+            }
+            wait(raw_empty + 8 * s, ((j / H::RS) & 1) ^ 1u);
+            if (lane == 0) mbar_arrive_tx(raw_full + 8 * s, have * UB);
+            __syncwarp();
+            if (lane < have)
+                bulk_g2s(raw_at + s * H::RAW + lane * UB, page_ptr(a.P, page, J.h, unit & ((1 << (a.P.page_shift - 4)) - 1)), UB,
+                         raw_full + 8 * s);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 4 * NQ + 4) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(H::COLS) : "memory");
+    }
+}
+
+/* Join the splits of a row tile: one warp per row. */
+template <int NB, int NQ>
+__global__ void __launch_bounds__(256) kv_prefill_join_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int D = 32 * NB, PS = 128 * (D + 2);
+    grid_dep_launch();
+    grid_dep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t item = (int64_t)blockIdx.x * 8 + warp; /* row r of tile: (((rt, b), h), row) */
+    int64_t i = item / (128 * NQ);
+    const int lr = (int)(item % (128 * NQ));
+    const int64_t tile = i;
+    const int h = (int)(i % a.P.n_heads);
+    i /= a.P.n_heads;
+    const int b = (int)(i % a.S.n_seqs);
+    const int64_t rt = a.row_tiles - 1 - i / a.S.n_seqs;
+    if (rt < 0) return;
+    const Seq q = seq_of(a.S, a.P.page_shift, b);
+    const int64_t r = rt * (128 * NQ) + lr;
+    if (r >= (int64_t)min(q.m, a.max_new) * a.group) return;
+    const float* p0 = a.part + (tile * a.splits * NQ + lr / 128) * PS;
+    float M = -FLT_MAX;
+    for (int s = 0; s < a.splits; ++s) M = fmaxf(M, p0[(int64_t)s * NQ * PS + 128 * D + lr % 128]);
+    float L = 0.f, v[NB];
+#pragma unroll
+    for (int k = 0; k < NB; ++k) v[k] = 0.f;
+    for (int s = 0; s < a.splits; ++s) {
+        const float* p = p0 + (int64_t)s * NQ * PS;
+        const float w = ex2(p[128 * D + lr % 128] - M);
+        L = fmaf(p[128 * D + 128 + lr % 128], w, L);
+#pragma unroll
+        for (int k = 0; k < NB; ++k) v[k] = fmaf(p[(int64_t)(lr % 128) * D + 32 * k + lane], w, v[k]);
+    }
+    const int64_t row = q.row0 + r / a.group;
+    const int head = h * a.group + (int)(r % a.group);
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) store_elem(a.out, row * a.out.row + (int64_t)head * a.out.head + 32 * k + lane, v[k] * inv);
+    if (lane == 0 && a.lse) a.lse[row * a.n_q_heads + head] = L == 0.f ? -INFINITY : (M - kPBias + log2f(L)) * 0.6931471805599453f;
+}
+
+/* ------------------------------------------------------------ launch */
+template <int NB, int NQ, int QT>
+static int run_prefill(AttnArgs a, const PrefillPlan& p, cudaStream_t stream) {
+    using H = PShape<NB, NQ, QT>;
+    static SmemOnce once;
+    int rc = once.set(kv_prefill_kernel<NB, NQ, QT>, H::SMEM);
+    if (rc != EC_OK) return rc;
+    a.splits = p.splits;
+    a.row_tiles = p.row_tiles;
+    rc = launch(kv_prefill_kernel<NB, NQ, QT>, dim3((unsigned)p.grid), H::WARPS * 32, H::SMEM, stream, a);
+    if (rc == EC_OK && p.splits > 1)
+        rc = launch(kv_prefill_join_kernel<NB, NQ>, dim3((unsigned)(p.grid / p.splits * 16 * NQ)), 256, 0, stream, a);
+    return rc;
+}
+
+/* Two row tiles per CTA where shared and tensor memory hold them: FP16 and BF16 queries of up to 128 channels. */
+static int row_tiles_per_cta(int nb, int dtype) { return nb <= 4 && dtype != EC_DTYPE_FP32 ? 2 : 1; }
+
+bool plan_prefill(const ec_kv* C, int sms, int n_seqs, int max_new, int64_t max_units, int group, int dtype, PrefillPlan* p) {
+    const int nb = C->p.head_dim / 32, nq = row_tiles_per_cta(nb, dtype), ut = nb <= 4 ? 8 : 4;
+    const int64_t rows = (int64_t)group * max_new, rt = (rows + 128 * nq - 1) / (128 * nq), tiles = rt * n_seqs * C->p.n_kv_heads;
+    const int64_t steps = (max_units + ut - 1) / ut;
+    int64_t s = 1;
+    /* fewer row tiles than SMs: split the tokens, no finer than 4 tiles each */
+    if (tiles < sms) s = sms / tiles;
+    if (s > (steps + 3) / 4) s = (steps + 3) / 4;
+    if (s < 1) s = 1;
+    if (tiles * s > 0x7FFFFFF || rt > 0x7FFFFFFF || tiles * 16 * nq > 0x7FFFFFFF) return false;
+    p->row_tiles = (int)rt;
+    p->splits = (int)s;
+    p->grid = tiles * s;
+    p->work = s > 1 ? (size_t)(tiles * s) * nq * 128 * (C->p.head_dim + 2) * sizeof(float) : 0;
+    return true;
+}
+
+int launch_prefill(const AttnArgs& a, const PrefillPlan& p, cudaStream_t stream) {
+    const bool two = a.q.dtype == EC_DTYPE_FP32;
+    switch (a.P.dim / 32) {
+        case 2: return two ? run_prefill<2, 1, 2>(a, p, stream) : run_prefill<2, 2, 1>(a, p, stream);
+        case 4: return two ? run_prefill<4, 1, 2>(a, p, stream) : run_prefill<4, 2, 1>(a, p, stream);
+        case 6: return two ? run_prefill<6, 1, 2>(a, p, stream) : run_prefill<6, 1, 1>(a, p, stream);
+        default: return two ? run_prefill<8, 1, 2>(a, p, stream) : run_prefill<8, 1, 1>(a, p, stream);
+    }
+}
+
+}  // namespace kv
