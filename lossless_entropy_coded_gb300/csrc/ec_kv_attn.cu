@@ -122,15 +122,16 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+__device__ __forceinline__ uint32_t both_halves(int v) { return ((uint32_t)v & 0xFFFFu) * 0x10001u; }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *(const uint32_t*)&h;
 }
 
 /* Bits of the probabilities: p is held as 2^kBias p in FP16, the running reference of a
- * row moves only when a score passes it by more than kSlack (powers of two), and value
+ * row moves only when weights pass 2^(kBias + 2), and value
  * scales lie up to 2^7 above their block's reference: 2^(6 + 2 + 7) < 65504. */
-constexpr float kBias = 6.f, kSlack = 2.f;
+constexpr float kBias = 6.f;
 
 /* Warps per CTA, CTAs per SM and stages of a warp's ring by the tile's registers; `keep`
  * floats hold a warp's partial result of a tile: [rows][LD], maxima, sums. */
@@ -139,7 +140,7 @@ struct Shape {
     static constexpr int D = 32 * NB, RB = 8 * NT, LD = D + 4, UB = 17 * D;
     static constexpr int W = NB <= 4 && NT == 1 ? 8 : 4;
     static constexpr int CTAS = NT == 2 ? 3 : 2;
-    static constexpr int S = NB == 2 ? 6 : NB == 8 ? 3 : 4;
+    static constexpr int S = NB == 2 ? 8 : 4; /* a power of two */
     static constexpr int KEEP = RB * LD + 2 * RB;
     static constexpr int WARP_BYTES = S * UB + KEEP * 4;
     static_assert(KEEP * 4 <= S * UB, "a second partial result fits the ring");
@@ -147,22 +148,6 @@ struct Shape {
         return (size_t)W * WARP_BYTES + W * S * 8 + 2 * W * 8 + 2 * W * 4 + 16 * (size_t)n_seqs + 8 * ((size_t)n_seqs + 1) + 16;
     }
 };
-
-template <int NB>
-__device__ __forceinline__ void key_scales(uint32_t row, uint32_t (&w)[(NB + 3) / 4]) {
-    if constexpr (NB % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < NB / 4; ++i) w[i] = lds32(row + 4 * i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < NB / 2; ++i) {
-            unsigned short v;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(row + 2 * i) : "memory");
-            if (i % 2 == 0) w[i / 2] = v;
-            else w[i / 2] |= (uint32_t)v << 16;
-        }
-    }
-}
 
 /* Four channels of a tile's row r from its unnormalised sums v, L relative to M. */
 __device__ __forceinline__ void write_row(const AttnArgs& a, int row0, int h, int r, int d, const float4& v, float M, float L) {
@@ -215,49 +200,50 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
     const int64_t x_end = min(x1, x + share / W);
     const int unit_mask = (1 << (a.P.page_shift - 4)) - 1;
 
-    /* the ring's filling side: a cursor of its own over the warp's segments */
+    /* the ring's filling side: a cursor of its own over the warp's segments.  Lane l holds
+     * the address of unit pu_base + l and issues that unit's copy itself. */
     int64_t px = x;
-    int pu = 0, pu_end = 0, pu_base = 0, p_sink = 0, p_lo = 0, p_h = 0, p_stage = 0, page_of = 0;
+    int pu = 0, pu_end = 0, pu_base = 0, p_sink = 0, p_lo = 0, p_h = 0;
+    uint32_t p_count = 0;
     const int32_t* p_table = nullptr;
+    const uint8_t* p_src = nullptr;
     auto fill = [&]() {
-        while (pu >= pu_end) {
-            if (px >= x_end) return;
-            const Seg s = seg_at(a, pre, info, RB, px, x_end);
-            const int4 f = info[s.b];
-            const Span sp = span_of(a, f.x, f.y);
-            px = s.next;
-            pu = s.u0;
-            pu_end = f.x > 0 ? s.u1 : 0;
-            pu_base = pu - 32;
-            p_sink = sp.sink_u, p_lo = sp.lo_u - sp.sink_u, p_h = s.h;
-            p_table = a.S.table + (int64_t)s.b * a.S.table_stride;
-        }
-        if (pu - pu_base >= 32) { /* lane l: the page of unit pu_base + l */
+        if (pu >= pu_end || pu - pu_base >= 32) {
+            while (pu >= pu_end) {
+                if (px >= x_end) return;
+                const Seg s = seg_at(a, pre, info, RB, px, x_end);
+                const int4 f = info[s.b];
+                const Span sp = span_of(a, f.x, f.y);
+                px = s.next;
+                pu = s.u0;
+                pu_end = f.x > 0 ? s.u1 : 0;
+                p_sink = sp.sink_u, p_lo = sp.lo_u - sp.sink_u, p_h = s.h;
+                p_table = a.S.table + (int64_t)s.b * a.S.table_stride;
+            }
             pu_base = pu;
-            const int u = pu + lane;
-            page_of = 0;
+            int u = pu + lane;
             if (u < pu_end) {
-                page_of = p_table[(u < p_sink ? u : u + p_lo) >> (a.P.page_shift - 4)];
-                if (page_of < 0 || page_of >= a.P.n_pages) {
-                    page_of = 0;
+                u = u < p_sink ? u : u + p_lo;
+                int page = p_table[u >> (a.P.page_shift - 4)];
+                if (page < 0 || page >= a.P.n_pages) {
+                    page = 0;
                     flag_corrupt(a.status);
                 }
+                p_src = page_ptr(a.P, page, p_h, u & unit_mask);
             }
         }
-        const int page = __shfl_sync(kAll, page_of, pu - pu_base);
-        if (lane == 0) {
-            const int u = pu < p_sink ? pu : pu + p_lo;
-            mbar_arrive_tx(bars + 8 * p_stage, UB);
-            bulk_g2s(ring + p_stage * UB, page_ptr(a.P, page, p_h, u & unit_mask), UB, bars + 8 * p_stage);
+        if (lane == pu - pu_base) {
+            const uint32_t st = p_count & (S - 1);
+            mbar_arrive_tx(bars + 8 * st, UB);
+            bulk_g2s(ring + st * UB, p_src, UB, bars + 8 * st);
         }
         ++pu;
-        p_stage = p_stage + 1 == S ? 0 : p_stage + 1;
+        ++p_count;
     };
 #pragma unroll 1
     for (int k = 0; k < S; ++k) fill();
 
-    int st = 0;
-    uint32_t phase = 0; /* one bit per stage */
+    uint32_t count = 0; /* units taken from the ring */
     bool live = true;
     while (x < x_end) {
         const Seg sg = seg_at(a, pre, info, RB, x, x_end);
@@ -317,7 +303,7 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
             const int E = (int)(top >> 23);
             const int up = E == 255 ? 127 : min(253, 268 - E);
             const float s = __uint_as_float((uint32_t)up << 23);
-            const float inv = __uint_as_float((uint32_t)(254 - up) << 23) * a.scale * kLog2e;
+            const float inv = fmaxf(__uint_as_float((uint32_t)(254 - up) << 23) * a.scale * kLog2e, FLT_MIN); /* > 0: a masked -inf stays one */
 #pragma unroll
             for (int k = 0; k < NB; ++k)
 #pragma unroll
@@ -336,10 +322,16 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
             }
         }
         const int pos_lo = first + min(r0, R - 1) / a.group, pos_hi = first + min(r0 + RB - 1, R - 1) / a.group;
+        /* units all_lo .. all_hi - 1 are seen whole by every row (with a window: those of its
+         * middle; the sinks' units take the masked way) */
+        const int skip = sp.lo_u - sp.sink_u;
+        const int all_hi = (pos_lo + 1 < 0 ? 0 : (pos_lo + 1) / kUnit) - skip;
+        const int all_lo = a.window ? max(sp.sink_u, (max(0, pos_hi - a.window + 1) + kUnit - 1) / kUnit - skip) : 0;
 
         float o[NT][2 * NB][4];
         float m[NT][2], l[NT][2];
         int ref[NB];
+        uint32_t add[NB]; /* 24 - ref in both halves */
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -350,28 +342,19 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
             l[t][0] = l[t][1] = 0.f;
         }
 #pragma unroll
-        for (int k = 0; k < NB; ++k) ref[k] = -8; /* any scale passes it: the first unit sets it */
+        for (int k = 0; k < NB; ++k) ref[k] = -8, add[k] = both_halves(32); /* any scale passes it: the first unit sets it */
 
 #pragma unroll 1
         for (int u = sg.u0; u < u1; ++u) {
-            const uint32_t buf = ring + st * UB;
-            if (live && !mbar_wait(bars + 8 * st, (phase >> st) & 1u)) {
+            const uint32_t st = count & (S - 1), buf = ring + st * UB;
+            if (live && !mbar_wait(bars + 8 * st, (count / S) & 1u)) {
                 live = false;
                 if (lane == 0) flag_corrupt(a.status);
             }
-            phase ^= 1u << st;
-            st = st + 1 == S ? 0 : st + 1;
-            const int tok = (u < sp.sink_u ? u : u - sp.sink_u + sp.lo_u) * kUnit;
+            ++count;
 
             /* S^T: rows = tokens g, g + 8, columns = query rows 2c, 2c + 1 */
             float s[NT][4];
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[t][j] = 0.f;
-            uint32_t ka[(NB + 3) / 4], kb[(NB + 3) / 4];
-            key_scales<NB>(buf + 16 * D + g * NB, ka);
-            key_scales<NB>(buf + 16 * D + (g + 8) * NB, kb);
 #pragma unroll
             for (int i4 = 0; i4 < NB / 2; ++i4) {
                 const uint4 w = lds128(buf + i4 * 512 + lane * 16);
@@ -382,8 +365,8 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
                     uint32_t ra[4], rb[4];
                     e2m1x8_f16(ww[2 * bb], ra);
                     e2m1x8_f16(ww[2 * bb + 1], rb);
-                    const float sa = __uint_as_float(((ka[blk / 4] >> (8 * (blk % 4))) & 0xFFu) << 23);
-                    const float sb = __uint_as_float(((kb[blk / 4] >> (8 * (blk % 4))) & 0xFFu) << 23);
+                    const float sa = __uint_as_float(lds8(buf + 16 * D + g * NB + blk) << 23);
+                    const float sb = __uint_as_float(lds8(buf + 16 * D + (g + 8) * NB + blk) << 23);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         float d[4] = {0.f, 0.f, 0.f, 0.f};
@@ -392,20 +375,26 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
                             mma16816(d, ra[0], rb[0], ra[1], rb[1], qf[t][q][blk][0], qf[t][q][blk][1]);
                             mma16816(d, ra[2], rb[2], ra[3], rb[3], qf[t][q][blk][2], qf[t][q][blk][3]);
                         }
-                        s[t][0] = fmaf(d[0], sa, s[t][0]);
-                        s[t][1] = fmaf(d[1], sa, s[t][1]);
-                        s[t][2] = fmaf(d[2], sb, s[t][2]);
-                        s[t][3] = fmaf(d[3], sb, s[t][3]);
+                        if (blk == 0) {
+                            s[t][0] = d[0] * sa, s[t][1] = d[1] * sa, s[t][2] = d[2] * sb, s[t][3] = d[3] * sb;
+                        } else {
+                            s[t][0] = fmaf(d[0], sa, s[t][0]);
+                            s[t][1] = fmaf(d[1], sa, s[t][1]);
+                            s[t][2] = fmaf(d[2], sb, s[t][2]);
+                            s[t][3] = fmaf(d[3], sb, s[t][3]);
+                        }
                     }
                 }
             }
-            const bool all = tok + kUnit - 1 <= pos_lo && (!a.window || tok > pos_hi - a.window || tok + kUnit - 1 < a.sinks);
-            uint32_t vmask = 0xFFFFFFFFu; /* bytes: tokens 2c, 2c + 1, 2c + 8, 2c + 9 that some row sees */
+            uint32_t vw[NB];
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[t][j] *= fac[t][j & 1];
-            if (!all) {
+            for (int i = 0; i < NB / 2; ++i) {
+                const uint32_t at = buf + 16 * D + D / 2 + (c * NB + 2 * i) * 4;
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vw[2 * i]), "=r"(vw[2 * i + 1]) : "r"(at) : "memory");
+            }
+            const bool all = u >= all_lo && u < all_hi;
+            if (!all) { /* a place that a row does not see: score -inf; scales of tokens that no row sees: 0 */
+                const int tok = (u < sp.sink_u ? u : u + skip) * kUnit;
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -414,26 +403,37 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
                         const bool see = at <= p && (!a.window || at > p - a.window || at < a.sinks);
                         if (!see) s[t][j] = -INFINITY;
                     }
-                vmask = 0;
+                uint32_t vmask = 0; /* bytes: tokens 2c, 2c + 1, 2c + 8, 2c + 9 */
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int at = tok + 2 * c + (j & 1) + 8 * (j >> 1);
                     if (at <= pos_hi && (!a.window || at > pos_lo - a.window || at < a.sinks)) vmask |= 0xFFu << (8 * j);
                 }
+#pragma unroll
+                for (int k2 = 0; k2 < NB; ++k2) vw[k2] &= vmask;
             }
 
-            /* the rows' references move when a score passes them by more than the slack */
-            bool move = false;
+            /* weights 2^(s - m + kBias); the references move when a lane's four weights add to
+             * more than 2^(kBias + 2) */
+            float p[NT][4], sum[NT][2];
+            auto weights = [&]() {
+                bool over = false;
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+                for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) move |= s[t][j] > m[t][j & 1] + kSlack;
-            if (__any_sync(kAll, move)) {
+                    for (int j = 0; j < 4; ++j) p[t][j] = ex2(fmaf(s[t][j], fac[t][j & 1], kBias - m[t][j & 1]));
+                    sum[t][0] = p[t][0] + p[t][2];
+                    sum[t][1] = p[t][1] + p[t][3];
+                    over |= sum[t][0] + sum[t][1] > 256.f;
+                }
+                return over;
+            };
+            if (__any_sync(kAll, weights())) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float mx = fmaxf(s[t][j], s[t][j + 2]);
+                        float mx = fmaxf(s[t][j], s[t][j + 2]) * fac[t][j];
 #pragma unroll
                         for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, w));
                         const float nm = fmaxf(m[t][j], mx), al = ex2(m[t][j] - nm);
@@ -445,36 +445,25 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
                             o[t][i][j + 2] *= al;
                         }
                     }
+                weights();
             }
-            /* weights, and their transposition into the second product's operand */
+            /* their transposition into the second product's operand */
             uint32_t p0[NT], p1[NT];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                float p[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    p[j] = ex2(s[t][j] - (m[t][j & 1] - kBias));
-                    l[t][j & 1] += p[j];
-                }
-                p0[t] = transpose8x8(pack_f16(p[0], p[1]));
-                p1[t] = transpose8x8(pack_f16(p[2], p[3]));
+                l[t][0] += sum[t][0];
+                l[t][1] += sum[t][1];
+                p0[t] = transpose8x8(pack_f16(p[t][0], p[t][1]));
+                p1[t] = transpose8x8(pack_f16(p[t][2], p[t][3]));
             }
 
             /* value scales 2^(e - ref) as FP16 pairs: exponent field z - 9 = e - ref + 15,
              * 0 where that is not positive; z >= 32 means more than 2^7 above the reference */
-            uint32_t vw[NB], z0[NB], z1[NB], over = 0;
-#pragma unroll
-            for (int i = 0; i < NB / 2; ++i) {
-                const uint32_t at = buf + 16 * D + D / 2 + (c * NB + 2 * i) * 4;
-                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vw[2 * i]), "=r"(vw[2 * i + 1]) : "r"(at) : "memory");
-            }
+            uint32_t z0[NB], z1[NB], over = 0;
 #pragma unroll
             for (int k2 = 0; k2 < NB; ++k2) {
-                vw[k2] &= vmask;
-                const uint32_t add = (uint32_t)(24 - ref[k2]) * 0x10001u; /* two halves; |24 - ref| < 2^15 */
-                const uint32_t add2 = ref[k2] > 24 ? add + 0x10000u : add; /* a negative low half borrows from the high one */
-                z0[k2] = __viaddmax_s16x2(__byte_perm(vw[k2], 0, 0x4140), add2, 0x00090009u);
-                z1[k2] = __viaddmax_s16x2(__byte_perm(vw[k2], 0, 0x4342), add2, 0x00090009u);
+                z0[k2] = __viaddmax_s16x2(__byte_perm(vw[k2], 0, 0x4140), add[k2], 0x00090009u);
+                z1[k2] = __viaddmax_s16x2(__byte_perm(vw[k2], 0, 0x4342), add[k2], 0x00090009u);
                 over |= z0[k2] | z1[k2];
             }
             bool bad = false;
@@ -485,7 +474,7 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int e = (vw[k2] >> (8 * j)) & 0xFF;
-                        if (e != 255 && ((vmask >> (8 * j)) & 1u)) mx = max(mx, e);
+                        if (e != 255) mx = max(mx, e);
                         bad |= e == 255;
                     }
                     mx = __reduce_max_sync(kAll, mx);
@@ -501,6 +490,7 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
                             }
                     }
                     const int r = 24 - ref[k2];
+                    add[k2] = both_halves(r);
                     z0[k2] = z1[k2] = 0;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -534,7 +524,7 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 if (((vw[blk] >> (8 * j)) & 0xFFu) != 255u) continue;
-                                const int at = tok + 2 * c + (j & 1) + 8 * (j >> 1);
+                                const int at = (u < sp.sink_u ? u : u + skip) * kUnit + 2 * c + (j & 1) + 8 * (j >> 1);
                                 const int p = first + min(r0 + 8 * t + g, R - 1) / a.group;
                                 if (at > p || (a.window && at <= p - a.window && at >= a.sinks)) continue;
                                 (j < 2 ? b0[t] : b1[t]) |= 0x7FFFu << (16 * (j & 1));
