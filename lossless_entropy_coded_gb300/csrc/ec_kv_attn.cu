@@ -129,9 +129,9 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 /* Bits of the probabilities: p is held as 2^kBias p in FP16, the running reference of a
- * row moves only when weights pass 2^(kBias + 2), and value
- * scales lie up to 2^7 above their block's reference: 2^(6 + 2 + 7) < 65504. */
-constexpr float kBias = 6.f;
+ * row moves only when weights pass 2^(kBias + 3), and value
+ * scales lie up to 2^7 above their block's reference: 2^(5 + 3 + 7) < 65504. */
+constexpr float kBias = 5.f;
 
 /* Warps per CTA, CTAs per SM and stages of a warp's ring by the tile's registers; `keep`
  * floats hold a warp's partial result of a tile: [rows][LD], maxima, sums. */
@@ -140,10 +140,10 @@ struct Shape {
     static constexpr int D = 32 * NB, RB = 8 * NT, LD = D + 4, UB = 17 * D;
     static constexpr int W = NB <= 4 && NT == 1 ? 8 : 4;
     static constexpr int CTAS = NT == 2 ? 3 : 2;
-    static constexpr int S = NB == 2 ? 8 : 4; /* a power of two */
+    static constexpr int S = NB == 2 ? 4 : 2; /* of two units each; a power of two */
     static constexpr int KEEP = RB * LD + 2 * RB;
-    static constexpr int WARP_BYTES = S * UB + KEEP * 4;
-    static_assert(KEEP * 4 <= S * UB, "a second partial result fits the ring");
+    static constexpr int RING = S * 2 * UB, WARP_BYTES = RING + KEEP * 4;
+    static_assert(KEEP * 4 <= RING, "a second partial result fits the ring");
     static constexpr size_t smem(int n_seqs) {
         return (size_t)W * WARP_BYTES + W * S * 8 + 2 * W * 8 + 2 * W * 4 + 16 * (size_t)n_seqs + 8 * ((size_t)n_seqs + 1) + 16;
     }
@@ -200,66 +200,82 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
     const int64_t x_end = min(x1, x + share / W);
     const int unit_mask = (1 << (a.P.page_shift - 4)) - 1;
 
-    /* the ring's filling side: a cursor of its own over the warp's segments.  Lane l holds
-     * the address of unit pu_base + l and issues that unit's copy itself. */
+    /* the ring's filling side: a cursor of its own over the warp's segments.  The lanes hold the
+     * next units' addresses, up to 32 at a time, and issue the copies, two units to a stage. */
     int64_t px = x;
-    int pu = 0, pu_end = 0, pu_base = 0, p_sink = 0, p_lo = 0, p_h = 0;
+    int pk = 0, pn = 0;
     uint32_t p_count = 0;
-    const int32_t* p_table = nullptr;
     const uint8_t* p_src = nullptr;
     auto fill = [&]() {
-        if (pu >= pu_end || pu - pu_base >= 32) {
-            while (pu >= pu_end) {
+        if (pk >= pn) {
+            pk = pn = 0;
+            while (pn == 0) {
                 if (px >= x_end) return;
                 const Seg s = seg_at(a, pre, info, RB, px, x_end);
                 const int4 f = info[s.b];
                 const Span sp = span_of(a, f.x, f.y);
-                px = s.next;
-                pu = s.u0;
-                pu_end = f.x > 0 ? s.u1 : 0;
-                p_sink = sp.sink_u, p_lo = sp.lo_u - sp.sink_u, p_h = s.h;
-                p_table = a.S.table + (int64_t)s.b * a.S.table_stride;
-            }
-            pu_base = pu;
-            int u = pu + lane;
-            if (u < pu_end) {
-                u = u < p_sink ? u : u + p_lo;
-                int page = p_table[u >> (a.P.page_shift - 4)];
-                if (page < 0 || page >= a.P.n_pages) {
-                    page = 0;
-                    flag_corrupt(a.status);
+                pn = f.x > 0 ? min(32, max(0, s.u1 - s.u0)) : 0;
+                px = pn == 32 ? s.tile + s.u0 + 32 : s.next;
+                if (lane < pn) {
+                    int u = s.u0 + lane;
+                    u = u < sp.sink_u ? u : u - sp.sink_u + sp.lo_u;
+                    int page = a.S.table[(int64_t)s.b * a.S.table_stride + (u >> (a.P.page_shift - 4))];
+                    if (page < 0 || page >= a.P.n_pages) {
+                        page = 0;
+                        flag_corrupt(a.status);
+                    }
+                    p_src = page_ptr(a.P, page, s.h, u & unit_mask);
                 }
-                p_src = page_ptr(a.P, page, p_h, u & unit_mask);
             }
         }
-        if (lane == pu - pu_base) {
+        /* two units, or a segment's last one (a reload starts a pair) */
+        const int n = min(2, pn - pk), k = lane - pk;
+        if (k >= 0 && k < n) {
             const uint32_t st = p_count & (S - 1);
-            mbar_arrive_tx(bars + 8 * st, UB);
-            bulk_g2s(ring + st * UB, p_src, UB, bars + 8 * st);
+            if (k == 0) mbar_arrive_tx(bars + 8 * st, n * UB);
+            bulk_g2s(ring + (2 * st + k) * UB, p_src, UB, bars + 8 * st);
         }
-        ++pu;
+        pk += 2;
         ++p_count;
     };
 #pragma unroll 1
     for (int k = 0; k < S; ++k) fill();
 
-    uint32_t count = 0; /* units taken from the ring */
+    uint32_t count = 0; /* stages taken from the ring */
     bool live = true;
     while (x < x_end) {
-        const Seg sg = seg_at(a, pre, info, RB, x, x_end);
-        x = sg.next;
-        if (sg.u0 >= sg.u1) continue;
-        const int4 f = info[sg.b];
-        const Span sp = span_of(a, f.x, f.y);
-        const int h = sg.h, r0 = sg.r0, len = f.x, R = f.y * a.group, first = len - f.y, u1 = len > 0 ? sg.u1 : 0;
+        /* (a segment's place in the work is looked up again where it is needed after the loop
+         * and at its masked ends, so that the loop need not keep it in registers) */
+        auto look_up = [&](Seg& sg, int4& f) {
+            asm volatile("" : "+l"(x));
+            sg = seg_at(a, pre, info, RB, x, x_end);
+            f = info[sg.b];
+        };
+        int u = 0, u1 = 0, all_lo = 0, all_hi = 0;
+        uint32_t qf[NT][QT][NB][4];
+        float fac[NT][2];
+        {
+            Seg sg;
+            int4 f;
+            look_up(sg, f);
+            if (sg.u0 >= sg.u1) {
+                x = sg.next;
+                continue;
+            }
+            const Span sp = span_of(a, f.x, f.y);
+            const int h = sg.h, r0 = sg.r0, R = f.y * a.group, first = f.x - f.y;
+            u = sg.u0;
+            u1 = f.x > 0 ? sg.u1 : 0;
+            /* units all_lo .. all_hi - 1 are seen whole by every row (with a window: those of
+             * its middle; the sinks' units take the masked way) */
+            const int pos_lo = first + min(r0, R - 1) / a.group, pos_hi = first + min(r0 + RB - 1, R - 1) / a.group, skip = sp.lo_u - sp.sink_u;
+            all_hi = min(u1, (pos_lo + 1 < 0 ? 0 : (pos_lo + 1) / kUnit) - skip);
+            all_lo = a.window ? max(sp.sink_u, (max(0, pos_hi - a.window + 1) + kUnit - 1) / kUnit - skip) : 0;
 
         /* queries: lane 4 g + c holds row g's channels 32 b + 8 c + 0..7, scaled by a power
          * of two so that the row's largest lies in [2^14, 2^15): BF16 and FP16 rows are
          * exact in one FP16 part but for elements 2^-28 of the row's largest, FP32 rows
          * take two parts (22 bits) */
-        uint32_t qf[NT][QT][NB][4];
-        float fac[NT][2];
-        int pos[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int r = r0 + 8 * t + g;
@@ -316,22 +332,13 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
                     }
                 }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                fac[t][j] = __shfl_sync(kAll, inv, 8 * c + 4 * j);
-                pos[t][j] = first + min(r0 + 8 * t + 2 * c + j, R - 1) / a.group;
-            }
+            for (int j = 0; j < 2; ++j) fac[t][j] = __shfl_sync(kAll, inv, 8 * c + 4 * j);
         }
-        const int pos_lo = first + min(r0, R - 1) / a.group, pos_hi = first + min(r0 + RB - 1, R - 1) / a.group;
-        /* units all_lo .. all_hi - 1 are seen whole by every row (with a window: those of its
-         * middle; the sinks' units take the masked way) */
-        const int skip = sp.lo_u - sp.sink_u;
-        const int all_hi = (pos_lo + 1 < 0 ? 0 : (pos_lo + 1) / kUnit) - skip;
-        const int all_lo = a.window ? max(sp.sink_u, (max(0, pos_hi - a.window + 1) + kUnit - 1) / kUnit - skip) : 0;
+        }
 
         float o[NT][2 * NB][4];
         float m[NT][2], l[NT][2];
-        int ref[NB];
-        uint32_t add[NB]; /* 24 - ref in both halves */
+        uint32_t add[NB]; /* 24 - the block's reference in both halves; 32: none yet, any scale passes it */
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -342,88 +349,94 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
             l[t][0] = l[t][1] = 0.f;
         }
 #pragma unroll
-        for (int k = 0; k < NB; ++k) ref[k] = -8, add[k] = both_halves(32); /* any scale passes it: the first unit sets it */
+        for (int k = 0; k < NB; ++k) add[k] = both_halves(32);
 
 #pragma unroll 1
-        for (int u = sg.u0; u < u1; ++u) {
-            const uint32_t st = count & (S - 1), buf = ring + st * UB;
+        for (; u < u1; u += 2) {
+            const uint32_t st = count & (S - 1), buf = ring + st * (2 * UB);
             if (live && !mbar_wait(bars + 8 * st, (count / S) & 1u)) {
                 live = false;
                 if (lane == 0) flag_corrupt(a.status);
             }
             ++count;
 
-            /* S^T: rows = tokens g, g + 8, columns = query rows 2c, 2c + 1 */
-            float s[NT][4];
+            /* S^T: rows = tokens g, g + 8 of unit v, columns = query rows 2c, 2c + 1 */
+            float s[2][NT][4];
 #pragma unroll
-            for (int i4 = 0; i4 < NB / 2; ++i4) {
-                const uint4 w = lds128(buf + i4 * 512 + lane * 16);
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            for (int v = 0; v < 2; ++v) {
 #pragma unroll
-                for (int bb = 0; bb < 2; ++bb) {
-                    const int blk = 2 * i4 + bb;
-                    uint32_t ra[4], rb[4];
-                    e2m1x8_f16(ww[2 * bb], ra);
-                    e2m1x8_f16(ww[2 * bb + 1], rb);
-                    const float sa = __uint_as_float(lds8(buf + 16 * D + g * NB + blk) << 23);
-                    const float sb = __uint_as_float(lds8(buf + 16 * D + (g + 8) * NB + blk) << 23);
+                for (int i4 = 0; i4 < NB / 2; ++i4) {
+                    const uint4 w = lds128(buf + v * UB + i4 * 512 + lane * 16);
+                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        float d[4] = {0.f, 0.f, 0.f, 0.f};
+                    for (int bb = 0; bb < 2; ++bb) {
+                        const int blk = 2 * i4 + bb;
+                        uint32_t ra[4], rb[4];
+                        e2m1x8_f16(ww[2 * bb], ra);
+                        e2m1x8_f16(ww[2 * bb + 1], rb);
+                        const float sa = __uint_as_float(lds8(buf + v * UB + 16 * D + g * NB + blk) << 23);
+                        const float sb = __uint_as_float(lds8(buf + v * UB + 16 * D + (g + 8) * NB + blk) << 23);
 #pragma unroll
-                        for (int q = 0; q < QT; ++q) {
-                            mma16816(d, ra[0], rb[0], ra[1], rb[1], qf[t][q][blk][0], qf[t][q][blk][1]);
-                            mma16816(d, ra[2], rb[2], ra[3], rb[3], qf[t][q][blk][2], qf[t][q][blk][3]);
-                        }
-                        if (blk == 0) {
-                            s[t][0] = d[0] * sa, s[t][1] = d[1] * sa, s[t][2] = d[2] * sb, s[t][3] = d[3] * sb;
-                        } else {
-                            s[t][0] = fmaf(d[0], sa, s[t][0]);
-                            s[t][1] = fmaf(d[1], sa, s[t][1]);
-                            s[t][2] = fmaf(d[2], sb, s[t][2]);
-                            s[t][3] = fmaf(d[3], sb, s[t][3]);
+                        for (int t = 0; t < NT; ++t) {
+                            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                            for (int q = 0; q < QT; ++q) {
+                                mma16816(d, ra[0], rb[0], ra[1], rb[1], qf[t][q][blk][0], qf[t][q][blk][1]);
+                                mma16816(d, ra[2], rb[2], ra[3], rb[3], qf[t][q][blk][2], qf[t][q][blk][3]);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) s[v][t][j] = blk == 0 ? d[j] * (j < 2 ? sa : sb) : fmaf(d[j], j < 2 ? sa : sb, s[v][t][j]);
                         }
                     }
                 }
             }
-            uint32_t vw[NB];
+            const bool masked = u < all_lo || u + 1 >= all_hi;
+            uint32_t vmask[2] = {0u, 0u}; /* masked: bytes of tokens 2c, 2c + 1, 2c + 8, 2c + 9 that some row sees */
+            if (masked) { /* a place that a row does not see: score -inf */
+                Seg sg;
+                int4 f;
+                look_up(sg, f);
+                const Span sp = span_of(a, f.x, f.y);
+                const int R = f.y * a.group, first = f.x - f.y, skip = sp.lo_u - sp.sink_u;
+                const int pos_lo = first + min(sg.r0, R - 1) / a.group, pos_hi = first + min(sg.r0 + RB - 1, R - 1) / a.group;
+                int tok[2];
 #pragma unroll
-            for (int i = 0; i < NB / 2; ++i) {
-                const uint32_t at = buf + 16 * D + D / 2 + (c * NB + 2 * i) * 4;
-                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vw[2 * i]), "=r"(vw[2 * i + 1]) : "r"(at) : "memory");
-            }
-            const bool all = u >= all_lo && u < all_hi;
-            if (!all) { /* a place that a row does not see: score -inf; scales of tokens that no row sees: 0 */
-                const int tok = (u < sp.sink_u ? u : u + skip) * kUnit;
+                for (int v = 0; v < 2; ++v) tok[v] = u + v < u1 ? (u + v < sp.sink_u ? u + v : u + v + skip) * kUnit : 0x7FFFFF00;
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int at = tok + g + 8 * (j >> 1), p = pos[t][j & 1];
-                        const bool see = at <= p && (!a.window || at > p - a.window || at < a.sinks);
-                        if (!see) s[t][j] = -INFINITY;
+                    for (int j = 0; j < 2; ++j) {
+                        const int p = first + min(sg.r0 + 8 * t + 2 * c + j, R - 1) / a.group;
+#pragma unroll
+                        for (int v = 0; v < 2; ++v)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int at = tok[v] + g + 8 * k;
+                                if (at > p || (a.window && at <= p - a.window && at >= a.sinks)) s[v][t][j + 2 * k] = -INFINITY;
+                            }
                     }
-                uint32_t vmask = 0; /* bytes: tokens 2c, 2c + 1, 2c + 8, 2c + 9 */
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int at = tok + 2 * c + (j & 1) + 8 * (j >> 1);
-                    if (at <= pos_hi && (!a.window || at > pos_lo - a.window || at < a.sinks)) vmask |= 0xFFu << (8 * j);
-                }
+                for (int v = 0; v < 2; ++v)
 #pragma unroll
-                for (int k2 = 0; k2 < NB; ++k2) vw[k2] &= vmask;
+                    for (int j = 0; j < 4; ++j) {
+                        const int at = tok[v] + 2 * c + (j & 1) + 8 * (j >> 1);
+                        if (at <= pos_hi && (!a.window || at > pos_lo - a.window || at < a.sinks)) vmask[v] |= 0xFFu << (8 * j);
+                    }
             }
 
-            /* weights 2^(s - m + kBias); the references move when a lane's four weights add to
-             * more than 2^(kBias + 2) */
-            float p[NT][4], sum[NT][2];
+            /* weights 2^(s - m + kBias); the references move when a lane's eight weights add to
+             * more than 2^(kBias + 3) (fac > 0, so a masked -inf stays one) */
+            float p[2][NT][4], sum[NT][2];
             auto weights = [&]() {
                 bool over = false;
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) p[t][j] = ex2(fmaf(s[t][j], fac[t][j & 1], kBias - m[t][j & 1]));
-                    sum[t][0] = p[t][0] + p[t][2];
-                    sum[t][1] = p[t][1] + p[t][3];
+                    for (int v = 0; v < 2; ++v)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) p[v][t][j] = ex2(fmaf(s[v][t][j], fac[t][j & 1], kBias - m[t][j & 1]));
+                    sum[t][0] = (p[0][t][0] + p[0][t][2]) + (p[1][t][0] + p[1][t][2]);
+                    sum[t][1] = (p[0][t][1] + p[0][t][3]) + (p[1][t][1] + p[1][t][3]);
                     over |= sum[t][0] + sum[t][1] > 256.f;
                 }
                 return over;
@@ -433,7 +446,7 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float mx = fmaxf(s[t][j], s[t][j + 2]) * fac[t][j];
+                        float mx = fmaxf(fmaxf(s[0][t][j], s[0][t][j + 2]), fmaxf(s[1][t][j], s[1][t][j + 2])) * fac[t][j];
 #pragma unroll
                         for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, w));
                         const float nm = fmaxf(m[t][j], mx), al = ex2(m[t][j] - nm);
@@ -448,39 +461,60 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
                 weights();
             }
             /* their transposition into the second product's operand */
-            uint32_t p0[NT], p1[NT];
+            uint32_t p0[2][NT], p1[2][NT];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 l[t][0] += sum[t][0];
                 l[t][1] += sum[t][1];
-                p0[t] = transpose8x8(pack_f16(p[t][0], p[t][1]));
-                p1[t] = transpose8x8(pack_f16(p[t][2], p[t][3]));
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    p0[v][t] = transpose8x8(pack_f16(p[v][t][0], p[v][t][1]));
+                    p1[v][t] = transpose8x8(pack_f16(p[v][t][2], p[v][t][3]));
+                }
             }
 
             /* value scales 2^(e - ref) as FP16 pairs: exponent field z - 9 = e - ref + 15,
              * 0 where that is not positive; z >= 32 means more than 2^7 above the reference */
-            uint32_t z0[NB], z1[NB], over = 0;
+            uint32_t vw[2][NB], z0[2][NB], z1[2][NB], over = 0;
 #pragma unroll
-            for (int k2 = 0; k2 < NB; ++k2) {
-                z0[k2] = __viaddmax_s16x2(__byte_perm(vw[k2], 0, 0x4140), add[k2], 0x00090009u);
-                z1[k2] = __viaddmax_s16x2(__byte_perm(vw[k2], 0, 0x4342), add[k2], 0x00090009u);
-                over |= z0[k2] | z1[k2];
+            for (int v = 0; v < 2; ++v)
+#pragma unroll
+                for (int i = 0; i < NB / 2; ++i) {
+                    const uint32_t at = buf + v * UB + 16 * D + D / 2 + (c * NB + 2 * i) * 4;
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vw[v][2 * i]), "=r"(vw[v][2 * i + 1]) : "r"(at) : "memory");
+                }
+            if (masked) { /* scales of tokens that no row sees: 0 */
+#pragma unroll
+                for (int v = 0; v < 2; ++v)
+#pragma unroll
+                    for (int k2 = 0; k2 < NB; ++k2) vw[v][k2] &= vmask[v];
             }
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+#pragma unroll
+                for (int k2 = 0; k2 < NB; ++k2) {
+                    z0[v][k2] = __viaddmax_s16x2(__byte_perm(vw[v][k2], 0, 0x4140), add[k2], 0x00090009u);
+                    z1[v][k2] = __viaddmax_s16x2(__byte_perm(vw[v][k2], 0, 0x4342), add[k2], 0x00090009u);
+                    over |= z0[v][k2] | z1[v][k2];
+                }
             bool bad = false;
             if (__any_sync(kAll, (over & 0xFFE0FFE0u) != 0)) {
 #pragma unroll
                 for (int k2 = 0; k2 < NB; ++k2) {
                     int mx = -8;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int e = (vw[k2] >> (8 * j)) & 0xFF;
-                        if (e != 255) mx = max(mx, e);
-                        bad |= e == 255;
-                    }
+                    for (int v = 0; v < 2; ++v)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int e = (vw[v][k2] >> (8 * j)) & 0xFF;
+                            if (e != 255) mx = max(mx, e);
+                            bad |= e == 255;
+                        }
                     mx = __reduce_max_sync(kAll, mx);
-                    if (mx > ref[k2]) {
-                        const float f = ref[k2] < 0 ? 0.f : ex2((float)(ref[k2] - mx));
-                        ref[k2] = mx;
+                    const int ref = 24 - (int)(int16_t)(add[k2] & 0xFFFFu);
+                    if (mx > ref) {
+                        const float f = ref < 0 ? 0.f : ex2((float)(ref - mx));
+                        add[k2] = both_halves(24 - mx);
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -489,15 +523,17 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
                                 o[t][2 * k2 + 1][j] *= f;
                             }
                     }
-                    const int r = 24 - ref[k2];
-                    add[k2] = both_halves(r);
-                    z0[k2] = z1[k2] = 0;
+                    const int r = (int)(int16_t)(add[k2] & 0xFFFFu);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int e = (vw[k2] >> (8 * j)) & 0xFF;
-                        const uint32_t z = e == 255 ? 9u : (uint32_t)max(e + r, 9);
-                        if (j < 2) z0[k2] |= z << (16 * j);
-                        else z1[k2] |= z << (16 * (j - 2));
+                    for (int v = 0; v < 2; ++v) {
+                        z0[v][k2] = z1[v][k2] = 0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int e = (vw[v][k2] >> (8 * j)) & 0xFF;
+                            const uint32_t z = e == 255 ? 9u : (uint32_t)max(e + r, 9);
+                            if (j < 2) z0[v][k2] |= z << (16 * j);
+                            else z1[v][k2] |= z << (16 * (j - 2));
+                        }
                     }
                 }
                 bad = __any_sync(kAll, bad);
@@ -505,40 +541,47 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
 
             /* O^T: rows = channels, columns = query rows */
 #pragma unroll
-            for (int i4 = 0; i4 < NB / 2; ++i4) {
-                const uint4 w = lds128(buf + 8 * D + i4 * 512 + lane * 16);
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            for (int v = 0; v < 2; ++v)
 #pragma unroll
-                for (int bb = 0; bb < 2; ++bb) {
-                    const int blk = 2 * i4 + bb;
-                    uint32_t s0 = z0[blk] * 1024u - 0x24002400u, s1 = z1[blk] * 1024u - 0x24002400u;
-                    uint32_t b0[NT], b1[NT];
+                for (int i4 = 0; i4 < NB / 2; ++i4) {
+                    const uint4 w = lds128(buf + v * UB + 8 * D + i4 * 512 + lane * 16);
+                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        b0[t] = hmul2(p0[t], s0);
-                        b1[t] = hmul2(p1[t], s1);
-                    }
-                    if (bad) { /* a block of NaN makes its channels NaN for every row that sees the token */
+                    for (int bb = 0; bb < 2; ++bb) {
+                        const int blk = 2 * i4 + bb;
+                        const uint32_t s0 = z0[v][blk] * 1024u - 0x24002400u, s1 = z1[v][blk] * 1024u - 0x24002400u;
+                        uint32_t b0[NT], b1[NT];
 #pragma unroll
-                        for (int t = 0; t < NT; ++t)
+                        for (int t = 0; t < NT; ++t) {
+                            b0[t] = hmul2(p0[v][t], s0);
+                            b1[t] = hmul2(p1[v][t], s1);
+                        }
+                        if (bad) { /* a block of NaN makes its channels NaN for every row that sees the token */
+                            Seg sg;
+                            int4 f;
+                            look_up(sg, f);
+                            const Span sp = span_of(a, f.x, f.y);
+                            const int R = f.y * a.group, tok = (u + v < sp.sink_u ? u + v : u + v + sp.lo_u - sp.sink_u) * kUnit;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                if (((vw[blk] >> (8 * j)) & 0xFFu) != 255u) continue;
-                                const int at = (u < sp.sink_u ? u : u + skip) * kUnit + 2 * c + (j & 1) + 8 * (j >> 1);
-                                const int p = first + min(r0 + 8 * t + g, R - 1) / a.group;
-                                if (at > p || (a.window && at <= p - a.window && at >= a.sinks)) continue;
-                                (j < 2 ? b0[t] : b1[t]) |= 0x7FFFu << (16 * (j & 1));
-                            }
-                    }
+                            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t ra[4];
-                        e2m1x8_f16(ww[2 * bb + j], ra);
+                                for (int j = 0; j < 4; ++j) {
+                                    if (((vw[v][blk] >> (8 * j)) & 0xFFu) != 255u) continue;
+                                    const int at = tok + 2 * c + (j & 1) + 8 * (j >> 1);
+                                    const int p = f.x - f.y + min(sg.r0 + 8 * t + g, R - 1) / a.group;
+                                    if (at > p || (a.window && at <= p - a.window && at >= a.sinks)) continue;
+                                    (j < 2 ? b0[t] : b1[t]) |= 0x7FFFu << (16 * (j & 1));
+                                }
+                        }
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) mma16816(o[t][2 * blk + j], ra[0], ra[1], ra[2], ra[3], b0[t], b1[t]);
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t ra[4];
+                            e2m1x8_f16(ww[2 * bb + j], ra);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) mma16816(o[t][2 * blk + j], ra[0], ra[1], ra[2], ra[3], b0[t], b1[t]);
+                        }
                     }
                 }
-            }
             __syncwarp(); /* every lane has read the stage */
             fill();
         }
@@ -551,9 +594,17 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int w = 4; w < 32; w <<= 1) l[t][j] += __shfl_xor_sync(kAll, l[t][j], w);
+        Seg sg;
+        int4 f;
+        look_up(sg, f);
+        x = sg.next;
+        const int h = sg.h, r0 = sg.r0, R = f.y * a.group;
         float back[NB];
 #pragma unroll
-        for (int k = 0; k < NB; ++k) back[k] = ref[k] > 0 ? __uint_as_float((uint32_t)ref[k] << 23) : 0.f;
+        for (int k = 0; k < NB; ++k) {
+            const int ref = 24 - (int)(int16_t)(add[k] & 0xFFFFu);
+            back[k] = ref > 0 ? __uint_as_float((uint32_t)ref << 23) : 0.f;
+        }
         if (sg.u0 == 0 && sg.u1 == sg.units) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
@@ -610,7 +661,7 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
             /* the end of a tile is the warp's first segment, the begin of another its last,
              * when the ring is empty */
             const int slot = sg.u0 == 0 ? 1 : 0;
-            float* mine = (float*)(at_smem + warp * H::WARP_BYTES + (slot ? 0 : S * UB));
+            float* mine = (float*)(at_smem + warp * H::WARP_BYTES + (slot ? 0 : H::RING));
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -658,7 +709,7 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int k = s0; k <= last; ++k) {
                 if (slot_tile[k] != tile) continue;
-                const float* p = (const float*)(at_smem + (k / 2) * H::WARP_BYTES + (k & 1 ? 0 : S * UB));
+                const float* p = (const float*)(at_smem + (k / 2) * H::WARP_BYTES + (k & 1 ? 0 : H::RING));
                 const float pm = p[RB * LD + r], nm = fmaxf(M, pm), fo = ex2(M - nm), fp = ex2(pm - nm);
                 const float4 y = *(const float4*)&p[r * LD + d];
                 M = nm;
