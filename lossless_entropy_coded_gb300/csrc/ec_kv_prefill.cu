@@ -14,8 +14,8 @@
  * back as FP16 in S's place and are the tensor-memory operand of O += P V.  The row's
  * reference m moves, and O with it, only when a score passes it by 2^8.
  *
- * Warps: NQ groups of four for the softmax, four that expand tiles, one that issues the
- * matrix instructions, one that copies units in.  Matrix instructions of the NQ row
+ * Warps: NQ groups of four for the softmax, eight that expand tiles, one that issues the
+ * matrix instructions, one that copies units in and finds their largest scales.  Matrix instructions of the NQ row
  * tiles alternate (P0 V, Q0 K', P1 V, Q1 K', ...), so that one tile's softmax runs under
  * the other's products.
  */
@@ -35,15 +35,17 @@ struct PShape {
     static constexpr int QBYTES = 128 * D * 2;           /* one row tile, one part */
     static constexpr int BUF = TN * D * 2;               /* one expanded tile */
     static constexpr int RAW = UT * UB;                  /* one tile in 4 bits */
+    static constexpr int SCAN = 16 + 32;                 /* a raw tile's references: kref, flags, vref[8] */
     static constexpr int META = 32 + 32 + TN;            /* kfac, flags, vref[8], NaN masks */
     static constexpr int RS = NB == 8 && QT == 2 ? 1 : 2; /* tiles in 4 bits */
-    static constexpr int FIXED = NQ * QT * QBYTES + RS * RAW + 1024;
+    static constexpr int FIXED = NQ * QT * QBYTES + RS * (RAW + SCAN) + 256;
     static constexpr int ROOM = (232448 - 1024 - FIXED) / (BUF + META);
     static constexpr int NBUF = ROOM > 4 ? 4 : ROOM;
     static_assert(NBUF >= 2, "a key and a value tile fit");
-    static_assert(NQ * QT * QBYTES + NBUF * (BUF + META) + RS * RAW + 256 + 1024 <= 232448, "shared memory");
-    static constexpr int WARPS = 4 * NQ + 6;
-    static constexpr int SMEM = NQ * QT * QBYTES + NBUF * (BUF + META) + RS * RAW + 256 + 1024;
+    static_assert(NQ * QT * QBYTES + NBUF * (BUF + META) + RS * (RAW + SCAN) + 256 + 1024 <= 232448, "shared memory");
+    static constexpr int EW = NB == 6 ? 4 : 8;           /* warps that expand */
+    static constexpr int WARPS = 4 * NQ + EW + 2;
+    static constexpr int SMEM = NQ * QT * QBYTES + NBUF * (BUF + META) + RS * (RAW + SCAN) + 256 + 1024;
     static constexpr int O_COL = NQ * TN;                /* accumulators behind the scores */
     static constexpr uint32_t COLS = NQ * (TN + D) <= 256 ? 256 : 512;
     static_assert(NQ * (TN + D) <= 512, "tensor memory");
@@ -123,21 +125,23 @@ __device__ __forceinline__ uint32_t half_mul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+__device__ __forceinline__ uint32_t both_halves(int v) { return ((uint32_t)v & 0xFFFFu) * 0x10001u; }
 __device__ __forceinline__ uint32_t half_pack(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *(const uint32_t*)&h;
 }
 
-/* The largest of a word's four bytes that is not 255; *nan is set where one is 255. */
-__device__ __forceinline__ int byte_max(uint32_t w, bool* nan) {
-    int m = 0;
+/* Largest bytes, as two 16-bit halves to be joined by half_max. */
+__device__ __forceinline__ uint32_t bytes_max(uint32_t m, uint32_t w) {
+    return __vmaxu2(m, __vmaxu2(w & 0x00FF00FFu, (w >> 8) & 0x00FF00FFu));
+}
+__device__ __forceinline__ int half_max(uint32_t m) { return (int)max(m & 0xFFFFu, m >> 16); }
+/* A word's bytes with 255 (NaN) as 0. */
+__device__ __forceinline__ uint32_t drop_nan(uint32_t w) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int e = (w >> (8 * i)) & 0xFF;
-        *nan |= e == 255;
-        m = max(m, e == 255 ? 0 : e);
-    }
-    return m;
+    for (int i = 0; i < 4; ++i)
+        if (((w >> (8 * i)) & 0xFFu) == 0xFFu) w &= ~(0xFFu << (8 * i));
+    return w;
 }
 
 /* What a CTA works on. */
@@ -156,18 +160,19 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const uint32_t base = (smem_u32(pf_smem) + 1023u) & ~1023u;
     const uint32_t q_at = base, buf_at = q_at + NQ * QT * H::QBYTES, raw_at = buf_at + NBUF * H::BUF, meta_at = raw_at + H::RS * H::RAW,
-                   bars = meta_at + NBUF * H::META;
+                   scan_at = meta_at + NBUF * H::META, bars = scan_at + H::RS * H::SCAN;
     static_assert(H::META % 16 == 0 && H::RAW % 16 == 0, "sections stay aligned");
     const uint32_t raw_full = bars, raw_empty = bars + 16, buf_full = bars + 32, buf_empty = buf_full + 8 * NBUF,
                    s_full = buf_empty + 8 * NBUF, p_full = s_full + 8 * NQ, o_done = p_full + 8 * NQ, q_full = o_done + 8 * NQ,
-                   tslot = q_full + 8;
+                   scanned = q_full + 8, tslot = scanned + 16;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(raw_full + 8 * i, 1);
-            mbar_init(raw_empty + 8 * i, 4);
+            mbar_init(raw_empty + 8 * i, H::EW);
+            mbar_init(scanned + 8 * i, 1);
         }
         for (int i = 0; i < NBUF; ++i) {
-            mbar_init(buf_full + 8 * i, 4);
+            mbar_init(buf_full + 8 * i, H::EW);
             mbar_init(buf_empty + 8 * i, 1);
         }
         for (int i = 0; i < NQ; ++i) {
@@ -178,7 +183,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
         mbar_init(q_full, 4 * NQ);
         mbar_fence_init();
     }
-    if (warp == 4 * NQ + 4) {
+    if (warp == 4 * NQ + H::EW) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tslot), "r"(H::COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -314,7 +319,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             wait(s_full + 8 * t, j & 1);
             wait(buf_full + 8 * vb, (vn / NBUF) & 1);
             tc_fence_after();
-            const float f = rowfac * __uint_as_float(lds32(meta));
+            const float f = fmaxf(rowfac * __uint_as_float(lds32(meta)), FLT_MIN); /* > 0: a masked -inf stays one */
             const uint32_t flags = lds32(meta + 4);
             const int ut = J.u0 + j * UT; /* the tile's first unit */
             bool moved = false;
@@ -329,45 +334,35 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             const int tok_a = unit_of(ut) * kUnit, tok_z = unit_of(min(ut + UT, J.u1) - 1) * kUnit + kUnit - 1;
             const bool all = ut + UT <= J.u1 && tok_z <= pos_lo &&
                              (!a.window || tok_a > pos_hi - a.window || tok_z < a.sinks);
-            uint32_t p[TN / 2];
-            float sum, tmax;
-            auto weights = [&](float mm) {
-                const float off = kPBias - mm;
-                float s0 = 0.f, s1 = 0.f, mx = -INFINITY;
+            /* first pass: the row's largest score.  A place that the row does not see is -inf */
+            auto scores_of = [&](int k, uint32_t (&v)[32]) {
+                tc_ld32(s_at + 32 * k, v);
+                tc_wait_ld(v);
+                if (!all) {
 #pragma unroll
-                for (int k = 0; k < TN / 32; ++k) {
-                    uint32_t v[32];
-                    tc_ld32(s_at + 32 * k, v);
-                    tc_wait_ld(v);
-                    if (!all) {
+                    for (int h2 = 0; h2 < 2; ++h2) {
+                        const int u = ut + 2 * k + h2, tok = u < J.u1 ? unit_of(u) * kUnit : 0x7FFFFF00;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int u = ut + 2 * k + (i >> 4), tok = unit_of(u) * kUnit + (i & 15);
-                            const bool see = u < J.u1 && tok <= pos && (!a.window || tok > pos - a.window || tok < a.sinks);
-                            v[i] = see ? v[i] : 0xFF800000u;
+                        for (int i = 0; i < 16; ++i) {
+                            const int at = tok + i;
+                            if (at > pos || (a.window && at <= pos - a.window && at >= a.sinks)) v[16 * h2 + i] = 0xFF800000u;
                         }
                     }
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float x0 = __uint_as_float(v[i]), x1 = __uint_as_float(v[i + 1]);
-                        /* a masked score stays -inf whatever the factor's sign of zero */
-                        const float t0 = !all && v[i] == 0xFF800000u ? -INFINITY : fmaf(x0, f, off);
-                        const float t1 = !all && v[i + 1] == 0xFF800000u ? -INFINITY : fmaf(x1, f, off);
-                        mx = fmaxf(mx, fmaxf(t0, t1));
-                        const float p0 = ex2(t0), p1 = ex2(t1);
-                        s0 += p0;
-                        s1 += p1;
-                        p[16 * k + i / 2] = half_pack(p0, p1);
-                    }
                 }
-                sum = s0 + s1;
-                tmax = mx - off;
             };
-            weights(m);
-            if (__any_sync(kAll, tmax > m + kPSlack || (!set && tmax > -INFINITY)) || moved) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < TN / 32; ++k) {
+                uint32_t v[32];
+                scores_of(k, v);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+            }
+            mx *= f; /* f > 0 */
+            if (__any_sync(kAll, mx > m + kPSlack || (!set && mx > -INFINITY)) || moved) {
                 /* references move: the accumulators follow once the products before are done */
-                const float nm = set ? fmaxf(m, tmax) : tmax > -INFINITY ? tmax : 0.f, al = set ? ex2(m - nm) : 0.f;
-                set |= tmax > -INFINITY;
+                const float nm = set ? fmaxf(m, mx) : mx > -INFINITY ? mx : 0.f, al = set ? ex2(m - nm) : 0.f;
+                set |= mx > -INFINITY;
                 if (j > 0) {
                     wait(o_done + 8 * t, (j - 1) & 1);
                     tc_fence_after();
@@ -388,11 +383,24 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                 }
                 m = nm;
                 l *= al;
-                weights(m);
             }
-            l += sum;
+            /* second pass: the weights take the scores' place, behind the reads */
+            const float off = kPBias - m;
+            float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-            for (int k = 0; k < TN / 32; ++k) tc_st16(s_at + 16 * k, &p[16 * k]);
+            for (int k = 0; k < TN / 32; ++k) {
+                uint32_t v[32], p[16];
+                scores_of(k, v);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const float p0 = ex2(fmaf(__uint_as_float(v[i]), f, off)), p1 = ex2(fmaf(__uint_as_float(v[i + 1]), f, off));
+                    s0 += p0;
+                    s1 += p1;
+                    p[i / 2] = half_pack(p0, p1);
+                }
+                tc_st16(s_at + 16 * k, p);
+            }
+            l += s0 + s1;
             tc_wait_st();
             tc_fence_before();
             if (flags & 1u) { /* tokens with NaN values: their blocks are NaN for the rows that see them */
@@ -453,56 +461,46 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                 part[128 * D + 128 + 32 * q4 + lane] = l;
             } else if (a.lse) a.lse[row * a.n_q_heads + head] = l == 0.f ? -INFINITY : (m - kPBias + log2f(l)) * 0.6931471805599453f;
         }
-    } else if (warp < 4 * NQ + 4) {
+    } else if (warp < 4 * NQ + H::EW) {
         /* ---------------------------------------------------------------- expansion */
-        const int w4 = warp - 4 * NQ;
-        int vref = 0; /* lane: of block lane % NB (0: unset) */
-        int n = 0;    /* tiles expanded: keys 2 j, values 2 j + 1 */
+        /* warp w takes unit w % UT of a tile, and of its blocks the w / UT-th part */
+        constexpr int PARTS = H::EW / UT, BP = NB / PARTS;
+        const int we = warp - 4 * NQ, u = we % UT, b0 = we / UT * BP;
+        static_assert(UT * PARTS == H::EW && BP * PARTS == NB, "the warps share a tile");
+        int n = 0; /* tiles expanded: keys 2 j, values 2 j + 1 */
         for (int j = 0; j < T; ++j) {
-            const uint32_t raw = raw_at + (j % H::RS) * H::RAW;
-            const int ut = J.u0 + j * UT, have = min(UT, J.u1 - ut);
-            wait(raw_full + 8 * (j % H::RS), (j / H::RS) & 1);
-            /* tokens that hold something: all but the last unit's end */
-            auto valid_in = [&](int u) { return u < have ? min(kUnit, J.len - unit_of(ut + u) * kUnit) : 0; };
-
-            /* the keys' largest scale: every warp looks at all of them, lane by lane a word
-             * of a token's scales (NB = 2, 6: two bytes at a time) */
-            int top = 0;
-            for (int i = lane; i < TN; i += 32) {
-                const int u = i >> 4, tk = i & 15;
-                if (tk < valid_in(u)) {
-                    const uint32_t at = raw + u * UB + 16 * D + tk * NB;
-                    bool nan = false;
-#pragma unroll
-                    for (int k = 0; k < NB; k += 2) {
-                        unsigned short x;
-                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at + k) : "memory");
-                        top = max(top, byte_max((uint32_t)x, &nan));
-                    }
-                }
-            }
-            const int kref = max(16, __reduce_max_sync(kAll, top));
+            const int rs = j % H::RS;
+            const uint32_t src = raw_at + rs * H::RAW + u * UB, scan = scan_at + rs * H::SCAN;
+            const int ut = J.u0 + j * UT;
+            wait(scanned + 8 * rs, (j / H::RS) & 1);
+            const int kref = (int)lds32(scan);
+            const uint32_t flags = lds32(scan + 4); /* bit 0: NaN values, bit 1: NaN keys */
+            const int nv = ut + u < J.u1 ? min(kUnit, J.len - unit_of(ut + u) * kUnit) : 0; /* tokens of the unit that hold something */
             {
                 const int buf = n % NBUF;
-                const uint32_t dst = buf_at + buf * H::BUF;
+                /* a row's 16-byte chunk 4 b + c goes to chunk (4 b + c) ^ (row % 8) of its 128 bytes */
+                const uint32_t dst = buf_at + buf * H::BUF + (u * kUnit + g) * 128;
+                const uint32_t even = dst + ((c ^ g) << 4), odd = dst + (((4 + c) ^ g) << 4);
+                const uint32_t add = both_halves(28 - kref);
                 wait(buf_empty + 8 * buf, ((n / NBUF) & 1) ^ 1u);
-                for (int u = w4; u < UT; u += 4) {
-                    const uint32_t src = raw + u * UB;
 #pragma unroll
-                    for (int i4 = 0; i4 < NB / 2; ++i4) {
-                        const uint4 wv = lds128(src + i4 * 512 + lane * 16);
-                        const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+                for (int k = 0; k < BP; k += 2) {
+                    const int blk = b0 + k;
+                    const uint4 wv = lds128(src + (blk >> 1) * 512 + lane * 16);
+                    const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int blk = 2 * i4 + (k >> 1), tk = g + 8 * (k & 1), rowt = u * kUnit + tk;
-                            const int e = (int)lds8(src + 16 * D + tk * NB + blk);
-                            /* 2^(e - kref + 13) twice, NaN for 255 */
-                            const uint32_t s = e == 255 ? 0x7E007E00u : (uint32_t)max(e - kref + 28, 0) * 0x04000400u;
+                    for (int r = 0; r < 2; ++r) { /* tokens g, g + 8 */
+                        unsigned short e2; /* scales of blocks blk, blk + 1 */
+                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e2) : "r"(src + 16 * D + (g + 8 * r) * NB + blk) : "memory");
+#pragma unroll
+                        for (int bb = 0; bb < 2; ++bb) {
+                            /* 2^(e - kref + 13) in both halves, 0 below 2^-27 of the largest */
+                            uint32_t sc = __viaddmax_s16x2(__byte_perm(e2, 0, bb ? 0x4141 : 0x4040), add, 0u) << 10;
+                            if ((flags & 2u) && ((e2 >> (8 * bb)) & 0xFFu) == 255u) sc = 0x7E007E00u;
                             uint32_t h4[4];
-                            e2m1x8_f16(ww[k], h4);
-                            const int chunk = 4 * blk + c;
-                            sts128(dst + (chunk >> 3) * (TN * 128) + rowt * 128 + (((chunk & 7) ^ (rowt & 7)) << 4),
-                                   half_mul2(h4[0], s), half_mul2(h4[1], s), half_mul2(h4[2], s), half_mul2(h4[3], s));
+                            e2m1x8_f16(ww[2 * bb + r], h4);
+                            sts128((bb ? odd : even) + (blk >> 1) * (TN * 128) + r * 1024, half_mul2(h4[0], sc), half_mul2(h4[1], sc),
+                                   half_mul2(h4[2], sc), half_mul2(h4[3], sc));
                         }
                     }
                 }
@@ -511,97 +509,78 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                 if (lane == 0) mbar_arrive(buf_full + 8 * buf);
                 ++n;
             }
-
-            /* the values' largest scale per block: word 32 k + lane is of block lane % NB */
             {
-                int vt = 0;
-                bool nan = false;
-                constexpr int WU = 4 * NB; /* words per unit */
-                for (int u = 0; u < have; ++u) {
-                    const int nv = valid_in(u);
-                    for (int i = lane; i < WU; i += 32) {
-                        uint32_t x = lds32(raw + u * UB + 16 * D + D / 2 + 4 * i);
-                        const int cc = i / NB;
-                        if (nv < kUnit) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (2 * cc + (k & 1) + 8 * (k >> 1) >= nv) x &= ~(0xFFu << (8 * k));
-                        }
-                        vt = max(vt, byte_max(x, &nan));
-                    }
-                }
-                /* lanes of one block: lane % NB equal (NB divides 32, or 24 of the lanes for NB = 6) */
-                int best = 0;
-#pragma unroll
-                for (int k = 0; k < (32 + NB - 1) / NB; ++k) {
-                    const int from = lane % NB + k * NB;
-                    const int y = __shfl_sync(kAll, vt, from & 31);
-                    if (from < 32) best = max(best, y);
-                }
-                if (vref == 0 || best > vref + 13) vref = max(vref, max(best, 1));
-                nan = __any_sync(kAll, nan);
-
                 const int buf = n % NBUF;
-                const uint32_t dst = buf_at + buf * H::BUF, meta = meta_at + buf * H::META;
+                const uint32_t meta = meta_at + buf * H::META;
                 wait(buf_empty + 8 * buf, ((n / NBUF) & 1) ^ 1u);
-                if (w4 == 0) {
+                if (we == 0) {
                     if (lane == 0) {
                         sts32(meta, (uint32_t)(kref - 13) << 23); /* 2^(kref - 140) */
-                        sts32(meta + 4, nan ? 1u : 0u);
+                        sts32(meta + 4, flags & 1u);
                     }
-                    if (lane < NB) sts32(meta + 32 + 4 * lane, (uint32_t)vref);
-                }
-                if (nan && w4 == 0) {
-                    for (int i = lane; i < TN; i += 32) {
-                        const int u = i >> 4, tk = i & 15;
-                        uint32_t mask = 0;
-                        if (tk < valid_in(u))
-                            for (int k = 0; k < NB; ++k)
-                                if (lds8(raw + u * UB + 16 * D + D / 2 + ((((tk >> 1) & 3) * NB + k) * 2 + (tk >> 3)) * 2 + (tk & 1)) == 255u)
-                                    mask |= 1u << k;
-                        asm volatile("st.shared.u8 [%0], %1;" ::"r"(meta + 64 + i), "r"(mask) : "memory");
+                    if (lane < NB) sts32(meta + 32 + 4 * lane, lds32(scan + 16 + 4 * lane));
+                    if (flags & 1u) { /* which blocks of which tokens are NaN */
+                        for (int i = lane; i < TN; i += 32) {
+                            const int v = i >> 4, tk = i & 15;
+                            const int mine = ut + v < J.u1 ? min(kUnit, J.len - unit_of(ut + v) * kUnit) : 0;
+                            uint32_t mask = 0;
+                            if (tk < mine)
+                                for (int k = 0; k < NB; ++k)
+                                    if (lds8(raw_at + rs * H::RAW + v * UB + 16 * D + D / 2 + ((((tk >> 1) & 3) * NB + k) * 2 + (tk >> 3)) * 2 +
+                                             (tk & 1)) == 255u)
+                                        mask |= 1u << k;
+                            asm volatile("st.shared.u8 [%0], %1;" ::"r"(meta + 64 + i), "r"(mask) : "memory");
+                        }
                     }
                 }
-                for (int u = w4; u < UT; u += 4) {
-                    const uint32_t src = raw + u * UB;
-                    const int nv = valid_in(u);
+                /* channel d's row: tokens 16 u + 8 p + 2 c, + 1 are 4 bytes of chunk 2 u + p */
+                const uint32_t dst = buf_at + buf * H::BUF + (u >> 2) * (D * 128) + g * 128 + 4 * c;
+                const uint32_t at0 = dst + (((2 * (u & 3)) ^ g) << 4), at1 = dst + (((2 * (u & 3) + 1) ^ g) << 4);
+                uint32_t vmask = 0xFFFFFFFFu;
+                if (nv < kUnit) {
 #pragma unroll
-                    for (int blk = 0; blk < NB; ++blk) {
-                        const int ref = __shfl_sync(kAll, vref, blk);
-                        const uint32_t x = lds32(src + 16 * D + D / 2 + (c * NB + blk) * 4);
-                        uint32_t s[2] = {0u, 0u};
+                    for (int k = 0; k < 4; ++k)
+                        if (2 * c + (k & 1) + 8 * (k >> 1) >= nv) vmask &= ~(0xFFu << (8 * k));
+                }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int e = (x >> (8 * k)) & 0xFF, tk = 2 * c + (k & 1) + 8 * (k >> 1);
-                            const int z = e == 255 || tk >= nv ? 0 : min(max(e - ref + 15, 0), 30);
-                            s[k >> 1] |= (uint32_t)z << (10 + 16 * (k & 1));
-                        }
-                        uint32_t wv[2];
-                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(wv[0]), "=r"(wv[1])
-                                     : "r"(src + 8 * D + (blk >> 1) * 512 + lane * 16 + (blk & 1) * 8) : "memory");
+                for (int k = 0; k < BP; ++k) {
+                    const int blk = b0 + k;
+                    const uint32_t add = both_halves(15 - (int)lds32(scan + 16 + 4 * blk));
+                    uint32_t x = lds32(src + 16 * D + D / 2 + (c * NB + blk) * 4);
+                    if (flags & 1u) x = drop_nan(x); /* (their codes are zeros: any finite scale does) */
+                    x &= vmask;
+                    /* 2^(e - vref): 0 below 2^-14, at most 2^13 by the choice of vref.  A masked
+                     * token's scale 0 gives 0 unless vref < 15, where the codes count: masked too */
+                    uint32_t s0 = __viaddmax_s16x2(__byte_perm(x, 0, 0x4140), add, 0u) << 10;
+                    uint32_t s1 = __viaddmax_s16x2(__byte_perm(x, 0, 0x4342), add, 0u) << 10;
+                    if (nv < kUnit) {
+                        s0 &= __byte_perm(vmask, 0, 0x1100);
+                        s1 &= __byte_perm(vmask, 0, 0x3322);
+                    }
+                    uint32_t wv[2];
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(wv[0]), "=r"(wv[1])
+                                 : "r"(src + 8 * D + (blk >> 1) * 512 + lane * 16 + (blk & 1) * 8) : "memory");
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t h4[4];
-                            e2m1x8_f16(wv[i], h4);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) { /* byte r + 2 p */
-                                const int d = 32 * blk + 16 * i + 8 * (k & 1) + g, p = k >> 1;
-                                const int chunk = 2 * u + p;
-                                sts32(dst + (chunk >> 3) * (D * 128) + d * 128 + (((chunk & 7) ^ (d & 7)) << 4) + 4 * c, half_mul2(h4[k], s[p]));
-                            }
-                        }
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t h4[4]; /* byte r + 2 p: channel 32 blk + 16 i + 8 r + g */
+                        e2m1x8_f16(wv[i], h4);
+                        const uint32_t o = (32 * blk + 16 * i) * 128;
+                        sts32(at0 + o, half_mul2(h4[0], s0));
+                        sts32(at0 + o + 1024, half_mul2(h4[1], s0));
+                        sts32(at1 + o, half_mul2(h4[2], s1));
+                        sts32(at1 + o + 1024, half_mul2(h4[3], s1));
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(buf_full + 8 * buf);
-                    mbar_arrive(raw_empty + 8 * (j % H::RS));
+                    mbar_arrive(raw_empty + 8 * rs);
                 }
                 ++n;
             }
         }
-    } else if (warp == 4 * NQ + 4) {
+    } else if (warp == 4 * NQ + H::EW) {
         /* ---------------------------------------------------------------- matrix instructions */
         if (T > 0) {
             /* kind::f16, FP32 accumulators, FP16 operands, both K-major: N / 8 at bit 17, M / 16 at bit 24 */
@@ -653,8 +632,8 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
         }
         __syncwarp();
     } else {
-        /* ---------------------------------------------------------------- copies */
-        for (int j = 0; j < T; ++j) {
+        /* ---------------------------------------------------------------- copies, references */
+        auto issue = [&](int j) {
             const int s = j % H::RS, ut = J.u0 + j * UT, have = min(UT, J.u1 - ut);
             int page = 0, unit = 0;
             if (lane < have) {
@@ -671,11 +650,74 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             if (lane < have)
                 bulk_g2s(raw_at + s * H::RAW + lane * UB, page_ptr(a.P, page, J.h, unit & ((1 << (a.P.page_shift - 4)) - 1)), UB,
                          raw_full + 8 * s);
+        };
+        int vref = 0; /* lane: of block lane % NB (0: unset) */
+        if (H::RS > 1 && T > 0) issue(0);
+        for (int j = 0; j < T; ++j) {
+            if (H::RS == 1) issue(j);
+            else if (j + 1 < T) issue(j + 1);
+            const int s = j % H::RS, ut = J.u0 + j * UT, have = min(UT, J.u1 - ut);
+            const uint32_t raw = raw_at + s * H::RAW, scan = scan_at + s * H::SCAN;
+            wait(raw_full + 8 * s, (j / H::RS) & 1);
+            const int last = ut + have >= J.units ? min(kUnit, J.len - unit_of(ut + have - 1) * kUnit) : kUnit; /* tokens of the last unit */
+            /* the largest key scale: words of the token-major scales, 4 bytes of one or two tokens */
+            uint32_t km = 0;
+            bool nan = false;
+            auto key_pass = [&](bool drop) {
+                km = 0;
+                for (int i = lane; i < have * 4 * NB; i += 32) {
+                    const int v = i / (4 * NB), k = i % (4 * NB); /* word k: bytes 4 k .. of [token][block] */
+                    uint32_t w = lds32(raw + v * UB + 16 * D + 4 * k);
+                    if (v == have - 1 && last < kUnit) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if ((4 * k + q) / NB >= last) w &= ~(0xFFu << (8 * q));
+                    }
+                    km = bytes_max(km, drop ? drop_nan(w) : w);
+                }
+                km = (uint32_t)__reduce_max_sync(kAll, half_max(km));
+            };
+            key_pass(false);
+            const bool knan = km == 255u;
+            if (knan) key_pass(true);
+            const int kref = max(16, (int)km);
+            /* the values' per block: word i is of block i % NB; lanes take words of one block */
+            constexpr int WU = 4 * NB, LANES = 32 / NB * NB; /* lanes that stride whole blocks */
+            uint32_t vm = 0;
+            auto value_pass = [&](bool drop) {
+                vm = 0;
+                if (lane < LANES)
+                    for (int i = lane; i < have * WU; i += LANES) {
+                        const int v = i / WU, cc = i % WU / NB;
+                        uint32_t w = lds32(raw + v * UB + 16 * D + D / 2 + 4 * (i % WU));
+                        if (v == have - 1 && last < kUnit) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                if (2 * cc + (q & 1) + 8 * (q >> 1) >= last) w &= ~(0xFFu << (8 * q));
+                        }
+                        vm = bytes_max(vm, drop ? drop_nan(w) : w);
+                    }
+            };
+            value_pass(false);
+            nan = __any_sync(kAll, half_max(vm) == 255);
+            if (nan) value_pass(true);
+            const int mine = half_max(vm);
+            int best = 0;
+#pragma unroll
+            for (int k = 0; k < LANES / NB; ++k) best = max(best, __shfl_sync(kAll, mine, lane % NB + k * NB));
+            if (vref == 0 || best > vref + 13) vref = max(vref, max(best, 1));
+            if (lane == 0) {
+                sts32(scan, (uint32_t)kref);
+                sts32(scan + 4, (nan ? 1u : 0u) | (knan ? 2u : 0u));
+            }
+            if (lane < NB) sts32(scan + 16 + 4 * lane, (uint32_t)vref);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(scanned + 8 * s);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 4 * NQ + 4) {
+    if (warp == 4 * NQ + H::EW) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(H::COLS) : "memory");
     }
