@@ -12,9 +12,9 @@
  *           (and the accumulators with it) only when a scale lies more than 2^13 above.
  * S (FP32, in tensor memory) is read one row per thread, the weights 2^(s - m + 6) go
  * back as FP16 in S's place and are the tensor-memory operand of O += P V.  The row's
- * reference m moves, and O with it, only when a score passes it by 2^8.
+ * reference m moves, and O with it, only when a tile's weights add to more than 2^14.
  *
- * Warps: NQ groups of four for the softmax, eight that expand tiles, one that issues the
+ * Warps: NQ groups of four for the softmax, four that expand tiles, one that issues the
  * matrix instructions, one that copies units in and finds their largest scales.  Matrix instructions of the NQ row
  * tiles alternate (P0 V, Q0 K', P1 V, Q1 K', ...), so that one tile's softmax runs under
  * the other's products.
@@ -25,7 +25,7 @@
 
 namespace kv {
 
-constexpr float kPBias = 6.f, kPSlack = 8.f;
+constexpr float kPBias = 6.f;
 
 template <int NB, int NQ, int QT>
 struct PShape {
@@ -43,8 +43,8 @@ struct PShape {
     static constexpr int NBUF = ROOM > 4 ? 4 : ROOM;
     static_assert(NBUF >= 2, "a key and a value tile fit");
     static_assert(NQ * QT * QBYTES + NBUF * (BUF + META) + RS * (RAW + SCAN) + 256 + 1024 <= 232448, "shared memory");
-    static constexpr int EW = NB == 6 ? 4 : 8;           /* warps that expand */
-    static constexpr int WARPS = 4 * NQ + EW + 2;
+    static constexpr int EW = 4;                         /* warps that expand */
+    static constexpr int WARPS = 4 * NQ + EW + 4;        /* whole warpgroups; two warps idle */
     static constexpr int SMEM = NQ * QT * QBYTES + NBUF * (BUF + META) + RS * (RAW + SCAN) + 256 + 1024;
     static constexpr int O_COL = NQ * TN;                /* accumulators behind the scores */
     static constexpr uint32_t COLS = NQ * (TN + D) <= 256 ? 256 : 512;
@@ -129,6 +129,23 @@ __device__ __forceinline__ uint32_t both_halves(int v) { return ((uint32_t)v & 0
 __device__ __forceinline__ uint32_t half_pack(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *(const uint32_t*)&h;
+}
+
+/* (a f + c, b f + c) and acc + (a, b): the two-wide FP32 instructions. */
+__device__ __forceinline__ float2 fma2(uint32_t a, uint32_t b, float f, float c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, d;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %5};\n\t"
+        "fma.rn.f32x2 d, x, y, z;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(a), "r"(b), "f"(f), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 acc, float a, float b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, d;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 d, x, y;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(acc.x), "f"(acc.y), "f"(a), "f"(b));
+    return r;
 }
 
 /* Largest bytes, as two 16-bit halves to be joined by half_max. */
@@ -238,6 +255,12 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
     };
     auto unit_of = [&](int u) { return u < J.sink_u ? u : u - J.sink_u + J.lo_u; };
 
+    /* The softmax warps take registers from the others: of 512 threads x 128, 256 x 184 and
+     * 256 x 72. */
+    if constexpr (NQ == 2) {
+        if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    }
     if (J.r0 >= J.R) {
         /* a row tile that this sequence does not have */
     } else if (warp < 4 * NQ) {
@@ -334,33 +357,64 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             const int tok_a = unit_of(ut) * kUnit, tok_z = unit_of(min(ut + UT, J.u1) - 1) * kUnit + kUnit - 1;
             const bool all = ut + UT <= J.u1 && tok_z <= pos_lo &&
                              (!a.window || tok_a > pos_hi - a.window || tok_z < a.sinks);
-            /* first pass: the row's largest score.  A place that the row does not see is -inf */
-            auto scores_of = [&](int k, uint32_t (&v)[32]) {
-                tc_ld32(s_at + 32 * k, v);
-                tc_wait_ld(v);
-                if (!all) {
-#pragma unroll
-                    for (int h2 = 0; h2 < 2; ++h2) {
-                        const int u = ut + 2 * k + h2, tok = u < J.u1 ? unit_of(u) * kUnit : 0x7FFFFF00;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int at = tok + i;
-                            if (at > pos || (a.window && at <= pos - a.window && at >= a.sinks)) v[16 * h2 + i] = 0xFF800000u;
-                        }
-                    }
+            /* scores of 32 columns; a place that the row does not see is -inf */
+            auto mask_of = [&](int u) { /* tokens of a unit that the row sees */
+                if (u >= J.u1) return 0u;
+                const int tok = unit_of(u) * kUnit, last = pos - tok;
+                uint32_t w = last < 0 ? 0u : last >= 15 ? 0xFFFFu : (2u << last) - 1u;
+                if (a.window) {
+                    const int gone = last - a.window + 1; /* the first `gone` tokens lie before the window, */
+                    uint32_t x = gone <= 0 ? 0xFFFFu : gone >= 16 ? 0u : 0xFFFFu << gone;
+                    const int keep = a.sinks - tok;       /* but the first `keep` stay */
+                    x |= keep <= 0 ? 0u : keep >= 16 ? 0xFFFFu : (1u << keep) - 1u;
+                    w &= x;
                 }
+                return w;
             };
-            float mx = -INFINITY;
+            auto hide = [&](int k, uint32_t (&v)[32]) {
+                const uint32_t w = mask_of(ut + 2 * k) | mask_of(ut + 2 * k + 1) << 16;
 #pragma unroll
-            for (int k = 0; k < TN / 32; ++k) {
-                uint32_t v[32];
-                scores_of(k, v);
+                for (int i = 0; i < 32; ++i) v[i] = w >> i & 1u ? v[i] : 0xFF800000u;
+            };
+            /* weights 2^(s - m + kPBias), kept in registers until it is certain that m holds: a
+             * row's sum above 2^14, or its first token, or a moved value reference sends the
+             * warp round again */
+            uint32_t p[TN / 2];
+            float sum;
+            for (int round = 0;; ++round) {
+                const float off = kPBias - m;
+                float2 acc = make_float2(0.f, 0.f);
+                uint32_t v[2][32];
+                tc_ld32(s_at, v[0]);
+                tc_wait_ld(v[0]);
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
-            }
-            mx *= f; /* f > 0 */
-            if (__any_sync(kAll, mx > m + kPSlack || (!set && mx > -INFINITY)) || moved) {
+                for (int k = 0; k < TN / 32; ++k) {
+                    uint32_t (&x)[32] = v[k & 1];
+                    if (k + 1 < TN / 32) tc_ld32(s_at + 32 * (k + 1), v[(k + 1) & 1]);
+                    if (!all) hide(k, x);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 y = fma2(x[i], x[i + 1], f, off);
+                        const float p0 = ex2(y.x), p1 = ex2(y.y);
+                        acc = add2(acc, p0, p1);
+                        p[16 * k + i / 2] = half_pack(p0, p1);
+                    }
+                    if (k + 1 < TN / 32) tc_wait_ld(v[(k + 1) & 1]);
+                }
+                sum = acc.x + acc.y;
+                if (!__any_sync(kAll, (round == 0 && !set) || sum > 16384.f) && !moved) break;
+                if (round == 2) break; /* (an infinite score: the sum is one whatever m) */
                 /* references move: the accumulators follow once the products before are done */
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int k = 0; k < TN / 32; ++k) {
+                    tc_ld32(s_at + 32 * k, v[0]);
+                    tc_wait_ld(v[0]);
+                    if (!all) hide(k, v[0]);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[0][i]));
+                }
+                mx *= f; /* f > 0 */
                 const float nm = set ? fmaxf(m, mx) : mx > -INFINITY ? mx : 0.f, al = set ? ex2(m - nm) : 0.f;
                 set |= mx > -INFINITY;
                 if (j > 0) {
@@ -368,39 +422,25 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                     tc_fence_after();
 #pragma unroll 1
                     for (int k = 0; k < NB; ++k) {
-                        uint32_t v[32];
-                        tc_ld32(o_at + 32 * k, v);
-                        tc_wait_ld(v);
+                        tc_ld32(o_at + 32 * k, v[0]);
+                        tc_wait_ld(v[0]);
                         float fk = 1.f;
 #pragma unroll
                         for (int k2 = 0; k2 < NB; ++k2) fk = k2 == k ? vfac[k2] : fk;
                         fk *= al;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * fk);
-                        tc_st32(o_at + 32 * k, v);
+                        for (int i = 0; i < 32; ++i) v[0][i] = __float_as_uint(__uint_as_float(v[0][i]) * fk);
+                        tc_st32(o_at + 32 * k, v[0]);
                     }
                     tc_wait_st();
                 }
                 m = nm;
                 l *= al;
+                moved = false;
             }
-            /* second pass: the weights take the scores' place, behind the reads */
-            const float off = kPBias - m;
-            float s0 = 0.f, s1 = 0.f;
+            l += sum;
 #pragma unroll
-            for (int k = 0; k < TN / 32; ++k) {
-                uint32_t v[32], p[16];
-                scores_of(k, v);
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const float p0 = ex2(fmaf(__uint_as_float(v[i]), f, off)), p1 = ex2(fmaf(__uint_as_float(v[i + 1]), f, off));
-                    s0 += p0;
-                    s1 += p1;
-                    p[i / 2] = half_pack(p0, p1);
-                }
-                tc_st16(s_at + 16 * k, p);
-            }
-            l += s0 + s1;
+            for (int k = 0; k < TN / 32; ++k) tc_st16(s_at + 16 * k, &p[16 * k]);
             tc_wait_st();
             tc_fence_before();
             if (flags & 1u) { /* tokens with NaN values: their blocks are NaN for the rows that see them */
@@ -463,44 +503,47 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
         }
     } else if (warp < 4 * NQ + H::EW) {
         /* ---------------------------------------------------------------- expansion */
-        /* warp w takes unit w % UT of a tile, and of its blocks the w / UT-th part */
-        constexpr int PARTS = H::EW / UT, BP = NB / PARTS;
-        const int we = warp - 4 * NQ, u = we % UT, b0 = we / UT * BP;
-        static_assert(UT * PARTS == H::EW && BP * PARTS == NB, "the warps share a tile");
+        /* warp w takes the units w, w + 4 of a tile */
+        const int we = warp - 4 * NQ;
+        /* which words a lane takes of the keys: rows q and q + 4 share a quarter of the warp, so
+         * that its eight 16-byte stores fall into eight different bank groups */
+        const int kg = (lane >> 3) + 4 * ((lane >> 2) & 1), kl = kg * 4 + c;
         int n = 0; /* tiles expanded: keys 2 j, values 2 j + 1 */
         for (int j = 0; j < T; ++j) {
             const int rs = j % H::RS;
-            const uint32_t src = raw_at + rs * H::RAW + u * UB, scan = scan_at + rs * H::SCAN;
+            const uint32_t raw = raw_at + rs * H::RAW, scan = scan_at + rs * H::SCAN;
             const int ut = J.u0 + j * UT;
             wait(scanned + 8 * rs, (j / H::RS) & 1);
             const int kref = (int)lds32(scan);
             const uint32_t flags = lds32(scan + 4); /* bit 0: NaN values, bit 1: NaN keys */
-            const int nv = ut + u < J.u1 ? min(kUnit, J.len - unit_of(ut + u) * kUnit) : 0; /* tokens of the unit that hold something */
             {
                 const int buf = n % NBUF;
-                /* a row's 16-byte chunk 4 b + c goes to chunk (4 b + c) ^ (row % 8) of its 128 bytes */
-                const uint32_t dst = buf_at + buf * H::BUF + (u * kUnit + g) * 128;
-                const uint32_t even = dst + ((c ^ g) << 4), odd = dst + (((4 + c) ^ g) << 4);
                 const uint32_t add = both_halves(28 - kref);
                 wait(buf_empty + 8 * buf, ((n / NBUF) & 1) ^ 1u);
+#pragma unroll 1
+                for (int u = we; u < UT; u += 4) {
+                    const uint32_t src = raw + u * UB;
+                    /* a row's 16-byte chunk 4 b + c goes to chunk (4 b + c) ^ (row % 8) of its 128 bytes */
+                    const uint32_t dst = buf_at + buf * H::BUF + (u * kUnit + kg) * 128;
+                    const uint32_t even = dst + ((c ^ kg) << 4), odd = dst + (((4 + c) ^ kg) << 4);
 #pragma unroll
-                for (int k = 0; k < BP; k += 2) {
-                    const int blk = b0 + k;
-                    const uint4 wv = lds128(src + (blk >> 1) * 512 + lane * 16);
-                    const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+                    for (int blk = 0; blk < NB; blk += 2) {
+                        const uint4 wv = lds128(src + (blk >> 1) * 512 + kl * 16);
+                        const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) { /* tokens g, g + 8 */
-                        unsigned short e2; /* scales of blocks blk, blk + 1 */
-                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e2) : "r"(src + 16 * D + (g + 8 * r) * NB + blk) : "memory");
+                        for (int r = 0; r < 2; ++r) { /* tokens kg, kg + 8 */
+                            unsigned short e2; /* scales of blocks blk, blk + 1 */
+                            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e2) : "r"(src + 16 * D + (kg + 8 * r) * NB + blk) : "memory");
 #pragma unroll
-                        for (int bb = 0; bb < 2; ++bb) {
-                            /* 2^(e - kref + 13) in both halves, 0 below 2^-27 of the largest */
-                            uint32_t sc = __viaddmax_s16x2(__byte_perm(e2, 0, bb ? 0x4141 : 0x4040), add, 0u) << 10;
-                            if ((flags & 2u) && ((e2 >> (8 * bb)) & 0xFFu) == 255u) sc = 0x7E007E00u;
-                            uint32_t h4[4];
-                            e2m1x8_f16(ww[2 * bb + r], h4);
-                            sts128((bb ? odd : even) + (blk >> 1) * (TN * 128) + r * 1024, half_mul2(h4[0], sc), half_mul2(h4[1], sc),
-                                   half_mul2(h4[2], sc), half_mul2(h4[3], sc));
+                            for (int bb = 0; bb < 2; ++bb) {
+                                /* 2^(e - kref + 13) in both halves, 0 below 2^-27 of the largest */
+                                uint32_t sc = __viaddmax_s16x2(__byte_perm(e2, 0, bb ? 0x4141 : 0x4040), add, 0u) << 10;
+                                if ((flags & 2u) && ((e2 >> (8 * bb)) & 0xFFu) == 255u) sc = 0x7E007E00u;
+                                uint32_t h4[4];
+                                e2m1x8_f16(ww[2 * bb + r], h4);
+                                sts128((bb ? odd : even) + (blk >> 1) * (TN * 128) + r * 1024, half_mul2(h4[0], sc), half_mul2(h4[1], sc),
+                                       half_mul2(h4[2], sc), half_mul2(h4[3], sc));
+                            }
                         }
                     }
                 }
@@ -526,49 +569,52 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                             uint32_t mask = 0;
                             if (tk < mine)
                                 for (int k = 0; k < NB; ++k)
-                                    if (lds8(raw_at + rs * H::RAW + v * UB + 16 * D + D / 2 + ((((tk >> 1) & 3) * NB + k) * 2 + (tk >> 3)) * 2 +
-                                             (tk & 1)) == 255u)
+                                    if (lds8(raw + v * UB + 16 * D + D / 2 + ((((tk >> 1) & 3) * NB + k) * 2 + (tk >> 3)) * 2 + (tk & 1)) == 255u)
                                         mask |= 1u << k;
                             asm volatile("st.shared.u8 [%0], %1;" ::"r"(meta + 64 + i), "r"(mask) : "memory");
                         }
                     }
                 }
-                /* channel d's row: tokens 16 u + 8 p + 2 c, + 1 are 4 bytes of chunk 2 u + p */
-                const uint32_t dst = buf_at + buf * H::BUF + (u >> 2) * (D * 128) + g * 128 + 4 * c;
-                const uint32_t at0 = dst + (((2 * (u & 3)) ^ g) << 4), at1 = dst + (((2 * (u & 3) + 1) ^ g) << 4);
-                uint32_t vmask = 0xFFFFFFFFu;
-                if (nv < kUnit) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (2 * c + (k & 1) + 8 * (k >> 1) >= nv) vmask &= ~(0xFFu << (8 * k));
-                }
-#pragma unroll
-                for (int k = 0; k < BP; ++k) {
-                    const int blk = b0 + k;
-                    const uint32_t add = both_halves(15 - (int)lds32(scan + 16 + 4 * blk));
-                    uint32_t x = lds32(src + 16 * D + D / 2 + (c * NB + blk) * 4);
-                    if (flags & 1u) x = drop_nan(x); /* (their codes are zeros: any finite scale does) */
-                    x &= vmask;
-                    /* 2^(e - vref): 0 below 2^-14, at most 2^13 by the choice of vref.  A masked
-                     * token's scale 0 gives 0 unless vref < 15, where the codes count: masked too */
-                    uint32_t s0 = __viaddmax_s16x2(__byte_perm(x, 0, 0x4140), add, 0u) << 10;
-                    uint32_t s1 = __viaddmax_s16x2(__byte_perm(x, 0, 0x4342), add, 0u) << 10;
+#pragma unroll 1
+                for (int u = we; u < UT; u += 4) {
+                    const uint32_t src = raw + u * UB;
+                    const int nv = ut + u < J.u1 ? min(kUnit, J.len - unit_of(ut + u) * kUnit) : 0; /* tokens of the unit that hold something */
+                    /* channel d's row: tokens 16 u + 8 p + 2 c, + 1 are 4 bytes of chunk 2 u + p */
+                    const uint32_t dst = buf_at + buf * H::BUF + (u >> 2) * (D * 128) + g * 128 + 4 * c;
+                    const uint32_t at0 = dst + (((2 * (u & 3)) ^ g) << 4), at1 = dst + (((2 * (u & 3) + 1) ^ g) << 4);
+                    uint32_t vmask = 0xFFFFFFFFu;
                     if (nv < kUnit) {
-                        s0 &= __byte_perm(vmask, 0, 0x1100);
-                        s1 &= __byte_perm(vmask, 0, 0x3322);
-                    }
-                    uint32_t wv[2];
-                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(wv[0]), "=r"(wv[1])
-                                 : "r"(src + 8 * D + (blk >> 1) * 512 + lane * 16 + (blk & 1) * 8) : "memory");
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t h4[4]; /* byte r + 2 p: channel 32 blk + 16 i + 8 r + g */
-                        e2m1x8_f16(wv[i], h4);
-                        const uint32_t o = (32 * blk + 16 * i) * 128;
-                        sts32(at0 + o, half_mul2(h4[0], s0));
-                        sts32(at0 + o + 1024, half_mul2(h4[1], s0));
-                        sts32(at1 + o, half_mul2(h4[2], s1));
-                        sts32(at1 + o + 1024, half_mul2(h4[3], s1));
+                        for (int k = 0; k < 4; ++k)
+                            if (2 * c + (k & 1) + 8 * (k >> 1) >= nv) vmask &= ~(0xFFu << (8 * k));
+                    }
+#pragma unroll
+                    for (int blk = 0; blk < NB; ++blk) {
+                        const uint32_t add = both_halves(15 - (int)lds32(scan + 16 + 4 * blk));
+                        uint32_t x = lds32(src + 16 * D + D / 2 + (c * NB + blk) * 4);
+                        if (flags & 1u) x = drop_nan(x); /* (their codes are zeros: any finite scale does) */
+                        x &= vmask;
+                        /* 2^(e - vref): 0 below 2^-14, at most 2^13 by the choice of vref.  A masked
+                         * token's scale 0 gives 0 unless vref < 15, where the codes count: masked too */
+                        uint32_t s0 = __viaddmax_s16x2(__byte_perm(x, 0, 0x4140), add, 0u) << 10;
+                        uint32_t s1 = __viaddmax_s16x2(__byte_perm(x, 0, 0x4342), add, 0u) << 10;
+                        if (nv < kUnit) {
+                            s0 &= __byte_perm(vmask, 0, 0x1100);
+                            s1 &= __byte_perm(vmask, 0, 0x3322);
+                        }
+                        uint32_t wv[2];
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(wv[0]), "=r"(wv[1])
+                                     : "r"(src + 8 * D + (blk >> 1) * 512 + lane * 16 + (blk & 1) * 8) : "memory");
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t h4[4]; /* byte r + 2 p: channel 32 blk + 16 i + 8 r + g */
+                            e2m1x8_f16(wv[i], h4);
+                            const uint32_t o = (32 * blk + 16 * i) * 128;
+                            sts32(at0 + o, half_mul2(h4[0], s0));
+                            sts32(at0 + o + 1024, half_mul2(h4[1], s0));
+                            sts32(at1 + o, half_mul2(h4[2], s1));
+                            sts32(at1 + o + 1024, half_mul2(h4[3], s1));
+                        }
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -631,7 +677,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             }
         }
         __syncwarp();
-    } else {
+    } else if (warp == 4 * NQ + H::EW + 1) {
         /* ---------------------------------------------------------------- copies, references */
         auto issue = [&](int j) {
             const int s = j % H::RS, ut = J.u0 + j * UT, have = min(UT, J.u1 - ut);
