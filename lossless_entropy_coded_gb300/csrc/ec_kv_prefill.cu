@@ -15,7 +15,7 @@
  * reference m moves, and O with it, only when a tile's weights add to more than 2^14.
  *
  * Warps: NQ groups of four for the softmax, four that expand tiles, one that issues the
- * matrix instructions, one that copies units in and finds their largest scales.  Matrix instructions of the NQ row
+ * matrix instructions, one that copies units in, one that finds their largest scales.  Matrix instructions of the NQ row
  * tiles alternate (P0 V, Q0 K', P1 V, Q1 K', ...), so that one tile's softmax runs under
  * the other's products.
  */
@@ -35,17 +35,17 @@ struct PShape {
     static constexpr int QBYTES = 128 * D * 2;           /* one row tile, one part */
     static constexpr int BUF = TN * D * 2;               /* one expanded tile */
     static constexpr int RAW = UT * UB;                  /* one tile in 4 bits */
-    static constexpr int SCAN = 16 + 32;                 /* a raw tile's references: kref, flags, vref[8] */
-    static constexpr int META = 32 + 32 + TN;            /* kfac, flags, vref[8], NaN masks */
+    static constexpr int META = 16 + 32 + TN;            /* kref, flags, vref[8], NaN masks */
+    static constexpr int MS = 4;                         /* tiles' metas */
     static constexpr int RS = NB == 8 && QT == 2 ? 1 : 2; /* tiles in 4 bits */
-    static constexpr int FIXED = NQ * QT * QBYTES + RS * (RAW + SCAN) + 256;
-    static constexpr int ROOM = (232448 - 1024 - FIXED) / (BUF + META);
+    static constexpr int FIXED = NQ * QT * QBYTES + RS * RAW + MS * META + 256;
+    static constexpr int ROOM = (232448 - 1024 - FIXED) / BUF;
     static constexpr int NBUF = ROOM > 4 ? 4 : ROOM;
     static_assert(NBUF >= 2, "a key and a value tile fit");
-    static_assert(NQ * QT * QBYTES + NBUF * (BUF + META) + RS * (RAW + SCAN) + 256 + 1024 <= 232448, "shared memory");
+    static_assert(NQ * QT * QBYTES + NBUF * BUF + RS * RAW + MS * META + 256 + 1024 <= 232448, "shared memory");
     static constexpr int EW = 4;                         /* warps that expand */
-    static constexpr int WARPS = 4 * NQ + EW + 4;        /* whole warpgroups; two warps idle */
-    static constexpr int SMEM = NQ * QT * QBYTES + NBUF * (BUF + META) + RS * (RAW + SCAN) + 256 + 1024;
+    static constexpr int WARPS = 4 * NQ + EW + 4;        /* whole warpgroups; one warp idles */
+    static constexpr int SMEM = NQ * QT * QBYTES + NBUF * BUF + RS * RAW + MS * META + 256 + 1024;
     static constexpr int O_COL = NQ * TN;                /* accumulators behind the scores */
     static constexpr uint32_t COLS = NQ * (TN + D) <= 256 ? 256 : 512;
     static_assert(NQ * (TN + D) <= 512, "tensor memory");
@@ -177,16 +177,15 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const uint32_t base = (smem_u32(pf_smem) + 1023u) & ~1023u;
     const uint32_t q_at = base, buf_at = q_at + NQ * QT * H::QBYTES, raw_at = buf_at + NBUF * H::BUF, meta_at = raw_at + H::RS * H::RAW,
-                   scan_at = meta_at + NBUF * H::META, bars = scan_at + H::RS * H::SCAN;
+                   bars = meta_at + H::MS * H::META;
     static_assert(H::META % 16 == 0 && H::RAW % 16 == 0, "sections stay aligned");
     const uint32_t raw_full = bars, raw_empty = bars + 16, buf_full = bars + 32, buf_empty = buf_full + 8 * NBUF,
                    s_full = buf_empty + 8 * NBUF, p_full = s_full + 8 * NQ, o_done = p_full + 8 * NQ, q_full = o_done + 8 * NQ,
-                   scanned = q_full + 8, tslot = scanned + 16;
+                   meta_full = q_full + 8, tslot = meta_full + 8 * H::MS;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(raw_full + 8 * i, 1);
             mbar_init(raw_empty + 8 * i, H::EW);
-            mbar_init(scanned + 8 * i, 1);
         }
         for (int i = 0; i < NBUF; ++i) {
             mbar_init(buf_full + 8 * i, H::EW);
@@ -197,6 +196,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             mbar_init(p_full + 8 * i, 4);
             mbar_init(o_done + 8 * i, 1);
         }
+        for (int i = 0; i < H::MS; ++i) mbar_init(meta_full + 8 * i, 1);
         mbar_init(q_full, 4 * NQ);
         mbar_fence_init();
     }
@@ -337,19 +337,18 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
         const int pos_lo = __shfl_sync(kAll, pos, 0), pos_hi = __shfl_sync(kAll, pos, 31);
 
         for (int j = 0; j < T; ++j) {
-            const int vn = 2 * j + 1, vb = vn % NBUF;
-            const uint32_t meta = meta_at + vb * H::META;
+            const uint32_t meta = meta_at + j % H::MS * H::META;
+            wait(meta_full + 8 * (j % H::MS), (j / H::MS) & 1);
             wait(s_full + 8 * t, j & 1);
-            wait(buf_full + 8 * vb, (vn / NBUF) & 1);
             tc_fence_after();
-            const float f = fmaxf(rowfac * __uint_as_float(lds32(meta)), FLT_MIN); /* > 0: a masked -inf stays one */
+            const float f = fmaxf(rowfac * __uint_as_float((lds32(meta) - 13u) << 23), FLT_MIN); /* > 0: a masked -inf stays one */
             const uint32_t flags = lds32(meta + 4);
             const int ut = J.u0 + j * UT; /* the tile's first unit */
             bool moved = false;
             float vfac[NB];
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
-                const int nv = (int)lds32(meta + 32 + 4 * k);
+                const int nv = (int)lds32(meta + 16 + 4 * k);
                 vfac[k] = ex2((float)(vref[k] - nv));
                 moved |= nv != vref[k];
                 vref[k] = nv;
@@ -447,7 +446,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                 for (int i = 0; i < TN; ++i) {
                     const int u = ut + (i >> 4);
                     if (u >= J.u1) break;
-                    const uint32_t w = lds8(meta + 64 + i);
+                    const uint32_t w = lds8(meta + 48 + i);
                     const int tok = unit_of(u) * kUnit + (i & 15);
                     if (w && tok <= pos && (!a.window || tok > pos - a.window || tok < a.sinks)) nan_blocks |= w;
                 }
@@ -510,41 +509,45 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
         const int kg = (lane >> 3) + 4 * ((lane >> 2) & 1), kl = kg * 4 + c;
         int n = 0; /* tiles expanded: keys 2 j, values 2 j + 1 */
         for (int j = 0; j < T; ++j) {
-            const int rs = j % H::RS;
-            const uint32_t raw = raw_at + rs * H::RAW, scan = scan_at + rs * H::SCAN;
-            const int ut = J.u0 + j * UT;
-            wait(scanned + 8 * rs, (j / H::RS) & 1);
-            const int kref = (int)lds32(scan);
-            const uint32_t flags = lds32(scan + 4); /* bit 0: NaN values, bit 1: NaN keys */
+            const int rs = j % H::RS, ut = J.u0 + j * UT;
+            const uint32_t raw = raw_at + rs * H::RAW, meta = meta_at + j % H::MS * H::META;
+            wait(raw_full + 8 * rs, (j / H::RS) & 1);
+            wait(meta_full + 8 * (j % H::MS), (j / H::MS) & 1);
+            const uint32_t flags = lds32(meta + 4); /* bit 0: NaN values, bit 1: NaN keys */
             {
                 const int buf = n % NBUF;
-                const uint32_t add = both_halves(28 - kref);
+                const uint32_t add = both_halves(28 - (int)lds32(meta));
                 wait(buf_empty + 8 * buf, ((n / NBUF) & 1) ^ 1u);
-#pragma unroll 1
+#pragma unroll
                 for (int u = we; u < UT; u += 4) {
                     const uint32_t src = raw + u * UB;
                     /* a row's 16-byte chunk 4 b + c goes to chunk (4 b + c) ^ (row % 8) of its 128 bytes */
                     const uint32_t dst = buf_at + buf * H::BUF + (u * kUnit + kg) * 128;
                     const uint32_t even = dst + ((c ^ kg) << 4), odd = dst + (((4 + c) ^ kg) << 4);
+                    /* a unit's words and scales first, so that one wait covers them */
+                    uint4 wv[NB / 2];
+                    uint32_t e2[NB / 2][2]; /* scales of two blocks, tokens kg and kg + 8 */
 #pragma unroll
-                    for (int blk = 0; blk < NB; blk += 2) {
-                        const uint4 wv = lds128(src + (blk >> 1) * 512 + kl * 16);
-                        const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+                    for (int i = 0; i < NB / 2; ++i) {
+                        wv[i] = lds128(src + i * 512 + kl * 16);
+                        e2[i][0] = lds16(src + 16 * D + kg * NB + 2 * i);
+                        e2[i][1] = lds16(src + 16 * D + (kg + 8) * NB + 2 * i);
+                    }
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) { /* tokens kg, kg + 8 */
-                            unsigned short e2; /* scales of blocks blk, blk + 1 */
-                            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e2) : "r"(src + 16 * D + (kg + 8 * r) * NB + blk) : "memory");
+                    for (int i = 0; i < NB / 2; ++i) {
+                        const uint32_t ww[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
 #pragma unroll
                             for (int bb = 0; bb < 2; ++bb) {
                                 /* 2^(e - kref + 13) in both halves, 0 below 2^-27 of the largest */
-                                uint32_t sc = __viaddmax_s16x2(__byte_perm(e2, 0, bb ? 0x4141 : 0x4040), add, 0u) << 10;
-                                if ((flags & 2u) && ((e2 >> (8 * bb)) & 0xFFu) == 255u) sc = 0x7E007E00u;
+                                uint32_t sc = __viaddmax_s16x2(__byte_perm(e2[i][r], 0, bb ? 0x4141 : 0x4040), add, 0u) * 1024u;
+                                if ((flags & 2u) && ((e2[i][r] >> (8 * bb)) & 0xFFu) == 255u) sc = 0x7E007E00u;
                                 uint32_t h4[4];
                                 e2m1x8_f16(ww[2 * bb + r], h4);
-                                sts128((bb ? odd : even) + (blk >> 1) * (TN * 128) + r * 1024, half_mul2(h4[0], sc), half_mul2(h4[1], sc),
+                                sts128((bb ? odd : even) + i * (TN * 128) + r * 1024, half_mul2(h4[0], sc), half_mul2(h4[1], sc),
                                        half_mul2(h4[2], sc), half_mul2(h4[3], sc));
                             }
-                        }
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -554,66 +557,64 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             }
             {
                 const int buf = n % NBUF;
-                const uint32_t meta = meta_at + buf * H::META;
+                uint32_t add[NB]; /* 15 - vref in both halves */
+#pragma unroll
+                for (int k = 0; k < NB; ++k) add[k] = both_halves(15 - (int)lds32(meta + 16 + 4 * k));
                 wait(buf_empty + 8 * buf, ((n / NBUF) & 1) ^ 1u);
-                if (we == 0) {
-                    if (lane == 0) {
-                        sts32(meta, (uint32_t)(kref - 13) << 23); /* 2^(kref - 140) */
-                        sts32(meta + 4, flags & 1u);
-                    }
-                    if (lane < NB) sts32(meta + 32 + 4 * lane, lds32(scan + 16 + 4 * lane));
-                    if (flags & 1u) { /* which blocks of which tokens are NaN */
-                        for (int i = lane; i < TN; i += 32) {
-                            const int v = i >> 4, tk = i & 15;
-                            const int mine = ut + v < J.u1 ? min(kUnit, J.len - unit_of(ut + v) * kUnit) : 0;
-                            uint32_t mask = 0;
-                            if (tk < mine)
-                                for (int k = 0; k < NB; ++k)
-                                    if (lds8(raw + v * UB + 16 * D + D / 2 + ((((tk >> 1) & 3) * NB + k) * 2 + (tk >> 3)) * 2 + (tk & 1)) == 255u)
-                                        mask |= 1u << k;
-                            asm volatile("st.shared.u8 [%0], %1;" ::"r"(meta + 64 + i), "r"(mask) : "memory");
-                        }
-                    }
-                }
-#pragma unroll 1
+#pragma unroll
                 for (int u = we; u < UT; u += 4) {
                     const uint32_t src = raw + u * UB;
                     const int nv = ut + u < J.u1 ? min(kUnit, J.len - unit_of(ut + u) * kUnit) : 0; /* tokens of the unit that hold something */
                     /* channel d's row: tokens 16 u + 8 p + 2 c, + 1 are 4 bytes of chunk 2 u + p */
                     const uint32_t dst = buf_at + buf * H::BUF + (u >> 2) * (D * 128) + g * 128 + 4 * c;
                     const uint32_t at0 = dst + (((2 * (u & 3)) ^ g) << 4), at1 = dst + (((2 * (u & 3) + 1) ^ g) << 4);
-                    uint32_t vmask = 0xFFFFFFFFu;
-                    if (nv < kUnit) {
+                    uint4 wv[NB / 2];
+                    uint32_t s0[NB], s1[NB];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (2 * c + (k & 1) + 8 * (k >> 1) >= nv) vmask &= ~(0xFFu << (8 * k));
+                    for (int i = 0; i < NB / 2; ++i) wv[i] = lds128(src + 8 * D + i * 512 + lane * 16);
+#pragma unroll
+                    for (int k = 0; k < NB; k += 2)
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(s0[k]), "=r"(s0[k + 1]) : "r"(src + 16 * D + D / 2 + (c * NB + k) * 4) : "memory");
+                    if ((flags & 1u) || nv < kUnit) {
+                        /* scales of NaN blocks (their codes are zeros) and of tokens that hold nothing */
+#pragma unroll
+                        for (int k = 0; k < NB; ++k) {
+                            s0[k] = drop_nan(s0[k]);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                if (2 * c + (q & 1) + 8 * (q >> 1) >= nv) s0[k] &= ~(0xFFu << (8 * q));
+                        }
                     }
 #pragma unroll
-                    for (int blk = 0; blk < NB; ++blk) {
-                        const uint32_t add = both_halves(15 - (int)lds32(scan + 16 + 4 * blk));
-                        uint32_t x = lds32(src + 16 * D + D / 2 + (c * NB + blk) * 4);
-                        if (flags & 1u) x = drop_nan(x); /* (their codes are zeros: any finite scale does) */
-                        x &= vmask;
-                        /* 2^(e - vref): 0 below 2^-14, at most 2^13 by the choice of vref.  A masked
-                         * token's scale 0 gives 0 unless vref < 15, where the codes count: masked too */
-                        uint32_t s0 = __viaddmax_s16x2(__byte_perm(x, 0, 0x4140), add, 0u) << 10;
-                        uint32_t s1 = __viaddmax_s16x2(__byte_perm(x, 0, 0x4342), add, 0u) << 10;
-                        if (nv < kUnit) {
-                            s0 &= __byte_perm(vmask, 0, 0x1100);
-                            s1 &= __byte_perm(vmask, 0, 0x3322);
-                        }
-                        uint32_t wv[2];
-                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(wv[0]), "=r"(wv[1])
-                                     : "r"(src + 8 * D + (blk >> 1) * 512 + lane * 16 + (blk & 1) * 8) : "memory");
+                    for (int k = 0; k < NB; ++k) {
+                        /* 2^(e - vref): 0 below 2^-14, at most 2^13 by the choice of vref */
+                        const uint32_t x = s0[k];
+                        s0[k] = __viaddmax_s16x2(__byte_perm(x, 0, 0x4140), add[k], 0u) * 1024u;
+                        s1[k] = __viaddmax_s16x2(__byte_perm(x, 0, 0x4342), add[k], 0u) * 1024u;
+                    }
+                    if (nv < kUnit) { /* with vref < 15 a scale byte of 0 is no zero: the codes of nothing must not count */
+                        uint32_t m0 = 0, m1 = 0;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t h4[4]; /* byte r + 2 p: channel 32 blk + 16 i + 8 r + g */
-                            e2m1x8_f16(wv[i], h4);
-                            const uint32_t o = (32 * blk + 16 * i) * 128;
-                            sts32(at0 + o, half_mul2(h4[0], s0));
-                            sts32(at0 + o + 1024, half_mul2(h4[1], s0));
-                            sts32(at1 + o, half_mul2(h4[2], s1));
-                            sts32(at1 + o + 1024, half_mul2(h4[3], s1));
+                        for (int q = 0; q < 2; ++q) {
+                            if (2 * c + q < nv) m0 |= 0xFFFFu << (16 * q);
+                            if (2 * c + q + 8 < nv) m1 |= 0xFFFFu << (16 * q);
+                        }
+#pragma unroll
+                        for (int k = 0; k < NB; ++k) s0[k] &= m0, s1[k] &= m1;
+                    }
+#pragma unroll
+                    for (int i4 = 0; i4 < NB / 2; ++i4) {
+                        const uint32_t ww[4] = {wv[i4].x, wv[i4].y, wv[i4].z, wv[i4].w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) { /* channels 16 (4 i4 + i) .. + 15: block 2 i4 + i / 2 */
+                            const int k = 2 * i4 + i / 2;
+                            uint32_t h4[4]; /* byte r + 2 p: channel 8 r + g of them */
+                            e2m1x8_f16(ww[i], h4);
+                            const uint32_t o = (64 * i4 + 16 * i) * 128;
+                            sts32(at0 + o, half_mul2(h4[0], s0[k]));
+                            sts32(at0 + o + 1024, half_mul2(h4[1], s0[k]));
+                            sts32(at1 + o, half_mul2(h4[2], s1[k]));
+                            sts32(at1 + o + 1024, half_mul2(h4[3], s1[k]));
                         }
                     }
                 }
@@ -678,8 +679,8 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
         }
         __syncwarp();
     } else if (warp == 4 * NQ + H::EW + 1) {
-        /* ---------------------------------------------------------------- copies, references */
-        auto issue = [&](int j) {
+        /* ---------------------------------------------------------------- copies */
+        for (int j = 0; j < T; ++j) {
             const int s = j % H::RS, ut = J.u0 + j * UT, have = min(UT, J.u1 - ut);
             int page = 0, unit = 0;
             if (lane < have) {
@@ -690,75 +691,85 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                     flag_corrupt(a.status);
                 }
             }
+            const uint8_t* src = page_ptr(a.P, page, J.h, unit & ((1 << (a.P.page_shift - 4)) - 1));
             wait(raw_empty + 8 * s, ((j / H::RS) & 1) ^ 1u);
             if (lane == 0) mbar_arrive_tx(raw_full + 8 * s, have * UB);
             __syncwarp();
-            if (lane < have)
-                bulk_g2s(raw_at + s * H::RAW + lane * UB, page_ptr(a.P, page, J.h, unit & ((1 << (a.P.page_shift - 4)) - 1)), UB,
-                         raw_full + 8 * s);
-        };
+            if (lane < have) bulk_g2s(raw_at + s * H::RAW + lane * UB, src, UB, raw_full + 8 * s);
+        }
+    } else if (warp == 4 * NQ + H::EW + 2) {
+        /* ---------------------------------------------------------------- references */
+        constexpr int WU = 4 * NB;             /* words of scales per unit, keys' or values' */
+        constexpr int LANES = 32 / NB * NB;    /* lanes that stride whole blocks: word i of the values' is of block i % NB */
+        constexpr int PER = (UT * WU + LANES - 1) / LANES;
         int vref = 0; /* lane: of block lane % NB (0: unset) */
-        if (H::RS > 1 && T > 0) issue(0);
         for (int j = 0; j < T; ++j) {
-            if (H::RS == 1) issue(j);
-            else if (j + 1 < T) issue(j + 1);
             const int s = j % H::RS, ut = J.u0 + j * UT, have = min(UT, J.u1 - ut);
-            const uint32_t raw = raw_at + s * H::RAW, scan = scan_at + s * H::SCAN;
+            const uint32_t raw = raw_at + s * H::RAW, meta = meta_at + j % H::MS * H::META;
             wait(raw_full + 8 * s, (j / H::RS) & 1);
             const int last = ut + have >= J.units ? min(kUnit, J.len - unit_of(ut + have - 1) * kUnit) : kUnit; /* tokens of the last unit */
-            /* the largest key scale: words of the token-major scales, 4 bytes of one or two tokens */
-            uint32_t km = 0;
-            bool nan = false;
-            auto key_pass = [&](bool drop) {
-                km = 0;
-                for (int i = lane; i < have * 4 * NB; i += 32) {
-                    const int v = i / (4 * NB), k = i % (4 * NB); /* word k: bytes 4 k .. of [token][block] */
-                    uint32_t w = lds32(raw + v * UB + 16 * D + 4 * k);
-                    if (v == have - 1 && last < kUnit) {
+            uint32_t kw[PER], vw[PER];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if ((4 * k + q) / NB >= last) w &= ~(0xFFu << (8 * q));
-                    }
-                    km = bytes_max(km, drop ? drop_nan(w) : w);
+            for (int q = 0; q < PER; ++q) {
+                const int i = lane + q * LANES, v = i / WU;
+                kw[q] = vw[q] = 0;
+                if (lane < LANES && v < have) {
+                    const uint32_t at = raw + v * UB + 16 * D + 4 * (i % WU);
+                    kw[q] = lds32(at);
+                    vw[q] = lds32(at + D / 2);
                 }
-                km = (uint32_t)__reduce_max_sync(kAll, half_max(km));
-            };
-            key_pass(false);
-            const bool knan = km == 255u;
-            if (knan) key_pass(true);
-            const int kref = max(16, (int)km);
-            /* the values' per block: word i is of block i % NB; lanes take words of one block */
-            constexpr int WU = 4 * NB, LANES = 32 / NB * NB; /* lanes that stride whole blocks */
-            uint32_t vm = 0;
-            auto value_pass = [&](bool drop) {
-                vm = 0;
-                if (lane < LANES)
-                    for (int i = lane; i < have * WU; i += LANES) {
-                        const int v = i / WU, cc = i % WU / NB;
-                        uint32_t w = lds32(raw + v * UB + 16 * D + D / 2 + 4 * (i % WU));
-                        if (v == have - 1 && last < kUnit) {
+            }
+            if (last < kUnit) { /* scales past the sequence's end are none */
 #pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                if (2 * cc + (q & 1) + 8 * (q >> 1) >= last) w &= ~(0xFFu << (8 * q));
-                        }
-                        vm = bytes_max(vm, drop ? drop_nan(w) : w);
+                for (int q = 0; q < PER; ++q) {
+                    const int i = lane + q * LANES, k = i % WU;
+                    if (i / WU != have - 1) continue;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        if ((4 * k + x) / NB >= last) kw[q] &= ~(0xFFu << (8 * x));
+                        if (2 * (k / NB) + (x & 1) + 8 * (x >> 1) >= last) vw[q] &= ~(0xFFu << (8 * x));
                     }
-            };
-            value_pass(false);
-            nan = __any_sync(kAll, half_max(vm) == 255);
-            if (nan) value_pass(true);
-            const int mine = half_max(vm);
-            int best = 0;
+                }
+            }
+            uint32_t km = 0, vm = 0;
 #pragma unroll
-            for (int k = 0; k < LANES / NB; ++k) best = max(best, __shfl_sync(kAll, mine, lane % NB + k * NB));
+            for (int q = 0; q < PER; ++q) km = bytes_max(km, kw[q]), vm = bytes_max(vm, vw[q]);
+            uint32_t flags = 0;
+            if (__any_sync(kAll, half_max(km) == 255 || half_max(vm) == 255)) {
+                flags = (__any_sync(kAll, half_max(vm) == 255) ? 1u : 0u) | (__any_sync(kAll, half_max(km) == 255) ? 2u : 0u);
+                km = vm = 0;
+#pragma unroll
+                for (int q = 0; q < PER; ++q) km = bytes_max(km, drop_nan(kw[q])), vm = bytes_max(vm, drop_nan(vw[q]));
+            }
+            const int kref = max(16, __reduce_max_sync(kAll, half_max(km)));
+            int best = half_max(vm);
+            if constexpr (32 % NB == 0) {
+#pragma unroll
+                for (int o = NB; o < 32; o <<= 1) best = max(best, __shfl_xor_sync(kAll, best, o));
+            } else {
+                const int mine = best;
+#pragma unroll
+                for (int k = 0; k < LANES / NB; ++k) best = max(best, __shfl_sync(kAll, mine, lane % NB + k * NB));
+            }
             if (vref == 0 || best > vref + 13) vref = max(vref, max(best, 1));
             if (lane == 0) {
-                sts32(scan, (uint32_t)kref);
-                sts32(scan + 4, (nan ? 1u : 0u) | (knan ? 2u : 0u));
+                sts32(meta, (uint32_t)kref);
+                sts32(meta + 4, flags);
             }
-            if (lane < NB) sts32(scan + 16 + 4 * lane, (uint32_t)vref);
+            if (lane < NB) sts32(meta + 16 + 4 * lane, (uint32_t)vref);
+            if (flags & 1u) { /* which blocks of which tokens are NaN */
+                for (int i = lane; i < TN; i += 32) {
+                    const int v = i >> 4, tk = i & 15;
+                    uint32_t mask = 0;
+                    if (v < have && (v < have - 1 || tk < last))
+                        for (int k = 0; k < NB; ++k)
+                            if (lds8(raw + v * UB + 16 * D + D / 2 + ((((tk >> 1) & 3) * NB + k) * 2 + (tk >> 3)) * 2 + (tk & 1)) == 255u)
+                                mask |= 1u << k;
+                    asm volatile("st.shared.u8 [%0], %1;" ::"r"(meta + 48 + i), "r"(mask) : "memory");
+                }
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(scanned + 8 * s);
+            if (lane == 0) mbar_arrive(meta_full + 8 * (j % H::MS));
         }
     }
     tc_fence_before();
