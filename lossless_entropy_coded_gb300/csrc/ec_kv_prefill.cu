@@ -12,7 +12,7 @@
  *           (and the accumulators with it) only when a scale lies more than 2^13 above.
  * S (FP32, in tensor memory) is read one row per thread, the weights 2^(s - m + 6) go
  * back as FP16 in S's place and are the tensor-memory operand of O += P V.  The row's
- * reference m moves, and O with it, only when a tile's weights add to more than 2^14.
+ * reference m moves, and O with it, only when a score passes it by 2^8.
  *
  * Warps: NQ groups of four for the softmax, four that expand tiles, one that issues the
  * matrix instructions, one that copies units in, one that finds their largest scales.  Matrix instructions of the NQ row
@@ -25,7 +25,7 @@
 
 namespace kv {
 
-constexpr float kPBias = 6.f;
+constexpr float kPBias = 6.f, kPSlack = 8.f;
 
 template <int NB, int NQ, int QT>
 struct PShape {
@@ -35,7 +35,7 @@ struct PShape {
     static constexpr int QBYTES = 128 * D * 2;           /* one row tile, one part */
     static constexpr int BUF = TN * D * 2;               /* one expanded tile */
     static constexpr int RAW = UT * UB;                  /* one tile in 4 bits */
-    static constexpr int META = 16 + 32 + TN;            /* kref, flags, vref[8], NaN masks */
+    static constexpr int META = 16 + 64 + TN;            /* kref, flags, vref[8], factors[8], NaN masks */
     static constexpr int MS = 4;                         /* tiles' metas */
     static constexpr int RS = NB == 8 && QT == 2 ? 1 : 2; /* tiles in 4 bits */
     static constexpr int FIXED = NQ * QT * QBYTES + RS * RAW + MS * META + 256;
@@ -129,23 +129,6 @@ __device__ __forceinline__ uint32_t both_halves(int v) { return ((uint32_t)v & 0
 __device__ __forceinline__ uint32_t half_pack(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *(const uint32_t*)&h;
-}
-
-/* (a f + c, b f + c) and acc + (a, b): the two-wide FP32 instructions. */
-__device__ __forceinline__ float2 fma2(uint32_t a, uint32_t b, float f, float c) {
-    float2 r;
-    asm("{\n\t.reg .b64 x, y, z, d;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %5};\n\t"
-        "fma.rn.f32x2 d, x, y, z;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "r"(a), "r"(b), "f"(f), "f"(c));
-    return r;
-}
-__device__ __forceinline__ float2 add2(float2 acc, float a, float b) {
-    float2 r;
-    asm("{\n\t.reg .b64 x, y, d;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 d, x, y;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(acc.x), "f"(acc.y), "f"(a), "f"(b));
-    return r;
 }
 
 /* Largest bytes, as two 16-bit halves to be joined by half_max. */
@@ -255,12 +238,6 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
     };
     auto unit_of = [&](int u) { return u < J.sink_u ? u : u - J.sink_u + J.lo_u; };
 
-    /* The softmax warps take registers from the others: of 512 threads x 128, 256 x 184 and
-     * 256 x 72. */
-    if constexpr (NQ == 2) {
-        if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    }
     if (J.r0 >= J.R) {
         /* a row tile that this sequence does not have */
     } else if (warp < 4 * NQ) {
@@ -330,10 +307,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
 
         float m = 0.f, l = 0.f;
         bool set = false; /* the row has seen a token: m is its reference */
-        int vref[NB];
         uint32_t nan_blocks = 0;
-#pragma unroll
-        for (int k = 0; k < NB; ++k) vref[k] = 0;
         const int pos_lo = __shfl_sync(kAll, pos, 0), pos_hi = __shfl_sync(kAll, pos, 31);
 
         for (int j = 0; j < T; ++j) {
@@ -344,15 +318,6 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             const float f = fmaxf(rowfac * __uint_as_float((lds32(meta) - 13u) << 23), FLT_MIN); /* > 0: a masked -inf stays one */
             const uint32_t flags = lds32(meta + 4);
             const int ut = J.u0 + j * UT; /* the tile's first unit */
-            bool moved = false;
-            float vfac[NB];
-#pragma unroll
-            for (int k = 0; k < NB; ++k) {
-                const int nv = (int)lds32(meta + 16 + 4 * k);
-                vfac[k] = ex2((float)(vref[k] - nv));
-                moved |= nv != vref[k];
-                vref[k] = nv;
-            }
             const int tok_a = unit_of(ut) * kUnit, tok_z = unit_of(min(ut + UT, J.u1) - 1) * kUnit + kUnit - 1;
             const bool all = ut + UT <= J.u1 && tok_z <= pos_lo &&
                              (!a.window || tok_a > pos_hi - a.window || tok_z < a.sinks);
@@ -375,45 +340,21 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = w >> i & 1u ? v[i] : 0xFF800000u;
             };
-            /* weights 2^(s - m + kPBias), kept in registers until it is certain that m holds: a
-             * row's sum above 2^14, or its first token, or a moved value reference sends the
-             * warp round again */
-            uint32_t p[TN / 2];
-            float sum;
-            for (int round = 0;; ++round) {
-                const float off = kPBias - m;
-                float2 acc = make_float2(0.f, 0.f);
-                uint32_t v[2][32];
-                tc_ld32(s_at, v[0]);
-                tc_wait_ld(v[0]);
-#pragma unroll
-                for (int k = 0; k < TN / 32; ++k) {
-                    uint32_t (&x)[32] = v[k & 1];
-                    if (k + 1 < TN / 32) tc_ld32(s_at + 32 * (k + 1), v[(k + 1) & 1]);
-                    if (!all) hide(k, x);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float2 y = fma2(x[i], x[i + 1], f, off);
-                        const float p0 = ex2(y.x), p1 = ex2(y.y);
-                        acc = add2(acc, p0, p1);
-                        p[16 * k + i / 2] = half_pack(p0, p1);
-                    }
-                    if (k + 1 < TN / 32) tc_wait_ld(v[(k + 1) & 1]);
-                }
-                sum = acc.x + acc.y;
-                if (!__any_sync(kAll, (round == 0 && !set) || sum > 16384.f) && !moved) break;
-                if (round == 2) break; /* (an infinite score: the sum is one whatever m) */
-                /* references move: the accumulators follow once the products before are done */
-                float mx = -INFINITY;
+            /* (the loops stay rolled: with five roles side by side the instruction cache decides;
+             * unrolled they took 2.2 times as long) */
+            float mx = -INFINITY;
 #pragma unroll 1
-                for (int k = 0; k < TN / 32; ++k) {
-                    tc_ld32(s_at + 32 * k, v[0]);
-                    tc_wait_ld(v[0]);
-                    if (!all) hide(k, v[0]);
+            for (int k = 0; k < TN / 32; ++k) {
+                uint32_t v[32];
+                tc_ld32(s_at + 32 * k, v);
+                tc_wait_ld(v);
+                if (!all) hide(k, v);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[0][i]));
-                }
-                mx *= f; /* f > 0 */
+                for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+            }
+            mx *= f; /* f > 0 */
+            if (__any_sync(kAll, mx > m + kPSlack || (!set && mx > -INFINITY)) || (flags & 4u)) {
+                /* references move: the accumulators follow once the products before are done */
                 const float nm = set ? fmaxf(m, mx) : mx > -INFINITY ? mx : 0.f, al = set ? ex2(m - nm) : 0.f;
                 set |= mx > -INFINITY;
                 if (j > 0) {
@@ -421,32 +362,45 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                     tc_fence_after();
 #pragma unroll 1
                     for (int k = 0; k < NB; ++k) {
-                        tc_ld32(o_at + 32 * k, v[0]);
-                        tc_wait_ld(v[0]);
-                        float fk = 1.f;
+                        uint32_t v[32];
+                        tc_ld32(o_at + 32 * k, v);
+                        tc_wait_ld(v);
+                        const float fk = al * __uint_as_float(lds32(meta + 48 + 4 * k));
 #pragma unroll
-                        for (int k2 = 0; k2 < NB; ++k2) fk = k2 == k ? vfac[k2] : fk;
-                        fk *= al;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[0][i] = __float_as_uint(__uint_as_float(v[0][i]) * fk);
-                        tc_st32(o_at + 32 * k, v[0]);
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * fk);
+                        tc_st32(o_at + 32 * k, v);
                     }
                     tc_wait_st();
                 }
                 m = nm;
                 l *= al;
-                moved = false;
             }
-            l += sum;
+            /* weights 2^(s - m + kPBias) take the scores' place, behind the reads */
+            const float off = kPBias - m;
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+            for (int k = 0; k < TN / 32; ++k) {
+                uint32_t v[32], p[16];
+                tc_ld32(s_at + 32 * k, v);
+                tc_wait_ld(v);
+                if (!all) hide(k, v);
 #pragma unroll
-            for (int k = 0; k < TN / 32; ++k) tc_st16(s_at + 16 * k, &p[16 * k]);
+                for (int i = 0; i < 32; i += 2) {
+                    const float p0 = ex2(fmaf(__uint_as_float(v[i]), f, off)), p1 = ex2(fmaf(__uint_as_float(v[i + 1]), f, off));
+                    acc[i & 2] += p0;
+                    acc[(i & 2) + 1] += p1;
+                    p[i / 2] = half_pack(p0, p1);
+                }
+                tc_st16(s_at + 16 * k, p);
+            }
+            l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
             tc_wait_st();
             tc_fence_before();
             if (flags & 1u) { /* tokens with NaN values: their blocks are NaN for the rows that see them */
                 for (int i = 0; i < TN; ++i) {
                     const int u = ut + (i >> 4);
                     if (u >= J.u1) break;
-                    const uint32_t w = lds8(meta + 48 + i);
+                    const uint32_t w = lds8(meta + 80 + i);
                     const int tok = unit_of(u) * kUnit + (i & 15);
                     if (w && tok <= pos && (!a.window || tok > pos - a.window || tok < a.sinks)) nan_blocks |= w;
                 }
@@ -465,9 +419,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
 #pragma unroll 1
         for (int k = 0; k < NB; ++k) {
             uint32_t v[32];
-            int vr = 0;
-#pragma unroll
-            for (int k2 = 0; k2 < NB; ++k2) vr = k2 == k ? vref[k2] : vr;
+            const int vr = T > 0 ? (int)lds32(meta_at + (T - 1) % H::MS * H::META + 16 + 4 * k) : 0;
             const float back = vr > 0 ? __uint_as_float((uint32_t)vr << 23) : 0.f;
             if (T > 0) {
                 tc_ld32(o_at + 32 * k, v);
@@ -518,31 +470,26 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                 const int buf = n % NBUF;
                 const uint32_t add = both_halves(28 - (int)lds32(meta));
                 wait(buf_empty + 8 * buf, ((n / NBUF) & 1) ^ 1u);
-#pragma unroll
+#pragma unroll 1
                 for (int u = we; u < UT; u += 4) {
                     const uint32_t src = raw + u * UB;
                     /* a row's 16-byte chunk 4 b + c goes to chunk (4 b + c) ^ (row % 8) of its 128 bytes */
                     const uint32_t dst = buf_at + buf * H::BUF + (u * kUnit + kg) * 128;
                     const uint32_t even = dst + ((c ^ kg) << 4), odd = dst + (((4 + c) ^ kg) << 4);
-                    /* a unit's words and scales first, so that one wait covers them */
-                    uint4 wv[NB / 2];
-                    uint32_t e2[NB / 2][2]; /* scales of two blocks, tokens kg and kg + 8 */
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < NB / 2; ++i) {
-                        wv[i] = lds128(src + i * 512 + kl * 16);
-                        e2[i][0] = lds16(src + 16 * D + kg * NB + 2 * i);
-                        e2[i][1] = lds16(src + 16 * D + (kg + 8) * NB + 2 * i);
-                    }
-#pragma unroll
-                    for (int i = 0; i < NB / 2; ++i) {
-                        const uint32_t ww[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
+                        const uint4 wv = lds128(src + i * 512 + kl * 16);
+                        uint32_t e2[2]; /* scales of blocks 2 i, 2 i + 1, tokens kg and kg + 8 */
+                        e2[0] = lds16(src + 16 * D + kg * NB + 2 * i);
+                        e2[1] = lds16(src + 16 * D + (kg + 8) * NB + 2 * i);
+                        const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
                         for (int r = 0; r < 2; ++r)
 #pragma unroll
                             for (int bb = 0; bb < 2; ++bb) {
                                 /* 2^(e - kref + 13) in both halves, 0 below 2^-27 of the largest */
-                                uint32_t sc = __viaddmax_s16x2(__byte_perm(e2[i][r], 0, bb ? 0x4141 : 0x4040), add, 0u) * 1024u;
-                                if ((flags & 2u) && ((e2[i][r] >> (8 * bb)) & 0xFFu) == 255u) sc = 0x7E007E00u;
+                                uint32_t sc = __viaddmax_s16x2(__byte_perm(e2[r], 0, bb ? 0x4141 : 0x4040), add, 0u) * 1024u;
+                                if ((flags & 2u) && ((e2[r] >> (8 * bb)) & 0xFFu) == 255u) sc = 0x7E007E00u;
                                 uint32_t h4[4];
                                 e2m1x8_f16(ww[2 * bb + r], h4);
                                 sts128((bb ? odd : even) + i * (TN * 128) + r * 1024, half_mul2(h4[0], sc), half_mul2(h4[1], sc),
@@ -557,64 +504,51 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             }
             {
                 const int buf = n % NBUF;
-                uint32_t add[NB]; /* 15 - vref in both halves */
-#pragma unroll
-                for (int k = 0; k < NB; ++k) add[k] = both_halves(15 - (int)lds32(meta + 16 + 4 * k));
                 wait(buf_empty + 8 * buf, ((n / NBUF) & 1) ^ 1u);
-#pragma unroll
+#pragma unroll 1
                 for (int u = we; u < UT; u += 4) {
                     const uint32_t src = raw + u * UB;
                     const int nv = ut + u < J.u1 ? min(kUnit, J.len - unit_of(ut + u) * kUnit) : 0; /* tokens of the unit that hold something */
                     /* channel d's row: tokens 16 u + 8 p + 2 c, + 1 are 4 bytes of chunk 2 u + p */
                     const uint32_t dst = buf_at + buf * H::BUF + (u >> 2) * (D * 128) + g * 128 + 4 * c;
                     const uint32_t at0 = dst + (((2 * (u & 3)) ^ g) << 4), at1 = dst + (((2 * (u & 3) + 1) ^ g) << 4);
-                    uint4 wv[NB / 2];
-                    uint32_t s0[NB], s1[NB];
-#pragma unroll
-                    for (int i = 0; i < NB / 2; ++i) wv[i] = lds128(src + 8 * D + i * 512 + lane * 16);
-#pragma unroll
-                    for (int k = 0; k < NB; k += 2)
-                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(s0[k]), "=r"(s0[k + 1]) : "r"(src + 16 * D + D / 2 + (c * NB + k) * 4) : "memory");
-                    if ((flags & 1u) || nv < kUnit) {
-                        /* scales of NaN blocks (their codes are zeros) and of tokens that hold nothing */
-#pragma unroll
-                        for (int k = 0; k < NB; ++k) {
-                            s0[k] = drop_nan(s0[k]);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                if (2 * c + (q & 1) + 8 * (q >> 1) >= nv) s0[k] &= ~(0xFFu << (8 * q));
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < NB; ++k) {
-                        /* 2^(e - vref): 0 below 2^-14, at most 2^13 by the choice of vref */
-                        const uint32_t x = s0[k];
-                        s0[k] = __viaddmax_s16x2(__byte_perm(x, 0, 0x4140), add[k], 0u) * 1024u;
-                        s1[k] = __viaddmax_s16x2(__byte_perm(x, 0, 0x4342), add[k], 0u) * 1024u;
-                    }
-                    if (nv < kUnit) { /* with vref < 15 a scale byte of 0 is no zero: the codes of nothing must not count */
-                        uint32_t m0 = 0, m1 = 0;
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            if (2 * c + q < nv) m0 |= 0xFFFFu << (16 * q);
-                            if (2 * c + q + 8 < nv) m1 |= 0xFFFFu << (16 * q);
-                        }
-#pragma unroll
-                        for (int k = 0; k < NB; ++k) s0[k] &= m0, s1[k] &= m1;
-                    }
-#pragma unroll
+                    const bool odd = (flags & 1u) || nv < kUnit;
+#pragma unroll 1
                     for (int i4 = 0; i4 < NB / 2; ++i4) {
-                        const uint32_t ww[4] = {wv[i4].x, wv[i4].y, wv[i4].z, wv[i4].w};
+                        const uint4 wv = lds128(src + 8 * D + i4 * 512 + lane * 16);
+                        uint32_t x[2], v[2], s0[2], s1[2];
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(src + 16 * D + D / 2 + (c * NB + 2 * i4) * 4) : "memory");
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(meta + 16 + 8 * i4) : "memory");
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            if (odd) { /* scales of NaN blocks (their codes are zeros) and of tokens that hold nothing */
+                                x[k] = drop_nan(x[k]);
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    if (2 * c + (q & 1) + 8 * (q >> 1) >= nv) x[k] &= ~(0xFFu << (8 * q));
+                            }
+                            /* 2^(e - vref): 0 below 2^-14, at most 2^13 by the choice of vref */
+                            const uint32_t add = both_halves(15 - (int)v[k]);
+                            s0[k] = __viaddmax_s16x2(__byte_perm(x[k], 0, 0x4140), add, 0u) * 1024u;
+                            s1[k] = __viaddmax_s16x2(__byte_perm(x[k], 0, 0x4342), add, 0u) * 1024u;
+                            if (odd) { /* with vref < 15 a scale byte of 0 is no zero: the codes of nothing must not count */
+#pragma unroll
+                                for (int q = 0; q < 2; ++q) {
+                                    if (2 * c + q >= nv) s0[k] &= ~(0xFFFFu << (16 * q));
+                                    if (2 * c + q + 8 >= nv) s1[k] &= ~(0xFFFFu << (16 * q));
+                                }
+                            }
+                        }
+                        const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) { /* channels 16 (4 i4 + i) .. + 15: block 2 i4 + i / 2 */
-                            const int k = 2 * i4 + i / 2;
                             uint32_t h4[4]; /* byte r + 2 p: channel 8 r + g of them */
                             e2m1x8_f16(ww[i], h4);
                             const uint32_t o = (64 * i4 + 16 * i) * 128;
-                            sts32(at0 + o, half_mul2(h4[0], s0[k]));
-                            sts32(at0 + o + 1024, half_mul2(h4[1], s0[k]));
-                            sts32(at1 + o, half_mul2(h4[2], s1[k]));
-                            sts32(at1 + o + 1024, half_mul2(h4[3], s1[k]));
+                            sts32(at0 + o, half_mul2(h4[0], s0[i / 2]));
+                            sts32(at0 + o + 1024, half_mul2(h4[1], s0[i / 2]));
+                            sts32(at1 + o, half_mul2(h4[2], s1[i / 2]));
+                            sts32(at1 + o + 1024, half_mul2(h4[3], s1[i / 2]));
                         }
                     }
                 }
@@ -751,12 +685,17 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
 #pragma unroll
                 for (int k = 0; k < LANES / NB; ++k) best = max(best, __shfl_sync(kAll, mine, lane % NB + k * NB));
             }
+            const int was = vref;
             if (vref == 0 || best > vref + 13) vref = max(vref, max(best, 1));
+            if (__any_sync(kAll, was != 0 && was != vref)) flags |= 4u;
             if (lane == 0) {
                 sts32(meta, (uint32_t)kref);
                 sts32(meta + 4, flags);
             }
-            if (lane < NB) sts32(meta + 16 + 4 * lane, (uint32_t)vref);
+            if (lane < NB) {
+                sts32(meta + 16 + 4 * lane, (uint32_t)vref);
+                sts32(meta + 48 + 4 * lane, __float_as_uint(was ? ex2((float)(was - vref)) : 1.f));
+            }
             if (flags & 1u) { /* which blocks of which tokens are NaN */
                 for (int i = lane; i < TN; i += 32) {
                     const int v = i >> 4, tk = i & 15;
@@ -765,7 +704,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                         for (int k = 0; k < NB; ++k)
                             if (lds8(raw + v * UB + 16 * D + D / 2 + ((((tk >> 1) & 3) * NB + k) * 2 + (tk >> 3)) * 2 + (tk & 1)) == 255u)
                                 mask |= 1u << k;
-                    asm volatile("st.shared.u8 [%0], %1;" ::"r"(meta + 48 + i), "r"(mask) : "memory");
+                    asm volatile("st.shared.u8 [%0], %1;" ::"r"(meta + 80 + i), "r"(mask) : "memory");
                 }
             }
             __syncwarp();
