@@ -66,6 +66,21 @@ __device__ __forceinline__ void tc_ld32(uint32_t at, uint32_t (&v)[32]) {
         : "r"(at)
         : "memory");
 }
+/* The same with the largest of the 32 columns (FP32), found on the way. */
+__device__ __forceinline__ void tc_ld32_max(uint32_t at, uint32_t (&v)[32], float& mx) {
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]), "=f"(mx)
+        : "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld(float& a, float& b) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(a), "+f"(b)::"memory");
+}
 __device__ __forceinline__ void tc_wait_ld(uint32_t (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
@@ -343,14 +358,26 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             /* (the loops stay rolled: with five roles side by side the instruction cache decides;
              * unrolled they took 2.2 times as long) */
             float mx = -INFINITY;
+            if (all) {
 #pragma unroll 1
-            for (int k = 0; k < TN / 32; ++k) {
-                uint32_t v[32];
-                tc_ld32(s_at + 32 * k, v);
-                tc_wait_ld(v);
-                if (!all) hide(k, v);
+                for (int k = 0; k < TN / 32; k += 2) {
+                    uint32_t va[32], vb[32];
+                    float ma, mb;
+                    tc_ld32_max(s_at + 32 * k, va, ma);
+                    tc_ld32_max(s_at + 32 * k + 32, vb, mb);
+                    tc_wait_ld(ma, mb);
+                    mx = fmaxf(mx, fmaxf(ma, mb));
+                }
+            } else {
+#pragma unroll 1
+                for (int k = 0; k < TN / 32; ++k) {
+                    uint32_t v[32];
+                    tc_ld32(s_at + 32 * k, v);
+                    tc_wait_ld(v);
+                    hide(k, v);
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+                    for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+                }
             }
             mx *= f; /* f > 0 */
             if (__any_sync(kAll, mx > m + kPSlack || (!set && mx > -INFINITY)) || (flags & 4u)) {
