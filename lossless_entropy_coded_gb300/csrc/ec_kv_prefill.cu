@@ -112,17 +112,26 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t at) {
     return (uint64_t)((at >> 4) & 0x3FFFu) | ((uint64_t)1u << 16) | ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1u << 46) |
            ((uint64_t)2u << 61);
 }
-/* One matrix instruction by one elected lane of a converged warp: A from shared or from tensor memory. */
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+/* Four matrix instructions, 16 columns of the operands each, by one elected lane of a
+ * converged warp: A from shared memory, or from tensor memory. */
+__device__ __forceinline__ void tc_mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\tadd.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\tadd.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\tadd.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void tc_mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 y;\n\t.reg .b32 x;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\tadd.s32 x, %1, 8;\n\tadd.s64 y, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n\tadd.s32 x, %1, 16;\n\tadd.s64 y, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n\tadd.s32 x, %1, 24;\n\tadd.s64 y, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
@@ -594,24 +603,30 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             /* kind::f16, FP32 accumulators, FP16 operands, both K-major: N / 8 at bit 17, M / 16 at bit 24 */
             const uint32_t id_s = (1u << 4) | ((uint32_t)(TN / 8) << 17) | (8u << 24), id_o = (1u << 4) | ((uint32_t)(D / 8) << 17) | (8u << 24);
             auto scores = [&](int t, int kb) {
-                const uint32_t qa = q_at + t * QT * H::QBYTES, ka = buf_at + kb * H::BUF;
-#pragma unroll
-                for (int x = 0; x < QT; ++x)
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        tc_mma_ss(tmem + t * TN, sw128_desc(qa + x * H::QBYTES + (k >> 2) * (128 * 128)) + 2 * (k & 3),
-                                  sw128_desc(ka + (k >> 2) * (TN * 128)) + 2 * (k & 3), id_s, x > 0 || k > 0);
+                uint64_t qa = sw128_desc(q_at + t * QT * H::QBYTES);
+#pragma unroll 1
+                for (int x = 0; x < QT; ++x) {
+                    uint64_t ka = sw128_desc(buf_at + kb * H::BUF);
+#pragma unroll 1
+                    for (int k = 0; k < D / 64; ++k) {
+                        tc_mma4_ss(tmem + t * TN, qa, ka, id_s, x + k);
+                        qa += (128 * 128) >> 4;
+                        ka += (TN * 128) >> 4;
+                    }
+                }
             };
-            auto values = [&](int t, int vb, bool acc) {
-                const uint32_t va = buf_at + vb * H::BUF;
-#pragma unroll
-                for (int k = 0; k < TN / 16; ++k)
-                    tc_mma_ts(tmem + H::O_COL + t * D, tmem + t * TN + 8 * k, sw128_desc(va + (k >> 2) * (D * 128)) + 2 * (k & 3), id_o,
-                              acc || k > 0);
+            auto values = [&](int t, int vb, int j) {
+                uint64_t va = sw128_desc(buf_at + vb * H::BUF);
+#pragma unroll 1
+                for (int k = 0; k < TN / 64; ++k) {
+                    tc_mma4_ts(tmem + H::O_COL + t * D, tmem + t * TN + 32 * k, va, id_o, j + k);
+                    va += (D * 128) >> 4;
+                }
             };
             wait(q_full, 0);
             wait(buf_full, 0);
             tc_fence_after();
+#pragma unroll 1
             for (int t = 0; t < NQ; ++t) {
                 scores(t, 0);
                 tc_commit(s_full + 8 * t);
@@ -620,10 +635,11 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             for (int j = 0; j < T; ++j) {
                 const int vn = 2 * j + 1, kn = 2 * j + 2, vb = vn % NBUF, kb = kn % NBUF;
                 wait(buf_full + 8 * vb, (vn / NBUF) & 1);
+#pragma unroll 1
                 for (int t = 0; t < NQ; ++t) {
                     wait(p_full + 8 * t, j & 1);
                     tc_fence_after();
-                    values(t, vb, j > 0);
+                    values(t, vb, j);
                     tc_commit(o_done + 8 * t);
                     if (t == NQ - 1) tc_commit(buf_empty + 8 * vb);
                     if (j + 1 < T) {
