@@ -155,6 +155,23 @@ __device__ __forceinline__ uint32_t half_pack(float lo, float hi) {
     return *(const uint32_t*)&h;
 }
 
+/* (a f + c, b f + c) and acc + (a, b): the two-wide FP32 instructions. */
+__device__ __forceinline__ float2 fma2(uint32_t a, uint32_t b, float f, float c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, d;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %5};\n\t"
+        "fma.rn.f32x2 d, x, y, z;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(a), "r"(b), "f"(f), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 acc, float a, float b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, d;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 d, x, y;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(acc.x), "f"(acc.y), "f"(a), "f"(b));
+    return r;
+}
+
 /* Largest bytes, as two 16-bit halves to be joined by half_max. */
 __device__ __forceinline__ uint32_t bytes_max(uint32_t m, uint32_t w) {
     return __vmaxu2(m, __vmaxu2(w & 0x00FF00FFu, (w >> 8) & 0x00FF00FFu));
@@ -181,7 +198,8 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
     using H = PShape<NB, NQ, QT>;
     constexpr int D = H::D, TN = H::TN, UT = H::UT, UB = H::UB, NBUF = H::NBUF;
     extern __shared__ __align__(1024) uint8_t pf_smem[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    /* (warp-uniform values are taken from lane 0, so that the compiler knows them for such) */
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(kAll, (int)threadIdx.x >> 5, 0), g = lane >> 2, c = lane & 3;
     const uint32_t base = (smem_u32(pf_smem) + 1023u) & ~1023u;
     const uint32_t q_at = base, buf_at = q_at + NQ * QT * H::QBYTES, raw_at = buf_at + NBUF * H::BUF, meta_at = raw_at + H::RS * H::RAW,
                    bars = meta_at + H::MS * H::META;
@@ -214,7 +232,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = lds32(tslot);
+    const uint32_t tmem = __shfl_sync(kAll, lds32(tslot), 0);
     grid_dep_launch();
     grid_dep_wait();
 
@@ -251,7 +269,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             J.u1 = min(J.units, (sp + 1) * per * UT);
         }
     }
-    const int T = (J.u1 - J.u0 + UT - 1) / UT;
+    const int T = __shfl_sync(kAll, (J.u1 - J.u0 + UT - 1) / UT, 0);
     bool live = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (live && !mbar_wait(bar, parity)) {
@@ -413,7 +431,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             }
             /* weights 2^(s - m + kPBias) take the scores' place, behind the reads */
             const float off = kPBias - m;
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            float2 acc = make_float2(0.f, 0.f);
 #pragma unroll 1
             for (int k = 0; k < TN / 32; ++k) {
                 uint32_t v[32], p[16];
@@ -422,14 +440,14 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                 if (!all) hide(k, v);
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
-                    const float p0 = ex2(fmaf(__uint_as_float(v[i]), f, off)), p1 = ex2(fmaf(__uint_as_float(v[i + 1]), f, off));
-                    acc[i & 2] += p0;
-                    acc[(i & 2) + 1] += p1;
+                    const float2 y = fma2(v[i], v[i + 1], f, off);
+                    const float p0 = ex2(y.x), p1 = ex2(y.y);
+                    acc = add2(acc, p0, p1);
                     p[i / 2] = half_pack(p0, p1);
                 }
                 tc_st16(s_at + 16 * k, p);
             }
-            l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+            l += acc.x + acc.y;
             tc_wait_st();
             tc_fence_before();
             if (flags & 1u) { /* tokens with NaN values: their blocks are NaN for the rows that see them */
@@ -647,6 +665,9 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                             wait(buf_full + 8 * kb, (kn / NBUF) & 1);
                             tc_fence_after();
                         }
+                        /* the scores take the weights' place: not before their product is done
+                         * (products of other shapes and accumulators may overtake it) */
+                        wait(o_done + 8 * t, j & 1);
                         scores(t, kb);
                         tc_commit(s_full + 8 * t);
                         if (t == NQ - 1) tc_commit(buf_empty + 8 * kb);
