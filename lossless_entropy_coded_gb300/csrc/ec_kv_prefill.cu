@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
         }
     }
     const int T = __shfl_sync(kAll, (J.u1 - J.u0 + UT - 1) / UT, 0);
+    const int NA = __shfl_sync(kAll, min(NQ, (J.R - J.r0 + 127) / 128), 0); /* row tiles that hold rows */
     bool live = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (live && !mbar_wait(bar, parity)) {
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
         uint32_t nan_blocks = 0;
         const int pos_lo = __shfl_sync(kAll, pos, 0), pos_hi = __shfl_sync(kAll, pos, 31);
 
-        for (int j = 0; j < T; ++j) {
+        for (int j = 0; j < (t < NA ? T : 0); ++j) {
             const uint32_t meta = meta_at + j % H::MS * H::META;
             wait(meta_full + 8 * (j % H::MS), (j / H::MS) & 1);
             wait(s_full + 8 * t, j & 1);
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
         }
 
         /* outputs */
-        if (T > 0) {
+        if (t < NA && T > 0) {
             wait(o_done + 8 * t, (T - 1) & 1);
             tc_fence_after();
         }
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             uint32_t v[32];
             const int vr = T > 0 ? (int)lds32(meta_at + (T - 1) % H::MS * H::META + 16 + 4 * k) : 0;
             const float back = vr > 0 ? __uint_as_float((uint32_t)vr << 23) : 0.f;
-            if (T > 0) {
+            if (t < NA && T > 0) {
                 tc_ld32(o_at + 32 * k, v);
                 tc_wait_ld(v);
             } else {
@@ -645,7 +646,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             wait(buf_full, 0);
             tc_fence_after();
 #pragma unroll 1
-            for (int t = 0; t < NQ; ++t) {
+            for (int t = 0; t < NA; ++t) {
                 scores(t, 0);
                 tc_commit(s_full + 8 * t);
             }
@@ -654,12 +655,12 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                 const int vn = 2 * j + 1, kn = 2 * j + 2, vb = vn % NBUF, kb = kn % NBUF;
                 wait(buf_full + 8 * vb, (vn / NBUF) & 1);
 #pragma unroll 1
-                for (int t = 0; t < NQ; ++t) {
+                for (int t = 0; t < NA; ++t) {
                     wait(p_full + 8 * t, j & 1);
                     tc_fence_after();
                     values(t, vb, j);
                     tc_commit(o_done + 8 * t);
-                    if (t == NQ - 1) tc_commit(buf_empty + 8 * vb);
+                    if (t == NA - 1) tc_commit(buf_empty + 8 * vb);
                     if (j + 1 < T) {
                         if (t == 0) {
                             wait(buf_full + 8 * kb, (kn / NBUF) & 1);
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                         wait(o_done + 8 * t, j & 1);
                         scores(t, kb);
                         tc_commit(s_full + 8 * t);
-                        if (t == NQ - 1) tc_commit(buf_empty + 8 * kb);
+                        if (t == NA - 1) tc_commit(buf_empty + 8 * kb);
                     }
                 }
             }
