@@ -16,7 +16,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 /* Work is counted in units of 16 tokens of one tile (the rows of one key/value head's
  * group, 8 or 16 at a time), plus kTileCost for a tile's queries and outputs. */
-constexpr int kTileCost = 6;
+constexpr int kTileCost = 10;
 
 /* The keys that a sequence's new rows see, in units: the sinks' units, then lo_u ..
  * ceil(len / 16) - 1. */
@@ -35,41 +35,49 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int len, int m) {
 __device__ __forceinline__ int tile_cost(const AttnArgs& a, int units) { return a.solo ? a.solo : units + kTileCost; }
 
 /* Per sequence, in shared memory: pre[b], the work in front of it (pre[n_seqs]: all work),
- * and {len, new tokens, first row, units}.  Every thread of the CTA takes part; one warp
- * scans. */
+ * and {len, new tokens, first row, units}.  Every thread of the CTA takes part. */
+template <int W>
 __device__ __forceinline__ void scan_seqs(const AttnArgs& a, int rows_per_tile, int64_t* pre, int4* info, bool flag) {
-    const int lane = threadIdx.x & 31;
-    if (threadIdx.x < 32) {
-        int64_t at = 0;
-        for (int base = 0; base < a.S.n_seqs; base += 32) {
-            const int b = base + lane;
-            int64_t n = 0;
-            if (b < a.S.n_seqs) {
-                Seq q = seq_of(a.S, a.P.page_shift, b);
-                if (q.len > a.max_len) {
-                    q.len = a.max_len;
-                    q.bad = true;
-                }
-                if (q.m > a.max_new) {
-                    q.m = a.max_new;
-                    q.bad = true;
-                }
-                if (flag && q.bad) flag_corrupt(a.status);
-                const int units = span_of(a, q.len, q.m).units;
-                info[b] = make_int4(q.len, q.m, (int)q.row0, units);
-                n = (int64_t)((q.m * a.group + rows_per_tile - 1) / rows_per_tile) * a.P.n_heads * tile_cost(a, units);
+    __shared__ int64_t warp_sum[W];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t at = 0;
+    for (int base = 0; base < a.S.n_seqs; base += 32 * W) {
+        const int b = base + threadIdx.x;
+        int64_t n = 0;
+        if (b < a.S.n_seqs) {
+            Seq q = seq_of(a.S, a.P.page_shift, b);
+            if (q.len > a.max_len) {
+                q.len = a.max_len;
+                q.bad = true;
             }
-            int64_t x = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(kAll, x, o);
-                if (lane >= o) x += y;
+            if (q.m > a.max_new) {
+                q.m = a.max_new;
+                q.bad = true;
             }
-            if (b < a.S.n_seqs) pre[b] = at + x - n;
-            at += __shfl_sync(kAll, x, 31);
+            if (flag && q.bad) flag_corrupt(a.status);
+            const int units = span_of(a, q.len, q.m).units;
+            info[b] = make_int4(q.len, q.m, (int)q.row0, units);
+            n = (int64_t)((q.m * a.group + rows_per_tile - 1) / rows_per_tile) * a.P.n_heads * tile_cost(a, units);
         }
-        if (lane == 0) pre[a.S.n_seqs] = at;
+        int64_t x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(kAll, x, o);
+            if (lane >= o) x += y;
+        }
+        if (base) __syncthreads(); /* the sums of the sequences before have been read */
+        if (lane == 31) warp_sum[warp] = x;
+        __syncthreads();
+        int64_t front = at;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const int64_t y = warp_sum[w];
+            if (w < warp) front += y;
+            at += y;
+        }
+        if (b < a.S.n_seqs) pre[b] = front + x - n;
     }
+    if (threadIdx.x == 0) pre[a.S.n_seqs] = at;
     __syncthreads();
 }
 
@@ -98,6 +106,11 @@ __device__ __forceinline__ Seg seg_at(const AttnArgs& a, const int64_t* pre, con
     s.r0 = (int)(tile / (uint32_t)a.P.n_heads) * rows_per_tile;
     return s;
 }
+
+/* The tile that begins in a share and ends in a later one. */
+struct JoinJob {
+    int parts, h, r0, R, row0, pad[3];
+};
 
 /* The share of CTA i of n: places i * share .. . */
 __device__ __forceinline__ int64_t share_of(const AttnArgs& a, int64_t X, int n, int warps) {
@@ -142,7 +155,7 @@ struct Shape {
     static constexpr int CTAS = NT == 2 ? 3 : 2;
     static constexpr int S = NB == 2 ? 4 : 2; /* of two units each; a power of two */
     static constexpr int KEEP = RB * LD + 2 * RB;
-    static constexpr int RING = S * 2 * UB, WARP_BYTES = RING + KEEP * 4;
+    static constexpr int RING = S * 2 * UB, WARP_BYTES = RING + KEEP * 4 + 64; /* + the warp's segment */
     static_assert(KEEP * 4 <= RING, "a second partial result fits the ring");
     static constexpr size_t smem(int n_seqs) {
         return (size_t)W * WARP_BYTES + W * S * 8 + 2 * W * 8 + 2 * W * 4 + 16 * (size_t)n_seqs + 8 * ((size_t)n_seqs + 1) + 16;
@@ -178,7 +191,7 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const uint32_t ring = smem_u32(at_smem) + warp * H::WARP_BYTES;
     uint8_t* tail = at_smem + W * H::WARP_BYTES;
-    const uint32_t bars = smem_u32(tail) + warp * S * 8;
+    const uint32_t bars = smem_u32(tail) + warp * S * 8, own = ring + H::RING + H::KEEP * 4;
     int64_t* slot_tile = (int64_t*)(tail + W * S * 8);   /* [2 W]: a warp's first and last partial tile, -1: none */
     int32_t* slot_flags = (int32_t*)(slot_tile + 2 * W); /* bit 0: the tile's first unit is in, bit 1: its last */
     int4* info = (int4*)(slot_flags + 2 * W);
@@ -191,10 +204,12 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
     }
     grid_dep_launch();
     grid_dep_wait();
-    scan_seqs(a, RB, pre, info, blockIdx.x == 0);
+    scan_seqs<W>(a, RB, pre, info, blockIdx.x == 0);
     const int64_t X = pre[a.S.n_seqs];
     const int64_t share = share_of(a, X, gridDim.x, W);
     const int64_t x0 = min(X, blockIdx.x * share), x1 = min(X, x0 + share);
+    JoinJob* todo = (JoinJob*)(a.part + (int64_t)gridDim.x * 2 * RB * (D + 2)) + blockIdx.x;
+    if (!a.solo && threadIdx.x == 0) todo->parts = 0;
     if (x0 >= x1) return;
     int64_t x = min(x1, x0 + warp * (share / W));
     const int64_t x_end = min(x1, x + share / W);
@@ -244,24 +259,30 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
     uint32_t count = 0; /* stages taken from the ring */
     bool live = true;
     while (x < x_end) {
-        /* (a segment's place in the work is looked up again where it is needed after the loop
-         * and at its masked ends, so that the loop need not keep it in registers) */
+        /* (the segment lies in shared memory for its masked ends and for what follows the loop,
+         * so that the loop need not keep it in registers) */
         auto look_up = [&](Seg& sg, int4& f) {
-            asm volatile("" : "+l"(x));
-            sg = seg_at(a, pre, info, RB, x, x_end);
-            f = info[sg.b];
+            const uint4 p = lds128(own), q = lds128(own + 16), r = lds128(own + 32);
+            sg.b = (int)p.x, sg.h = (int)p.y, sg.r0 = (int)p.z, sg.u0 = (int)p.w;
+            sg.u1 = (int)q.x, sg.units = (int)q.y, sg.tile = (int64_t)((uint64_t)q.w << 32 | q.z);
+            f = make_int4((int)r.x, (int)r.y, (int)r.z, (int)r.w);
         };
         int u = 0, u1 = 0, all_lo = 0, all_hi = 0;
         uint32_t qf[NT][QT][NB][4];
         float fac[NT][2];
         {
-            Seg sg;
-            int4 f;
-            look_up(sg, f);
-            if (sg.u0 >= sg.u1) {
-                x = sg.next;
-                continue;
+            const Seg sg = seg_at(a, pre, info, RB, x, x_end);
+            const int4 f = info[sg.b];
+            x = sg.next;
+            if (sg.u0 >= sg.u1) continue;
+            __syncwarp();
+            if (lane == 0) {
+                uint4* o = (uint4*)(at_smem + warp * H::WARP_BYTES + H::RING + H::KEEP * 4);
+                o[0] = make_uint4(sg.b, sg.h, sg.r0, sg.u0);
+                o[1] = make_uint4(sg.u1, sg.units, (uint32_t)sg.tile, (uint32_t)((uint64_t)sg.tile >> 32));
+                o[2] = make_uint4(f.x, f.y, f.z, f.w);
             }
+            __syncwarp();
             const Span sp = span_of(a, f.x, f.y);
             const int h = sg.h, r0 = sg.r0, R = f.y * a.group, first = f.x - f.y;
             u = sg.u0;
@@ -597,7 +618,6 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
         Seg sg;
         int4 f;
         look_up(sg, f);
-        x = sg.next;
         const int h = sg.h, r0 = sg.r0, R = f.y * a.group;
         float back[NB];
 #pragma unroll
@@ -701,6 +721,10 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
         const Seg sg = seg_at(a, pre, info, RB, tile, X);
         const int4 f = info[sg.b];
         const int R = f.y * a.group;
+        if (threadIdx.x == 0 && !whole && (slot_flags[s0] & 1)) { /* the tile begins here: how many shares it covers */
+            todo->parts = (int)((tile + sg.units - 1) / share) - (int)blockIdx.x + 1;
+            todo->h = sg.h, todo->r0 = sg.r0, todo->R = R, todo->row0 = f.z;
+        }
         float* part = a.part + ((int64_t)blockIdx.x * 2 + (slot_flags[s0] & 1)) * (RB * (D + 2));
         for (int e = threadIdx.x; e < RB * (D / 4); e += W * 32) {
             const int r = e / (D / 4), d = 4 * (e % (D / 4));
@@ -729,33 +753,22 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
     }
 }
 
-/* Join the partial results of a tile that several shares cover: CTA i looks at the tile
- * in which share i ends; if it begins there, the CTA adds the shares' parts in order. */
+/* Join the partial results of a tile that several shares cover: CTA i adds, in order, the
+ * parts of the tile that begins in share i and does not end there (if there is one). */
 template <int NB, int NT>
-__global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ AttnArgs a, int grid) {
+__global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ AttnArgs a) {
     using H = Shape<NB, NT>;
     constexpr int D = H::D, RB = H::RB, PS = RB * (D + 2);
-    extern __shared__ __align__(128) uint8_t at_smem[];
-    int4* info = (int4*)at_smem;
-    int64_t* pre = (int64_t*)(info + a.S.n_seqs);
     grid_dep_launch();
     grid_dep_wait();
-    scan_seqs(a, RB, pre, info, false);
-    const int64_t X = pre[a.S.n_seqs];
-    const int64_t share = share_of(a, X, grid, H::W);
-    const int64_t x0 = blockIdx.x * share, x1 = min(X, x0 + share);
-    if (x0 >= x1) return;
-    const Seg sg = seg_at(a, pre, info, RB, x1 - 1, X);
-    const int64_t t1 = sg.tile + sg.units; /* places past the units hold no work */
-    if (sg.tile < x0 || t1 <= x1) return;
-    const int n = (int)((t1 - 1) / share) - (int)blockIdx.x + 1;
-    const int4 f = info[sg.b];
-    const int R = f.y * a.group;
+    const JoinJob job = ((const JoinJob*)(a.part + (int64_t)gridDim.x * 2 * PS))[blockIdx.x];
+    const int n = job.parts;
+    if (n == 0) return;
     const float* p0 = a.part + ((int64_t)blockIdx.x * 2 + 1) * PS;  /* the first share's part */
     const float* p1 = a.part + ((int64_t)blockIdx.x * 2) * PS;      /* share i's: p1 + 2 i PS */
     for (int e = threadIdx.x; e < RB * (D / 4); e += 256) {
         const int r = e / (D / 4), d = 4 * (e % (D / 4));
-        if (sg.r0 + r >= R) continue;
+        if (job.r0 + r >= job.R) continue;
         float M = p0[RB * D + r];
         for (int i = 1; i < n; ++i) M = fmaxf(M, p1[(int64_t)2 * i * PS + RB * D + r]);
         float L = 0.f;
@@ -768,7 +781,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ At
             const float4 y = *(const float4*)&p[r * D + d];
             v.x = fmaf(y.x, w, v.x), v.y = fmaf(y.y, w, v.y), v.z = fmaf(y.z, w, v.z), v.w = fmaf(y.w, w, v.w);
         }
-        write_row(a, f.z, sg.h, sg.r0 + r, d, v, M, L);
+        write_row(a, job.row0, job.h, job.r0 + r, d, v, M, L);
     }
 }
 
@@ -786,7 +799,7 @@ static void plan_shape(Plan* p, int sms, int64_t tiles, int64_t units) {
     /* up to 4 units per warp there is nothing to gain from splitting a tile, and one launch does */
     p->solo = units <= 4 * H::W && tiles < 0x7FFFFFFF ? (int)((units + H::W - 1) / H::W) * H::W : 0;
     p->grid = p->solo ? (int)tiles : sms * H::CTAS;
-    p->work = p->solo ? 0 : (size_t)p->grid * 2 * H::RB * (H::D + 2) * sizeof(float);
+    p->work = p->solo ? 0 : (size_t)p->grid * (2 * H::RB * (H::D + 2) * sizeof(float) + sizeof(JoinJob));
 }
 
 /* Query rows per key/value head up to which the register form runs (it expands the tokens
@@ -828,7 +841,7 @@ static int run_attn(const AttnArgs& a, const Plan& p, cudaStream_t stream) {
     if (rc != EC_OK) return rc;
     rc = launch(kv_attn_kernel<NB, NT, QT>, dim3(p.grid), H::W * 32, H::smem(a.S.n_seqs), stream, a);
     if (rc == EC_OK && !p.solo)
-        rc = launch(kv_join_kernel<NB, NT>, dim3(p.grid), 256, 16 * (size_t)a.S.n_seqs + 8 * ((size_t)a.S.n_seqs + 1), stream, a, p.grid);
+        rc = launch(kv_join_kernel<NB, NT>, dim3(p.grid), 256, 0, stream, a);
     return rc;
 }
 
