@@ -110,43 +110,117 @@ static int check_call(const ec_kv* C, int layer, const ec_kv_seqs* seqs, const i
 }
 
 /* ============================================================ append and read */
-/* One warp owns one unit of 16 tokens of one head: the unit is put together in shared
- * memory (an existing unit that keeps older tokens is brought in first) and written with
- * 16-byte stores, so nothing else writes its bytes and a token's nibbles can share bytes
- * with its neighbour's.  Lane 4 g + c reads channels 32 b + 8 c + 0..7 of tokens g and
- * g + 8: a quad of lanes holds a block, whose largest magnitude takes two shuffles. */
+/* One warp owns the keys, another the values of a unit of 16 tokens of one head, so nothing
+ * else writes its bytes and a token's nibbles can share bytes with its neighbour's.  Lane
+ * 4 g + c takes channels 32 b + 8 c + 0..7 of tokens g and g + 8: a quad of lanes holds a
+ * block, whose largest magnitude takes two shuffles, and the eight codes are one word.
+ *
+ * A word of the keys is a word of the unit: it is stored as it is.  A word of the values
+ * holds 2 channels of 4 tokens; lanes 4 apart (the tokens of a pair) and 1 apart (channels
+ * 8 apart) exchange halves: with own words w0, w1 (tokens g, g + 8)
+ *   pair step     lane with g even keeps channels 0..3 of both tokens, g odd 4..7: a byte
+ *                 per channel, the even token in the low nibble; x[p] for p = 0, 1
+ *   channel step  lane with c even keeps the first two of its four channels, c odd the last
+ *                 two, of both lanes: bytes (r, p) of two words, r = c % 2
+ * which land at words i = 2 b + c / 2 of lanes 4 (4 (g % 2) + k) + g / 2, k = 2 (c % 2), + 1.
+ * Reading runs the same steps backwards.  Bound by HBM: every byte moves once; all loads of
+ * a warp are issued before the first is used. */
 constexpr int kIoWarps = 4;
 
-struct AppendArgs {
+struct IoArgs {
     Pool P;
     Seqs S;
     Rows k, v;
+    int32_t has_k, has_v;
     int32_t units;       /* units that max_new tokens can touch */
     int32_t max_new;
     int* status;
 };
 
-/* 8 consecutive elements of a row */
-__device__ __forceinline__ void load8(const Rows& R, int64_t off, float (&x)[8]) {
+/* Which unit of which head a warp works on. */
+struct UnitJob {
+    int b, h, which, unit, tok0;  /* sequence, head, keys (0) or values (1), unit of the sequence, token of its first place */
+    int u;                        /* unit among those that the call can touch */
+    int64_t row0;                 /* dense row of token tok0 (may lie before the first) */
+    int lo, hi;                   /* places of the unit that the call covers */
+    bool in, any;
+    Seq q;
+};
+
+__device__ __forceinline__ UnitJob unit_job(const IoArgs& a) {
+    UnitJob j;
+    const int64_t item = (int64_t)blockIdx.x * kIoWarps + (threadIdx.x >> 5);
+    j.which = (int)(item & 1);
+    const uint32_t r = (uint32_t)(item >> 1), rh = r / (uint32_t)a.P.n_heads; /* fewer than 2^31 items */
+    j.h = (int)(r - rh * (uint32_t)a.P.n_heads);
+    j.b = (int)(rh / (uint32_t)a.units);
+    j.u = (int)(rh - (uint32_t)j.b * (uint32_t)a.units);
+    j.in = j.b < a.S.n_seqs;
+    j.any = false;
+    if (!j.in) return j;
+    j.q = seq_of(a.S, a.P.page_shift, j.b);
+    if ((j.q.bad || j.q.m > a.max_new) && j.u == 0 && j.h == 0 && (threadIdx.x & 31) == 0) flag_corrupt(a.status);
+    const int first = j.q.len - j.q.m; /* position of the first new token; < 0: rows without a token */
+    const int f = first < 0 ? 0 : first;
+    j.unit = f / kUnit + j.u;
+    j.tok0 = j.unit * kUnit;
+    j.lo = f - j.tok0 > 0 ? f - j.tok0 : 0;
+    j.hi = j.q.len - j.tok0 < kUnit ? j.q.len - j.tok0 : kUnit;
+    j.row0 = j.q.row0 + (j.tok0 - first);
+    j.any = j.hi > j.lo && !(j.which == 0 ? !a.has_k : !a.has_v);
+    return j;
+}
+
+__device__ __forceinline__ int32_t page_at(const IoArgs& a, const UnitJob& j) {
+    return a.S.table[(int64_t)j.b * a.S.table_stride + (j.tok0 >> a.P.page_shift)];
+}
+__device__ __forceinline__ uint8_t* unit_ptr(const IoArgs& a, const UnitJob& j, int32_t page) {
+    if (page < 0 || page >= a.P.n_pages) {
+        if ((threadIdx.x & 31) == 0) flag_corrupt(a.status);
+        return nullptr;
+    }
+    return (uint8_t*)page_ptr(a.P, page, j.h, (j.tok0 & ((1 << a.P.page_shift) - 1)) / kUnit);
+}
+
+/* Eight consecutive elements as they lie in memory: 16-bit types fill the first half. */
+struct Raw8 {
+    uint4 a, b;
+};
+__device__ __forceinline__ Raw8 load_raw(const Rows& R, int64_t off, bool on) {
+    Raw8 r;
+    r.a = r.b = make_uint4(0, 0, 0, 0);
+    if (!on) return r;
     if (R.wide) {
         if (R.dtype == EC_DTYPE_FP32) {
-            const float4 a = *(const float4*)((const float*)R.data + off), b = *(const float4*)((const float*)R.data + off + 4);
-            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-        } else {
-            const uint4 w = *(const uint4*)((const uint16_t*)R.data + off);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            const uint4* p = (const uint4*)((const float*)R.data + off);
+            r.a = p[0];
+            r.b = p[1];
+        } else r.a = *(const uint4*)((const uint16_t*)R.data + off);
+    } else if (R.dtype == EC_DTYPE_FP32) {
+        const uint32_t* p = (const uint32_t*)R.data + off;
+        r.a = make_uint4(p[0], p[1], p[2], p[3]);
+        r.b = make_uint4(p[4], p[5], p[6], p[7]);
+    } else {
+        const uint16_t* p = (const uint16_t*)R.data + off;
+        r.a = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16, p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
+    }
+    return r;
+}
+__device__ __forceinline__ void raw_values(const Raw8& r, int dtype, float (&x)[8]) {
+    const uint32_t u[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+    if (dtype == EC_DTYPE_FP32) {
+        const uint32_t w[4] = {r.b.x, r.b.y, r.b.z, r.b.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float2 f;
-                if (R.dtype == EC_DTYPE_FP16) f = __half22float2(*(const __half2*)&u[i]);
-                else f = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
-                x[2 * i] = f.x;
-                x[2 * i + 1] = f.y;
-            }
+        for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(u[i]), x[4 + i] = __uint_as_float(w[i]);
+    } else if (dtype == EC_DTYPE_FP16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*(const __half2*)&u[i]);
+            x[2 * i] = f.x, x[2 * i + 1] = f.y;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = load_elem(R, off + i);
+        for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(u[i] << 16), x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
     }
 }
 
@@ -167,184 +241,214 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], int& e) {
     return w;
 }
 
-/* Which unit of which head a warp works on. */
-struct UnitJob {
-    int b, h, unit, tok0;  /* sequence, head, unit of the sequence, token of its first place */
-    int64_t row0;          /* dense row of token tok0 (may lie before the first) */
-    int lo, hi;            /* places of the unit that the call covers */
-    bool any;
-    Seq q;
-};
-
-__device__ __forceinline__ UnitJob unit_job(const Pool& P, const Seqs& S, int units, int max_new, int* status) {
-    UnitJob j;
-    const int64_t item = (int64_t)blockIdx.x * kIoWarps + (threadIdx.x >> 5);
-    j.h = (int)(item % P.n_heads);
-    const int64_t r = item / P.n_heads;
-    const int u = (int)(r % units);
-    j.b = (int)(r / units);
-    j.any = false;
-    if (j.b >= S.n_seqs) return j;
-    j.q = seq_of(S, P.page_shift, j.b);
-    if ((j.q.bad || j.q.m > max_new) && u == 0 && j.h == 0 && (threadIdx.x & 31) == 0) flag_corrupt(status);
-    const int first = j.q.len - j.q.m; /* position of the first new token; < 0: rows without a token */
-    const int f = first < 0 ? 0 : first;
-    j.unit = f / kUnit + u;
-    j.tok0 = j.unit * kUnit;
-    j.lo = f - j.tok0 > 0 ? f - j.tok0 : 0;
-    j.hi = j.q.len - j.tok0 < kUnit ? j.q.len - j.tok0 : kUnit;
-    j.row0 = j.q.row0 + (j.tok0 - first);
-    j.any = j.hi > j.lo;
-    return j;
+/* Four nibbles to the low halves of four bytes, and back. */
+__device__ __forceinline__ uint32_t spread4(uint32_t x) {
+    x = (x | x << 8) & 0x00FF00FFu;
+    return (x | x << 4) & 0x0F0F0F0Fu;
+}
+__device__ __forceinline__ uint32_t gather4(uint32_t x) {
+    x = (x | x >> 4) & 0x00FF00FFu;
+    return (x | x >> 8) & 0xFFFFu;
 }
 
-__device__ __forceinline__ uint8_t* unit_ptr(const Pool& P, const Seqs& S, const UnitJob& j, int* status) {
-    const int slot = j.tok0 >> P.page_shift;
-    const int page = S.table[(int64_t)j.b * S.table_stride + slot];
-    if (page < 0 || page >= P.n_pages) {
-        if ((threadIdx.x & 31) == 0) flag_corrupt(status);
-        return nullptr;
-    }
-    return (uint8_t*)page_ptr(P, page, j.h, (j.tok0 & ((1 << P.page_shift) - 1)) / kUnit);
-}
-
-__global__ void __launch_bounds__(kIoWarps * 32) kv_append_kernel(const __grid_constant__ AppendArgs a) {
-    extern __shared__ __align__(16) uint8_t io_smem[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    const int D = a.P.dim, nb = D / 32;
-    uint8_t* buf = io_smem + warp * a.P.unit_bytes;
+template <int NB>
+__global__ void __launch_bounds__(kIoWarps * 32) kv_append_kernel(const __grid_constant__ IoArgs a) {
+    constexpr int D = 32 * NB, SECTION = 8 * D + D / 2; /* a warp's codes and scales */
+    __shared__ __align__(16) uint8_t io_smem[kIoWarps][SECTION];
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    uint8_t* buf = io_smem[threadIdx.x >> 5];
     grid_dep_launch();
     grid_dep_wait();
-    const UnitJob j = unit_job(a.P, a.S, a.units, a.max_new, a.status);
+    const UnitJob j = unit_job(a);
     if (!j.any) return;
-    uint8_t* dst = unit_ptr(a.P, a.S, j, a.status);
+    const int32_t page = page_at(a, j);
+    const Rows& R = j.which ? a.v : a.k;
+    const bool on[2] = {g >= j.lo && g < j.hi, g + 8 >= j.lo && g + 8 < j.hi};
+    Raw8 raw[NB][2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) raw[b][r] = load_raw(R, (j.row0 + g + 8 * r) * R.row + (int64_t)j.h * R.head + 32 * b + 8 * c, on[r]);
+    uint8_t* dst = unit_ptr(a, j, page);
     if (!dst) return;
-    const int n16 = a.P.unit_bytes / 16;
-    if (j.lo > 0 || j.hi < kUnit) {
-        /* older tokens stay; places past the sequence's end are zeros */
-        for (int i = lane; i < n16; i += 32) ((uint4*)buf)[i] = j.lo > 0 ? ((const uint4*)dst)[i] : make_uint4(0, 0, 0, 0);
-    }
-    __syncwarp();
-    for (int b = 0; b < nb; ++b) {
-        /* keys */
+    const bool full = j.lo == 0 && j.hi == kUnit;
+    if (j.which == 0) {
+        uint32_t word[2 * NB];
+        uint8_t es[2][NB];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int t = g + 8 * r;
-            const bool on = t >= j.lo && t < j.hi;
-            float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (on) load8(a.k, (j.row0 + t) * a.k.row + (int64_t)j.h * a.k.head + 32 * b + 8 * c, x);
-            int e;
-            const uint32_t w = quantise8(x, e);
-            if (on) {
-                const int i = 2 * b + r;
-                *(uint32_t*)(buf + (i >> 2) * 512 + lane * 16 + (i & 3) * 4) = w;
-                if (c == 0) buf[16 * D + t * nb + b] = (uint8_t)e;
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float x[8];
+                raw_values(raw[b][r], R.dtype, x);
+                int e;
+                word[2 * b + r] = quantise8(x, e);
+                es[r][b] = (uint8_t)e;
+            }
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) {
+            uint32_t* at = (uint32_t*)(dst + i * 512 + lane * 16);
+            if (full) *(uint4*)at = make_uint4(word[4 * i], word[4 * i + 1], word[4 * i + 2], word[4 * i + 3]);
+            else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (on[k & 1]) at[k] = word[4 * i + k];
             }
         }
-        /* values: a byte holds a channel of tokens 2m and 2m + 1, lanes 4 apart */
+        if (c == 0) { /* a token's scales, two at a time */
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int t = g + 8 * r;
-            const bool on = t >= j.lo && t < j.hi;
-            float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (on) load8(a.v, (j.row0 + t) * a.v.row + (int64_t)j.h * a.v.head + 32 * b + 8 * c, x);
-            int e;
-            const uint32_t own = quantise8(x, e), other = __shfl_xor_sync(kAll, own, 4);
-            const int p = r, cc = (t >> 1) & 3; /* the pair's place: token 8 p + 2 cc (+1) */
-            if (on && c == 0) buf[16 * D + D / 2 + ((cc * nb + b) * 2 + p) * 2 + (t & 1)] = (uint8_t)e;
-            /* the even token's lane writes channels 0..3 of the eight, the odd one's 4..7 */
-            const bool odd = g & 1;
-            const bool on_even = (t & ~1) >= j.lo && (t & ~1) < j.hi, on_odd = (t | 1) >= j.lo && (t | 1) < j.hi;
-            const uint32_t ev = (odd ? other : own) >> (odd ? 16 : 0), od = (odd ? own : other) >> (odd ? 16 : 0);
+            for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int d = 32 * b + 8 * c + (odd ? 4 : 0) + k; /* channel */
-                const int i = d >> 4;
-                uint8_t* at = buf + 8 * D + (i >> 2) * 512 + ((d & 7) * 4 + cc) * 16 + (i & 3) * 4 + ((d >> 3) & 1) + 2 * p;
-                const uint32_t lo = (ev >> (4 * k)) & 15u, hi = (od >> (4 * k)) & 15u;
-                if (on_even && on_odd) *at = (uint8_t)(lo | hi << 4);
-                else if (on_even) *at = (uint8_t)((*at & 0xF0u) | lo);
-                else if (on_odd) *at = (uint8_t)((*at & 0x0Fu) | hi << 4);
+                for (int b = 0; b < NB; b += 2)
+                    if (on[r]) *(uint16_t*)(dst + 16 * D + (g + 8 * r) * NB + b) = (uint16_t)(es[r][b] | es[r][b + 1] << 8);
+        }
+    } else {
+        uint8_t* codes = dst + 8 * D;
+        uint8_t* scales = dst + 16 * D + D / 2;
+        if (j.lo > 0) { /* older tokens stay */
+            for (int i = lane; i < 8 * D / 16; i += 32) ((uint4*)buf)[i] = ((const uint4*)codes)[i];
+            for (int i = lane; i < D / 2 / 16; i += 32) ((uint4*)(buf + 8 * D))[i] = ((const uint4*)scales)[i];
+            __syncwarp();
+        }
+        /* nibbles of the pair's places that are written: tokens 2 m, 2 m + 1, + 8 of pair m = g / 2 */
+        const int m = g >> 1;
+        uint32_t mask = 0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int tok = 2 * m + (t & 1) + 8 * (t >> 1);
+            if (tok >= j.lo && tok < j.hi) mask |= (t & 1 ? 0xF0F0u : 0x0F0Fu) << (16 * (t >> 1));
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            uint32_t w[2], x[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float y[8];
+                raw_values(raw[b][r], R.dtype, y);
+                int e;
+                w[r] = quantise8(y, e);
+                if (c == 0 && on[r]) buf[8 * D + ((m * NB + b) * 2 + r) * 2 + (g & 1)] = (uint8_t)e;
+                /* pair step */
+                const uint32_t other = __shfl_xor_sync(kAll, w[r], 4), sh = g & 1 ? 16 : 0;
+                const uint32_t ev = ((g & 1 ? other : w[r]) >> sh) & 0xFFFFu, od = ((g & 1 ? w[r] : other) >> sh) & 0xFFFFu;
+                x[r] = spread4(ev) | spread4(od) << 4;
+            }
+            /* channel step: word k = bytes (r 0, p 0), (r 1, p 0), (r 0, p 1), (r 1, p 1) of channel k */
+            const uint32_t y0 = __shfl_xor_sync(kAll, x[0], 1), y1 = __shfl_xor_sync(kAll, x[1], 1);
+            const uint32_t a0 = c & 1 ? y0 : x[0], b0 = c & 1 ? x[0] : y0, a1 = c & 1 ? y1 : x[1], b1 = c & 1 ? x[1] : y1;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int ch = 2 * (c & 1) + k;
+                const uint32_t sel = (uint32_t)ch | (uint32_t)(4 + ch) << 4;
+                const uint32_t lo = __byte_perm(a0, b0, sel), hi = __byte_perm(a1, b1, sel);
+                const uint32_t word = __byte_perm(lo, hi, 0x5410);
+                const int i = 2 * b + (c >> 1);
+                uint32_t* at = (uint32_t*)(buf + (i >> 2) * 512 + ((4 * (g & 1) + ch) * 4 + m) * 16 + (i & 3) * 4);
+                *at = full ? word : ((j.lo > 0 ? *at : 0u) & ~mask) | (word & mask);
+            }
+        }
+        __syncwarp();
+        for (int i = lane; i < 8 * D / 16; i += 32) ((uint4*)codes)[i] = ((const uint4*)buf)[i];
+        if (full || j.lo > 0) {
+            for (int i = lane; i < D / 2 / 16; i += 32) ((uint4*)scales)[i] = ((const uint4*)(buf + 8 * D))[i];
+        } else { /* a new unit with places left: bytes of its tokens only */
+            for (int i = lane; i < D / 2; i += 32) {
+                const int tok = 2 * (i / (4 * NB)) + (i & 1) + 8 * ((i >> 1) & 1);
+                if (tok < j.hi) scales[i] = buf[8 * D + i];
             }
         }
     }
-    __syncwarp();
-    for (int i = lane; i < n16; i += 32) ((uint4*)dst)[i] = ((const uint4*)buf)[i];
-}
-
-struct ReadArgs {
-    Pool P;
-    Seqs S;
-    Rows k, v;
-    int32_t has_k, has_v;
-    int32_t units, max_new;
-    int* status;
-};
-
-__device__ __forceinline__ float nib_value(uint32_t code, float s) {
-    const __half2 h = [&] {
-        const uint32_t r = e2m1x2_f16x2(code & 15u);
-        return *(const __half2*)&r;
-    }();
-    return __low2float(h) * s;
 }
 
 /* 2^(e - 127), NaN for 255 (e = 0: blocks of zeros). */
 __device__ __forceinline__ float scale_value(int e) {
     return e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)e << 23);
 }
+__device__ __forceinline__ void word_values(uint32_t w, float s, float (&x)[8]) {
+    uint32_t h[4];
+    e2m1x8_f16(w, h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*(const __half2*)&h[i]);
+        x[2 * i] = f.x * s, x[2 * i + 1] = f.y * s;
+    }
+}
 
-__global__ void __launch_bounds__(kIoWarps * 32) kv_read_kernel(const __grid_constant__ ReadArgs a) {
-    extern __shared__ __align__(16) uint8_t io_smem[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    const int D = a.P.dim, nb = D / 32;
-    uint8_t* buf = io_smem + warp * a.P.unit_bytes;
+template <int NB>
+__global__ void __launch_bounds__(kIoWarps * 32) kv_read_kernel(const __grid_constant__ IoArgs a) {
+    constexpr int D = 32 * NB;
+    __shared__ __align__(16) uint8_t io_smem[kIoWarps][8 * D];
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    uint8_t* buf = io_smem[threadIdx.x >> 5];
     grid_dep_launch();
     grid_dep_wait();
-    UnitJob j = unit_job(a.P, a.S, a.units, a.max_new, a.status);
-    const int64_t item = (int64_t)blockIdx.x * kIoWarps + warp;
-    const int u = (int)(item / a.P.n_heads % a.units);
-    if (j.b < a.S.n_seqs) {
-        /* rows of tokens before the sequence's first: zeros, 16 at a time */
-        const int none = j.q.m - j.q.len;
+    const UnitJob j = unit_job(a);
+    if (!j.in) return;
+    const Rows& R = j.which ? a.v : a.k;
+    const int none = j.q.m - j.q.len;
+    if (none > 0 && (j.which ? a.has_v : a.has_k)) { /* rows of tokens before the sequence's first: zeros, 16 at a time */
         const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int r0 = u * kUnit; r0 < none; r0 += a.units * kUnit)
+        for (int r0 = j.u * kUnit; r0 < none; r0 += a.units * kUnit)
             for (int r = r0; r < min(none, r0 + kUnit); ++r)
-                for (int d = 8 * lane; d < D; d += 256) {
-                    if (a.has_k) store8(a.k, (j.q.row0 + r) * a.k.row + (int64_t)j.h * a.k.head + d, z);
-                    if (a.has_v) store8(a.v, (j.q.row0 + r) * a.v.row + (int64_t)j.h * a.v.head + d, z);
-                }
+                for (int d = 8 * lane; d < D; d += 256) store8(R, (j.q.row0 + r) * R.row + (int64_t)j.h * R.head + d, z);
     }
     if (!j.any) return;
-    const uint8_t* src = unit_ptr(a.P, a.S, j, a.status);
+    const uint8_t* src = unit_ptr(a, j, page_at(a, j));
     if (!src) return;
-    for (int i = lane; i < a.P.unit_bytes / 16; i += 32) ((uint4*)buf)[i] = ((const uint4*)src)[i];
-    __syncwarp();
-    for (int b = 0; b < nb; ++b)
+    const bool on[2] = {g >= j.lo && g < j.hi, g + 8 >= j.lo && g + 8 < j.hi};
+    uint32_t word[2][NB]; /* channels 32 b + 8 c + 0..7 of tokens g, g + 8 */
+    uint32_t es[2][NB];
+    uint4 w[NB / 2];
+#pragma unroll
+    for (int i = 0; i < NB / 2; ++i) w[i] = *(const uint4*)(src + (j.which ? 8 * D : 0) + i * 512 + lane * 16);
+    if (j.which == 0) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) es[r][b] = src[16 * D + (g + 8 * r) * NB + b];
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) {
+            word[0][2 * i] = w[i].x, word[1][2 * i] = w[i].y;
+            word[0][2 * i + 1] = w[i].z, word[1][2 * i + 1] = w[i].w;
+        }
+    } else {
+        const int m = g >> 1;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) es[r][b] = src[16 * D + D / 2 + ((m * NB + b) * 2 + r) * 2 + (g & 1)];
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) *(uint4*)(buf + i * 512 + lane * 16) = w[i];
+        __syncwarp();
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int i = 2 * b + (c >> 1);
+            uint32_t v[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                v[k] = *(const uint32_t*)(buf + (i >> 2) * 512 + ((4 * (g & 1) + 2 * (c & 1) + k) * 4 + m) * 16 + (i & 3) * 4);
+            /* channel step: bytes (p 0 of channels k, k + 1 | p 1 of them) of r = c % 2, and of the other r for lane c ^ 1 */
+            const uint32_t mine = __byte_perm(v[0], v[1], c & 1 ? 0x7351 : 0x6240), theirs = __byte_perm(v[0], v[1], c & 1 ? 0x6240 : 0x7351);
+            const uint32_t got = __shfl_xor_sync(kAll, theirs, 1);
+            const uint32_t first = c & 1 ? got : mine, second = c & 1 ? mine : got; /* channels 0, 1 and 2, 3 of the four */
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint32_t x = __byte_perm(first, second, r ? 0x7632 : 0x5410);
+                /* pair step: low nibbles are the even token's */
+                const uint32_t ev = gather4(x & 0x0F0F0F0Fu), od = gather4((x >> 4) & 0x0F0F0F0Fu);
+                const uint32_t other = __shfl_xor_sync(kAll, g & 1 ? ev : od, 4);
+                word[r][b] = g & 1 ? other | od << 16 : ev | other << 16;
+            }
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const int t = g + 8 * r;
-            if (t < j.lo || t >= j.hi) continue;
+            if (!on[r]) continue;
             float x[8];
-            if (a.has_k) {
-                const int i = 2 * b + r;
-                const uint32_t w = *(const uint32_t*)(buf + (i >> 2) * 512 + lane * 16 + (i & 3) * 4);
-                const float s = scale_value(buf[16 * D + t * nb + b]);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] = nib_value(w >> (4 * k), s);
-                store8(a.k, (j.row0 + t) * a.k.row + (int64_t)j.h * a.k.head + 32 * b + 8 * c, x);
-            }
-            if (a.has_v) {
-                const int cc = (t >> 1) & 3;
-                const float s = scale_value(buf[16 * D + D / 2 + ((cc * nb + b) * 2 + r) * 2 + (t & 1)]);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int d = 32 * b + 8 * c + k, i = d >> 4;
-                    const uint32_t y = buf[8 * D + (i >> 2) * 512 + ((d & 7) * 4 + cc) * 16 + (i & 3) * 4 + ((d >> 3) & 1) + 2 * r];
-                    x[k] = nib_value(y >> (4 * (t & 1)), s);
-                }
-                store8(a.v, (j.row0 + t) * a.v.row + (int64_t)j.h * a.v.head + 32 * b + 8 * c, x);
-            }
+            word_values(word[r][b], scale_value((int)es[r][b]), x);
+            store8(R, (j.row0 + g + 8 * r) * R.row + (int64_t)j.h * R.head + 32 * b + 8 * c, x);
         }
 }
 
@@ -708,9 +812,19 @@ extern "C" int ec_kv_create(const ec_kv_params* params, void* pool, size_t pool_
 
 extern "C" void ec_kv_free(ec_kv* C) { delete C; }
 
+template <class Kernel>
+static int run_io(const ec_kv* C, const ec_kv_tokens* t, IoArgs& a, Kernel k2, Kernel k4, Kernel k6, Kernel k8, cudaStream_t stream) {
+    a.units = units_of(t->max_new);
+    a.max_new = t->max_new;
+    const int64_t items = (int64_t)a.S.n_seqs * a.units * a.P.n_heads * 2, grid = (items + kIoWarps - 1) / kIoWarps;
+    if (items > 0x7FFFFFFF) return EC_ERR_UNSUPPORTED;
+    const int nb = C->p.head_dim / 32;
+    return launch(nb == 2 ? k2 : nb == 4 ? k4 : nb == 6 ? k6 : k8, dim3((unsigned)grid), kIoWarps * 32, 0, stream, a);
+}
+
 extern "C" int ec_kv_append(const ec_kv* C, const ec_kv_tokens* t, cudaStream_t stream) {
     if (!C || !t) return EC_ERR_INVALID_ARG;
-    AppendArgs a{};
+    IoArgs a{};
     bool go = false;
     int rc = check_call(C, t->layer, &t->seqs, t->starts, t->n_rows, t->max_new, &a.P, &a.S, &go);
     if (rc == EC_OK) rc = check_rows(&t->k, a.P.n_heads, t->n_rows, &a.k);
@@ -719,17 +833,14 @@ extern "C" int ec_kv_append(const ec_kv* C, const ec_kv_tokens* t, cudaStream_t 
     Device d;
     if ((rc = device_of(C, &d)) != EC_OK) return rc;
     if (!go) return EC_OK;
-    a.units = units_of(t->max_new);
-    a.max_new = t->max_new;
+    a.has_k = a.has_v = 1;
     a.status = d.status;
-    const int64_t items = (int64_t)a.S.n_seqs * a.units * a.P.n_heads, grid = (items + kIoWarps - 1) / kIoWarps;
-    if (grid > 0x7FFFFFFF) return EC_ERR_UNSUPPORTED;
-    return launch(kv_append_kernel, dim3((unsigned)grid), kIoWarps * 32, (size_t)kIoWarps * a.P.unit_bytes, stream, a);
+    return run_io(C, t, a, kv_append_kernel<2>, kv_append_kernel<4>, kv_append_kernel<6>, kv_append_kernel<8>, stream);
 }
 
 extern "C" int ec_kv_read(const ec_kv* C, const ec_kv_tokens* t, cudaStream_t stream) {
     if (!C || !t) return EC_ERR_INVALID_ARG;
-    ReadArgs a{};
+    IoArgs a{};
     bool go = false;
     int rc = check_call(C, t->layer, &t->seqs, t->starts, t->n_rows, t->max_new, &a.P, &a.S, &go);
     a.has_k = t->k.data != nullptr;
@@ -741,12 +852,8 @@ extern "C" int ec_kv_read(const ec_kv* C, const ec_kv_tokens* t, cudaStream_t st
     Device d;
     if ((rc = device_of(C, &d)) != EC_OK) return rc;
     if (!go) return EC_OK;
-    a.units = units_of(t->max_new);
-    a.max_new = t->max_new;
     a.status = d.status;
-    const int64_t items = (int64_t)a.S.n_seqs * a.units * a.P.n_heads, grid = (items + kIoWarps - 1) / kIoWarps;
-    if (grid > 0x7FFFFFFF) return EC_ERR_UNSUPPORTED;
-    return launch(kv_read_kernel, dim3((unsigned)grid), kIoWarps * 32, (size_t)kIoWarps * a.P.unit_bytes, stream, a);
+    return run_io(C, t, a, kv_read_kernel<2>, kv_read_kernel<4>, kv_read_kernel<6>, kv_read_kernel<8>, stream);
 }
 
 extern "C" int ec_kv_pages_work_bytes(const ec_kv* C, int n_from, int n_to, size_t* bytes) {
