@@ -182,45 +182,52 @@ __device__ __forceinline__ uint8_t* unit_ptr(const IoArgs& a, const UnitJob& j, 
     return (uint8_t*)page_ptr(a.P, page, j.h, (j.tok0 & ((1 << a.P.page_shift) - 1)) / kUnit);
 }
 
-/* Eight consecutive elements as they lie in memory: 16-bit types fill the first half. */
+/* Eight consecutive elements as they lie in memory. */
+template <bool F32>
 struct Raw8 {
-    uint4 a, b;
+    uint32_t w[F32 ? 8 : 4];
 };
-__device__ __forceinline__ Raw8 load_raw(const Rows& R, int64_t off, bool on) {
-    Raw8 r;
-    r.a = r.b = make_uint4(0, 0, 0, 0);
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load_raw(const Rows& R, int64_t off, bool on) {
+    Raw8<F32> r;
+#pragma unroll
+    for (int i = 0; i < (F32 ? 8 : 4); ++i) r.w[i] = 0;
     if (!on) return r;
-    if (R.wide) {
-        if (R.dtype == EC_DTYPE_FP32) {
-            const uint4* p = (const uint4*)((const float*)R.data + off);
-            r.a = p[0];
-            r.b = p[1];
-        } else r.a = *(const uint4*)((const uint16_t*)R.data + off);
-    } else if (R.dtype == EC_DTYPE_FP32) {
+    if constexpr (F32) {
         const uint32_t* p = (const uint32_t*)R.data + off;
-        r.a = make_uint4(p[0], p[1], p[2], p[3]);
-        r.b = make_uint4(p[4], p[5], p[6], p[7]);
+        if (R.wide) {
+            const uint4 x = *(const uint4*)p, y = *(const uint4*)(p + 4);
+            r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w, r.w[4] = y.x, r.w[5] = y.y, r.w[6] = y.z, r.w[7] = y.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r.w[i] = p[i];
+        }
     } else {
         const uint16_t* p = (const uint16_t*)R.data + off;
-        r.a = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16, p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
+        if (R.wide) {
+            const uint4 x = *(const uint4*)p;
+            r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r.w[i] = p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
+        }
     }
     return r;
 }
-__device__ __forceinline__ void raw_values(const Raw8& r, int dtype, float (&x)[8]) {
-    const uint32_t u[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
-    if (dtype == EC_DTYPE_FP32) {
-        const uint32_t w[4] = {r.b.x, r.b.y, r.b.z, r.b.w};
+template <bool F32>
+__device__ __forceinline__ void raw_values(const Raw8<F32>& r, int dtype, float (&x)[8]) {
+    if constexpr (F32) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(u[i]), x[4 + i] = __uint_as_float(w[i]);
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r.w[i]);
     } else if (dtype == EC_DTYPE_FP16) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*(const __half2*)&u[i]);
+            const float2 f = __half22float2(*(const __half2*)&r.w[i]);
             x[2 * i] = f.x, x[2 * i + 1] = f.y;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(u[i] << 16), x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(r.w[i] << 16), x[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
     }
 }
 
@@ -251,7 +258,7 @@ __device__ __forceinline__ uint32_t gather4(uint32_t x) {
     return (x | x >> 8) & 0xFFFFu;
 }
 
-template <int NB>
+template <int NB, bool F32>
 __global__ void __launch_bounds__(kIoWarps * 32) kv_append_kernel(const __grid_constant__ IoArgs a) {
     constexpr int D = 32 * NB, SECTION = 8 * D + D / 2; /* a warp's codes and scales */
     __shared__ __align__(16) uint8_t io_smem[kIoWarps][SECTION];
@@ -264,11 +271,11 @@ __global__ void __launch_bounds__(kIoWarps * 32) kv_append_kernel(const __grid_c
     const int32_t page = page_at(a, j);
     const Rows& R = j.which ? a.v : a.k;
     const bool on[2] = {g >= j.lo && g < j.hi, g + 8 >= j.lo && g + 8 < j.hi};
-    Raw8 raw[NB][2];
+    Raw8<F32> raw[NB][2];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) raw[b][r] = load_raw(R, (j.row0 + g + 8 * r) * R.row + (int64_t)j.h * R.head + 32 * b + 8 * c, on[r]);
+        for (int r = 0; r < 2; ++r) raw[b][r] = load_raw<F32>(R, (j.row0 + g + 8 * r) * R.row + (int64_t)j.h * R.head + 32 * b + 8 * c, on[r]);
     uint8_t* dst = unit_ptr(a, j, page);
     if (!dst) return;
     const bool full = j.lo == 0 && j.hi == kUnit;
@@ -458,7 +465,11 @@ static int units_of(int n) { return (n + 14) / kUnit + 1; }
 /* ============================================================ page operations */
 /* What a plan leaves in `work` for the copy kernel: the number of copies, then
  * (source page, destination page, units per head) triples.  A fork has at most one copy
- * per sequence, a compaction at most n_pages / 2. */
+ * per sequence, a compaction at most n_pages / 2.
+ *
+ * A plan is one CTA: the work is a few passes over small integer arrays with a barrier
+ * between them, bound by the latency of each pass; up to kSmallPool pages the counts are
+ * kept in shared memory, above that in refs_out itself. */
 struct PlanArgs {
     Pool P;
     const int32_t *table, *lens, *refs, *parents, *grow;
@@ -467,30 +478,31 @@ struct PlanArgs {
     int32_t n_in, n_out;
     int32_t* count;     /* [1] */
     int32_t* copies;    /* [.][3] */
-    int32_t *first;     /* [n_in] lowest child, or n_out */
-    int32_t *kept, *need, *begin; /* [n_out] pages shared, pages in all, first new page's rank */
     int* status;
 };
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024; /* one sequence each: EC_KV_MAX_SEQS */
+constexpr int kSmallPool = 24576;  /* 96 KB of counts */
+static_assert(EC_KV_MAX_SEQS <= kPlanThreads, "one thread per sequence");
 
 /* Exclusive scan of one value per thread over the CTA; *total gets the sum. */
-__device__ __forceinline__ int block_scan(int v, int* total, int* tmp /* [33] */) {
+template <class T>
+__device__ __forceinline__ T block_scan(T v, T* total, T* tmp /* [33] */) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
+    T x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(kAll, x, o);
+        const T y = __shfl_up_sync(kAll, x, o);
         if (lane >= o) x += y;
     }
     __syncthreads();
     if (lane == 31) tmp[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        int y = tmp[lane];
+        T y = tmp[lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int z = __shfl_up_sync(kAll, y, o);
+            const T z = __shfl_up_sync(kAll, y, o);
             if (lane >= o) y += z;
         }
         tmp[lane] = y;
@@ -502,173 +514,149 @@ __device__ __forceinline__ int block_scan(int v, int* total, int* tmp /* [33] */
 }
 
 __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const __grid_constant__ PlanArgs a) {
-    __shared__ int tmp[33];
-    __shared__ int free_total, n_copies;
-    const int tid = threadIdx.x, T = 1 << a.P.page_shift;
-    const int64_t in_cap = a.in_stride << a.P.page_shift;
+    extern __shared__ __align__(16) int32_t plan_smem[];
+    __shared__ int64_t tmp[33];
+    __shared__ int n_copies;
+    __shared__ int32_t first[EC_KV_MAX_SEQS], len_of[EC_KV_MAX_SEQS], kept_of[EC_KV_MAX_SEQS], need_of[EC_KV_MAX_SEQS],
+        parent_of[EC_KV_MAX_SEQS];
+    __shared__ int64_t begin_of[EC_KV_MAX_SEQS];
+    const int tid = threadIdx.x, lane = tid & 31, shift = a.P.page_shift, T = 1 << shift, N = a.P.n_pages;
+    const int64_t in_cap = a.in_stride << shift;
+    int32_t* cnt = N <= kSmallPool ? plan_smem : a.refs_out;
     grid_dep_launch();
     grid_dep_wait();
-    for (int i = tid; i < a.P.n_pages; i += kPlanThreads) a.refs_out[i] = a.refs[i];
-    for (int i = tid; i < a.n_in; i += kPlanThreads) a.first[i] = a.n_out;
+    for (int i = tid; i < N; i += kPlanThreads) cnt[i] = a.refs[i];
+    int parent = -1;
+    int64_t more = 0;
+    if (tid < a.n_in) {
+        const int64_t n = a.lens[tid];
+        len_of[tid] = (int)(n < 0 ? 0 : n > in_cap ? in_cap : n);
+        first[tid] = a.n_out;
+    }
+    if (tid < a.n_out) {
+        const int p = a.parents ? a.parents[tid] : tid;
+        if (p < -1 || p >= a.n_in) flag_corrupt(a.status);
+        else parent = p;
+        more = a.grow ? max(a.grow[tid], 0) : 0;
+        parent_of[tid] = parent;
+    }
     if (tid == 0) n_copies = 0;
     __syncthreads();
-    auto len_in = [&](int s) {
-        const int64_t n = a.lens[s];
-        return (int)(n < 0 ? 0 : n > in_cap ? in_cap : n);
-    };
-    auto parent_of = [&](int i) {
-        const int p = a.parents ? a.parents[i] : i;
-        return p < 0 || p >= a.n_in ? -1 : p;
-    };
+    if (parent >= 0) atomicMin(&first[parent], tid);
+    __syncthreads();
     auto page_in = [&](int s, int k) {
         const int p = a.table[(int64_t)s * a.in_stride + k];
-        return p < 0 || p >= a.P.n_pages ? -1 : p;
+        return p < 0 || p >= N ? -1 : p;
     };
-    for (int i = tid; i < a.n_out; i += kPlanThreads) {
-        const int p = parent_of(i);
-        if (p >= 0) atomicMin(&a.first[p], i);
-        else if (a.parents && (a.parents[i] < -1 || a.parents[i] >= a.n_in)) flag_corrupt(a.status);
+    /* pages shared (kept) and wanted */
+    int kept = 0, need = 0;
+    int64_t want = 0, now = 0;
+    if (parent >= 0) {
+        const int len = len_of[parent];
+        now = len + more;
+        kept = (len >> shift) + ((len & (T - 1)) && first[parent] == tid ? 1 : 0);
+        const int64_t n = (now + T - 1) >> shift;
+        need = n > a.out_stride || now > 0x7FFFFFFF ? -1 : (int)n;
+        want = need < 0 ? 0 : need - kept;
     }
-    __syncthreads();
-    /* pages shared and wanted */
-    int at = 0;
-    for (int base = 0; base < a.n_out; base += kPlanThreads) {
-        const int i = base + tid;
-        int want = 0;
-        if (i < a.n_out) {
-            const int p = parent_of(i);
-            int kept = 0, need = 0;
-            if (p >= 0) {
-                const int len = len_in(p);
-                const int64_t g = a.grow ? max(a.grow[i], 0) : 0;
-                const int64_t now = len + g;
-                kept = len / T + (len % T && a.first[p] == i ? 1 : 0);
-                const int64_t n = (now + T - 1) / T;
-                need = n > a.out_stride || now > 0x7FFFFFFF ? -1 : (int)n;
-                want = need < 0 ? 0 : need - kept;
-            }
-            a.kept[i] = kept;
-            a.need[i] = need;
-        }
-        int total;
-        const int x = block_scan(want, &total, tmp);
-        if (i < a.n_out) a.begin[i] = at + x;
-        at += total;
-    }
+    int64_t wanted;
+    const int64_t begin = block_scan(want, &wanted, tmp);
+    if (tid < a.n_out) kept_of[tid] = kept, need_of[tid] = need, begin_of[tid] = begin;
     __syncthreads();
     /* reference counts: sequences without a child give their pages up; children past the
      * first add theirs (a first child takes its parent's place in every count) */
     for (int s = tid >> 5; s < a.n_in; s += kPlanThreads / 32)
-        if (a.first[s] == a.n_out)
-            for (int k = tid & 31; k < (len_in(s) + T - 1) / T; k += 32) {
+        if (first[s] == a.n_out)
+            for (int k = lane; k < (len_of[s] + T - 1) >> shift; k += 32) {
                 const int p = page_in(s, k);
-                if (p >= 0) atomicSub(&a.refs_out[p], 1);
+                if (p >= 0) atomicSub(&cnt[p], 1);
                 else flag_corrupt(a.status);
             }
     for (int i = tid >> 5; i < a.n_out; i += kPlanThreads / 32) {
-        const int s = parent_of(i);
-        if (s < 0) continue;
-        for (int k = tid & 31; k < a.kept[i]; k += 32) {
+        const int s = parent_of[i];
+        if (s < 0 || first[s] == i) continue;
+        for (int k = lane; k < kept_of[i]; k += 32) {
             const int p = page_in(s, k);
             if (p < 0) flag_corrupt(a.status);
-            else if (a.first[s] != i) atomicAdd(&a.refs_out[p], 1);
+            else atomicAdd(&cnt[p], 1);
         }
     }
     __syncthreads();
-    /* how many pages are free; which sequences fit */
-    int mine = 0;
-    for (int i = tid; i < a.P.n_pages; i += kPlanThreads) mine += a.refs_out[i] == 0;
-    {
-        int total;
-        block_scan(mine, &total, tmp);
-        if (tid == 0) free_total = total;
-    }
-    __syncthreads();
-    const int F = free_total;
-    auto fits = [&](int i) { return a.need[i] >= 0 && (a.need[i] == a.kept[i] || a.begin[i] + (a.need[i] - a.kept[i]) <= F); };
-    /* the free pages in ascending order go to the ranks begin[i] .. */
-    int rank0 = 0;
-    for (int base = 0; base < a.P.n_pages && rank0 < at; base += kPlanThreads) {
-        const int page = base + tid;
-        const int is = page < a.P.n_pages && a.refs_out[page] == 0 ? 1 : 0;
-        int total;
-        const int r = rank0 + block_scan(is, &total, tmp);
-        if (is && r < at) {
-            int lo = 0, hi = a.n_out - 1; /* the last sequence that begins at r or before and wants something */
+    /* the free pages in ascending order go to the ranks begin .. ; a thread looks at a run of pages */
+    const int run = (N + kPlanThreads - 1) / kPlanThreads, p0 = min(N, tid * run), p1 = min(N, p0 + run);
+    int64_t mine = 0, F;
+    for (int p = p0; p < p1; ++p) mine += cnt[p] == 0;
+    int64_t rank = block_scan(mine, &F, tmp);
+    auto fits = [&](int i) { return need_of[i] >= 0 && (need_of[i] == kept_of[i] || begin_of[i] + (need_of[i] - kept_of[i]) <= F); };
+    if (mine)
+        for (int p = p0; p < p1 && rank < wanted; ++p) {
+            if (cnt[p] != 0) continue;
+            int lo = 0, hi = a.n_out - 1; /* the last sequence that begins at the rank or before (those that want nothing come before it) */
             while (lo < hi) {
                 const int mid = (lo + hi + 1) / 2;
-                if (a.begin[mid] <= r) lo = mid;
+                if (begin_of[mid] <= rank) lo = mid;
                 else hi = mid - 1;
             }
             if (fits(lo)) {
-                a.table_out[(int64_t)lo * a.out_stride + a.kept[lo] + (r - a.begin[lo])] = page;
-                a.refs_out[page] = 1;
+                a.table_out[(int64_t)lo * a.out_stride + kept_of[lo] + (int)(rank - begin_of[lo])] = p;
+                cnt[p] = 1;
             }
+            ++rank;
         }
-        rank0 += total;
-        __syncthreads();
-    }
     __syncthreads();
     /* rows, lengths, copies */
     for (int i = tid >> 5; i < a.n_out; i += kPlanThreads / 32) {
-        const int lane = tid & 31, s = parent_of(i);
+        const int s = parent_of[i], k0 = kept_of[i], k1 = need_of[i];
         const bool ok = fits(i);
         int32_t* row = a.table_out + (int64_t)i * a.out_stride;
-        const int kept = a.kept[i], need = a.need[i];
         for (int64_t k = lane; k < a.out_stride; k += 32) {
-            if (ok && k < kept) row[k] = a.table[(int64_t)s * a.in_stride + k];
-            else if (!ok || k >= need) row[k] = -1;
+            if (ok && k < k0) {
+                const int p = a.table[(int64_t)s * a.in_stride + k];
+                if (p < 0 || p >= N) flag_corrupt(a.status);
+                row[k] = p;
+            } else if (!ok || k >= k1) row[k] = -1;
         }
         if (!ok)
-            for (int k = lane; k < kept; k += 32) {
+            for (int k = lane; k < k0; k += 32) {
                 const int p = page_in(s, k);
-                if (p >= 0) atomicSub(&a.refs_out[p], 1);
+                if (p >= 0) atomicSub(&cnt[p], 1);
             }
-        __syncwarp();
-        if (lane == 0) {
-            const int len = s >= 0 ? len_in(s) : 0;
-            a.lens_out[i] = !ok ? -1 : s < 0 ? 0 : len + (a.grow ? max(a.grow[i], 0) : 0);
-            if (ok && s >= 0 && len % T && a.first[s] != i) {
-                const int from = page_in(s, len / T);
-                if (from >= 0) {
-                    const int n = atomicAdd(&n_copies, 1);
-                    a.copies[3 * n] = from;
-                    a.copies[3 * n + 1] = row[kept];
-                    a.copies[3 * n + 2] = (len % T + kUnit - 1) / kUnit;
-                } else flag_corrupt(a.status);
-            }
+        if (lane == 0 && ok && s >= 0 && (len_of[s] & (T - 1)) && first[s] != i) {
+            const int from = page_in(s, len_of[s] >> shift);
+            if (from >= 0) {
+                const int n = atomicAdd(&n_copies, 1);
+                a.copies[3 * n] = from;
+                a.copies[3 * n + 1] = row[k0];
+                a.copies[3 * n + 2] = ((len_of[s] & (T - 1)) + kUnit - 1) / kUnit;
+            } else flag_corrupt(a.status);
         }
     }
+    if (tid < a.n_out) a.lens_out[tid] = !fits(tid) ? -1 : (int)now;
     __syncthreads();
+    if (cnt != a.refs_out)
+        for (int i = tid; i < N; i += kPlanThreads) a.refs_out[i] = cnt[i];
     if (tid == 0) *a.count = n_copies;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const __grid_constant__ PlanArgs a) {
-    __shared__ int tmp[33];
-    __shared__ int live_total;
+    __shared__ int64_t tmp[33];
     const int tid = threadIdx.x, N = a.P.n_pages;
     grid_dep_launch();
     grid_dep_wait();
-    int mine = 0;
+    int64_t mine = 0, total;
     for (int i = tid; i < N; i += kPlanThreads) mine += a.refs[i] > 0;
-    {
-        int total;
-        block_scan(mine, &total, tmp);
-        if (tid == 0) live_total = total;
-    }
-    __syncthreads();
-    const int n = live_total;
+    block_scan(mine, &total, tmp);
+    const int n = (int)total;
     int holes = 0, movers = 0;
     for (int base = 0; base < N; base += kPlanThreads) {
         const int i = base + tid;
         const int ref = i < N ? a.refs[i] : 0;
         const bool live = ref > 0, hole = i < n && !live, mover = live && i >= n;
-        int total;
-        const int x = block_scan((hole ? 1 : 0) | (mover ? 1 << 16 : 0), &total, tmp);
-        if (hole) a.copies[3 * (holes + (x & 0xFFFF)) + 1] = i;
-        if (mover) a.copies[3 * (movers + (x >> 16))] = i;
-        holes += total & 0xFFFF;
-        movers += total >> 16;
+        const int64_t x = block_scan<int64_t>((hole ? 1 : 0) | (mover ? int64_t(1) << 32 : 0), &total, tmp);
+        if (hole) a.copies[3 * (holes + (int)x) + 1] = i;
+        if (mover) a.copies[3 * (movers + (int)(x >> 32))] = i;
+        holes += (int)total;
+        movers += (int)(total >> 32);
         if (i < N) {
             a.refs_out[i] = live && i < n ? ref : 0;
             a.map[i] = live && i < n ? i : -1;
@@ -684,12 +672,11 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const __g
     __syncthreads();
     if (tid == 0) *a.count = movers;
     for (int s = tid; s < a.n_in; s += kPlanThreads) a.lens_out[s] = a.lens[s];
-    const int64_t cells = (int64_t)a.n_in * a.out_stride;
-    for (int64_t k = tid; k < cells; k += kPlanThreads) {
-        const int64_t s = k / a.out_stride, col = k % a.out_stride;
-        const int p = col < a.in_stride ? a.table[s * a.in_stride + col] : -1;
-        a.table_out[k] = p >= 0 && p < N ? a.map[p] : p;
-    }
+    for (int s = tid >> 5; s < a.n_in; s += kPlanThreads / 32)
+        for (int64_t col = tid & 31; col < a.out_stride; col += 32) {
+            const int p = col < a.in_stride ? a.table[s * a.in_stride + col] : -1;
+            a.table_out[s * a.out_stride + col] = p >= 0 && p < N ? a.map[p] : p;
+        }
 }
 
 struct CopyArgs {
@@ -726,9 +713,9 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_cons
 
 static size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
 
-/* work: count (16 bytes) | copies | first, kept, need, begin (fork) or map (compact) */
-static size_t pages_work(const ec_kv* C, int64_t n_in, int64_t n_out) {
-    const size_t fork = 16 + align16(12 * (size_t)n_out) + align16(4 * (size_t)n_in) + 3 * align16(4 * (size_t)n_out);
+/* work: count (16 bytes) | copies | map (compact) */
+static size_t pages_work(const ec_kv* C, int64_t n_out) {
+    const size_t fork = 16 + align16(12 * (size_t)n_out);
     const size_t compact = 16 + align16(12 * ((size_t)C->p.n_pages / 2 + 1)) + align16(4 * (size_t)C->p.n_pages);
     return fork > compact ? fork : compact;
 }
@@ -744,7 +731,7 @@ static int check_pages(const ec_kv* C, const ec_kv_pages* g) {
     if (rc == EC_OK) rc = check_seqs(&to);
     if (rc != EC_OK) return rc;
     if (!g->refs || !g->refs_out || !g->work || (uintptr_t)g->work % 16) return EC_ERR_INVALID_ARG;
-    if (g->work_bytes < pages_work(C, from.n_seqs, to.n_seqs)) return EC_ERR_INVALID_ARG;
+    if (g->work_bytes < pages_work(C, to.n_seqs)) return EC_ERR_INVALID_ARG;
     const size_t in = sizeof(int32_t) * (size_t)(from.n_seqs * from.table_stride), nr = sizeof(int32_t) * (size_t)C->p.n_pages,
                  out = sizeof(int32_t) * (size_t)(to.n_seqs * to.table_stride);
     if (overlap(from.table, in, to.table, out) || overlap(g->refs, nr, g->refs_out, nr) ||
@@ -830,12 +817,16 @@ extern "C" int ec_kv_append(const ec_kv* C, const ec_kv_tokens* t, cudaStream_t 
     if (rc == EC_OK) rc = check_rows(&t->k, a.P.n_heads, t->n_rows, &a.k);
     if (rc == EC_OK) rc = check_rows(&t->v, a.P.n_heads, t->n_rows, &a.v);
     if (rc != EC_OK) return rc;
+    if (t->k.dtype != t->v.dtype && (t->k.dtype == EC_DTYPE_FP32 || t->v.dtype == EC_DTYPE_FP32)) return EC_ERR_UNSUPPORTED;
     Device d;
     if ((rc = device_of(C, &d)) != EC_OK) return rc;
     if (!go) return EC_OK;
     a.has_k = a.has_v = 1;
     a.status = d.status;
-    return run_io(C, t, a, kv_append_kernel<2>, kv_append_kernel<4>, kv_append_kernel<6>, kv_append_kernel<8>, stream);
+    /* (16-bit rows in half the registers: more warps at a time) */
+    if (t->k.dtype == EC_DTYPE_FP32)
+        return run_io(C, t, a, kv_append_kernel<2, true>, kv_append_kernel<4, true>, kv_append_kernel<6, true>, kv_append_kernel<8, true>, stream);
+    return run_io(C, t, a, kv_append_kernel<2, false>, kv_append_kernel<4, false>, kv_append_kernel<6, false>, kv_append_kernel<8, false>, stream);
 }
 
 extern "C" int ec_kv_read(const ec_kv* C, const ec_kv_tokens* t, cudaStream_t stream) {
@@ -860,7 +851,7 @@ extern "C" int ec_kv_pages_work_bytes(const ec_kv* C, int n_from, int n_to, size
     if (!C || !bytes) return EC_ERR_INVALID_ARG;
     if (n_from < 0 || n_to < 0) return EC_ERR_SHAPE;
     if (n_from > EC_KV_MAX_SEQS || n_to > EC_KV_MAX_SEQS) return EC_ERR_UNSUPPORTED;
-    *bytes = pages_work(C, n_from, n_to);
+    *bytes = pages_work(C, n_to);
     return EC_OK;
 }
 
@@ -881,16 +872,11 @@ extern "C" int ec_kv_fork(const ec_kv* C, const ec_kv_pages* g, cudaStream_t str
     a.count = (int32_t*)w;
     w += 16;
     a.copies = (int32_t*)w;
-    w += align16(12 * (size_t)a.n_out);
-    a.first = (int32_t*)w;
-    w += align16(4 * (size_t)a.n_in);
-    a.kept = (int32_t*)w;
-    w += align16(4 * (size_t)a.n_out);
-    a.need = (int32_t*)w;
-    w += align16(4 * (size_t)a.n_out);
-    a.begin = (int32_t*)w;
     a.status = d.status;
-    if ((rc = launch(kv_fork_plan_kernel, dim3(1), kPlanThreads, 0, stream, a)) != EC_OK) return rc;
+    static SmemOnce once;
+    if ((rc = once.set(kv_fork_plan_kernel, sizeof(int32_t) * kSmallPool)) != EC_OK) return rc;
+    const size_t counts = a.P.n_pages <= kSmallPool ? sizeof(int32_t) * (size_t)a.P.n_pages : 0;
+    if ((rc = launch(kv_fork_plan_kernel, dim3(1), kPlanThreads, counts, stream, a)) != EC_OK) return rc;
     return run_copies(C, a, a.n_out, d, stream);
 }
 

@@ -475,6 +475,43 @@ def test_fork(ec, seed):
     assert drefs.cpu().tolist() == refs
 
 
+def test_fork_in_a_large_pool(ec):
+    """More pages than the counts in shared memory hold; new pages come from far into the pool."""
+    c = Case(ec, [40, 90, 7], 1, 64, 16, spare=40000)
+    refs = [1] * c.n_pages
+    for p in range(30000, c.n_pages, 7):
+        refs[p] = 0
+    for row in c.rows:
+        for p in row:
+            if p >= 0:
+                refs[p] = 1
+    parents, grow = [1, 1, 0, 1, -1], [0, 40, 100, 3, 9]
+    to = ec.kv_seqs(torch.zeros((5, 12), dtype=torch.int32, device="cuda"), torch.zeros(5, dtype=torch.int32, device="cuda"))
+    out = torch.empty(c.n_pages, dtype=torch.int32, device="cuda")
+    c.pool.random_(0, 256)
+    before = c.pool.clone()
+    ec.kv_fork(c.cache, c.seqs, i32(refs), to, out, parents=i32(parents), grow=i32(grow))
+    assert ec.status() == 0
+    rows, lens, new_refs, copies = R.fork(16, c.n_pages, c.rows, c.lens, refs, parents, grow, 12)
+    assert to.table.cpu().tolist() == rows and to.lens.cpu().tolist() == lens and out.cpu().tolist() == new_refs
+    for s, d, u in copies:
+        before[d, :, :, :u] = before[s, :, :, :u]
+    assert torch.equal(c.pool, before)
+
+
+def test_mixed_types(ec):
+    """16-bit keys and values of different types go together, FP32 with them does not."""
+    c = Case(ec, [20], 1, 64, 16)
+    k, v = c.tensors(7, BF16)[0], c.tensors(8, FP16)[1]
+    c.fill(k, v)
+    got = c.read()
+    assert np.array_equal(got[0].double().cpu().numpy(), R.stored(k.double().cpu().numpy()))
+    assert np.array_equal(got[1].double().cpu().numpy(), R.stored(v.double().cpu().numpy()))
+    with pytest.raises(ec.EcError) as x:
+        c.fill(k.float(), v)
+    assert x.value.code == -4
+
+
 def test_fork_without_growth_and_to_nothing(ec):
     c = Case(ec, [40, 16], 1, 64, 16, layers=1, spare=5)
     refs = i32([1 if any(p in row for row in c.rows) else 0 for p in range(c.n_pages)])
