@@ -121,7 +121,7 @@ __device__ __forceinline__ int64_t share_of(const AttnArgs& a, int64_t X, int n,
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -802,9 +802,12 @@ static void plan_shape(Plan* p, int sms, int64_t tiles, int64_t units) {
     p->work = p->solo ? 0 : (size_t)p->grid * (2 * H::RB * (H::D + 2) * sizeof(float) + sizeof(JoinJob));
 }
 
-/* Query rows per key/value head up to which the register form runs (it expands the tokens
- * once per 8 or 16 rows, the tensor-memory form once per 128 or 256). */
-constexpr int64_t kFewRows = 16;
+/* Query rows per key/value head up to which the register form runs: it expands the tokens
+ * once per 16 rows (8 above 128 channels), the tensor-memory form once per 128 or 256.
+ * Measured with 128 channels (us, register form / tensor-memory form): 16 sequences with a
+ * window of 4096, 24 rows 61 / 69, 40 rows 82 / 69; 32 sequences of 500 to 3000 tokens, 32
+ * rows 53 / 63; one of 30000, 40 rows 52 / 42. */
+constexpr int64_t few_rows(int nb) { return nb <= 4 ? 32 : 16; }
 
 /* false: more work than the kernels count (one sequence's places fit 31 bits) */
 static bool plan_of(const ec_kv* C, int sms, int n_seqs, int max_new, int64_t max_len, const ec_kv_attn* at, int dtype, Plan* p) {
@@ -817,7 +820,7 @@ static bool plan_of(const ec_kv* C, int sms, int n_seqs, int max_new, int64_t ma
         if (w < units) units = w;
     }
     if (units < 1) units = 1;
-    p->many = rows > kFewRows;
+    p->many = rows > few_rows(nb);
     if (p->many) {
         p->grid = p->solo = 0;
         if (!plan_prefill(C, sms, n_seqs, max_new, units, group, dtype, &p->pre)) return false;
