@@ -214,38 +214,45 @@ __device__ __forceinline__ Raw8<F32> load_raw(const Rows& R, int64_t off, bool o
     }
     return r;
 }
+/* Eight channels of one token -> their word and the block's scale byte (the quad's four
+ * lanes take part).  The largest magnitude is found on the bits (NaN and infinity are the
+ * largest), for 16-bit types two at a time. */
 template <bool F32>
-__device__ __forceinline__ void raw_values(const Raw8<F32>& r, int dtype, float (&x)[8]) {
+__device__ __forceinline__ uint32_t quantise8(const Raw8<F32>& r, bool fp16, int& e) {
+    uint32_t top = 0;
+    float x[8];
     if constexpr (F32) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r.w[i]);
-    } else if (dtype == EC_DTYPE_FP16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*(const __half2*)&r.w[i]);
-            x[2 * i] = f.x, x[2 * i + 1] = f.y;
+        for (int i = 0; i < 8; ++i) {
+            x[i] = __uint_as_float(r.w[i]);
+            top = max(top, r.w[i] & 0x7FFFFFFFu);
         }
     } else {
+        uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(r.w[i] << 16), x[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
+        for (int i = 0; i < 4; ++i) m = __vmaxu2(m, r.w[i] & 0x7FFF7FFFu);
+        m = max(m & 0xFFFFu, m >> 16);
+        top = fp16 ? __float_as_uint(__half2float(__ushort_as_half((unsigned short)m))) : m << 16;
+        if (fp16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = __half22float2(*(const __half2*)&r.w[i]);
+                x[2 * i] = f.x, x[2 * i + 1] = f.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(r.w[i] << 16), x[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
+        }
     }
-}
-
-/* Eight channels of one token -> their word and the block's scale byte (the quad's four
- * lanes take part). */
-__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], int& e) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu); /* NaN and infinity are the largest */
     top = max(top, __shfl_xor_sync(kAll, top, 1));
     top = max(top, __shfl_xor_sync(kAll, top, 2));
     e = scale_byte(top);
-    if (e == 0 || e == 255) return 0u;
-    const float s = inv_scale(e);
-    uint32_t w = 0;
+    const bool none = e == 0 || e == 255;
+    const float s = inv_scale(none ? 127 : e);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w |= f32x2_e2m1x2(x[2 * i + 1] * s, x[2 * i] * s) << (8 * i);
-    return w;
+    for (int i = 0; i < 8; ++i) x[i] *= s;
+    const uint32_t w = f32x8_e2m1(x);
+    return none ? 0u : w;
 }
 
 /* Four nibbles to the low halves of four bytes, and back. */
@@ -273,12 +280,14 @@ __global__ void __launch_bounds__(kIoWarps * 32) kv_append_kernel(const __grid_c
     const bool on[2] = {g >= j.lo && g < j.hi, g + 8 >= j.lo && g + 8 < j.hi};
     Raw8<F32> raw[NB][2];
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int r = 0; r < 2; ++r) {
+        const int64_t off = (j.row0 + g + 8 * r) * R.row + (int64_t)j.h * R.head + 8 * c;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) raw[b][r] = load_raw<F32>(R, (j.row0 + g + 8 * r) * R.row + (int64_t)j.h * R.head + 32 * b + 8 * c, on[r]);
+        for (int b = 0; b < NB; ++b) raw[b][r] = load_raw<F32>(R, off + 32 * b, on[r]);
+    }
     uint8_t* dst = unit_ptr(a, j, page);
     if (!dst) return;
-    const bool full = j.lo == 0 && j.hi == kUnit;
+    const bool full = j.lo == 0 && j.hi == kUnit, fp16 = R.dtype == EC_DTYPE_FP16;
     if (j.which == 0) {
         uint32_t word[2 * NB];
         uint8_t es[2][NB];
@@ -286,10 +295,8 @@ __global__ void __launch_bounds__(kIoWarps * 32) kv_append_kernel(const __grid_c
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float x[8];
-                raw_values(raw[b][r], R.dtype, x);
                 int e;
-                word[2 * b + r] = quantise8(x, e);
+                word[2 * b + r] = quantise8(raw[b][r], fp16, e);
                 es[r][b] = (uint8_t)e;
             }
 #pragma unroll
@@ -330,10 +337,8 @@ __global__ void __launch_bounds__(kIoWarps * 32) kv_append_kernel(const __grid_c
             uint32_t w[2], x[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float y[8];
-                raw_values(raw[b][r], R.dtype, y);
                 int e;
-                w[r] = quantise8(y, e);
+                w[r] = quantise8(raw[b][r], fp16, e);
                 if (c == 0 && on[r]) buf[8 * D + ((m * NB + b) * 2 + r) * 2 + (g & 1)] = (uint8_t)e;
                 /* pair step */
                 const uint32_t other = __shfl_xor_sync(kAll, w[r], 4), sh = g & 1 ? 16 : 0;
@@ -449,14 +454,36 @@ __global__ void __launch_bounds__(kIoWarps * 32) kv_read_kernel(const __grid_con
         }
     }
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int r = 0; r < 2; ++r) {
+        if (!on[r]) continue;
+        const int64_t off = (j.row0 + g + 8 * r) * R.row + (int64_t)j.h * R.head + 8 * c;
+        if (R.wide && R.dtype == EC_DTYPE_BF16) {
+            uint16_t* at = (uint16_t*)R.data + off;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            if (!on[r]) continue;
-            float x[8];
-            word_values(word[r][b], scale_value((int)es[r][b]), x);
-            store8(R, (j.row0 + g + 8 * r) * R.row + (int64_t)j.h * R.head + 32 * b + 8 * c, x);
+            for (int b = 0; b < NB; ++b) {
+                float x[8];
+                word_values(word[r][b], scale_value((int)es[r][b]), x);
+                uint32_t u[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                    u[i] = *(const uint32_t*)&y;
+                }
+                *(uint4*)(at + 32 * b) = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+        } else {
+#pragma unroll 1
+            for (int b = 0; b < NB; ++b) {
+                float x[8];
+                uint32_t w2 = 0, e2 = 0;
+#pragma unroll
+                for (int k = 0; k < NB; ++k)
+                    if (k == b) w2 = word[r][k], e2 = es[r][k];
+                word_values(w2, scale_value((int)e2), x);
+                store8(R, off + 32 * b, x);
+            }
         }
+    }
 }
 
 /* units that n consecutive tokens can touch */

@@ -109,11 +109,15 @@ __device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&r)[4]) {
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
         : "r"(w));
 }
-/* Two FP32 values -> a byte of two elements (lo in the low nibble), nearest even, 6 the largest. */
-__device__ __forceinline__ uint32_t f32x2_e2m1x2(float hi, float lo) {
+/* Eight FP32 values -> a word of eight elements (the first in the low nibble), nearest even, 6 the largest. */
+__device__ __forceinline__ uint32_t f32x8_e2m1(const float (&x)[8]) {
     uint32_t r;
-    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tmov.b32 %0, {b, b, b, b};\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
-    r &= 0xFFu;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
     return r;
 }
 /* The scale byte of a block whose largest magnitude is `top`: the smallest e >= 1 with
