@@ -529,8 +529,8 @@ typedef struct {
     ec_kv_rows k, v;
 } ec_kv_tokens;
 
-/* Quantise the new tokens' keys and values into the cache (FP32 keys with 16-bit values, or
- * the other way round: EC_ERR_UNSUPPORTED).
+/* Quantise the new tokens' keys and values into the cache (k and v of one type, else
+ * EC_ERR_UNSUPPORTED).
  * Pages that receive tokens must not be shared with a sequence that reads those places
  * (ec_kv_fork gives every sequence a partly filled page of its own). */
 int ec_kv_append(const ec_kv* C, const ec_kv_tokens* a, cudaStream_t stream);

@@ -182,73 +182,67 @@ __device__ __forceinline__ uint8_t* unit_ptr(const IoArgs& a, const UnitJob& j, 
     return (uint8_t*)page_ptr(a.P, page, j.h, (j.tok0 & ((1 << a.P.page_shift) - 1)) / kUnit);
 }
 
-/* Eight consecutive elements as they lie in memory. */
-template <bool F32>
+/* Eight consecutive elements of type T (EC_DTYPE_*) as they lie in memory. */
+template <int T>
 struct Raw8 {
-    uint32_t w[F32 ? 8 : 4];
+    uint32_t w[T == EC_DTYPE_FP32 ? 8 : 4];
 };
-template <bool F32>
-__device__ __forceinline__ Raw8<F32> load_raw(const Rows& R, int64_t off, bool on) {
-    Raw8<F32> r;
+template <int T, bool kWide>
+__device__ __forceinline__ Raw8<T> load_raw(const void* data, int64_t off, bool on) {
+    constexpr int N = T == EC_DTYPE_FP32 ? 8 : 4;
+    Raw8<T> r;
 #pragma unroll
-    for (int i = 0; i < (F32 ? 8 : 4); ++i) r.w[i] = 0;
+    for (int i = 0; i < N; ++i) r.w[i] = 0;
     if (!on) return r;
-    if constexpr (F32) {
-        const uint32_t* p = (const uint32_t*)R.data + off;
-        if (R.wide) {
-            const uint4 x = *(const uint4*)p, y = *(const uint4*)(p + 4);
-            r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w, r.w[4] = y.x, r.w[5] = y.y, r.w[6] = y.z, r.w[7] = y.w;
-        } else {
+    if constexpr (kWide) {
+        const uint4* p = (const uint4*)((const uint8_t*)data + off * (T == EC_DTYPE_FP32 ? 4 : 2));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) r.w[i] = p[i];
+        for (int i = 0; i < N / 4; ++i) {
+            const uint4 x = p[i];
+            r.w[4 * i] = x.x, r.w[4 * i + 1] = x.y, r.w[4 * i + 2] = x.z, r.w[4 * i + 3] = x.w;
         }
+    } else if constexpr (T == EC_DTYPE_FP32) {
+        const uint32_t* p = (const uint32_t*)data + off;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.w[i] = p[i];
     } else {
-        const uint16_t* p = (const uint16_t*)R.data + off;
-        if (R.wide) {
-            const uint4 x = *(const uint4*)p;
-            r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
-        } else {
+        const uint16_t* p = (const uint16_t*)data + off;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) r.w[i] = p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
-        }
+        for (int i = 0; i < 4; ++i) r.w[i] = p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
     }
     return r;
 }
+
 /* Eight channels of one token -> their word and the block's scale byte (the quad's four
  * lanes take part).  The largest magnitude is found on the bits (NaN and infinity are the
  * largest), for 16-bit types two at a time. */
-template <bool F32>
-__device__ __forceinline__ uint32_t quantise8(const Raw8<F32>& r, bool fp16, int& e) {
+template <int T>
+__device__ __forceinline__ uint32_t quantise8(const Raw8<T>& r, int& e) {
     uint32_t top = 0;
     float x[8];
-    if constexpr (F32) {
+    if constexpr (T == EC_DTYPE_FP32) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             x[i] = __uint_as_float(r.w[i]);
             top = max(top, r.w[i] & 0x7FFFFFFFu);
         }
     } else {
-        uint32_t m = 0;
+        const uint32_t m2 = __vmaxu2(__vmaxu2(r.w[0] & 0x7FFF7FFFu, r.w[1] & 0x7FFF7FFFu), __vmaxu2(r.w[2] & 0x7FFF7FFFu, r.w[3] & 0x7FFF7FFFu));
+        const uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m = __vmaxu2(m, r.w[i] & 0x7FFF7FFFu);
-        m = max(m & 0xFFFFu, m >> 16);
-        top = fp16 ? __float_as_uint(__half2float(__ushort_as_half((unsigned short)m))) : m << 16;
-        if (fp16) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (T == EC_DTYPE_FP16) {
                 const float2 f = __half22float2(*(const __half2*)&r.w[i]);
                 x[2 * i] = f.x, x[2 * i + 1] = f.y;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(r.w[i] << 16), x[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
+            } else x[2 * i] = __uint_as_float(r.w[i] << 16), x[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
         }
+        top = T == EC_DTYPE_FP16 ? __float_as_uint(__half2float(__ushort_as_half((unsigned short)m))) : m << 16;
     }
     top = max(top, __shfl_xor_sync(kAll, top, 1));
     top = max(top, __shfl_xor_sync(kAll, top, 2));
-    e = scale_byte(top);
-    const bool none = e == 0 || e == 255;
-    const float s = inv_scale(none ? 127 : e);
+    bool none;
+    e = scale_byte(top, &none);
+    const float s = none ? 0.f : inv_scale(e);
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] *= s;
     const uint32_t w = f32x8_e2m1(x);
@@ -265,7 +259,7 @@ __device__ __forceinline__ uint32_t gather4(uint32_t x) {
     return (x | x >> 8) & 0xFFFFu;
 }
 
-template <int NB, bool F32>
+template <int NB, int T>
 __global__ void __launch_bounds__(kIoWarps * 32) kv_append_kernel(const __grid_constant__ IoArgs a) {
     constexpr int D = 32 * NB, SECTION = 8 * D + D / 2; /* a warp's codes and scales */
     __shared__ __align__(16) uint8_t io_smem[kIoWarps][SECTION];
@@ -278,16 +272,22 @@ __global__ void __launch_bounds__(kIoWarps * 32) kv_append_kernel(const __grid_c
     const int32_t page = page_at(a, j);
     const Rows& R = j.which ? a.v : a.k;
     const bool on[2] = {g >= j.lo && g < j.hi, g + 8 >= j.lo && g + 8 < j.hi};
-    Raw8<F32> raw[NB][2];
+    Raw8<T> raw[NB][2];
+    const int64_t off = (j.row0 + g) * R.row + (int64_t)j.h * R.head + 8 * c;
+    if (R.wide) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int64_t off = (j.row0 + g + 8 * r) * R.row + (int64_t)j.h * R.head + 8 * c;
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) raw[b][r] = load_raw<F32>(R, off + 32 * b, on[r]);
+            for (int b = 0; b < NB; ++b) raw[b][r] = load_raw<T, true>(R.data, off + 8 * r * R.row + 32 * b, on[r]);
+    } else {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) raw[b][r] = load_raw<T, false>(R.data, off + 8 * r * R.row + 32 * b, on[r]);
     }
     uint8_t* dst = unit_ptr(a, j, page);
     if (!dst) return;
-    const bool full = j.lo == 0 && j.hi == kUnit, fp16 = R.dtype == EC_DTYPE_FP16;
+    const bool full = j.lo == 0 && j.hi == kUnit;
     if (j.which == 0) {
         uint32_t word[2 * NB];
         uint8_t es[2][NB];
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kIoWarps * 32) kv_append_kernel(const __grid_c
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 int e;
-                word[2 * b + r] = quantise8(raw[b][r], fp16, e);
+                word[2 * b + r] = quantise8<T>(raw[b][r], e);
                 es[r][b] = (uint8_t)e;
             }
 #pragma unroll
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kIoWarps * 32) kv_append_kernel(const __grid_c
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 int e;
-                w[r] = quantise8(raw[b][r], fp16, e);
+                w[r] = quantise8<T>(raw[b][r], e);
                 if (c == 0 && on[r]) buf[8 * D + ((m * NB + b) * 2 + r) * 2 + (g & 1)] = (uint8_t)e;
                 /* pair step */
                 const uint32_t other = __shfl_xor_sync(kAll, w[r], 4), sh = g & 1 ? 16 : 0;
@@ -836,6 +836,11 @@ static int run_io(const ec_kv* C, const ec_kv_tokens* t, IoArgs& a, Kernel k2, K
     return launch(nb == 2 ? k2 : nb == 4 ? k4 : nb == 6 ? k6 : k8, dim3((unsigned)grid), kIoWarps * 32, 0, stream, a);
 }
 
+template <int T>
+static int run_append(const ec_kv* C, const ec_kv_tokens* t, IoArgs& a, cudaStream_t stream) {
+    return run_io(C, t, a, kv_append_kernel<2, T>, kv_append_kernel<4, T>, kv_append_kernel<6, T>, kv_append_kernel<8, T>, stream);
+}
+
 extern "C" int ec_kv_append(const ec_kv* C, const ec_kv_tokens* t, cudaStream_t stream) {
     if (!C || !t) return EC_ERR_INVALID_ARG;
     IoArgs a{};
@@ -844,16 +849,17 @@ extern "C" int ec_kv_append(const ec_kv* C, const ec_kv_tokens* t, cudaStream_t 
     if (rc == EC_OK) rc = check_rows(&t->k, a.P.n_heads, t->n_rows, &a.k);
     if (rc == EC_OK) rc = check_rows(&t->v, a.P.n_heads, t->n_rows, &a.v);
     if (rc != EC_OK) return rc;
-    if (t->k.dtype != t->v.dtype && (t->k.dtype == EC_DTYPE_FP32 || t->v.dtype == EC_DTYPE_FP32)) return EC_ERR_UNSUPPORTED;
+    if (t->k.dtype != t->v.dtype) return EC_ERR_UNSUPPORTED;
     Device d;
     if ((rc = device_of(C, &d)) != EC_OK) return rc;
     if (!go) return EC_OK;
     a.has_k = a.has_v = 1;
     a.status = d.status;
-    /* (16-bit rows in half the registers: more warps at a time) */
-    if (t->k.dtype == EC_DTYPE_FP32)
-        return run_io(C, t, a, kv_append_kernel<2, true>, kv_append_kernel<4, true>, kv_append_kernel<6, true>, kv_append_kernel<8, true>, stream);
-    return run_io(C, t, a, kv_append_kernel<2, false>, kv_append_kernel<4, false>, kv_append_kernel<6, false>, kv_append_kernel<8, false>, stream);
+    switch (t->k.dtype) {
+        case EC_DTYPE_FP32: return run_append<EC_DTYPE_FP32>(C, t, a, stream);
+        case EC_DTYPE_FP16: return run_append<EC_DTYPE_FP16>(C, t, a, stream);
+        default: return run_append<EC_DTYPE_BF16>(C, t, a, stream);
+    }
 }
 
 extern "C" int ec_kv_read(const ec_kv* C, const ec_kv_tokens* t, cudaStream_t stream) {

@@ -120,20 +120,17 @@ __device__ __forceinline__ uint32_t f32x8_e2m1(const float (&x)[8]) {
         : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
     return r;
 }
-/* The scale byte of a block whose largest magnitude is `top`: the smallest e >= 1 with
- * top <= 6 * 2^(e - 127), 0 for a block of zeros, 255 for one with an infinity or NaN.
- * With top = 1.f * 2^(E - 127) that e is E - 2, or E - 1 when 1.f > 1.5. */
-__device__ __forceinline__ int scale_byte(uint32_t top_bits) {
-    const int E = (int)(top_bits >> 23);
-    if (top_bits == 0) return 0;
-    if (E == 255) return 255;
-    const int e = E - 2 + ((top_bits & 0x7FFFFFu) > 0x400000u ? 1 : 0);
-    return e < 1 ? 1 : e;
+/* The scale byte of a block whose largest magnitude has these bits: the smallest e >= 1 with
+ * top <= 6 * 2^(e - 127), 0 for a block of zeros, 255 for one with an infinity or NaN
+ * (*none in both cases).  With top = 1.f * 2^(E - 127) that e is E - 2, or E - 1 when 1.f >
+ * 1.5, which is when adding 2^22 - 1 carries into the exponent; at most 253. */
+__device__ __forceinline__ int scale_byte(uint32_t top, bool* none) {
+    *none = top - 1u >= 0x7F7FFFFFu;
+    const int e = max((int)((top + 0x3FFFFFu) >> 23) - 2, 1);
+    return *none ? (top ? 255 : 0) : e;
 }
-/* 2^(127 - e) and 2^(e - 127) for e in 1..254. */
-__device__ __forceinline__ float inv_scale(int e) {
-    return e == 254 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(254 - e) << 23);
-}
+/* 2^(127 - e), e in 1..253. */
+__device__ __forceinline__ float inv_scale(int e) { return __uint_as_float((uint32_t)(254 - e) << 23); }
 
 /* ------------------------------------------------------------ PTX helpers */
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }

@@ -500,16 +500,18 @@ def test_fork_in_a_large_pool(ec):
 
 
 def test_mixed_types(ec):
-    """16-bit keys and values of different types go together, FP32 with them does not."""
+    """Keys and values of one append have one type; what is read may have two."""
     c = Case(ec, [20], 1, 64, 16)
-    k, v = c.tensors(7, BF16)[0], c.tensors(8, FP16)[1]
+    k, v = c.tensors(7, BF16)
+    for bad in (k.float(), k.to(FP16)):
+        with pytest.raises(ec.EcError) as x:
+            c.fill(bad, v)
+        assert x.value.code == -4
     c.fill(k, v)
-    got = c.read()
-    assert np.array_equal(got[0].double().cpu().numpy(), R.stored(k.double().cpu().numpy()))
-    assert np.array_equal(got[1].double().cpu().numpy(), R.stored(v.double().cpu().numpy()))
-    with pytest.raises(ec.EcError) as x:
-        c.fill(k.float(), v)
-    assert x.value.code == -4
+    a, b = torch.empty((20, 1, 64), device="cuda"), torch.empty((20, 1, 64), dtype=FP16, device="cuda")
+    ec.kv_read(c.cache, 0, c.seqs, a, b, starts=starts_of([20]), max_new=20)
+    assert np.array_equal(a.double().cpu().numpy(), R.stored(k.double().cpu().numpy()))
+    assert torch.equal(b, c.read()[1].to(FP16))
 
 
 def test_fork_without_growth_and_to_nothing(ec):
