@@ -20,6 +20,9 @@
  * The fused decode + multiply-accumulate follows MINE ("Entropy-coded
  * Memory-efficient Inference for LLMs"), section 4 "Fused mvm" (Fig. 2).
  *
+ * Next to the weights it holds what attention reads between their products: a paged
+ * key/value cache in microscaled 4-bit floating point (ec_kv_*, at the end).
+ *
  * Conventions (all entry points):
  *  - Return EC_OK (0) or a negative EC_ERR_* code; no exception crosses the ABI.
  *  - Shapes are checked with overflow-safe 64-bit arithmetic before anything is

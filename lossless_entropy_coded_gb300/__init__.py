@@ -1,5 +1,6 @@
 """Entropy-coded LLM weights on GB300: lossless Huffman-exponent BF16 and rANS
-4-bit codecs with fused decode + GEMV kernels for sm_103a.
+4-bit codecs with fused decode + GEMV kernels for sm_103a, and a paged key/value
+cache in microscaled 4-bit floating point with the attention that reads it.
 
 The work happens in libec.so (include/ec.h); this package only marshals arguments.
 The library is loaded on first use of any attribute below; if libec.so has not been

@@ -123,8 +123,13 @@ static int check_call(const ec_kv* C, int layer, const ec_kv_seqs* seqs, const i
  *   channel step  lane with c even keeps the first two of its four channels, c odd the last
  *                 two, of both lanes: bytes (r, p) of two words, r = c % 2
  * which land at words i = 2 b + c / 2 of lanes 4 (4 (g % 2) + k) + g / 2, k = 2 (c % 2), + 1.
- * Reading runs the same steps backwards.  Bound by HBM: every byte moves once; all loads of
- * a warp are issued before the first is used. */
+ * Reading runs the same steps backwards.
+ *
+ * Every byte moves once; all loads of a warp are issued before the first is used.  The floor
+ * is HBM, the integer pipe (magnitudes, conversions, exchanges) is next: 65 % busy.  18900
+ * rows of 8 heads x 128 channels in BF16: append 21 us, read 17 us back to back, 39.6 us
+ * together for 196 MB (4.95 TB/s); 64 single tokens take 8.3 us for both, which is the
+ * latency of lens, table and rows, one after the other. */
 constexpr int kIoWarps = 4;
 
 struct IoArgs {
@@ -495,8 +500,9 @@ static int units_of(int n) { return (n + 14) / kUnit + 1; }
  * per sequence, a compaction at most n_pages / 2.
  *
  * A plan is one CTA: the work is a few passes over small integer arrays with a barrier
- * between them, bound by the latency of each pass; up to kSmallPool pages the counts are
- * kept in shared memory, above that in refs_out itself. */
+ * between them, bound by the latency of each pass (about 4 us of the 7.7 us of a step of 8
+ * beams over 32 layers); up to kSmallPool pages the counts are kept in shared memory, above
+ * that in refs_out itself. */
 struct PlanArgs {
     Pool P;
     const int32_t *table, *lens, *refs, *parents, *grow;
@@ -714,7 +720,9 @@ struct CopyArgs {
 };
 
 /* A copy moves the first `units` units of every head of every layer of a page: runs of
- * units * 17 D contiguous bytes, one CTA per (copy, head) run at a time. */
+ * units * 17 D contiguous bytes, one CTA per (copy, head) run at a time.  Bound by HBM: a
+ * compaction that moves 0.2 GB takes 69 us with its plan (5.8 TB/s, 0.86 of the measured
+ * copy rate), 64 samples of 6 prompts over 32 layers 22 us (112 MB, 5.0 TB/s). */
 constexpr int kCopyThreads = 256;
 __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_constant__ CopyArgs a) {
     grid_dep_launch();

@@ -5,6 +5,19 @@
  * (s - m), o = sum p v / sum p.  All rows of a key/value head's query group, times a few
  * new tokens, form the 8 or 16 columns of the products S^T = K Q^T and O^T = V^T P^T, so
  * each 4-bit key or value is read from memory and expanded once for all of them.
+ *
+ * Bounds.  The floor is HBM: 4.25 bits per element of every visible key and value.  An SM
+ * gets 45 bytes/ns of it, a unit (16 tokens, 2176 bytes at 128 channels) every 94 clocks;
+ * the four schedulers then have 375 issue slots for it.  A unit takes about 275
+ * instructions, 140 of them on the integer pipe, which issues every second clock (the
+ * expansion of E2M1 to FP16 alone is 64), so the integer pipe and the dependent chain of
+ * a warp bound the kernel, not HBM.  Measured, 128 channels, 32 query over 8 key/value
+ * heads: 400003 tokens 93.4 us (4.66 TB/s, 0.69 of the measured copy rate; 113 us with
+ * one unit per step and all segment state in registers); 64 sequences of 1 to 8192 tokens
+ * 39.7 us for 92 MB (245 us with one CTA per tile and fixed chunks: most tiles are short,
+ * and their fixed cost, about that of 10 units, has to be shared out too).
+ * mma.sync rather than tcgen05: the products have 8 columns, a tcgen05 tile 128 rows; the
+ * legacy pipe is 27 % busy at the rate above.
  */
 #include <float.h>
 
@@ -15,7 +28,8 @@ namespace kv {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 /* Work is counted in units of 16 tokens of one tile (the rows of one key/value head's
- * group, 8 or 16 at a time), plus kTileCost for a tile's queries and outputs. */
+ * group, 8 or 16 at a time), plus kTileCost for a tile's queries and outputs
+ * (3, 6, 10 and 16 took 55.7, 44.7, 40.0 and 41.4 us on the 64 ragged sequences). */
 constexpr int kTileCost = 10;
 
 /* The keys that a sequence's new rows see, in units: the sinks' units, then lo_u ..
@@ -796,7 +810,8 @@ struct Plan {
 template <int NB, int NT>
 static void plan_shape(Plan* p, int sms, int64_t tiles, int64_t units) {
     using H = Shape<NB, NT>;
-    /* up to 4 units per warp there is nothing to gain from splitting a tile, and one launch does */
+    /* up to 4 units per warp there is nothing to gain from splitting a tile, and one launch does
+     * (17 tokens: 8 us; the split way adds the join's launch, about 4 us) */
     p->solo = units <= 4 * H::W && tiles < 0x7FFFFFFF ? (int)((units + H::W - 1) / H::W) * H::W : 0;
     p->grid = p->solo ? (int)tiles : sms * H::CTAS;
     p->work = p->solo ? 0 : (size_t)p->grid * (2 * H::RB * (H::D + 2) * sizeof(float) + sizeof(JoinJob));

@@ -95,12 +95,6 @@ __device__ __forceinline__ const uint8_t* page_ptr(const Pool& P, int32_t page, 
 __device__ __forceinline__ void flag_corrupt(int* status) { atomicOr(status, 1); }
 
 /* ------------------------------------------------------------ E2M1 and E8M0 */
-/* Two elements (one byte) -> two FP16 values, exact. */
-__device__ __forceinline__ uint32_t e2m1x2_f16x2(uint32_t byte) {
-    uint32_t r;
-    asm("{\n\t.reg .b8 b, z1, z2, z3;\n\tmov.b32 {b, z1, z2, z3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(byte));
-    return r;
-}
 /* The four bytes of a word -> four FP16 pairs. */
 __device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&r)[4]) {
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
@@ -189,13 +183,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
     for (int i = 0; i < (1 << 20); ++i)
         if (mbar_try_wait(bar, parity)) return true;
-    return false;
-}
-
-/* The same for a converged warp. */
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
-    for (int i = 0; i < (1 << 20); ++i)
-        if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
     return false;
 }
 
