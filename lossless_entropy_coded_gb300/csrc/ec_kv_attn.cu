@@ -3,8 +3,11 @@
  *
  * For a query row q, head by head: s_t = scale q . k_t over the visible tokens, p = exp
  * (s - m), o = sum p v / sum p.  All rows of a key/value head's query group, times a few
- * new tokens, form the 8 or 16 columns of the products S^T = K Q^T and O^T = V^T P^T, so
- * each 4-bit key or value is read from memory and expanded once for all of them.
+ * new tokens, form the columns of the products S^T = K Q^T and O^T = V^T P^T, 8 to a tile,
+ * so each 4-bit key or value is expanded once for 8 rows (and read from HBM once; further
+ * tiles of a head find it in L2).  16 columns per tile need 168 registers and leave 12
+ * warps per SM for 16: 16 rows over 400000 tokens 154 us for 160, but 63 for 51 with 1 to 5
+ * new tokens of 16 sequences and 72 for 54 over 100000 tokens, so there is one width.
  *
  * Bounds.  The floor is HBM: 4.25 bits per element of every visible key and value.  An SM
  * gets 45 bytes/ns of it, a unit (16 tokens, 2176 bytes at 128 channels) every 94 clocks;
@@ -28,7 +31,7 @@ namespace kv {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 /* Work is counted in units of 16 tokens of one tile (the rows of one key/value head's
- * group, 8 or 16 at a time), plus kTileCost for a tile's queries and outputs
+ * group, 8 at a time), plus kTileCost for a tile's queries and outputs
  * (3, 6, 10 and 16 took 55.7, 44.7, 40.0 and 41.4 us on the 64 ragged sequences). */
 constexpr int kTileCost = 10;
 
@@ -162,11 +165,11 @@ constexpr float kBias = 5.f;
 
 /* Warps per CTA, CTAs per SM and stages of a warp's ring by the tile's registers; `keep`
  * floats hold a warp's partial result of a tile: [rows][LD], maxima, sums. */
-template <int NB, int NT>
+template <int NB>
 struct Shape {
-    static constexpr int D = 32 * NB, RB = 8 * NT, LD = D + 4, UB = 17 * D;
-    static constexpr int W = NB <= 4 && NT == 1 ? 8 : 4;
-    static constexpr int CTAS = NT == 2 ? 3 : 2;
+    static constexpr int D = 32 * NB, RB = 8, LD = D + 4, UB = 17 * D;
+    static constexpr int W = NB <= 4 ? 8 : 4;
+    static constexpr int CTAS = 2;
     static constexpr int S = NB == 2 ? 4 : 2; /* of two units each; a power of two */
     static constexpr int KEEP = RB * LD + 2 * RB;
     static constexpr int RING = S * 2 * UB, WARP_BYTES = RING + KEEP * 4 + 64; /* + the warp's segment */
@@ -197,9 +200,9 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int row0, int h, in
  * meet in shared memory at the end, and what the CTA has not seen whole goes to `part`.
  * Units come by bulk copies through a ring of the warp's own, several ahead and across
  * tiles. */
-template <int NB, int NT, int QT>
-__global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv_attn_kernel(const __grid_constant__ AttnArgs a) {
-    using H = Shape<NB, NT>;
+template <int NB, int QT>
+__global__ void __launch_bounds__(Shape<NB>::W * 32, Shape<NB>::CTAS) kv_attn_kernel(const __grid_constant__ AttnArgs a) {
+    using H = Shape<NB>;
     constexpr int D = H::D, RB = H::RB, S = H::S, UB = H::UB, LD = H::LD, W = H::W;
     extern __shared__ __align__(128) uint8_t at_smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
@@ -282,8 +285,8 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
             f = make_int4((int)r.x, (int)r.y, (int)r.z, (int)r.w);
         };
         int u = 0, u1 = 0, all_lo = 0, all_hi = 0;
-        uint32_t qf[NT][QT][NB][4];
-        float fac[NT][2];
+        uint32_t qf[QT][NB][4];
+        float fac[2];
         {
             const Seg sg = seg_at(a, pre, info, RB, x, x_end);
             const int4 f = info[sg.b];
@@ -307,13 +310,11 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
             all_hi = min(u1, (pos_lo + 1 < 0 ? 0 : (pos_lo + 1) / kUnit) - skip);
             all_lo = a.window ? max(sp.sink_u, (max(0, pos_hi - a.window + 1) + kUnit - 1) / kUnit - skip) : 0;
 
-        /* queries: lane 4 g + c holds row g's channels 32 b + 8 c + 0..7, scaled by a power
-         * of two so that the row's largest lies in [2^14, 2^15): BF16 and FP16 rows are
-         * exact in one FP16 part but for elements 2^-28 of the row's largest, FP32 rows
-         * take two parts (22 bits) */
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int r = r0 + 8 * t + g;
+            /* queries: lane 4 g + c holds row g's channels 32 b + 8 c + 0..7, scaled by a power
+             * of two so that the row's largest lies in [2^14, 2^15): BF16 and FP16 rows are
+             * exact in one FP16 part but for elements 2^-28 of the row's largest, FP32 rows
+             * take two parts (22 bits) */
+            const int r = r0 + g;
             const bool on = r < R;
             const int64_t off = on ? (int64_t)(f.z + r / a.group) * a.q.row + (int64_t)(h * a.group + r % a.group) * a.q.head : 0;
             float xq[NB][8];
@@ -360,29 +361,25 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float y0 = xq[k][2 * i] * s, y1 = xq[k][2 * i + 1] * s;
-                    qf[t][0][k][i] = pack_f16(y0, y1);
+                    qf[0][k][i] = pack_f16(y0, y1);
                     if constexpr (QT == 2) {
-                        const float2 hi = __half22float2(*(const __half2*)&qf[t][0][k][i]);
-                        qf[t][QT - 1][k][i] = pack_f16(y0 - hi.x, y1 - hi.y);
+                        const float2 hi = __half22float2(*(const __half2*)&qf[0][k][i]);
+                        qf[QT - 1][k][i] = pack_f16(y0 - hi.x, y1 - hi.y);
                     }
                 }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) fac[t][j] = __shfl_sync(kAll, inv, 8 * c + 4 * j);
-        }
+            for (int j = 0; j < 2; ++j) fac[j] = __shfl_sync(kAll, inv, 8 * c + 4 * j);
         }
 
-        float o[NT][2 * NB][4];
-        float m[NT][2], l[NT][2];
+        float o[2 * NB][4];
+        float m[2], l[2];
         uint32_t add[NB]; /* 24 - the block's reference in both halves; 32: none yet, any scale passes it */
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
+        for (int i = 0; i < 2 * NB; ++i)
 #pragma unroll
-            for (int i = 0; i < 2 * NB; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[t][i][j] = 0.f;
-            m[t][0] = m[t][1] = -FLT_MAX;
-            l[t][0] = l[t][1] = 0.f;
-        }
+            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+        m[0] = m[1] = -FLT_MAX;
+        l[0] = l[1] = 0.f;
 #pragma unroll
         for (int k = 0; k < NB; ++k) add[k] = both_halves(32);
 
@@ -396,7 +393,7 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
             ++count;
 
             /* S^T: rows = tokens g, g + 8 of unit v, columns = query rows 2c, 2c + 1 */
-            float s[2][NT][4];
+            float s[2][4];
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
 #pragma unroll
@@ -411,17 +408,14 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
                         e2m1x8_f16(ww[2 * bb + 1], rb);
                         const float sa = __uint_as_float(lds8(buf + v * UB + 16 * D + g * NB + blk) << 23);
                         const float sb = __uint_as_float(lds8(buf + v * UB + 16 * D + (g + 8) * NB + blk) << 23);
+                        float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                            for (int q = 0; q < QT; ++q) {
-                                mma16816(d, ra[0], rb[0], ra[1], rb[1], qf[t][q][blk][0], qf[t][q][blk][1]);
-                                mma16816(d, ra[2], rb[2], ra[3], rb[3], qf[t][q][blk][2], qf[t][q][blk][3]);
-                            }
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) s[v][t][j] = blk == 0 ? d[j] * (j < 2 ? sa : sb) : fmaf(d[j], j < 2 ? sa : sb, s[v][t][j]);
+                        for (int q = 0; q < QT; ++q) {
+                            mma16816(d, ra[0], rb[0], ra[1], rb[1], qf[q][blk][0], qf[q][blk][1]);
+                            mma16816(d, ra[2], rb[2], ra[3], rb[3], qf[q][blk][2], qf[q][blk][3]);
                         }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[v][j] = blk == 0 ? d[j] * (j < 2 ? sa : sb) : fmaf(d[j], j < 2 ? sa : sb, s[v][j]);
                     }
                 }
             }
@@ -438,18 +432,16 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
 #pragma unroll
                 for (int v = 0; v < 2; ++v) tok[v] = u + v < u1 ? (u + v < sp.sink_u ? u + v : u + v + skip) * kUnit : 0x7FFFFF00;
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int j = 0; j < 2; ++j) {
+                    const int p = first + min(sg.r0 + 2 * c + j, R - 1) / a.group;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int p = first + min(sg.r0 + 8 * t + 2 * c + j, R - 1) / a.group;
+                    for (int v = 0; v < 2; ++v)
 #pragma unroll
-                        for (int v = 0; v < 2; ++v)
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const int at = tok[v] + g + 8 * k;
-                                if (at > p || (a.window && at <= p - a.window && at >= a.sinks)) s[v][t][j + 2 * k] = -INFINITY;
-                            }
-                    }
+                        for (int k = 0; k < 2; ++k) {
+                            const int at = tok[v] + g + 8 * k;
+                            if (at > p || (a.window && at <= p - a.window && at >= a.sinks)) s[v][j + 2 * k] = -INFINITY;
+                        }
+                }
 #pragma unroll
                 for (int v = 0; v < 2; ++v)
 #pragma unroll
@@ -461,51 +453,41 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
 
             /* weights 2^(s - m + kBias); the references move when a lane's eight weights add to
              * more than 2^(kBias + 3) (fac > 0, so a masked -inf stays one) */
-            float p[2][NT][4], sum[NT][2];
+            float p[2][4], sum[2];
             auto weights = [&]() {
-                bool over = false;
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
+                for (int v = 0; v < 2; ++v)
 #pragma unroll
-                    for (int v = 0; v < 2; ++v)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) p[v][t][j] = ex2(fmaf(s[v][t][j], fac[t][j & 1], kBias - m[t][j & 1]));
-                    sum[t][0] = (p[0][t][0] + p[0][t][2]) + (p[1][t][0] + p[1][t][2]);
-                    sum[t][1] = (p[0][t][1] + p[0][t][3]) + (p[1][t][1] + p[1][t][3]);
-                    over |= sum[t][0] + sum[t][1] > 256.f;
-                }
-                return over;
+                    for (int j = 0; j < 4; ++j) p[v][j] = ex2(fmaf(s[v][j], fac[j & 1], kBias - m[j & 1]));
+                sum[0] = (p[0][0] + p[0][2]) + (p[1][0] + p[1][2]);
+                sum[1] = (p[0][1] + p[0][3]) + (p[1][1] + p[1][3]);
+                return sum[0] + sum[1] > 256.f;
             };
             if (__any_sync(kAll, weights())) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int j = 0; j < 2; ++j) {
+                    float mx = fmaxf(fmaxf(s[0][j], s[0][j + 2]), fmaxf(s[1][j], s[1][j + 2])) * fac[j];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        float mx = fmaxf(fmaxf(s[0][t][j], s[0][t][j + 2]), fmaxf(s[1][t][j], s[1][t][j + 2])) * fac[t][j];
+                    for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, w));
+                    const float nm = fmaxf(m[j], mx), al = ex2(m[j] - nm);
+                    m[j] = nm;
+                    l[j] *= al;
 #pragma unroll
-                        for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, w));
-                        const float nm = fmaxf(m[t][j], mx), al = ex2(m[t][j] - nm);
-                        m[t][j] = nm;
-                        l[t][j] *= al;
-#pragma unroll
-                        for (int i = 0; i < 2 * NB; ++i) {
-                            o[t][i][j] *= al;
-                            o[t][i][j + 2] *= al;
-                        }
+                    for (int i = 0; i < 2 * NB; ++i) {
+                        o[i][j] *= al;
+                        o[i][j + 2] *= al;
                     }
+                }
                 weights();
             }
             /* their transposition into the second product's operand */
-            uint32_t p0[2][NT], p1[2][NT];
+            uint32_t p0[2], p1[2];
+            l[0] += sum[0];
+            l[1] += sum[1];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                l[t][0] += sum[t][0];
-                l[t][1] += sum[t][1];
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    p0[v][t] = transpose8x8(pack_f16(p[v][t][0], p[v][t][1]));
-                    p1[v][t] = transpose8x8(pack_f16(p[v][t][2], p[v][t][3]));
-                }
+            for (int v = 0; v < 2; ++v) {
+                p0[v] = transpose8x8(pack_f16(p[v][0], p[v][1]));
+                p1[v] = transpose8x8(pack_f16(p[v][2], p[v][3]));
             }
 
             /* value scales 2^(e - ref) as FP16 pairs: exponent field z - 9 = e - ref + 15,
@@ -551,12 +533,10 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
                         const float f = ref < 0 ? 0.f : ex2((float)(ref - mx));
                         add[k2] = both_halves(24 - mx);
 #pragma unroll
-                        for (int t = 0; t < NT; ++t)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                o[t][2 * k2][j] *= f;
-                                o[t][2 * k2 + 1][j] *= f;
-                            }
+                        for (int j = 0; j < 4; ++j) {
+                            o[2 * k2][j] *= f;
+                            o[2 * k2 + 1][j] *= f;
+                        }
                     }
                     const int r = (int)(int16_t)(add[k2] & 0xFFFFu);
 #pragma unroll
@@ -585,12 +565,7 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
                     for (int bb = 0; bb < 2; ++bb) {
                         const int blk = 2 * i4 + bb;
                         const uint32_t s0 = z0[v][blk] * 1024u - 0x24002400u, s1 = z1[v][blk] * 1024u - 0x24002400u;
-                        uint32_t b0[NT], b1[NT];
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            b0[t] = hmul2(p0[v][t], s0);
-                            b1[t] = hmul2(p1[v][t], s1);
-                        }
+                        uint32_t b0 = hmul2(p0[v], s0), b1 = hmul2(p1[v], s1);
                         if (bad) { /* a block of NaN makes its channels NaN for every row that sees the token */
                             Seg sg;
                             int4 f;
@@ -598,22 +573,19 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
                             const Span sp = span_of(a, f.x, f.y);
                             const int R = f.y * a.group, tok = (u + v < sp.sink_u ? u + v : u + v + sp.lo_u - sp.sink_u) * kUnit;
 #pragma unroll
-                            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    if (((vw[v][blk] >> (8 * j)) & 0xFFu) != 255u) continue;
-                                    const int at = tok + 2 * c + (j & 1) + 8 * (j >> 1);
-                                    const int p = f.x - f.y + min(sg.r0 + 8 * t + g, R - 1) / a.group;
-                                    if (at > p || (a.window && at <= p - a.window && at >= a.sinks)) continue;
-                                    (j < 2 ? b0[t] : b1[t]) |= 0x7FFFu << (16 * (j & 1));
-                                }
+                            for (int j = 0; j < 4; ++j) {
+                                if (((vw[v][blk] >> (8 * j)) & 0xFFu) != 255u) continue;
+                                const int at = tok + 2 * c + (j & 1) + 8 * (j >> 1);
+                                const int p = f.x - f.y + min(sg.r0 + g, R - 1) / a.group;
+                                if (at > p || (a.window && at <= p - a.window && at >= a.sinks)) continue;
+                                (j < 2 ? b0 : b1) |= 0x7FFFu << (16 * (j & 1));
+                            }
                         }
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             uint32_t ra[4];
                             e2m1x8_f16(ww[2 * bb + j], ra);
-#pragma unroll
-                            for (int t = 0; t < NT; ++t) mma16816(o[t][2 * blk + j], ra[0], ra[1], ra[2], ra[3], b0[t], b1[t]);
+                            mma16816(o[2 * blk + j], ra[0], ra[1], ra[2], ra[3], b0, b1);
                         }
                     }
                 }
@@ -624,11 +596,9 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
         /* the lanes' sums; values are held relative to 2^(ref - 127) per block (ref = 0 or
          * -8: nothing but blocks of zeros so far, a NaN there stays one) */
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int w = 4; w < 32; w <<= 1) l[t][j] += __shfl_xor_sync(kAll, l[t][j], w);
+            for (int w = 4; w < 32; w <<= 1) l[j] += __shfl_xor_sync(kAll, l[j], w);
         Seg sg;
         int4 f;
         look_up(sg, f);
@@ -640,54 +610,51 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
             back[k] = ref > 0 ? __uint_as_float((uint32_t)ref << 23) : 0.f;
         }
         if (sg.u0 == 0 && sg.u1 == sg.units) {
+            float inv[2];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                float inv[2];
+            for (int j = 0; j < 2; ++j) {
+                inv[j] = l[j] == 0.f ? 0.f : 1.f / l[j];
+                const int r = r0 + 2 * c + j;
+                if (a.lse && g == 0 && r < R)
+                    a.lse[(int64_t)(f.z + r / a.group) * a.n_q_heads + h * a.group + r % a.group] =
+                        l[j] == 0.f ? -INFINITY : (m[j] - kBias + log2f(l[j])) * kLn2;
+            }
+            /* 8 x 8 transpositions turn channels g of rows 2c, 2c + 1 into channels 2c,
+             * 2c + 1 of row g (FP32 rows are stored as they lie) */
+            if (a.out.dtype != EC_DTYPE_FP32) {
+                const int r = r0 + g;
+                const int64_t off = (int64_t)(f.z + r / a.group) * a.out.row + (int64_t)(h * a.group + r % a.group) * a.out.head + 2 * c;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    inv[j] = l[t][j] == 0.f ? 0.f : 1.f / l[t][j];
-                    const int r = r0 + 8 * t + 2 * c + j;
-                    if (a.lse && g == 0 && r < R)
-                        a.lse[(int64_t)(f.z + r / a.group) * a.n_q_heads + h * a.group + r % a.group] =
-                            l[t][j] == 0.f ? -INFINITY : (m[t][j] - kBias + log2f(l[t][j])) * kLn2;
-                }
-                /* 8 x 8 transpositions turn channels g of rows 2c, 2c + 1 into channels 2c,
-                 * 2c + 1 of row g (FP32 rows are stored as they lie) */
-                if (a.out.dtype != EC_DTYPE_FP32) {
-                    const int r = r0 + 8 * t + g;
-                    const int64_t off = (int64_t)(f.z + r / a.group) * a.out.row + (int64_t)(h * a.group + r % a.group) * a.out.head + 2 * c;
-#pragma unroll
-                    for (int i = 0; i < 2 * NB; ++i)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const float v0 = o[t][i][2 * j] * back[i / 2] * inv[0], v1 = o[t][i][2 * j + 1] * back[i / 2] * inv[1];
-                            uint32_t w;
-                            if (a.out.dtype == EC_DTYPE_FP16) w = pack_f16(v0, v1);
-                            else {
-                                const __nv_bfloat162 y = __floats2bfloat162_rn(v0, v1);
-                                w = *(const uint32_t*)&y;
-                            }
-                            w = transpose8x8(w);
-                            if (r < R) {
-                                uint16_t* at = (uint16_t*)a.out.data + off + 16 * i + 8 * j;
-                                if (a.out.wide) *(uint32_t*)at = w;
-                                else {
-                                    at[0] = (uint16_t)w;
-                                    at[1] = (uint16_t)(w >> 16);
-                                }
-                            }
-                        }
-                } else {
+                for (int i = 0; i < 2 * NB; ++i)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const int r = r0 + 8 * t + 2 * c + j;
-                        if (r >= R) continue;
-                        float* at = (float*)a.out.data + (int64_t)(f.z + r / a.group) * a.out.row + (int64_t)(h * a.group + r % a.group) * a.out.head + g;
-#pragma unroll
-                        for (int i = 0; i < 2 * NB; ++i) {
-                            at[16 * i] = o[t][i][j] * back[i / 2] * inv[j];
-                            at[16 * i + 8] = o[t][i][j + 2] * back[i / 2] * inv[j];
+                        const float v0 = o[i][2 * j] * back[i / 2] * inv[0], v1 = o[i][2 * j + 1] * back[i / 2] * inv[1];
+                        uint32_t w;
+                        if (a.out.dtype == EC_DTYPE_FP16) w = pack_f16(v0, v1);
+                        else {
+                            const __nv_bfloat162 y = __floats2bfloat162_rn(v0, v1);
+                            w = *(const uint32_t*)&y;
                         }
+                        w = transpose8x8(w);
+                        if (r < R) {
+                            uint16_t* at = (uint16_t*)a.out.data + off + 16 * i + 8 * j;
+                            if (a.out.wide) *(uint32_t*)at = w;
+                            else {
+                                at[0] = (uint16_t)w;
+                                at[1] = (uint16_t)(w >> 16);
+                            }
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int r = r0 + 2 * c + j;
+                    if (r >= R) continue;
+                    float* at = (float*)a.out.data + (int64_t)(f.z + r / a.group) * a.out.row + (int64_t)(h * a.group + r % a.group) * a.out.head + g;
+#pragma unroll
+                    for (int i = 0; i < 2 * NB; ++i) {
+                        at[16 * i] = o[i][j] * back[i / 2] * inv[j];
+                        at[16 * i + 8] = o[i][j + 2] * back[i / 2] * inv[j];
                     }
                 }
             }
@@ -697,20 +664,18 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
             const int slot = sg.u0 == 0 ? 1 : 0;
             float* mine = (float*)(at_smem + warp * H::WARP_BYTES + (slot ? 0 : H::RING));
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int r = 8 * t + 2 * c + j;
-                    if (g == 0) {
-                        mine[RB * LD + r] = m[t][j];
-                        mine[RB * LD + RB + r] = l[t][j];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2 * NB; ++i) {
-                        mine[r * LD + 16 * i + g] = o[t][i][j] * back[i / 2];
-                        mine[r * LD + 16 * i + 8 + g] = o[t][i][j + 2] * back[i / 2];
-                    }
+            for (int j = 0; j < 2; ++j) {
+                const int r = 2 * c + j;
+                if (g == 0) {
+                    mine[RB * LD + r] = m[j];
+                    mine[RB * LD + RB + r] = l[j];
                 }
+#pragma unroll
+                for (int i = 0; i < 2 * NB; ++i) {
+                    mine[r * LD + 16 * i + g] = o[i][j] * back[i / 2];
+                    mine[r * LD + 16 * i + 8 + g] = o[i][j + 2] * back[i / 2];
+                }
+            }
             if (lane == 0) {
                 slot_tile[2 * warp + slot] = sg.tile;
                 slot_flags[2 * warp + slot] = (sg.u0 == 0 ? 1 : 0) | (sg.u1 == sg.units ? 2 : 0);
@@ -769,9 +734,9 @@ __global__ void __launch_bounds__(Shape<NB, NT>::W * 32, Shape<NB, NT>::CTAS) kv
 
 /* Join the partial results of a tile that several shares cover: CTA i adds, in order, the
  * parts of the tile that begins in share i and does not end there (if there is one). */
-template <int NB, int NT>
+template <int NB>
 __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ AttnArgs a) {
-    using H = Shape<NB, NT>;
+    using H = Shape<NB>;
     constexpr int D = H::D, RB = H::RB, PS = RB * (D + 2);
     grid_dep_launch();
     grid_dep_wait();
@@ -801,15 +766,15 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ At
 
 /* ------------------------------------------------------------ launch */
 struct Plan {
-    int nt, grid, solo;
+    int grid, solo;
     size_t work;
     bool many;         /* the tensor-memory form */
     PrefillPlan pre;
 };
 
-template <int NB, int NT>
+template <int NB>
 static void plan_shape(Plan* p, int sms, int64_t tiles, int64_t units) {
-    using H = Shape<NB, NT>;
+    using H = Shape<NB>;
     /* up to 4 units per warp there is nothing to gain from splitting a tile, and one launch does
      * (17 tokens: 8 us; the split way adds the join's launch, about 4 us) */
     p->solo = units <= 4 * H::W && tiles < 0x7FFFFFFF ? (int)((units + H::W - 1) / H::W) * H::W : 0;
@@ -817,55 +782,59 @@ static void plan_shape(Plan* p, int sms, int64_t tiles, int64_t units) {
     p->work = p->solo ? 0 : (size_t)p->grid * (2 * H::RB * (H::D + 2) * sizeof(float) + sizeof(JoinJob));
 }
 
-/* Query rows per key/value head up to which the register form runs: it expands the tokens
- * once per 16 rows (8 above 128 channels), the tensor-memory form once per 128 or 256.
- * Measured with 128 channels (us, register form / tensor-memory form): 16 sequences with a
- * window of 4096, 24 rows 61 / 69, 40 rows 82 / 69; 32 sequences of 500 to 3000 tokens, 32
- * rows 53 / 63; one of 30000, 40 rows 52 / 42. */
-constexpr int64_t few_rows(int nb) { return nb <= 4 ? 32 : 16; }
+/* Query rows per sequence and key/value head, on average, up to which the register form
+ * runs (with up to twice as many in any one sequence): it expands the tokens once per 8
+ * rows, the tensor-memory form once per 128 or 256.
+ * Measured (us, register form / tensor-memory form), 16 sequences of 4100 tokens, 128
+ * channels: 16 rows 40 / 66, 24 rows 53 / 66, 32 rows 65 / 66, 40 rows 78 / 66, 8 to 40 rows
+ * (24 on average) 51 / 68; 64 channels: 40 rows 50 / 61, 64 rows 72 / 61; 256 channels: 16
+ * rows 81 / 118, 24 rows 109 / 119, 32 rows 137 / 118; 192 channels: 24 rows 78 / 107, 40
+ * rows 118 / 107.  One sequence of 30000 and 128 channels, 40 rows: 41 / 42. */
+constexpr int64_t few_rows(int nb) { return nb == 2 ? 40 : nb == 4 ? 32 : 24; }
 
 /* false: more work than the kernels count (one sequence's places fit 31 bits) */
-static bool plan_of(const ec_kv* C, int sms, int n_seqs, int max_new, int64_t max_len, const ec_kv_attn* at, int dtype, Plan* p) {
+static bool plan_of(const ec_kv* C, int sms, int n_seqs, int64_t n_rows, int max_new, int64_t max_len, const ec_kv_attn* at, int dtype, Plan* p) {
     const int group = at->n_q_heads / C->p.n_kv_heads, nb = C->p.head_dim / 32;
     const int64_t rows = (int64_t)group * max_new;
-    p->nt = rows > 8 && nb <= 4 ? 2 : 1;
     int64_t units = (max_len + kUnit - 1) / kUnit;
     if (at->window) {
         const int64_t w = ((int64_t)at->window + max_new + kUnit) / kUnit + 1 + (at->sinks + kUnit - 1) / kUnit;
         if (w < units) units = w;
     }
     if (units < 1) units = 1;
-    p->many = rows > few_rows(nb);
+    const int64_t per_seq = (rows + 7) / 8 * C->p.n_kv_heads, tiles = per_seq * n_seqs;
+    p->many = rows > 2 * few_rows(nb) || (rows > few_rows(nb) && n_rows > few_rows(nb) * n_seqs / group) ||
+              per_seq > 0x7FFFFFFF / (units + kTileCost);
     if (p->many) {
         p->grid = p->solo = 0;
         if (!plan_prefill(C, sms, n_seqs, max_new, units, group, dtype, &p->pre)) return false;
         p->work = p->pre.work;
         return true;
     }
-    const int64_t row_tiles = (rows + 8 * p->nt - 1) / (8 * p->nt), per_seq = row_tiles * C->p.n_kv_heads, tiles = per_seq * n_seqs;
-    if (rows > 0x7FFFFFFF || per_seq > 0x7FFFFFFF / (units + kTileCost)) return false;
-    if (nb == 2) p->nt == 1 ? plan_shape<2, 1>(p, sms, tiles, units) : plan_shape<2, 2>(p, sms, tiles, units);
-    else if (nb == 4) p->nt == 1 ? plan_shape<4, 1>(p, sms, tiles, units) : plan_shape<4, 2>(p, sms, tiles, units);
-    else if (nb == 6) plan_shape<6, 1>(p, sms, tiles, units);
-    else plan_shape<8, 1>(p, sms, tiles, units);
+    switch (nb) {
+        case 2: plan_shape<2>(p, sms, tiles, units); break;
+        case 4: plan_shape<4>(p, sms, tiles, units); break;
+        case 6: plan_shape<6>(p, sms, tiles, units); break;
+        default: plan_shape<8>(p, sms, tiles, units);
+    }
     return true;
 }
 
-template <int NB, int NT, int QT>
+template <int NB, int QT>
 static int run_attn(const AttnArgs& a, const Plan& p, cudaStream_t stream) {
-    using H = Shape<NB, NT>;
+    using H = Shape<NB>;
     static SmemOnce once;
-    int rc = once.set(kv_attn_kernel<NB, NT, QT>, H::smem(EC_KV_MAX_SEQS));
+    int rc = once.set(kv_attn_kernel<NB, QT>, H::smem(EC_KV_MAX_SEQS));
     if (rc != EC_OK) return rc;
-    rc = launch(kv_attn_kernel<NB, NT, QT>, dim3(p.grid), H::W * 32, H::smem(a.S.n_seqs), stream, a);
+    rc = launch(kv_attn_kernel<NB, QT>, dim3(p.grid), H::W * 32, H::smem(a.S.n_seqs), stream, a);
     if (rc == EC_OK && !p.solo)
-        rc = launch(kv_join_kernel<NB, NT>, dim3(p.grid), 256, 0, stream, a);
+        rc = launch(kv_join_kernel<NB>, dim3(p.grid), 256, 0, stream, a);
     return rc;
 }
 
-template <int NB, int NT>
+template <int NB>
 static int run_terms(const AttnArgs& a, const Plan& p, cudaStream_t stream) {
-    return a.q.dtype == EC_DTYPE_FP32 ? run_attn<NB, NT, 2>(a, p, stream) : run_attn<NB, NT, 1>(a, p, stream);
+    return a.q.dtype == EC_DTYPE_FP32 ? run_attn<NB, 2>(a, p, stream) : run_attn<NB, 1>(a, p, stream);
 }
 
 static int check_attn(const ec_kv* C, int n_seqs, int64_t n_rows, int max_new, int64_t max_len, const ec_kv_attn* at) {
@@ -894,11 +863,15 @@ extern "C" int ec_kv_attend_work_bytes(const ec_kv* C, int n_seqs, int64_t n_row
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return EC_ERR_CUDA;
     } else sms = 152;
-    Plan p, f; /* FP32 queries take smaller row tiles */
-    if (!plan_of(C, sms, n_seqs, max_new, max_len, attn, EC_DTYPE_BF16, &p) ||
-        !plan_of(C, sms, n_seqs, max_new, max_len, attn, EC_DTYPE_FP32, &f))
-        return EC_ERR_UNSUPPORTED;
-    *bytes = p.work > f.work ? p.work : f.work;
+    /* FP32 queries take smaller row tiles, and fewer rows may take the other form: the largest,
+     * so that a buffer for n_rows serves calls with fewer */
+    *bytes = 0;
+    for (int64_t rows : {n_rows, (int64_t)0})
+        for (int dtype : {EC_DTYPE_BF16, EC_DTYPE_FP32}) {
+            Plan p;
+            if (!plan_of(C, sms, n_seqs, rows, max_new, max_len, attn, dtype, &p)) return EC_ERR_UNSUPPORTED;
+            if (p.work > *bytes) *bytes = p.work;
+        }
     return EC_OK;
 }
 
@@ -923,7 +896,7 @@ extern "C" int ec_kv_attend(const ec_kv* C, const ec_kv_attention* t, cudaStream
     if ((rc = device_of(C, &d)) != EC_OK) return rc;
     if (t->seqs.n_seqs == 0 || t->n_rows == 0 || t->max_new == 0) return EC_OK;
     Plan p;
-    if (!plan_of(C, d.sms, t->seqs.n_seqs, t->max_new, max_len, &at, t->q.dtype, &p)) return EC_ERR_UNSUPPORTED;
+    if (!plan_of(C, d.sms, t->seqs.n_seqs, t->n_rows, t->max_new, max_len, &at, t->q.dtype, &p)) return EC_ERR_UNSUPPORTED;
     if (p.work && (!t->work || (uintptr_t)t->work % 16 || t->work_bytes < p.work)) return EC_ERR_INVALID_ARG;
     a.S = Seqs{t->seqs.table, t->seqs.lens, t->starts, t->seqs.table_stride, t->n_rows, t->seqs.n_seqs};
     a.lse = t->lse;
@@ -939,9 +912,9 @@ extern "C" int ec_kv_attend(const ec_kv* C, const ec_kv_attention* t, cudaStream
     a.status = d.status;
     if (p.many) return launch_prefill(a, p.pre, stream);
     switch (C->p.head_dim / 32) {
-        case 2: return p.nt == 1 ? run_terms<2, 1>(a, p, stream) : run_terms<2, 2>(a, p, stream);
-        case 4: return p.nt == 1 ? run_terms<4, 1>(a, p, stream) : run_terms<4, 2>(a, p, stream);
-        case 6: return run_terms<6, 1>(a, p, stream);
-        default: return run_terms<8, 1>(a, p, stream);
+        case 2: return run_terms<2>(a, p, stream);
+        case 4: return run_terms<4>(a, p, stream);
+        case 6: return run_terms<6>(a, p, stream);
+        default: return run_terms<8>(a, p, stream);
     }
 }

@@ -252,6 +252,34 @@ def test_prompts(ec, qh, kvh, dim, dtype):
     check_attend(ec, c, k, v, [130, 129, 1, 333], qh, dtype, FP16 if dtype == FP16 else BF16)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("new", [[8, 1, 0, 1, 2], [8, 8, 8, 8, 7], [3, 3, 3, 3, 3], [4, 4, 4, 4, 4], [6, 1, 6, 1, 6], [11, 1, 1, 1, 1]])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_tens_of_rows(ec, dim, new, dtype):
+    """Row counts around those where few rows become many, alike and unlike in a batch."""
+    c = Case(ec, [900, 15, 0, 1, 333], 1, dim, 32)
+    k, v = c.tensors(15, dtype)
+    c.fill(k, v)
+    check_attend(ec, c, k, v, new, 8, dtype)
+    check_attend(ec, c, k, v, new, 8, dtype, window=50, sinks=4)
+
+
+def test_work_for_many_rows_serves_fewer(ec):
+    """A buffer sized for the most rows serves every call of the same bounds with fewer."""
+    c = Case(ec, [2000, 1500, 900, 40], 2, 128, 64)
+    k, v = c.tensors(16)
+    c.fill(k, v)
+    most = ec.kv_attend_work_bytes(c.cache, 4, 20, 16, 5, 2000)
+    for new in ([5, 5, 5, 5], [5, 1, 1, 1], [1, 0, 0, 5]):
+        assert ec.kv_attend_work_bytes(c.cache, 4, sum(new), 16, 5, 2000) <= most
+        q = torch.randn((sum(new), 16, 128), device="cuda").to(BF16)
+        outs = [torch.empty_like(q) for _ in range(2)]
+        ec.kv_attend(c.cache, 0, c.seqs, q, outs[0], starts=starts_of(new), max_new=5, max_len=2000,
+                     work=torch.empty(most, dtype=torch.uint8, device="cuda"))
+        ec.kv_attend(c.cache, 0, c.seqs, q, outs[1], starts=starts_of(new), max_new=5, max_len=2000)
+        assert torch.equal(outs[0], outs[1])
+
+
 @pytest.mark.parametrize("window,sinks", [(100, 0), (17, 3), (128, 130), (1, 1)])
 @pytest.mark.parametrize("qh,kvh,dim", [(8, 2, 128), (4, 4, 64), (6, 2, 192), (4, 2, 256)])
 def test_prompts_with_windows(ec, window, sinks, qh, kvh, dim):
