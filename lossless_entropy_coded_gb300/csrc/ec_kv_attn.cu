@@ -52,11 +52,10 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int len, int m) {
 __device__ __forceinline__ int tile_cost(const AttnArgs& a, int units) { return a.solo ? a.solo : units + kTileCost; }
 
 /* Per sequence, in shared memory: pre[b], the work in front of it (pre[n_seqs]: all work),
- * and {len, new tokens, first row, units}.  Every thread of the CTA takes part. */
-template <int W>
-__device__ __forceinline__ void scan_seqs(const AttnArgs& a, int rows_per_tile, int64_t* pre, int4* info, bool flag) {
-    __shared__ int64_t warp_sum[W];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+ * and {len, new tokens, first row}.  Every thread of the CTA takes part. */
+__device__ __forceinline__ void scan_seqs(const AttnArgs& a, int rows_per_tile, int64_t* pre, int3* info, bool flag) {
+    __shared__ int64_t warp_work[16];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
     int64_t at = 0;
     for (int base = 0; base < a.S.n_seqs; base += 32 * W) {
         const int b = base + threadIdx.x;
@@ -73,7 +72,7 @@ __device__ __forceinline__ void scan_seqs(const AttnArgs& a, int rows_per_tile, 
             }
             if (flag && q.bad) flag_corrupt(a.status);
             const int units = span_of(a, q.len, q.m).units;
-            info[b] = make_int4(q.len, q.m, (int)q.row0, units);
+            info[b] = make_int3(q.len, q.m, (int)q.row0);
             n = (int64_t)((q.m * a.group + rows_per_tile - 1) / rows_per_tile) * a.P.n_heads * tile_cost(a, units);
         }
         int64_t x = n;
@@ -83,12 +82,11 @@ __device__ __forceinline__ void scan_seqs(const AttnArgs& a, int rows_per_tile, 
             if (lane >= o) x += y;
         }
         if (base) __syncthreads(); /* the sums of the sequences before have been read */
-        if (lane == 31) warp_sum[warp] = x;
+        if (lane == 31) warp_work[warp] = x;
         __syncthreads();
         int64_t front = at;
-#pragma unroll
         for (int w = 0; w < W; ++w) {
-            const int64_t y = warp_sum[w];
+            const int64_t y = warp_work[w];
             if (w < warp) front += y;
             at += y;
         }
@@ -104,7 +102,7 @@ struct Seg {
     int b, h, r0, u0, u1, units;
     int64_t tile, next;
 };
-__device__ __forceinline__ Seg seg_at(const AttnArgs& a, const int64_t* pre, const int4* info, int rows_per_tile, int64_t x, int64_t end) {
+__device__ __forceinline__ Seg seg_at(const AttnArgs& a, const int64_t* pre, const int3* info, int rows_per_tile, int64_t x, int64_t end) {
     int lo = 0, hi = a.S.n_seqs - 1; /* the last sequence whose work begins at x or before (those without any come before it) */
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
@@ -113,7 +111,7 @@ __device__ __forceinline__ Seg seg_at(const AttnArgs& a, const int64_t* pre, con
     }
     Seg s;
     s.b = lo;
-    s.units = info[lo].w;
+    s.units = span_of(a, info[lo].x, info[lo].y).units;
     const uint32_t per = (uint32_t)tile_cost(a, s.units), local = (uint32_t)(x - pre[lo]), tile = local / per, off = local - tile * per;
     s.tile = x - off;
     s.next = min(s.tile + per, end);
@@ -163,21 +161,35 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
  * scales lie up to 2^7 above their block's reference: 2^(5 + 3 + 7) < 65504. */
 constexpr float kBias = 5.f;
 
-/* Warps per CTA, CTAs per SM and stages of a warp's ring by the tile's registers; `keep`
- * floats hold a warp's partial result of a tile: [rows][LD], maxima, sums. */
+/* Warps per SM and stages of a warp's ring by the tile's registers; `keep` floats hold a
+ * warp's partial result of a tile: [rows][LD], maxima, sums.  All warps of an SM form one
+ * CTA: of two CTAs the SM favours one, whose warps are done at 66 us of 81 with 400000
+ * tokens, and the other's go on alone.  Where a tile has a CTA of its own (solo) it has half
+ * the warps. */
 template <int NB>
 struct Shape {
     static constexpr int D = 32 * NB, RB = 8, LD = D + 4, UB = 17 * D;
-    static constexpr int W = NB <= 4 ? 8 : 4;
-    static constexpr int CTAS = 2;
+    static constexpr int W = NB <= 4 ? 16 : 8;
     static constexpr int S = NB == 2 ? 4 : 2; /* of two units each; a power of two */
     static constexpr int KEEP = RB * LD + 2 * RB;
     static constexpr int RING = S * 2 * UB, WARP_BYTES = RING + KEEP * 4 + 64; /* + the warp's segment */
     static_assert(KEEP * 4 <= RING, "a second partial result fits the ring");
-    static constexpr size_t smem(int n_seqs) {
-        return (size_t)W * WARP_BYTES + W * S * 8 + 2 * W * 8 + 2 * W * 4 + 16 * (size_t)n_seqs + 8 * ((size_t)n_seqs + 1) + 16;
+    static constexpr size_t smem(int n_seqs, int warps) {
+        return (size_t)warps * (WARP_BYTES + 8 * S + 2 * 8 + 2 * 4) + 8 * ((size_t)n_seqs + 1) + 12 * (size_t)n_seqs;
     }
+    static_assert(W <= 16 && smem(EC_KV_MAX_SEQS, W) + 16 * 8 <= 232448, "shared memory");
 };
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, w));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) v += __shfl_xor_sync(kAll, v, w);
+    return v;
+}
 
 /* Four channels of a tile's row r from its unnormalised sums v, L relative to M. */
 __device__ __forceinline__ void write_row(const AttnArgs& a, int row0, int h, int r, int d, const float4& v, float M, float L) {
@@ -201,19 +213,18 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int row0, int h, in
  * Units come by bulk copies through a ring of the warp's own, several ahead and across
  * tiles. */
 template <int NB, int QT>
-__global__ void __launch_bounds__(Shape<NB>::W * 32, Shape<NB>::CTAS) kv_attn_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __grid_constant__ AttnArgs a) {
     using H = Shape<NB>;
-    constexpr int D = H::D, RB = H::RB, S = H::S, UB = H::UB, LD = H::LD, W = H::W;
+    constexpr int D = H::D, RB = H::RB, S = H::S, UB = H::UB, LD = H::LD;
     extern __shared__ __align__(128) uint8_t at_smem[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5, g = lane >> 2, c = lane & 3;
     const uint32_t ring = smem_u32(at_smem) + warp * H::WARP_BYTES;
     uint8_t* tail = at_smem + W * H::WARP_BYTES;
     const uint32_t bars = smem_u32(tail) + warp * S * 8, own = ring + H::RING + H::KEEP * 4;
     int64_t* slot_tile = (int64_t*)(tail + W * S * 8);   /* [2 W]: a warp's first and last partial tile, -1: none */
     int32_t* slot_flags = (int32_t*)(slot_tile + 2 * W); /* bit 0: the tile's first unit is in, bit 1: its last */
-    int4* info = (int4*)(slot_flags + 2 * W);
-    int64_t* pre = (int64_t*)(info + a.S.n_seqs);
-    static_assert((W * S * 8 + 2 * W * 8 + 2 * W * 4) % 16 == 0, "info is 16-byte aligned");
+    int64_t* pre = (int64_t*)(slot_flags + 2 * W);
+    int3* info = (int3*)(pre + a.S.n_seqs + 1);
     if (lane == 0) {
         for (int s = 0; s < S; ++s) mbar_init(bars + 8 * s, 1);
         mbar_fence_init();
@@ -221,7 +232,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, Shape<NB>::CTAS) kv_attn_ke
     }
     grid_dep_launch();
     grid_dep_wait();
-    scan_seqs<W>(a, RB, pre, info, blockIdx.x == 0);
+    scan_seqs(a, RB, pre, info, blockIdx.x == 0);
     const int64_t X = pre[a.S.n_seqs];
     const int64_t share = share_of(a, X, gridDim.x, W);
     const int64_t x0 = min(X, blockIdx.x * share), x1 = min(X, x0 + share);
@@ -244,7 +255,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, Shape<NB>::CTAS) kv_attn_ke
             while (pn == 0) {
                 if (px >= x_end) return;
                 const Seg s = seg_at(a, pre, info, RB, px, x_end);
-                const int4 f = info[s.b];
+                const int3 f = info[s.b];
                 const Span sp = span_of(a, f.x, f.y);
                 pn = f.x > 0 ? min(32, max(0, s.u1 - s.u0)) : 0;
                 px = pn == 32 ? s.tile + s.u0 + 32 : s.next;
@@ -278,18 +289,18 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, Shape<NB>::CTAS) kv_attn_ke
     while (x < x_end) {
         /* (the segment lies in shared memory for its masked ends and for what follows the loop,
          * so that the loop need not keep it in registers) */
-        auto look_up = [&](Seg& sg, int4& f) {
+        auto look_up = [&](Seg& sg, int3& f) {
             const uint4 p = lds128(own), q = lds128(own + 16), r = lds128(own + 32);
             sg.b = (int)p.x, sg.h = (int)p.y, sg.r0 = (int)p.z, sg.u0 = (int)p.w;
             sg.u1 = (int)q.x, sg.units = (int)q.y, sg.tile = (int64_t)((uint64_t)q.w << 32 | q.z);
-            f = make_int4((int)r.x, (int)r.y, (int)r.z, (int)r.w);
+            f = make_int3((int)r.x, (int)r.y, (int)r.z);
         };
         int u = 0, u1 = 0, all_lo = 0, all_hi = 0;
         uint32_t qf[QT][NB][4];
         float fac[2];
         {
             const Seg sg = seg_at(a, pre, info, RB, x, x_end);
-            const int4 f = info[sg.b];
+            const int3 f = info[sg.b];
             x = sg.next;
             if (sg.u0 >= sg.u1) continue;
             __syncwarp();
@@ -297,7 +308,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, Shape<NB>::CTAS) kv_attn_ke
                 uint4* o = (uint4*)(at_smem + warp * H::WARP_BYTES + H::RING + H::KEEP * 4);
                 o[0] = make_uint4(sg.b, sg.h, sg.r0, sg.u0);
                 o[1] = make_uint4(sg.u1, sg.units, (uint32_t)sg.tile, (uint32_t)((uint64_t)sg.tile >> 32));
-                o[2] = make_uint4(f.x, f.y, f.z, f.w);
+                o[2] = make_uint4(f.x, f.y, f.z, 0);
             }
             __syncwarp();
             const Span sp = span_of(a, f.x, f.y);
@@ -423,7 +434,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, Shape<NB>::CTAS) kv_attn_ke
             uint32_t vmask[2] = {0u, 0u}; /* masked: bytes of tokens 2c, 2c + 1, 2c + 8, 2c + 9 that some row sees */
             if (masked) { /* a place that a row does not see: score -inf */
                 Seg sg;
-                int4 f;
+                int3 f;
                 look_up(sg, f);
                 const Span sp = span_of(a, f.x, f.y);
                 const int R = f.y * a.group, first = f.x - f.y, skip = sp.lo_u - sp.sink_u;
@@ -568,7 +579,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, Shape<NB>::CTAS) kv_attn_ke
                         uint32_t b0 = hmul2(p0[v], s0), b1 = hmul2(p1[v], s1);
                         if (bad) { /* a block of NaN makes its channels NaN for every row that sees the token */
                             Seg sg;
-                            int4 f;
+                            int3 f;
                             look_up(sg, f);
                             const Span sp = span_of(a, f.x, f.y);
                             const int R = f.y * a.group, tok = (u + v < sp.sink_u ? u + v : u + v + sp.lo_u - sp.sink_u) * kUnit;
@@ -600,7 +611,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, Shape<NB>::CTAS) kv_attn_ke
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1) l[j] += __shfl_xor_sync(kAll, l[j], w);
         Seg sg;
-        int4 f;
+        int3 f;
         look_up(sg, f);
         const int h = sg.h, r0 = sg.r0, R = f.y * a.group;
         float back[NB];
@@ -683,90 +694,108 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, Shape<NB>::CTAS) kv_attn_ke
         }
     }
 
-    /* join the warps' parts, tile by tile, in order */
+    /* join the warps' parts, tile by tile, in order: lane k holds slot k's tile, 8 warps take a
+     * tile, a row each */
     __syncthreads();
-    for (int s0 = 0; s0 < 2 * W;) {
-        const int64_t tile = slot_tile[s0];
-        if (tile < 0) {
-            ++s0;
-            continue;
-        }
-        int s1 = s0, last = s0;
-        while (s1 < 2 * W && (slot_tile[s1] < 0 || slot_tile[s1] == tile)) {
-            if (slot_tile[s1] == tile) last = s1;
-            ++s1;
-        }
-        const bool whole = (slot_flags[s0] & 1) && (slot_flags[last] & 2);
+    const int64_t slot = lane < 2 * W ? slot_tile[lane] : -1;
+    const int flags = lane < 2 * W ? slot_flags[lane] : 0;
+    const float* kept = (const float*)(at_smem + (lane / 2) * H::WARP_BYTES + (lane & 1 ? 0 : H::RING));
+    uint32_t left = __ballot_sync(kAll, slot >= 0);
+    for (int n = 0; left; ++n) {
+        const int s0 = __ffs(left) - 1;
+        const int64_t tile = __shfl_sync(kAll, slot, s0);
+        const uint32_t of = __ballot_sync(kAll, slot == tile);
+        left &= ~of;
+        const bool begins = __shfl_sync(kAll, flags, s0) & 1, whole = begins && (__shfl_sync(kAll, flags, 31 - __clz(of)) & 2);
+        if (W > RB && n % (W / RB) != warp / RB) continue;
         const Seg sg = seg_at(a, pre, info, RB, tile, X);
-        const int4 f = info[sg.b];
+        const int3 f = info[sg.b];
         const int R = f.y * a.group;
-        if (threadIdx.x == 0 && !whole && (slot_flags[s0] & 1)) { /* the tile begins here: how many shares it covers */
+        if (warp % RB == 0 && lane == 0 && !whole && begins) { /* the tile begins here: how many shares it covers */
             todo->parts = (int)((tile + sg.units - 1) / share) - (int)blockIdx.x + 1;
             todo->h = sg.h, todo->r0 = sg.r0, todo->R = R, todo->row0 = f.z;
         }
-        float* part = a.part + ((int64_t)blockIdx.x * 2 + (slot_flags[s0] & 1)) * (RB * (D + 2));
-        for (int e = threadIdx.x; e < RB * (D / 4); e += W * 32) {
-            const int r = e / (D / 4), d = 4 * (e % (D / 4));
-            if (sg.r0 + r >= R) continue;
-            float M = -FLT_MAX, L = 0.f;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = s0; k <= last; ++k) {
-                if (slot_tile[k] != tile) continue;
-                const float* p = (const float*)(at_smem + (k / 2) * H::WARP_BYTES + (k & 1 ? 0 : H::RING));
-                const float pm = p[RB * LD + r], nm = fmaxf(M, pm), fo = ex2(M - nm), fp = ex2(pm - nm);
-                const float4 y = *(const float4*)&p[r * LD + d];
-                M = nm;
-                L = L * fo + p[RB * LD + RB + r] * fp;
-                v.x = v.x * fo + y.x * fp, v.y = v.y * fo + y.y * fp, v.z = v.z * fo + y.z * fp, v.w = v.w * fo + y.w * fp;
-            }
-            if (whole) write_row(a, f.z, sg.h, sg.r0 + r, d, v, M, L);
-            else {
-                *(float4*)&part[r * D + d] = v;
-                if (d == 0) {
-                    part[RB * D + r] = M;
-                    part[RB * D + RB + r] = L;
+        float* part = a.part + ((int64_t)blockIdx.x * 2 + begins) * (RB * (D + 2));
+        for (int r = warp % RB; r < min(RB, R - sg.r0); r += W) {
+            const bool in = (of >> lane) & 1u;
+            const float pm = in ? kept[RB * LD + r] : -FLT_MAX;
+            const float M = warp_max(pm);
+            const float w = in ? ex2(pm - M) : 0.f;
+            const float L = warp_sum(in ? w * kept[RB * LD + RB + r] : 0.f);
+#pragma unroll
+            for (int d0 = 0; d0 < D; d0 += 128) {
+                const int d = d0 + 4 * lane;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (uint32_t k = of; k; k &= k - 1) {
+                    const int i = __ffs(k) - 1;
+                    const float wi = __shfl_sync(kAll, w, i);
+                    if (d >= D) continue;
+                    const float4 y = *(const float4*)((const float*)(at_smem + (i / 2) * H::WARP_BYTES + (i & 1 ? 0 : H::RING)) + r * LD + d);
+                    v.x = fmaf(y.x, wi, v.x), v.y = fmaf(y.y, wi, v.y), v.z = fmaf(y.z, wi, v.z), v.w = fmaf(y.w, wi, v.w);
                 }
+                if (d >= D) continue;
+                if (whole) write_row(a, f.z, sg.h, sg.r0 + r, d, v, M, L);
+                else *(float4*)&part[r * D + d] = v;
+            }
+            if (!whole && lane == 0) {
+                part[RB * D + r] = M;
+                part[RB * D + RB + r] = L;
             }
         }
-        s0 = s1;
     }
 }
 
 /* Join the partial results of a tile that several shares cover: CTA i adds, in order, the
- * parts of the tile that begins in share i and does not end there (if there is one). */
+ * parts of the tile that begins in share i and does not end there (if there is one).  A
+ * warp takes a row, 32 parts at a time: each lane one part's weight, then four channels of
+ * every part, whose loads do not wait for one another. */
 template <int NB>
-__global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(256, 2) kv_join_kernel(const __grid_constant__ AttnArgs a) {
     using H = Shape<NB>;
-    constexpr int D = H::D, RB = H::RB, PS = RB * (D + 2);
+    constexpr int D = H::D, RB = H::RB, PS = RB * (D + 2), NV = (D + 127) / 128;
     grid_dep_launch();
     grid_dep_wait();
     const JoinJob job = ((const JoinJob*)(a.part + (int64_t)gridDim.x * 2 * PS))[blockIdx.x];
-    const int n = job.parts;
-    if (n == 0) return;
-    const float* p0 = a.part + ((int64_t)blockIdx.x * 2 + 1) * PS;  /* the first share's part */
-    const float* p1 = a.part + ((int64_t)blockIdx.x * 2) * PS;      /* share i's: p1 + 2 i PS */
-    for (int e = threadIdx.x; e < RB * (D / 4); e += 256) {
-        const int r = e / (D / 4), d = 4 * (e % (D / 4));
-        if (job.r0 + r >= job.R) continue;
-        float M = p0[RB * D + r];
-        for (int i = 1; i < n; ++i) M = fmaxf(M, p1[(int64_t)2 * i * PS + RB * D + r]);
-        float L = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float* p = i ? p1 + (int64_t)2 * i * PS : p0;
-            const float w = ex2(p[RB * D + r] - M);
+    const int n = job.parts, lane = threadIdx.x & 31, r = threadIdx.x >> 5;
+    if (n == 0 || job.r0 + r >= job.R) return;
+    const float* p1 = a.part + ((int64_t)blockIdx.x * 2) * PS; /* share i's part; the first share's is its second */
+    auto part = [&](int i) { return p1 + (int64_t)(i ? 2 * i : 1) * PS; };
+    float M = -FLT_MAX;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, part(i)[RB * D + r]);
+    M = warp_max(M);
+    float L = 0.f;
+    float4 v[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int cnt = min(32, n - i0);
+        float w = 0.f;
+        if (lane < cnt) {
+            const float* p = part(i0 + lane);
+            w = ex2(p[RB * D + r] - M);
             L = fmaf(p[RB * D + RB + r], w, L);
-            const float4 y = *(const float4*)&p[r * D + d];
-            v.x = fmaf(y.x, w, v.x), v.y = fmaf(y.y, w, v.y), v.z = fmaf(y.z, w, v.z), v.w = fmaf(y.w, w, v.w);
         }
-        write_row(a, job.row0, job.h, job.r0 + r, d, v, M, L);
+#pragma unroll 8
+        for (int j = 0; j < cnt; ++j) {
+            const float wj = __shfl_sync(kAll, w, j);
+            const float* p = part(i0 + j) + r * D + 4 * lane;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                if (128 * k + 4 * lane >= D) continue;
+                const float4 y = *(const float4*)(p + 128 * k);
+                v[k].x = fmaf(y.x, wj, v[k].x), v[k].y = fmaf(y.y, wj, v[k].y), v[k].z = fmaf(y.z, wj, v[k].z), v[k].w = fmaf(y.w, wj, v[k].w);
+            }
+        }
     }
+    L = warp_sum(L);
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+        if (128 * k + 4 * lane < D) write_row(a, job.row0, job.h, job.r0 + r, 128 * k + 4 * lane, v[k], M, L);
 }
 
 /* ------------------------------------------------------------ launch */
 struct Plan {
-    int grid, solo;
+    int grid, solo, warps;
     size_t work;
     bool many;         /* the tensor-memory form */
     PrefillPlan pre;
@@ -776,10 +805,13 @@ template <int NB>
 static void plan_shape(Plan* p, int sms, int64_t tiles, int64_t units) {
     using H = Shape<NB>;
     /* up to 4 units per warp there is nothing to gain from splitting a tile, and one launch does
-     * (17 tokens: 8 us; the split way adds the join's launch, about 4 us) */
-    p->solo = units <= 4 * H::W && tiles < 0x7FFFFFFF ? (int)((units + H::W - 1) / H::W) * H::W : 0;
-    p->grid = p->solo ? (int)tiles : sms * H::CTAS;
-    p->work = p->solo ? 0 : (size_t)p->grid * (2 * H::RB * (H::D + 2) * sizeof(float) + sizeof(JoinJob));
+     * (17 tokens: 8 us; the split way adds the join's launch, about 3 us) */
+    const int w = H::W / 2;
+    const bool solo = units <= 4 * w && tiles < 0x7FFFFFFF;
+    p->solo = solo ? (int)((units + w - 1) / w) * w : 0;
+    p->warps = solo ? w : H::W;
+    p->grid = solo ? (int)tiles : sms;
+    p->work = solo ? 0 : (size_t)p->grid * (2 * H::RB * (H::D + 2) * sizeof(float) + sizeof(JoinJob));
 }
 
 /* Query rows per sequence and key/value head, on average, up to which the register form
@@ -824,9 +856,9 @@ template <int NB, int QT>
 static int run_attn(const AttnArgs& a, const Plan& p, cudaStream_t stream) {
     using H = Shape<NB>;
     static SmemOnce once;
-    int rc = once.set(kv_attn_kernel<NB, QT>, H::smem(EC_KV_MAX_SEQS));
+    int rc = once.set(kv_attn_kernel<NB, QT>, H::smem(EC_KV_MAX_SEQS, H::W));
     if (rc != EC_OK) return rc;
-    rc = launch(kv_attn_kernel<NB, QT>, dim3(p.grid), H::W * 32, H::smem(a.S.n_seqs), stream, a);
+    rc = launch(kv_attn_kernel<NB, QT>, dim3(p.grid), p.warps * 32, H::smem(a.S.n_seqs, p.warps), stream, a);
     if (rc == EC_OK && !p.solo)
         rc = launch(kv_join_kernel<NB>, dim3(p.grid), 256, 0, stream, a);
     return rc;
