@@ -257,6 +257,12 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
                 const Seg s = seg_at(a, pre, info, RB, px, x_end);
                 const int3 f = info[s.b];
                 const Span sp = span_of(a, f.x, f.y);
+                /* the tile's queries, which would wait behind the units otherwise */
+                if (s.r0 + g < f.y * a.group) {
+                    const int r = s.r0 + g, es = a.q.dtype == EC_DTYPE_FP32 ? 4 : 2;
+                    const char* q = (const char*)a.q.data + ((int64_t)(f.z + r / a.group) * a.q.row + (int64_t)(s.h * a.group + r % a.group) * a.q.head) * es;
+                    for (int i = 128 * c; i < D * es; i += 512) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i));
+                }
                 pn = f.x > 0 ? min(32, max(0, s.u1 - s.u0)) : 0;
                 px = pn == 32 ? s.tile + s.u0 + 32 : s.next;
                 if (lane < pn) {
@@ -694,30 +700,33 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
         }
     }
 
-    /* join the warps' parts, tile by tile, in order: lane k holds slot k's tile, 8 warps take a
-     * tile, a row each */
+    /* join the warps' parts, tile by tile, in order: lane k holds slot k's tile; 8, 4, 2 or one
+     * warps take a tile, a row at a time, so that most warps have one */
     __syncthreads();
     const int64_t slot = lane < 2 * W ? slot_tile[lane] : -1;
     const int flags = lane < 2 * W ? slot_flags[lane] : 0;
     const float* kept = (const float*)(at_smem + (lane / 2) * H::WARP_BYTES + (lane & 1 ? 0 : H::RING));
-    uint32_t left = __ballot_sync(kAll, slot >= 0);
-    for (int n = 0; left; ++n) {
-        const int s0 = __ffs(left) - 1;
+    const uint32_t same = __match_any_sync(kAll, slot);
+    uint32_t firsts = __ballot_sync(kAll, slot >= 0 && __ffs(same) - 1 == lane);
+    const int nt = __popc(firsts);
+    const int G = 8 * nt <= W ? 8 : 4 * nt <= W ? 4 : 2 * nt <= W ? 2 : 1; /* 4 at most with 4 warps */
+    for (int n = 0; firsts; ++n, firsts &= firsts - 1) {
+        if (n % (W / G) != warp / G) continue;
+        const int s0 = __ffs(firsts) - 1;
         const int64_t tile = __shfl_sync(kAll, slot, s0);
-        const uint32_t of = __ballot_sync(kAll, slot == tile);
-        left &= ~of;
+        const uint32_t of = __shfl_sync(kAll, same, s0);
         const bool begins = __shfl_sync(kAll, flags, s0) & 1, whole = begins && (__shfl_sync(kAll, flags, 31 - __clz(of)) & 2);
-        if (W > RB && n % (W / RB) != warp / RB) continue;
         const Seg sg = seg_at(a, pre, info, RB, tile, X);
         const int3 f = info[sg.b];
         const int R = f.y * a.group;
-        if (warp % RB == 0 && lane == 0 && !whole && begins) { /* the tile begins here: how many shares it covers */
+        if (warp % G == 0 && lane == 0 && !whole && begins) { /* the tile begins here: how many shares it covers */
             todo->parts = (int)((tile + sg.units - 1) / share) - (int)blockIdx.x + 1;
             todo->h = sg.h, todo->r0 = sg.r0, todo->R = R, todo->row0 = f.z;
         }
         float* part = a.part + ((int64_t)blockIdx.x * 2 + begins) * (RB * (D + 2));
-        for (int r = warp % RB; r < min(RB, R - sg.r0); r += W) {
-            const bool in = (of >> lane) & 1u;
+        const bool in = (of >> lane) & 1u;
+#pragma unroll 1
+        for (int r = warp % G; r < min(RB, R - sg.r0); r += G) {
             const float pm = in ? kept[RB * LD + r] : -FLT_MAX;
             const float M = warp_max(pm);
             const float w = in ? ex2(pm - M) : 0.f;
@@ -726,12 +735,20 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
             for (int d0 = 0; d0 < D; d0 += 128) {
                 const int d = d0 + 4 * lane;
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (uint32_t k = of; k; k &= k - 1) {
-                    const int i = __ffs(k) - 1;
-                    const float wi = __shfl_sync(kAll, w, i);
-                    if (d >= D) continue;
-                    const float4 y = *(const float4*)((const float*)(at_smem + (i / 2) * H::WARP_BYTES + (i & 1 ? 0 : H::RING)) + r * LD + d);
-                    v.x = fmaf(y.x, wi, v.x), v.y = fmaf(y.y, wi, v.y), v.z = fmaf(y.z, wi, v.z), v.w = fmaf(y.w, wi, v.w);
+                for (uint32_t k = of; k;) {
+                    float wi[4];
+                    float4 y[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int i = k ? __ffs(k) - 1 : s0;
+                        wi[j] = __shfl_sync(kAll, w, i);
+                        y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (k && d < D) y[j] = *(const float4*)((const float*)(at_smem + (i / 2) * H::WARP_BYTES + (i & 1 ? 0 : H::RING)) + r * LD + d);
+                        k &= k - 1;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v.x = fmaf(y[j].x, wi[j], v.x), v.y = fmaf(y[j].y, wi[j], v.y), v.z = fmaf(y[j].z, wi[j], v.z), v.w = fmaf(y[j].w, wi[j], v.w);
                 }
                 if (d >= D) continue;
                 if (whole) write_row(a, f.z, sg.h, sg.r0 + r, d, v, M, L);
@@ -747,8 +764,8 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
 
 /* Join the partial results of a tile that several shares cover: CTA i adds, in order, the
  * parts of the tile that begins in share i and does not end there (if there is one).  A
- * warp takes a row, 32 parts at a time: each lane one part's weight, then four channels of
- * every part, whose loads do not wait for one another. */
+ * warp takes a row, 32 parts at a time: each lane one part's maximum and sum, then four
+ * channels of every part, eight parts at a time, whose loads wait for nothing. */
 template <int NB>
 __global__ void __launch_bounds__(256, 2) kv_join_kernel(const __grid_constant__ AttnArgs a) {
     using H = Shape<NB>;
@@ -760,30 +777,37 @@ __global__ void __launch_bounds__(256, 2) kv_join_kernel(const __grid_constant__
     if (n == 0 || job.r0 + r >= job.R) return;
     const float* p1 = a.part + ((int64_t)blockIdx.x * 2) * PS; /* share i's part; the first share's is its second */
     auto part = [&](int i) { return p1 + (int64_t)(i ? 2 * i : 1) * PS; };
-    float M = -FLT_MAX;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, part(i)[RB * D + r]);
-    M = warp_max(M);
-    float L = 0.f;
+    float M = -FLT_MAX, L = 0.f;
     float4 v[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0; i0 < n; i0 += 32) {
         const int cnt = min(32, n - i0);
-        float w = 0.f;
-        if (lane < cnt) {
-            const float* p = part(i0 + lane);
-            w = ex2(p[RB * D + r] - M);
-            L = fmaf(p[RB * D + RB + r], w, L);
-        }
-#pragma unroll 8
-        for (int j = 0; j < cnt; ++j) {
-            const float wj = __shfl_sync(kAll, w, j);
-            const float* p = part(i0 + j) + r * D + 4 * lane;
+        float4 y[8][NV];
+        auto load = [&](int j0) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                if (128 * k + 4 * lane >= D) continue;
-                const float4 y = *(const float4*)(p + 128 * k);
-                v[k].x = fmaf(y.x, wj, v[k].x), v[k].y = fmaf(y.y, wj, v[k].y), v[k].z = fmaf(y.z, wj, v[k].z), v[k].w = fmaf(y.w, wj, v[k].w);
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    y[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (j0 + j < cnt && 128 * k + 4 * lane < D) y[j][k] = *(const float4*)(part(i0 + j0 + j) + r * D + 128 * k + 4 * lane);
+                }
+        };
+        const float pm = lane < cnt ? part(i0 + lane)[RB * D + r] : -FLT_MAX, pl = lane < cnt ? part(i0 + lane)[RB * D + RB + r] : 0.f;
+        load(0);
+        const float top = fmaxf(M, warp_max(pm)), old = ex2(M - top), w = ex2(pm - top);
+        M = top;
+        L = fmaf(L, old, pl * w);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) v[k].x *= old, v[k].y *= old, v[k].z *= old, v[k].w *= old;
+        for (int j0 = 0; j0 < cnt; j0 += 8) {
+            if (j0) load(j0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float wj = __shfl_sync(kAll, w, j0 + j);
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    v[k].x = fmaf(y[j][k].x, wj, v[k].x), v[k].y = fmaf(y[j][k].y, wj, v[k].y), v[k].z = fmaf(y[j][k].z, wj, v[k].z), v[k].w = fmaf(y[j][k].w, wj, v[k].w);
             }
         }
     }
