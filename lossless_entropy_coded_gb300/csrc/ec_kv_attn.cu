@@ -257,12 +257,6 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
                 const Seg s = seg_at(a, pre, info, RB, px, x_end);
                 const int3 f = info[s.b];
                 const Span sp = span_of(a, f.x, f.y);
-                /* the tile's queries, which would wait behind the units otherwise */
-                if (s.r0 + g < f.y * a.group) {
-                    const int r = s.r0 + g, es = a.q.dtype == EC_DTYPE_FP32 ? 4 : 2;
-                    const char* q = (const char*)a.q.data + ((int64_t)(f.z + r / a.group) * a.q.row + (int64_t)(s.h * a.group + r % a.group) * a.q.head) * es;
-                    for (int i = 128 * c; i < D * es; i += 512) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i));
-                }
                 pn = f.x > 0 ? min(32, max(0, s.u1 - s.u0)) : 0;
                 px = pn == 32 ? s.tile + s.u0 + 32 : s.next;
                 if (lane < pn) {
@@ -335,38 +329,57 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
             const bool on = r < R;
             const int64_t off = on ? (int64_t)(f.z + r / a.group) * a.q.row + (int64_t)(h * a.group + r % a.group) * a.q.head : 0;
             float xq[NB][8];
-            uint32_t top = 0;
+            if constexpr (QT == 2) {
+                const float* p = (const float*)a.q.data + off + 8 * c;
 #pragma unroll
-            for (int k = 0; k < NB; ++k) {
+                for (int k = 0; k < NB; ++k)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) xq[k][i] = 0.f;
-                if (on) {
-                    if (a.q.wide && a.q.dtype == EC_DTYPE_FP32) {
-                        const float4* p = (const float4*)((const float*)a.q.data + off + 32 * k + 8 * c);
-                        const float4 u = p[0], v = p[1];
+                    for (int i = 0; i < 8; ++i) xq[k][i] = 0.f;
+                if (on && a.q.wide) {
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) {
+                        const float4 u = *(const float4*)(p + 32 * k), v = *(const float4*)(p + 32 * k + 4);
                         xq[k][0] = u.x, xq[k][1] = u.y, xq[k][2] = u.z, xq[k][3] = u.w;
                         xq[k][4] = v.x, xq[k][5] = v.y, xq[k][6] = v.z, xq[k][7] = v.w;
-                    } else if (a.q.wide) {
-                        const uint4 w = *(const uint4*)((const uint16_t*)a.q.data + off + 32 * k + 8 * c);
-                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    }
+                } else if (on) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (a.q.dtype == EC_DTYPE_FP16) {
-                                const float2 f = __half22float2(*(const __half2*)&u[i]);
-                                xq[k][2 * i] = f.x, xq[k][2 * i + 1] = f.y;
-                            } else {
-                                xq[k][2 * i] = __uint_as_float(u[i] << 16);
-                                xq[k][2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-                            }
-                        }
-                    } else {
+                    for (int k = 0; k < NB; ++k)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) xq[k][i] = load_elem(a.q, off + 32 * k + 8 * c + i);
+                        for (int i = 0; i < 8; ++i) xq[k][i] = p[32 * k + i];
+                }
+            } else {
+                const uint16_t* p = (const uint16_t*)a.q.data + off + 8 * c;
+                uint4 w[NB];
+#pragma unroll
+                for (int k = 0; k < NB; ++k) w[k] = make_uint4(0, 0, 0, 0);
+                if (on && a.q.wide) {
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) w[k] = *(const uint4*)(p + 32 * k);
+                } else if (on) {
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) {
+                        const uint16_t* e = p + 32 * k;
+                        w[k] = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
                     }
                 }
+                const bool half = a.q.dtype == EC_DTYPE_FP16;
+#pragma unroll
+                for (int k = 0; k < NB; ++k) {
+                    const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = __half22float2(*(const __half2*)&u[i]);
+                        xq[k][2 * i] = half ? f.x : __uint_as_float(u[i] << 16);
+                        xq[k][2 * i + 1] = half ? f.y : __uint_as_float(u[i] & 0xFFFF0000u);
+                    }
+                }
+            }
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < NB; ++k)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(xq[k][i]) & 0x7FFFFFFFu);
-            }
             top = max(top, __shfl_xor_sync(kAll, top, 1));
             top = max(top, __shfl_xor_sync(kAll, top, 2));
             const int E = (int)(top >> 23);
