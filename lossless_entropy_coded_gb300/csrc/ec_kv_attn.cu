@@ -32,7 +32,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 /* Work is counted in units of 16 tokens of one tile (the rows of one key/value head's
  * group, 8 at a time), plus kTileCost for a tile's queries and outputs
- * (3, 6, 10 and 16 took 55.7, 44.7, 40.0 and 41.4 us on the 64 ragged sequences). */
+ * (6, 10, 14 and 20 took 39.3, 34.4, 36.5 and 35.9 us on the 64 ragged sequences). */
 constexpr int kTileCost = 10;
 
 /* The keys that a sequence's new rows see, in units: the sinks' units, then lo_u ..
@@ -841,10 +841,11 @@ struct Plan {
 template <int NB>
 static void plan_shape(Plan* p, int sms, int64_t tiles, int64_t units) {
     using H = Shape<NB>;
-    /* up to 4 units per warp there is nothing to gain from splitting a tile, and one launch does
-     * (17 tokens: 8 us; the split way adds the join's launch, about 3 us) */
+    /* up to 4 units per warp there is nothing to gain from splitting a tile, and one launch
+     * does, as long as the tiles run at the same time (us, a CTA per tile / split: 8 tiles of
+     * 17 tokens 7.1 / 8.4, 128 of 500 12.1 / 15.2, 512 of 500 25.0 / 21.7, 2048 of 300 87 / 37) */
     const int w = H::W / 2;
-    const bool solo = units <= 4 * w && tiles < 0x7FFFFFFF;
+    const bool solo = units <= 4 * w && tiles <= 2 * sms;
     p->solo = solo ? (int)((units + w - 1) / w) * w : 0;
     p->warps = solo ? w : H::W;
     p->grid = solo ? (int)tiles : sms;
