@@ -15,12 +15,12 @@
  * instructions, 140 of them on the integer pipe, which issues every second clock (the
  * expansion of E2M1 to FP16 alone is 64), so the integer pipe and the dependent chain of
  * a warp bound the kernel, not HBM.  Measured, 128 channels, 32 query over 8 key/value
- * heads: 400003 tokens 93.4 us (4.66 TB/s, 0.69 of the measured copy rate; 113 us with
+ * heads: 400003 tokens 83.8 us (5.19 TB/s, 0.77 of the measured copy rate; 113 us with
  * one unit per step and all segment state in registers); 64 sequences of 1 to 8192 tokens
- * 39.7 us for 92 MB (245 us with one CTA per tile and fixed chunks: most tiles are short,
+ * 36.1 us for 92 MB (245 us with one CTA per tile and fixed chunks: most tiles are short,
  * and their fixed cost, about that of 10 units, has to be shared out too).
  * mma.sync rather than tcgen05: the products have 8 columns, a tcgen05 tile 128 rows; the
- * legacy pipe is 27 % busy at the rate above.
+ * legacy pipe is 28 % busy at the rate above.
  */
 #include <float.h>
 
@@ -778,7 +778,9 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
 /* Join the partial results of a tile that several shares cover: CTA i adds, in order, the
  * parts of the tile that begins in share i and does not end there (if there is one).  A
  * warp takes a row, 32 parts at a time: each lane one part's maximum and sum, then four
- * channels of every part, eight parts at a time, whose loads wait for nothing. */
+ * channels of every part, eight parts at a time, whose loads wait for nothing.  Bound by
+ * three round trips to memory: 2.3 us (19 parts of 8 tiles; 8.8 us with a loop over 38
+ * parts, 1.3 us where tiles have two or three). */
 template <int NB>
 __global__ void __launch_bounds__(256, 2) kv_join_kernel(const __grid_constant__ AttnArgs a) {
     using H = Shape<NB>;
