@@ -377,10 +377,6 @@ __global__ void __launch_bounds__(kIoWarps * 32) kv_append_kernel(const __grid_c
     }
 }
 
-/* 2^(e - 127), NaN for 255 (e = 0: blocks of zeros). */
-__device__ __forceinline__ float scale_value(int e) {
-    return e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)e << 23);
-}
 __device__ __forceinline__ void word_values(uint32_t w, float s, float (&x)[8]) {
     uint32_t h[4];
     e2m1x8_f16(w, h);

@@ -22,8 +22,6 @@
  * mma.sync rather than tcgen05: the products have 8 columns, a tcgen05 tile 128 rows; the
  * legacy pipe is 28 % busy at the rate above.
  */
-#include <float.h>
-
 #include "ec_kv_attn.h"
 
 namespace kv {
@@ -157,9 +155,16 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 /* Bits of the probabilities: p is held as 2^kBias p in FP16, the running reference of a
- * row moves only when weights pass 2^(kBias + 3), and value
- * scales lie up to 2^7 above their block's reference: 2^(5 + 3 + 7) < 65504. */
+ * row moves only when weights pass 2^(kBias + 3), and value scales lie up to 2^7 above their
+ * block's reference: 2^(5 + 3 + 7) < 65504.  They lie down to 2^-8 below it, where a weight is
+ * good to 2^-22 of the row's largest; what a step of two units holds outside moves the
+ * reference, up or down. */
 constexpr float kBias = 5.f;
+constexpr int kRefUp = 7, kRefDown = 8;
+/* A step whose scales span more than the two, or a reference that is more than kRefSpan from its
+ * segment's first, sends the warp's work to redo_wide: the accumulators' FP32 range is far from
+ * its ends, and tokens that weigh little cannot drown those that count. */
+constexpr int kRefSpan = 16;
 
 /* Warps per SM and stages of a warp's ring by the tile's registers; `keep` floats hold a
  * warp's partial result of a tile: [rows][LD], maxima, sums.  All warps of an SM form one
@@ -204,11 +209,37 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int row0, int h, in
     if (d == 0 && a.lse) a.lse[row * a.n_q_heads + head] = L == 0.f ? -INFINITY : (M - kBias + log2f(L)) * kLn2;
 }
 
+/* A warp's work again, row by row in FP32; `own`: the warp's shared memory. */
+template <int NB>
+__device__ __forceinline__ void redo_wide(const AttnArgs& a, const int64_t* pre, const int3* info, float* own) {
+    using H = Shape<NB>;
+    constexpr int RB = H::RB, LD = H::LD;
+    const int warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+    const int64_t X = pre[a.S.n_seqs], share = share_of(a, X, gridDim.x, W), x1 = min(X, (blockIdx.x + 1) * share);
+    int64_t x = min(x1, blockIdx.x * share + warp * (share / W));
+    const int64_t x_end = min(x1, x + share / W);
+    while (x < x_end) {
+        const Seg s = seg_at(a, pre, info, RB, x, x_end);
+        x = s.next;
+        const int3 f = info[s.b];
+        if (s.u0 >= s.u1 || f.x == 0) continue;
+        const Span sp = span_of(a, f.x, f.y);
+        float* mine = own + (s.u0 == 0 ? 0 : H::RING / 4);
+        for (int r = 0; r < min(RB, f.y * a.group - s.r0); ++r) {
+            const int t = (s.r0 + r) / a.group;
+            const RowJob j{s.b, s.h, s.h * a.group + (s.r0 + r) % a.group, f.x - f.y + t, sp.sink_u, sp.lo_u, s.u0, s.u1, (int64_t)f.z + t};
+            const bool whole = s.u0 == 0 && s.u1 == s.units;
+            wide_row<NB>(a, j, kBias, whole ? nullptr : mine + r * LD, mine + RB * LD + r, mine + RB * LD + RB + r);
+        }
+    }
+}
+
 /* Each CTA takes a share of the work (or one tile), each of its warps an even part of
  * that: a run of units, which may cover the end of a tile, whole tiles and the begin of
  * another.  Per unit: S^T, 32 channels at a time (each block with its own scale, applied
  * to the FP32 products), weights against a lazily moved reference, O^T with the value
- * scales folded into the FP16 weights.  A warp writes tiles that it has seen whole; parts
+ * scales folded into the FP16 weights; work whose value scales FP16 does not hold is done again
+ * in FP32 at the end.  A warp writes tiles that it has seen whole; parts
  * meet in shared memory at the end, and what the CTA has not seen whole goes to `part`.
  * Units come by bulk copies through a ring of the warp's own, several ahead and across
  * tiles. */
@@ -228,6 +259,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
     if (lane == 0) {
         for (int s = 0; s < S; ++s) mbar_init(bars + 8 * s, 1);
         mbar_fence_init();
+        sts32(own + 60, 0u); /* not 0: redo_wide takes the warp's work */
         slot_tile[2 * warp] = slot_tile[2 * warp + 1] = -1;
     }
     grid_dep_launch();
@@ -403,7 +435,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
 
         float o[2 * NB][4];
         float m[2], l[2];
-        uint32_t add[NB]; /* 24 - the block's reference in both halves; 32: none yet, any scale passes it */
+        uint32_t add[NB]; /* kRefDown - the block's reference in both halves; 300: none yet, any scale passes it */
 #pragma unroll
         for (int i = 0; i < 2 * NB; ++i)
 #pragma unroll
@@ -411,7 +443,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
         m[0] = m[1] = -FLT_MAX;
         l[0] = l[1] = 0.f;
 #pragma unroll
-        for (int k = 0; k < NB; ++k) add[k] = both_halves(32);
+        for (int k = 0; k < NB; ++k) add[k] = both_halves(300);
 
 #pragma unroll 1
         for (; u < u1; u += 2) {
@@ -520,8 +552,9 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
                 p1[v] = transpose8x8(pack_f16(p[v][2], p[v][3]));
             }
 
-            /* value scales 2^(e - ref) as FP16 pairs: exponent field z - 9 = e - ref + 15,
-             * 0 where that is not positive; z >= 32 means more than 2^7 above the reference */
+            /* value scales 2^(e - ref) as FP16 pairs: z = e - ref + kRefDown, exponent field z + 7;
+             * z outside 0..15 means more than 2^7 above the reference or 2^-8 below it (or a block
+             * of zeros or NaN) */
             uint32_t vw[2][NB], z0[2][NB], z1[2][NB], over = 0;
 #pragma unroll
             for (int v = 0; v < 2; ++v)
@@ -530,58 +563,67 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
                     const uint32_t at = buf + v * UB + 16 * D + D / 2 + (c * NB + 2 * i) * 4;
                     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vw[v][2 * i]), "=r"(vw[v][2 * i + 1]) : "r"(at) : "memory");
                 }
-            if (masked) { /* scales of tokens that no row sees: 0 */
+            if (masked) { /* scales of tokens that no row sees: the reference, or none (their weights are 0) */
 #pragma unroll
-                for (int v = 0; v < 2; ++v)
+                for (int k2 = 0; k2 < NB; ++k2) {
+                    const uint32_t ref = (uint32_t)max(kRefDown - (int)(int16_t)(add[k2] & 0xFFFFu), 0) * 0x01010101u;
 #pragma unroll
-                    for (int k2 = 0; k2 < NB; ++k2) vw[v][k2] &= vmask[v];
+                    for (int v = 0; v < 2; ++v) vw[v][k2] = (vw[v][k2] & vmask[v]) | (ref & ~vmask[v]);
+                }
             }
 #pragma unroll
             for (int v = 0; v < 2; ++v)
 #pragma unroll
                 for (int k2 = 0; k2 < NB; ++k2) {
-                    z0[v][k2] = __viaddmax_s16x2(__byte_perm(vw[v][k2], 0, 0x4140), add[k2], 0x00090009u);
-                    z1[v][k2] = __viaddmax_s16x2(__byte_perm(vw[v][k2], 0, 0x4342), add[k2], 0x00090009u);
+                    z0[v][k2] = __viaddmax_s16x2(__byte_perm(vw[v][k2], 0, 0x4140), add[k2], 0x80008000u);
+                    z1[v][k2] = __viaddmax_s16x2(__byte_perm(vw[v][k2], 0, 0x4342), add[k2], 0x80008000u);
                     over |= z0[v][k2] | z1[v][k2];
                 }
             bool bad = false;
-            if (__any_sync(kAll, (over & 0xFFE0FFE0u) != 0)) {
+            if (__any_sync(kAll, (over & 0xFFF0FFF0u) != 0)) {
+                uint32_t ends[NB]; /* the largest and smallest scale, but zeros and NaN */
+                uint32_t nan = 0;
 #pragma unroll
                 for (int k2 = 0; k2 < NB; ++k2) {
-                    int mx = -8;
-#pragma unroll
-                    for (int v = 0; v < 2; ++v)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int e = (vw[v][k2] >> (8 * j)) & 0xFF;
-                            if (e != 255) mx = max(mx, e);
-                            bad |= e == 255;
-                        }
-                    mx = __reduce_max_sync(kAll, mx);
-                    const int ref = 24 - (int)(int16_t)(add[k2] & 0xFFFFu);
-                    if (mx > ref) {
-                        const float f = ref < 0 ? 0.f : ex2((float)(ref - mx));
-                        add[k2] = both_halves(24 - mx);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            o[2 * k2][j] *= f;
-                            o[2 * k2 + 1][j] *= f;
-                        }
-                    }
-                    const int r = (int)(int16_t)(add[k2] & 0xFFFFu);
+                    uint32_t hi = 0, lo = 0xFFFFFFFFu;
 #pragma unroll
                     for (int v = 0; v < 2; ++v) {
-                        z0[v][k2] = z1[v][k2] = 0;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int e = (vw[v][k2] >> (8 * j)) & 0xFF;
-                            const uint32_t z = e == 255 ? 9u : (uint32_t)max(e + r, 9);
-                            if (j < 2) z0[v][k2] |= z << (16 * j);
-                            else z1[v][k2] |= z << (16 * (j - 2));
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t x = __byte_perm(vw[v][k2], 0, k ? 0x4342 : 0x4140), y = x + 0x00010001u;
+                            nan |= y;
+                            hi = __vmaxu2(hi, y & 0x00FF00FFu);
+                            lo = __viaddmin_u16x2(x, 0xFFFFFFFFu, lo);
                         }
                     }
+                    ends[k2] = __reduce_max_sync(kAll, max(hi & 0xFFFFu, hi >> 16)) | __reduce_min_sync(kAll, min(lo & 0xFFFFu, lo >> 16)) << 16;
                 }
-                bad = __any_sync(kAll, bad);
+                bad = __any_sync(kAll, (nan & 0x01000100u) != 0);
+                bool wide = false;
+#pragma unroll
+                for (int k2 = 0; k2 < NB; ++k2) {
+                    const int ref = kRefDown - (int)(int16_t)(add[k2] & 0xFFFFu); /* < 0: none yet, o is 0 or NaN */
+                    const int mx = (int)(ends[k2] & 0xFFFFu) - 1, mn = (int)(ends[k2] >> 16) + 1;
+                    const bool move = mx > 0 && (mx > ref + kRefUp || mn < ref - kRefDown), again = move && ref >= 0;
+                    const int to = !move ? ref : mx - mn <= kRefDown ? mx : max(mx - kRefUp, 1);
+                    const float f = again ? __uint_as_float((uint32_t)(127 + max(-126, min(126, ref - to))) << 23) : 1.f;
+                    add[k2] = both_halves(kRefDown - to);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        o[2 * k2][j] *= f;
+                        o[2 * k2 + 1][j] *= f;
+                    }
+                    wide |= move && mx - mn > kRefUp + kRefDown;
+                    if (again) wide |= abs(to - (int)lds8(own + 48 + k2)) > kRefSpan;
+                    else if (move) sts8(own + 48 + k2, (uint32_t)to);
+                    const uint32_t add7 = both_halves((int)(int16_t)(add[k2] & 0xFFFFu) + 7);
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) { /* (what lies outside is zeros, NaN, unseen, or wide_row's) */
+                        z0[v][k2] = __vmins2(__viaddmax_s16x2(__byte_perm(vw[v][k2], 0, 0x4140), add7, 0u), 0x00160016u) - 0x00070007u;
+                        z1[v][k2] = __vmins2(__viaddmax_s16x2(__byte_perm(vw[v][k2], 0, 0x4342), add7, 0u), 0x00160016u) - 0x00070007u;
+                    }
+                }
+                if (wide) sts32(own + 60, 1u);
             }
 
             /* O^T: rows = channels, columns = query rows */
@@ -594,7 +636,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
 #pragma unroll
                     for (int bb = 0; bb < 2; ++bb) {
                         const int blk = 2 * i4 + bb;
-                        const uint32_t s0 = z0[v][blk] * 1024u - 0x24002400u, s1 = z1[v][blk] * 1024u - 0x24002400u;
+                        const uint32_t s0 = z0[v][blk] * 1024u + 0x1C001C00u, s1 = z1[v][blk] * 1024u + 0x1C001C00u;
                         uint32_t b0 = hmul2(p0[v], s0), b1 = hmul2(p1[v], s1);
                         if (bad) { /* a block of NaN makes its channels NaN for every row that sees the token */
                             Seg sg;
@@ -604,10 +646,10 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
                             const int R = f.y * a.group, tok = (u + v < sp.sink_u ? u + v : u + v + sp.lo_u - sp.sink_u) * kUnit;
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                if (((vw[v][blk] >> (8 * j)) & 0xFFu) != 255u) continue;
+                                if (lds8(buf + v * UB + 16 * D + D / 2 + (c * NB + blk) * 4 + j) != 255u) continue;
                                 const int at = tok + 2 * c + (j & 1) + 8 * (j >> 1);
                                 const int p = f.x - f.y + min(sg.r0 + g, R - 1) / a.group;
-                                if (at > p || (a.window && at <= p - a.window && at >= a.sinks)) continue;
+                                if (u + v >= u1 || at > p || (a.window && at <= p - a.window && at >= a.sinks)) continue;
                                 (j < 2 ? b0 : b1) |= 0x7FFFu << (16 * (j & 1));
                             }
                         }
@@ -623,8 +665,8 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
             fill();
         }
 
-        /* the lanes' sums; values are held relative to 2^(ref - 127) per block (ref = 0 or
-         * -8: nothing but blocks of zeros so far, a NaN there stays one) */
+        /* the lanes' sums; values are held relative to 2^(ref - 127) per block (ref < 0:
+         * nothing but blocks of zeros so far, a NaN there stays one) */
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -636,7 +678,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
         float back[NB];
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const int ref = 24 - (int)(int16_t)(add[k] & 0xFFFFu);
+            const int ref = kRefDown - (int)(int16_t)(add[k] & 0xFFFFu);
             back[k] = ref > 0 ? __uint_as_float((uint32_t)ref << 23) : 0.f;
         }
         if (sg.u0 == 0 && sg.u1 == sg.units) {
@@ -712,6 +754,8 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
             }
         }
     }
+    __syncwarp();
+    if (lds32(own + 60)) redo_wide<NB>(a, pre, info, (float*)(at_smem + warp * H::WARP_BYTES));
 
     /* join the warps' parts, tile by tile, in order: lane k holds slot k's tile; 8, 4, 2 or one
      * warps take a tile, a row at a time, so that most warps have one */

@@ -123,6 +123,10 @@ __device__ __forceinline__ int scale_byte(uint32_t top, bool* none) {
     const int e = max((int)((top + 0x3FFFFFu) >> 23) - 2, 1);
     return *none ? (top ? 255 : 0) : e;
 }
+/* 2^(e - 127), NaN for 255 (e = 0: blocks of zeros). */
+__device__ __forceinline__ float scale_value(int e) {
+    return e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)e << 23);
+}
 /* 2^(127 - e), e in 1..253. */
 __device__ __forceinline__ float inv_scale(int e) { return __uint_as_float((uint32_t)(254 - e) << 23); }
 
@@ -145,6 +149,8 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
     return v;
 }
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t x) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory"); }
+__device__ __forceinline__ void sts8(uint32_t a, uint32_t x) { asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(x) : "memory"); }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");

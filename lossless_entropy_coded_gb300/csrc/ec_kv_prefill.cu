@@ -30,8 +30,6 @@
  * Matrix instructions of the NQ row tiles alternate (P0 V, Q0 K', P1 V, Q1 K', ...), so that
  * one tile's softmax runs under the other's products.
  */
-#include <float.h>
-
 #include "ec_kv_attn.h"
 
 namespace kv {
@@ -154,7 +152,6 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-__device__ __forceinline__ void sts32(uint32_t a, uint32_t x) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory"); }
 __device__ __forceinline__ uint32_t half_mul2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -780,7 +777,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                         for (int k = 0; k < NB; ++k)
                             if (lds8(raw + v * UB + 16 * D + D / 2 + ((((tk >> 1) & 3) * NB + k) * 2 + (tk >> 3)) * 2 + (tk & 1)) == 255u)
                                 mask |= 1u << k;
-                    asm volatile("st.shared.u8 [%0], %1;" ::"r"(meta + 80 + i), "r"(mask) : "memory");
+                    sts8(meta + 80 + i, mask);
                 }
             }
             __syncwarp();
