@@ -8,8 +8,10 @@
  * expanded from 4 bits once for all rows:
  *   keys    FP16 k 2^(e - kref + 13), kref the tile's largest scale, so S = Q K^T comes
  *           out times a power of two of the tile;
- *   values  FP16 v 2^(e - vref), vref per 32 channels for the CTA's whole walk: it moves
- *           (and the accumulators with it) only when a scale lies more than 2^13 above.
+ *   values  FP16 v 2^(e - vref), vref per 32 channels: it moves (and the accumulators with
+ *           it) only when a tile's scales lie more than 2^13 above or 2^14 below.
+ * Where a tile's value scales span more, or vref would go further than kVSpan from its
+ * first, the CTA's rows are done again in FP32 at the end (wide_row).
  * S (FP32, in tensor memory) is read one row per thread, the weights 2^(s - m + 6) go
  * back as FP16 in S's place and are the tensor-memory operand of O += P V.  The row's
  * reference m moves, and O with it, only when a score passes it by 2^8.
@@ -35,6 +37,7 @@
 namespace kv {
 
 constexpr float kPBias = 6.f, kPSlack = 8.f;
+constexpr int kVUp = 13, kVDown = 14, kVSpan = 16;
 
 template <int NB, int NQ, int QT>
 struct PShape {
@@ -184,6 +187,11 @@ __device__ __forceinline__ float2 add2(float2 acc, float a, float b) {
 __device__ __forceinline__ uint32_t bytes_max(uint32_t m, uint32_t w) {
     return __vmaxu2(m, __vmaxu2(w & 0x00FF00FFu, (w >> 8) & 0x00FF00FFu));
 }
+/* Smallest bytes but zeros, less 1 (65535: none). */
+__device__ __forceinline__ uint32_t bytes_min(uint32_t m, uint32_t w) {
+    return __viaddmin_u16x2(w & 0x00FF00FFu, 0xFFFFFFFFu, __viaddmin_u16x2((w >> 8) & 0x00FF00FFu, 0xFFFFFFFFu, m));
+}
+__device__ __forceinline__ int half_min(uint32_t m) { return (int)min(m & 0xFFFFu, m >> 16) + 1; }
 __device__ __forceinline__ int half_max(uint32_t m) { return (int)max(m & 0xFFFFu, m >> 16); }
 /* A word's bytes with 255 (NaN) as 0. */
 __device__ __forceinline__ uint32_t drop_nan(uint32_t w) {
@@ -214,7 +222,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
     static_assert(H::META % 16 == 0 && H::RAW % 16 == 0, "sections stay aligned");
     const uint32_t raw_full = bars, raw_empty = bars + 16, buf_full = bars + 32, buf_empty = buf_full + 8 * NBUF,
                    s_full = buf_empty + 8 * NBUF, p_full = s_full + 8 * NQ, o_done = p_full + 8 * NQ, q_full = o_done + 8 * NQ,
-                   meta_full = q_full + 8, tslot = meta_full + 8 * H::MS;
+                   meta_full = q_full + 8, tslot = meta_full + 8 * H::MS, wide = bars + 248;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(raw_full + 8 * i, 1);
@@ -231,6 +239,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
         }
         for (int i = 0; i < H::MS; ++i) mbar_init(meta_full + 8 * i, 1);
         mbar_init(q_full, 4 * NQ);
+        sts32(wide, 0u);
         mbar_fence_init();
     }
     if (warp == 4 * NQ + H::EW) {
@@ -709,7 +718,8 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
         constexpr int WU = 4 * NB;             /* words of scales per unit, keys' or values' */
         constexpr int LANES = 32 / NB * NB;    /* lanes that stride whole blocks: word i of the values' is of block i % NB */
         constexpr int PER = (UT * WU + LANES - 1) / LANES;
-        int vref = 0; /* lane: of block lane % NB (0: unset) */
+        int vref = 0, first = 0; /* lane: of block lane % NB, now and when it was set (0: not yet) */
+        bool far = false;
         for (int j = 0; j < T; ++j) {
             const int s = j % H::RS, ut = J.u0 + j * UT, have = min(UT, J.u1 - ut);
             const uint32_t raw = raw_at + s * H::RAW, meta = meta_at + j % H::MS * H::META;
@@ -738,9 +748,9 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                     }
                 }
             }
-            uint32_t km = 0, vm = 0;
+            uint32_t km = 0, vm = 0, vl = 0xFFFFFFFFu;
 #pragma unroll
-            for (int q = 0; q < PER; ++q) km = bytes_max(km, kw[q]), vm = bytes_max(vm, vw[q]);
+            for (int q = 0; q < PER; ++q) km = bytes_max(km, kw[q]), vm = bytes_max(vm, vw[q]), vl = bytes_min(vl, vw[q]);
             uint32_t flags = 0;
             if (__any_sync(kAll, half_max(km) == 255 || half_max(vm) == 255)) {
                 flags = (__any_sync(kAll, half_max(vm) == 255) ? 1u : 0u) | (__any_sync(kAll, half_max(km) == 255) ? 2u : 0u);
@@ -749,17 +759,27 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                 for (int q = 0; q < PER; ++q) km = bytes_max(km, drop_nan(kw[q])), vm = bytes_max(vm, drop_nan(vw[q]));
             }
             const int kref = max(16, __reduce_max_sync(kAll, half_max(km)));
-            int best = half_max(vm);
+            int best = half_max(vm), least = half_min(vl);
             if constexpr (32 % NB == 0) {
 #pragma unroll
-                for (int o = NB; o < 32; o <<= 1) best = max(best, __shfl_xor_sync(kAll, best, o));
+                for (int o = NB; o < 32; o <<= 1) {
+                    best = max(best, __shfl_xor_sync(kAll, best, o));
+                    least = min(least, __shfl_xor_sync(kAll, least, o));
+                }
             } else {
-                const int mine = best;
+                const int mine = best, low = least;
 #pragma unroll
-                for (int k = 0; k < LANES / NB; ++k) best = max(best, __shfl_sync(kAll, mine, lane % NB + k * NB));
+                for (int k = 0; k < LANES / NB; ++k) {
+                    best = max(best, __shfl_sync(kAll, mine, lane % NB + k * NB));
+                    least = min(least, __shfl_sync(kAll, low, lane % NB + k * NB));
+                }
             }
             const int was = vref;
-            if (vref == 0 || best > vref + 13) vref = max(vref, max(best, 1));
+            if (best > 0 && (vref == 0 || best > vref + kVUp || least < vref - kVDown)) {
+                vref = best - least <= kVDown ? best : max(best - kVUp, 1);
+                if (first == 0) first = vref;
+                far |= best - least > kVUp + kVDown || abs(vref - first) > kVSpan;
+            }
             if (__any_sync(kAll, was != 0 && was != vref)) flags |= 4u;
             if (lane == 0) {
                 sts32(meta, (uint32_t)kref);
@@ -783,12 +803,22 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             __syncwarp();
             if (lane == 0) mbar_arrive(meta_full + 8 * (j % H::MS));
         }
+        if (far) sts32(wide, 1u);
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 4 * NQ + H::EW) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(H::COLS) : "memory");
+    }
+    if (lds32(wide)) {
+#pragma unroll 1
+        for (int i = warp; i < min(128 * NQ, J.R - J.r0); i += H::WARPS) {
+            const int t = (J.r0 + i) / J.group;
+            const RowJob row{J.b, J.h, J.h * J.group + (J.r0 + i) % J.group, J.first + t, J.sink_u, J.lo_u, J.u0, J.u1, J.row0 + t};
+            float* part = a.part + ((int64_t)blockIdx.x * NQ + i / 128) * (128 * (D + 2)) + 128 * D + i % 128;
+            wide_row<NB>(a, row, kPBias, a.splits > 1 ? part - 128 * D - i % 128 + i % 128 * D : nullptr, part, part + 128);
+        }
     }
 }
 

@@ -89,7 +89,7 @@ def normal(seed, *shape):
 
 
 SPREADS = [9, 14, 15, 16, 20, 40, 100, -15, -40, -100]
-GROUPS = [(2, 1), (4, 1)]
+GROUPS = [(2, 1), (4, 1), (80, 1)]   # a few rows, and more than the register form takes
 
 
 # ------------------------------------------------------------------ values far apart
@@ -128,7 +128,24 @@ def test_loud_tokens_of_no_weight(ec, qh, kvh, power, dtype):
         check(ec, c, k, v, new, q, window=500, sinks=2)
 
 
-@pytest.mark.parametrize("new", [[1, 1], [3, 2]])
+@pytest.mark.parametrize("qh,kvh,dim", [(4, 1, 128), (8, 4, 64), (3, 1, 192), (2, 2, 256)])
+@pytest.mark.parametrize("power", [15, 30, 90])
+def test_prompt_with_loud_values(ec, qh, kvh, dim, power):
+    """Every row of a prompt against the tokens that it sees; loud values in the middle and at the end."""
+    n = 390
+    c = Case(ec, [n, 77], kvh, dim, 64)
+    k, v = normal(7, n + 77, kvh, dim), normal(8, n + 77, kvh, dim)
+    v[200:203] *= 2.0 ** power
+    v[n - 1, :, :32] *= 2.0 ** power
+    v[n + 30] *= 2.0 ** -power
+    c.fill(k, v)
+    new = [n, 77]
+    q = normal(9, sum(new), qh, dim)
+    check(ec, c, k, v, new, q)
+    check(ec, c, k, v, new, q.to(BF16), window=50, sinks=1)
+
+
+@pytest.mark.parametrize("new", [[1, 1], [3, 2], [60, 150]])
 def test_values_that_drift(ec, new):
     """Scales that grow and shrink along the sequence, by 2^12 and 2^60 each way."""
     c = Case(ec, [90, 1400], 2, 128, 32)
