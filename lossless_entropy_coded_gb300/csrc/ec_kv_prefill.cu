@@ -11,7 +11,8 @@
  *   values  FP16 v 2^(e - vref), vref per 32 channels: it moves (and the accumulators with
  *           it) only when a tile's scales lie more than 2^13 above or 2^14 below.
  * Where a tile's value scales span more, or vref would go further than kVSpan from its
- * first, the CTA's rows are done again in FP32 at the end (wide_row).
+ * first, or a key's scale lies 2^-28 below the largest kref, the CTA's rows are done again in
+ * FP32 at the end (wide_row).
  * S (FP32, in tensor memory) is read one row per thread, the weights 2^(s - m + 6) go
  * back as FP16 in S's place and are the tensor-memory operand of O += P V.  The row's
  * reference m moves, and O with it, only when a score passes it by 2^8.
@@ -719,6 +720,8 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
         constexpr int LANES = 32 / NB * NB;    /* lanes that stride whole blocks: word i of the values' is of block i % NB */
         constexpr int PER = (UT * WU + LANES - 1) / LANES;
         int vref = 0, first = 0; /* lane: of block lane % NB, now and when it was set (0: not yet) */
+        uint32_t kl = 0xFFFFFFFFu; /* of all keys; kmost the largest kref */
+        int kmost = 0;
         bool far = false;
         for (int j = 0; j < T; ++j) {
             const int s = j % H::RS, ut = J.u0 + j * UT, have = min(UT, J.u1 - ut);
@@ -802,8 +805,12 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(meta_full + 8 * (j % H::MS));
+            /* (nobody waits for this: ahead of the arrival it cost 29 us of 1146) */
+#pragma unroll
+            for (int q = 0; q < PER; ++q) kl = bytes_min(kl, kw[q]);
+            kmost = max(kmost, kref);
         }
-        if (far) sts32(wide, 1u);
+        if (far || half_min(kl) < kmost - 27) sts32(wide, 1u);
     }
     tc_fence_before();
     __syncthreads();

@@ -156,3 +156,16 @@ def test_values_that_drift(ec, new):
     v[100:110] = 0
     c.fill(k, v)
     check(ec, c, k, v, new, normal(19, sum(new), 8, 128))
+
+
+# ------------------------------------------------------------------ keys far apart
+@pytest.mark.parametrize("qh,new", [(2, 5), (2, 40), (80, 40)])
+@pytest.mark.parametrize("power", [26, 28, 30, 60])
+def test_a_later_key_leaves_earlier_rows_alone(ec, qh, new, power):
+    c = Case(ec, [40], 1, 128, 16)
+    k, v = normal(10, 40, 1, 128), normal(11, 40, 1, 128)
+    k[37] *= 2.0 ** power
+    c.fill(k, v)
+    q = normal(12, new, qh, 128)
+    q[-3:] *= 2.0 ** -power
+    check(ec, c, k, v, [new], q)
