@@ -514,7 +514,8 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
             }
 
             /* weights 2^(s - m + kBias); the references move when a lane's eight weights add to
-             * more than 2^(kBias + 3) (fac > 0, so a masked -inf stays one) */
+             * more than 2^(kBias + 3), or to NaN: one row's must not hide the other's (fac > 0, so
+             * a masked -inf stays one) */
             float p[2][4], sum[2];
             auto weights = [&]() {
 #pragma unroll
@@ -523,7 +524,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
                     for (int j = 0; j < 4; ++j) p[v][j] = ex2(fmaf(s[v][j], fac[j & 1], kBias - m[j & 1]));
                 sum[0] = (p[0][0] + p[0][2]) + (p[1][0] + p[1][2]);
                 sum[1] = (p[0][1] + p[0][3]) + (p[1][1] + p[1][3]);
-                return sum[0] + sum[1] > 256.f;
+                return !(sum[0] + sum[1] <= 256.f);
             };
             if (__any_sync(kAll, weights())) {
 #pragma unroll

@@ -169,3 +169,38 @@ def test_a_later_key_leaves_earlier_rows_alone(ec, qh, new, power):
     q = normal(12, new, qh, 128)
     q[-3:] *= 2.0 ** -power
     check(ec, c, k, v, [new], q)
+
+
+# ------------------------------------------------------------------ neighbours that are no numbers
+@pytest.mark.parametrize("qh,kvh", [(8, 4), (8, 2), (8, 1), (80, 1)])
+@pytest.mark.parametrize("poison", [math.nan, math.inf])
+def test_a_query_of_nan_spoils_its_own_row_only(ec, qh, kvh, poison):
+    """Scores and value scales rise along the sequence, so that every row's reference has to move."""
+    n = 1200
+    c = Case(ec, [n], kvh, 128, 16)
+    u = normal(20, 128) * 0.5
+    t = torch.arange(n, device="cuda").float()
+    k = (u * (t / n * 28 - 14)[:, None])[:, None].repeat(1, kvh, 1).contiguous()
+    v = normal(21, n, kvh, 128) * torch.exp2(t / n * 5)[:, None, None]
+    c.fill(k, v)
+    q = (u * 4 + 0.05 * normal(22, 1, qh, 128))
+    for h in range(min(qh, 8)):
+        bad = q.clone()
+        bad[0, h, 7] = poison
+        out, _ = check(ec, c, k, v, [1], bad, skip=[(0, h)])
+        assert torch.isnan(out[0, h]).all()
+
+
+@pytest.mark.parametrize("qh", [1, 2, 48])
+def test_a_key_of_nan_spoils_rows_that_see_it(ec, qh):
+    n = 1280
+    c = Case(ec, [n], 1, 128, 16)
+    u = normal(23, 128) * 0.5
+    a = torch.full((n,), -1.0, device="cuda")
+    a[n - 9] = 3   # outweighs the others; the same place of its unit as the last token
+    k = (u * a[:, None])[:, None].contiguous()
+    v = normal(24, n, 1, 128)
+    k[n - 1] = math.nan
+    c.fill(k, v)
+    out, _ = check(ec, c, k, v, [2], (u * 4 + 0.05 * normal(25, 2, qh, 128)))
+    assert not torch.isnan(out[0]).any() and torch.isnan(out[1]).all()
