@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
             const int E = (int)(top >> 23);
             const int up = E == 255 ? 127 : min(253, 268 - E);
             const float s = __uint_as_float((uint32_t)up << 23);
-            const float inv = fmaxf(__uint_as_float((uint32_t)(254 - up) << 23) * a.scale * kLog2e, FLT_MIN); /* > 0: a masked -inf stays one */
+            const float inv = fmaxf(__uint_as_float((uint32_t)(254 - up) << 23) * a.scale * kLog2e, kTiny); /* > 0: a masked -inf stays one */
 #pragma unroll
             for (int k = 0; k < NB; ++k)
 #pragma unroll

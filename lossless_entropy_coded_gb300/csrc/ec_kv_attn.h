@@ -26,6 +26,10 @@ struct AttnArgs {
     int* status;
 };
 
+/* The least factor of a score, so that no factor is 0 (the smallest denormal: FLT_MIN would raise
+ * the scores of queries near 2^-110, whose keys may be as large as 2^100). */
+constexpr float kTiny = 1.4e-45f;
+
 /* One query row, and the units of its sequence that are taken in: u0 .. u1 - 1 of sink_u units
  * at the front and those from lo_u on. */
 struct RowJob {

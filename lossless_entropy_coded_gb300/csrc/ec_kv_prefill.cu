@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             wait(meta_full + 8 * (j % H::MS), (j / H::MS) & 1);
             wait(s_full + 8 * t, j & 1);
             tc_fence_after();
-            const float f = fmaxf(rowfac * __uint_as_float((lds32(meta) - 13u) << 23), FLT_MIN); /* > 0: a masked -inf stays one */
+            const float f = fmaxf(rowfac * __uint_as_float((lds32(meta) - 13u) << 23), kTiny); /* > 0: a masked -inf stays one */
             const uint32_t flags = lds32(meta + 4);
             const int ut = J.u0 + j * UT; /* the tile's first unit */
             const int tok_a = unit_of(ut) * kUnit, tok_z = unit_of(min(ut + UT, J.u1) - 1) * kUnit + kUnit - 1;

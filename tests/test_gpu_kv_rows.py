@@ -171,6 +171,18 @@ def test_a_later_key_leaves_earlier_rows_alone(ec, qh, new, power):
     check(ec, c, k, v, [new], q)
 
 
+@pytest.mark.parametrize("new", [1, 40])
+def test_small_queries_and_large_keys(ec, new):
+    """Queries near the smallest numbers and keys near the largest that FP32 scores hold."""
+    c = Case(ec, [40], 1, 64, 16)
+    k, v = normal(13, 40, 1, 64) * 2.0 ** 104, normal(14, 40, 1, 64)
+    c.fill(k, v)
+    for power in (-104, -108, -111, -114):
+        q = normal(15, new, 2, 64) * 2.0 ** power
+        q[..., 4:] = 0
+        check(ec, c, k, v, [new], q, scale=2.0 ** -6)
+
+
 # ------------------------------------------------------------------ neighbours that are no numbers
 @pytest.mark.parametrize("qh,kvh", [(8, 4), (8, 2), (8, 1), (80, 1)])
 @pytest.mark.parametrize("poison", [math.nan, math.inf])
