@@ -909,6 +909,14 @@ static void plan_shape(Plan* p, int sms, int64_t tiles, int64_t units) {
  * rows 118 / 107.  One sequence of 30000 and 128 channels, 40 rows: 41 / 42. */
 constexpr int64_t few_rows(int nb) { return nb == 2 ? 40 : nb == 4 ? 32 : 24; }
 
+/* The mask as the kernels take it: a window that hides none of max_len tokens is none, and there
+ * are no more sinks than tokens, so that sums with either stay within 31 bits. */
+static ec_kv_attn within(ec_kv_attn at, int64_t max_len) {
+    if (at.window >= max_len) at.window = at.sinks = 0;
+    if (at.sinks > max_len) at.sinks = (int32_t)max_len;
+    return at;
+}
+
 /* false: more work than the kernels count (one sequence's places fit 31 bits) */
 static bool plan_of(const ec_kv* C, int sms, int n_seqs, int64_t n_rows, int max_new, int64_t max_len, const ec_kv_attn* at, int dtype, Plan* p) {
     const int group = at->n_q_heads / C->p.n_kv_heads, nb = C->p.head_dim / 32;
@@ -983,10 +991,11 @@ extern "C" int ec_kv_attend_work_bytes(const ec_kv* C, int n_seqs, int64_t n_row
     /* FP32 queries take smaller row tiles, and fewer rows may take the other form: the largest,
      * so that a buffer for n_rows serves calls with fewer */
     *bytes = 0;
+    const ec_kv_attn at = within(*attn, max_len);
     for (int64_t rows : {n_rows, (int64_t)0})
         for (int dtype : {EC_DTYPE_BF16, EC_DTYPE_FP32}) {
             Plan p;
-            if (!plan_of(C, sms, n_seqs, rows, max_new, max_len, attn, dtype, &p)) return EC_ERR_UNSUPPORTED;
+            if (!plan_of(C, sms, n_seqs, rows, max_new, max_len, &at, dtype, &p)) return EC_ERR_UNSUPPORTED;
             if (p.work > *bytes) *bytes = p.work;
         }
     return EC_OK;
@@ -1001,8 +1010,8 @@ extern "C" int ec_kv_attend(const ec_kv* C, const ec_kv_attention* t, cudaStream
         max_len = t->seqs.table_stride * C->p.page_tokens;
         if (max_len > 0x7FFFFFF0) max_len = 0x7FFFFFF0; /* lens are 32-bit */
     }
-    const ec_kv_attn& at = t->attn;
-    if ((rc = check_attn(C, t->seqs.n_seqs, t->n_rows, t->max_new, max_len, &at)) != EC_OK) return rc;
+    if ((rc = check_attn(C, t->seqs.n_seqs, t->n_rows, t->max_new, max_len, &t->attn)) != EC_OK) return rc;
+    const ec_kv_attn at = within(t->attn, max_len);
     if (!t->starts && t->n_rows < t->seqs.n_seqs) return EC_ERR_SHAPE;
     AttnArgs a{};
     if (!pool_view(C, t->layer, &a.P)) return EC_ERR_INVALID_ARG;

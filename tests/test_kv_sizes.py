@@ -1,0 +1,32 @@
+"""What ec_kv_attend_work_bytes answers on the CPU: sizes at the ends of their ranges."""
+import pytest
+
+INT_MAX = 2 ** 31 - 1
+
+
+@pytest.fixture(scope="module")
+def ec():
+    from lossless_entropy_coded_gb300 import build
+    build.build()
+    import lossless_entropy_coded_gb300 as ec
+    return ec
+
+
+@pytest.fixture(scope="module")
+def cache(ec):
+    return ec.kv_cache(1, 100, 8, 128, 64, device=-1)
+
+
+@pytest.mark.parametrize("max_new", [1, 5, 500])
+@pytest.mark.parametrize("max_len", [100, 8192, 400000])
+def test_sinks_and_windows_past_every_token(ec, cache, max_new, max_len):
+    """As many sinks or as wide a window as a number holds: the same as all tokens."""
+    def work(window, sinks):
+        return ec.kv_attend_work_bytes(cache, 4, 4 * max_new, 32, max_new, max_len, window, sinks)
+    whole = work(0, 0)
+    for sinks in (max_len, max_len + 1, INT_MAX - 16, INT_MAX - 14, INT_MAX):
+        assert work(64, sinks) == work(64, max_len) == whole, sinks
+        assert work(max_len - 1, sinks) == whole
+        assert work(INT_MAX, sinks) == whole
+    for window in (max_len, INT_MAX - 16, INT_MAX):
+        assert work(window, 0) == work(window, 4) == whole, window
