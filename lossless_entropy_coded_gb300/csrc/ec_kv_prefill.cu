@@ -889,14 +889,16 @@ static int row_tiles_per_cta(int nb, int dtype) { return nb <= 4 && dtype != EC_
 
 bool plan_prefill(const ec_kv* C, int sms, int n_seqs, int max_new, int64_t max_units, int group, int dtype, PrefillPlan* p) {
     const int nb = C->p.head_dim / 32, nq = row_tiles_per_cta(nb, dtype), ut = nb <= 4 ? 8 : 4;
-    const int64_t rows = (int64_t)group * max_new, rt = (rows + 128 * nq - 1) / (128 * nq), tiles = rt * n_seqs * C->p.n_kv_heads;
+    const int64_t rows = (int64_t)group * max_new;
+    if (rows > 0x7FFFFFFF - 255) return false; /* the kernel's row numbers, rounded up to a tile, are 32-bit */
+    const int64_t rt = (rows + 128 * nq - 1) / (128 * nq), tiles = rt * n_seqs * C->p.n_kv_heads;
     const int64_t steps = (max_units + ut - 1) / ut;
     int64_t s = 1;
     /* fewer row tiles than SMs: split the tokens, no finer than 4 tiles each */
     if (tiles < sms) s = sms / tiles;
     if (s > (steps + 3) / 4) s = (steps + 3) / 4;
     if (s < 1) s = 1;
-    if (tiles * s > 0x7FFFFFF || rt > 0x7FFFFFFF || tiles * 16 * nq > 0x7FFFFFFF) return false;
+    if (tiles * s > 0x7FFFFFF || tiles * 16 * nq > 0x7FFFFFFF) return false;
     p->row_tiles = (int)rt;
     p->splits = (int)s;
     p->grid = tiles * s;

@@ -30,3 +30,14 @@ def test_sinks_and_windows_past_every_token(ec, cache, max_new, max_len):
         assert work(INT_MAX, sinks) == whole
     for window in (max_len, INT_MAX - 16, INT_MAX):
         assert work(window, 0) == work(window, 4) == whole, window
+
+
+def test_rows_past_31_bits_are_refused(ec):
+    """Row numbers of a key/value head, rounded up to a tile, have to fit 31 bits."""
+    cache = ec.kv_cache(1, 100, 1, 128, 64, device=-1)
+    for heads, max_new in ((256, 1 << 24), (128, 1 << 24), (65536, 32768), (65536, 1 << 24)):
+        with pytest.raises(ec.EcError) as x:
+            ec.kv_attend_work_bytes(cache, 1, 1, heads, max_new, 1000)
+        assert x.value.code == -4, (heads, max_new)
+    for heads, max_new in ((64, 1 << 24), (256, 1 << 22), (65536, 16384)):
+        ec.kv_attend_work_bytes(cache, 1, 1, heads, max_new, 1000)
