@@ -988,9 +988,10 @@ extern "C" int ec_kv_attend_work_bytes(const ec_kv* C, int n_seqs, int64_t n_row
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return EC_ERR_CUDA;
     } else sms = 152;
+    *bytes = 0;
+    if (n_seqs == 0 || max_new == 0) return EC_OK;
     /* FP32 queries take smaller row tiles, and fewer rows may take the other form: the largest,
      * so that a buffer for n_rows serves calls with fewer */
-    *bytes = 0;
     const ec_kv_attn at = within(*attn, max_len);
     for (int64_t rows : {n_rows, (int64_t)0})
         for (int dtype : {EC_DTYPE_BF16, EC_DTYPE_FP32}) {

@@ -1,7 +1,12 @@
 """What ec_kv_attend_work_bytes answers on the CPU: sizes at the ends of their ranges."""
+import os
+import subprocess
+import sys
+
 import pytest
 
 INT_MAX = 2 ** 31 - 1
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -41,3 +46,14 @@ def test_rows_past_31_bits_are_refused(ec):
         assert x.value.code == -4, (heads, max_new)
     for heads, max_new in ((64, 1 << 24), (256, 1 << 22), (65536, 16384)):
         ec.kv_attend_work_bytes(cache, 1, 1, heads, max_new, 1000)
+
+
+def test_work_of_no_sequences(ec):
+    """A call without sequences or new tokens, whatever its bounds, needs no buffer (the question
+    is asked in a process of its own: a division by the number of row tiles would end it)."""
+    code = ("import lossless_entropy_coded_gb300 as ec\n"
+            "c = ec.kv_cache(1, 100, 8, 128, 64, device=-1)\n"
+            "print([ec.kv_attend_work_bytes(c, n, 0, 32, m, 100000) for n, m in ((0, 1), (0, 500), (0, 5000), (3, 0))])")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr
+    assert eval(r.stdout) == [0, 0, 0, 0]
