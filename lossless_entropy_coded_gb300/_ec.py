@@ -576,7 +576,7 @@ def kv_read(cache: KvCache, layer: int, seqs: KvSeqs, k=None, v=None, starts=Non
 
 def kv_attend_work_bytes(cache: KvCache, n_seqs: int, n_rows: int, n_q_heads: int, max_new: int = 1,
                          max_len: int = 0, window: int = 0, sinks: int = 0) -> int:
-    """ec_kv_attend_work_bytes: the work buffer of kv_attend for these sizes."""
+    """ec_kv_attend_work_bytes: the work buffer of kv_attend for calls of at most these sizes."""
     n = ctypes.c_size_t(0)
     at = KvAttn(n_q_heads, window, sinks, 0.0)
     _check(lib.ec_kv_attend_work_bytes(cache.handle, n_seqs, n_rows, max_new, max_len, ctypes.byref(at),

@@ -917,31 +917,66 @@ static ec_kv_attn within(ec_kv_attn at, int64_t max_len) {
     return at;
 }
 
-/* false: more work than the kernels count (one sequence's places fit 31 bits) */
-static bool plan_of(const ec_kv* C, int sms, int n_seqs, int64_t n_rows, int max_new, int64_t max_len, const ec_kv_attn* at, int dtype, Plan* p) {
-    const int group = at->n_q_heads / C->p.n_kv_heads, nb = C->p.head_dim / 32;
-    const int64_t rows = (int64_t)group * max_new;
-    int64_t units = (max_len + kUnit - 1) / kUnit;
+/* Sizes that both forms are planned by; none shrinks when a bound grows. */
+struct Extent {
+    int group, nb;
+    int64_t rows;            /* per sequence and key/value head */
+    int64_t units;           /* that a sequence's rows see */
+    int64_t per_seq, tiles;  /* of 8 rows */
+    bool past;               /* more work per sequence than the register form counts (31 bits) */
+};
+static Extent extent_of(const ec_kv* C, int n_seqs, int max_new, int64_t max_len, const ec_kv_attn* at) {
+    Extent x;
+    x.group = at->n_q_heads / C->p.n_kv_heads;
+    x.nb = C->p.head_dim / 32;
+    x.rows = (int64_t)x.group * max_new;
+    x.units = (max_len + kUnit - 1) / kUnit;
     if (at->window) {
         const int64_t w = ((int64_t)at->window + max_new + kUnit) / kUnit + 1 + (at->sinks + kUnit - 1) / kUnit;
-        if (w < units) units = w;
+        if (w < x.units) x.units = w;
     }
-    if (units < 1) units = 1;
-    const int64_t per_seq = (rows + 7) / 8 * C->p.n_kv_heads, tiles = per_seq * n_seqs;
-    p->many = rows > 2 * few_rows(nb) || (rows > few_rows(nb) && n_rows > few_rows(nb) * n_seqs / group) ||
-              per_seq > 0x7FFFFFFF / (units + kTileCost);
-    if (p->many) {
-        p->grid = p->solo = 0;
-        if (!plan_prefill(C, sms, n_seqs, max_new, units, group, dtype, &p->pre)) return false;
-        p->work = p->pre.work;
+    if (x.units < 1) x.units = 1;
+    x.per_seq = (x.rows + 7) / 8 * C->p.n_kv_heads;
+    x.tiles = x.per_seq * n_seqs;
+    x.past = x.per_seq > 0x7FFFFFFF / (x.units + kTileCost);
+    return x;
+}
+static void plan_few(Plan* p, int sms, const Extent& x) {
+    switch (x.nb) {
+        case 2: plan_shape<2>(p, sms, x.tiles, x.units); break;
+        case 4: plan_shape<4>(p, sms, x.tiles, x.units); break;
+        case 6: plan_shape<6>(p, sms, x.tiles, x.units); break;
+        default: plan_shape<8>(p, sms, x.tiles, x.units);
+    }
+}
+
+/* false: more work than the kernels count */
+static bool plan_of(const ec_kv* C, int sms, int n_seqs, int64_t n_rows, int max_new, int64_t max_len, const ec_kv_attn* at, int dtype, Plan* p) {
+    const Extent x = extent_of(C, n_seqs, max_new, max_len, at);
+    const int64_t few = few_rows(x.nb);
+    p->many = x.rows > 2 * few || (x.rows > few && n_rows > few * n_seqs / x.group) || x.past;
+    if (!p->many) {
+        plan_few(p, sms, x);
         return true;
     }
-    switch (nb) {
-        case 2: plan_shape<2>(p, sms, tiles, units); break;
-        case 4: plan_shape<4>(p, sms, tiles, units); break;
-        case 6: plan_shape<6>(p, sms, tiles, units); break;
-        default: plan_shape<8>(p, sms, tiles, units);
-    }
+    p->grid = p->solo = 0;
+    if (!plan_prefill(C, sms, n_seqs, max_new, x.units, x.group, dtype, &p->pre)) return false;
+    p->work = p->pre.work;
+    return true;
+}
+
+/* The most work that any call of at most these sizes plans.  Both forms' parts are bounded: the
+ * register form's by its grid of one CTA per SM (a call whose tiles have a CTA each has smaller
+ * ones that do too), the tensor-memory form's by the same many row tiles and splits; fewer rows
+ * of the same bounds may take either. */
+static bool most_work(const ec_kv* C, int sms, int n_seqs, int max_new, int64_t max_len, const ec_kv_attn* at, int dtype, size_t* bytes) {
+    const Extent x = extent_of(C, n_seqs, max_new, max_len, at);
+    Plan p;
+    plan_few(&p, sms, x);
+    *bytes = p.work;
+    if (x.rows <= few_rows(x.nb) && !x.past) return true;
+    if (!plan_prefill(C, sms, n_seqs, max_new, x.units, x.group, dtype, &p.pre)) return false;
+    if (p.pre.most > *bytes) *bytes = p.pre.most;
     return true;
 }
 
@@ -990,15 +1025,12 @@ extern "C" int ec_kv_attend_work_bytes(const ec_kv* C, int n_seqs, int64_t n_row
     } else sms = 152;
     *bytes = 0;
     if (n_seqs == 0 || max_new == 0) return EC_OK;
-    /* FP32 queries take smaller row tiles, and fewer rows may take the other form: the largest,
-     * so that a buffer for n_rows serves calls with fewer */
     const ec_kv_attn at = within(*attn, max_len);
-    for (int64_t rows : {n_rows, (int64_t)0})
-        for (int dtype : {EC_DTYPE_BF16, EC_DTYPE_FP32}) {
-            Plan p;
-            if (!plan_of(C, sms, n_seqs, rows, max_new, max_len, &at, dtype, &p)) return EC_ERR_UNSUPPORTED;
-            if (p.work > *bytes) *bytes = p.work;
-        }
+    for (int dtype : {EC_DTYPE_BF16, EC_DTYPE_FP32}) {
+        size_t most = 0;
+        if (!most_work(C, sms, n_seqs, max_new, max_len, &at, dtype, &most)) return EC_ERR_UNSUPPORTED;
+        if (most > *bytes) *bytes = most;
+    }
     return EC_OK;
 }
 

@@ -150,7 +150,7 @@ __device__ __forceinline__ void wide_row(const AttnArgs& a, const RowJob& j, flo
 struct PrefillPlan {
     int row_tiles, splits;
     int64_t grid;
-    size_t work;
+    size_t work, most; /* bytes of this call's parts, and of any call's of at most these sizes */
 };
 bool plan_prefill(const ec_kv* C, int sms, int n_seqs, int max_new, int64_t max_units, int group, int dtype, PrefillPlan* p);
 int launch_prefill(const AttnArgs& a, const PrefillPlan& p, cudaStream_t stream);

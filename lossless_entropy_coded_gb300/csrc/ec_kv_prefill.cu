@@ -892,17 +892,20 @@ bool plan_prefill(const ec_kv* C, int sms, int n_seqs, int max_new, int64_t max_
     const int64_t rows = (int64_t)group * max_new;
     if (rows > 0x7FFFFFFF - 255) return false; /* the kernel's row numbers, rounded up to a tile, are 32-bit */
     const int64_t rt = (rows + 128 * nq - 1) / (128 * nq), tiles = rt * n_seqs * C->p.n_kv_heads;
-    const int64_t steps = (max_units + ut - 1) / ut;
+    const int64_t steps = (max_units + ut - 1) / ut, finest = (steps + 3) / 4;
     int64_t s = 1;
     /* fewer row tiles than SMs: split the tokens, no finer than 4 tiles each */
     if (tiles < sms) s = sms / tiles;
-    if (s > (steps + 3) / 4) s = (steps + 3) / 4;
+    if (s > finest) s = finest;
     if (s < 1) s = 1;
     if (tiles * s > 0x7FFFFFF || tiles * 16 * nq > 0x7FFFFFFF) return false;
     p->row_tiles = (int)rt;
     p->splits = (int)s;
     p->grid = tiles * s;
-    p->work = s > 1 ? (size_t)(tiles * s) * nq * 128 * (C->p.head_dim + 2) * sizeof(float) : 0;
+    const size_t part = (size_t)nq * 128 * (C->p.head_dim + 2) * sizeof(float);
+    const int64_t most = tiles < (sms + finest - 1) / finest ? tiles * finest : sms;
+    p->work = s > 1 ? tiles * s * part : 0;
+    p->most = finest > 1 ? most * part : 0;
     return true;
 }
 

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from test_gpu_kv import FP32, Case, ec, i32  # noqa: F401 (ec is a fixture)
+from test_gpu_kv import FP32, Case, ec, i32, starts_of  # noqa: F401 (ec is a fixture)
 from test_gpu_kv_rows import check, normal
 
 pytestmark = pytest.mark.gpu
@@ -18,3 +18,19 @@ def test_sinks_and_windows_past_every_token(ec, window, sinks, qh):
     k, v = normal(30, sum(lens), 1, 128), normal(31, sum(lens), 1, 128)
     c.fill(k, v)
     check(ec, c, k, v, new, normal(32, sum(new), qh, 128), FP32, window=window, sinks=sinks)
+
+
+def test_one_buffer_for_the_longest_chunk(ec):
+    """A buffer sized once for the largest call serves every smaller one."""
+    lens = [3000, 2500]
+    c = Case(ec, lens, 2, 128, 64)
+    c.fill(normal(33, sum(lens), 2, 128), normal(34, sum(lens), 2, 128))
+    most = ec.kv_attend_work_bytes(c.cache, 2, 1000, 8, 500, 3000)
+    work = torch.empty(most, dtype=torch.uint8, device="cuda")
+    for new in ([500, 500], [400, 3], [100, 64], [20, 7], [12, 1], [9, 0], [1, 1]):
+        for dtype in (torch.bfloat16, FP32):
+            q = normal(35, sum(new), 8, 128).to(dtype)
+            outs = [torch.empty_like(q) for _ in range(2)]
+            ec.kv_attend(c.cache, 0, c.seqs, q, outs[0], starts=starts_of(new), max_new=max(new), max_len=3000, work=work)
+            ec.kv_attend(c.cache, 0, c.seqs, q, outs[1], starts=starts_of(new), max_new=max(new), max_len=3000)
+            assert ec.status() == 0 and torch.equal(outs[0], outs[1]), new

@@ -57,3 +57,20 @@ def test_work_of_no_sequences(ec):
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=600)
     assert r.returncode == 0, r.stderr
     assert eval(r.stdout) == [0, 0, 0, 0]
+
+
+SIZES = [(n, m, t) for n in (1, 2, 7, 64) for m in (1, 2, 5, 9, 16, 64, 100, 400, 5003) for t in (1, 100, 700, 3000, 20000, 500000)]
+
+
+@pytest.mark.parametrize("heads,kvh,dim", [(32, 8, 128), (8, 8, 64), (48, 1, 128), (12, 4, 192), (16, 2, 256)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (600, 4)])
+def test_a_buffer_for_larger_sizes_serves_smaller_ones(ec, heads, kvh, dim, window, sinks):
+    """The work size grows with every bound, so one buffer for the largest serves all."""
+    cache = ec.kv_cache(1, 100, kvh, dim, 64, device=-1)
+    work = {s: ec.kv_attend_work_bytes(cache, s[0], s[0] * s[1], heads, s[1], s[2], window, sinks) for s in SIZES}
+    for a in SIZES:
+        for b in SIZES:
+            if all(x <= y for x, y in zip(a, b)):
+                assert work[a] <= work[b], (a, b)
+    for n, m, t in SIZES:  # fewer rows of the same bounds
+        assert ec.kv_attend_work_bytes(cache, n, 1, heads, m, t, window, sinks) <= work[n, m, t]
