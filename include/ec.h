@@ -576,7 +576,7 @@ int ec_kv_attend(const ec_kv* C, const ec_kv_attention* a, cudaStream_t stream);
 
 /* Work bytes of ec_kv_attend on the current device (host only): enough for every call with
  * these heads, window and sinks whose n_seqs, n_rows, max_new and max_len are no larger than
- * these. */
+ * these (max_len 0: of any length). */
 int ec_kv_attend_work_bytes(const ec_kv* C, int n_seqs, int64_t n_rows, int max_new, int64_t max_len,
                             const ec_kv_attn* attn, size_t* bytes);
 

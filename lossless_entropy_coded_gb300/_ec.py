@@ -410,6 +410,7 @@ def status(stream=None) -> int:
 # ---------------------------------------------------------------- key/value cache
 EC_DTYPE_FP16, EC_DTYPE_FP32 = 3, 4
 EC_KV_MAX_SEQS = 1024
+_KV_MAX_LEN = 0x7FFFFFF0  # tokens of a sequence; a table may hold more
 _ROW_DTYPES = {}   # torch dtype -> EC_DTYPE_*, filled on first use (torch is imported when needed)
 _I32 = [None]
 _RAW_STREAM = [None]
@@ -576,7 +577,8 @@ def kv_read(cache: KvCache, layer: int, seqs: KvSeqs, k=None, v=None, starts=Non
 
 def kv_attend_work_bytes(cache: KvCache, n_seqs: int, n_rows: int, n_q_heads: int, max_new: int = 1,
                          max_len: int = 0, window: int = 0, sinks: int = 0) -> int:
-    """ec_kv_attend_work_bytes: the work buffer of kv_attend for calls of at most these sizes."""
+    """ec_kv_attend_work_bytes: the work buffer of kv_attend for calls of at most these sizes
+    (max_len 0: of any length)."""
     n = ctypes.c_size_t(0)
     at = KvAttn(n_q_heads, window, sinks, 0.0)
     _check(lib.ec_kv_attend_work_bytes(cache.handle, n_seqs, n_rows, max_new, max_len, ctypes.byref(at),
@@ -601,7 +603,7 @@ def kv_attend(cache: KvCache, layer: int, seqs: KvSeqs, q, out, starts=None, max
     if work is None:
         import torch
         work = torch.empty(kv_attend_work_bytes(cache, seqs.n, n, heads, max_new,
-                                                max_len or seqs.pages * cache.params.page_tokens, window, sinks),
+                                                max_len or min(seqs.pages * cache.params.page_tokens, _KV_MAX_LEN), window, sinks),
                            dtype=torch.uint8, device=q.device)
     args = _ATTENTION.pack(_seqs(seqs, cache, "ec_kv_attend"), _int32_ptr(starts, cache, seqs.n + 1, "ec_kv_attend"), n, layer,
                            max_new, max_len, heads, window, sinks, scale, qr, orr,

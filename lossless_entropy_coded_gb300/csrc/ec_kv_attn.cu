@@ -909,6 +909,8 @@ static void plan_shape(Plan* p, int sms, int64_t tiles, int64_t units) {
  * rows 118 / 107.  One sequence of 30000 and 128 channels, 40 rows: 41 / 42. */
 constexpr int64_t few_rows(int nb) { return nb == 2 ? 40 : nb == 4 ? 32 : 24; }
 
+constexpr int64_t kMaxLen = 0x7FFFFFF0; /* lens are 32-bit */
+
 /* The mask as the kernels take it: a window that hides none of max_len tokens is none, and there
  * are no more sinks than tokens, so that sums with either stay within 31 bits. */
 static ec_kv_attn within(ec_kv_attn at, int64_t max_len) {
@@ -1000,7 +1002,7 @@ static int run_terms(const AttnArgs& a, const Plan& p, cudaStream_t stream) {
 static int check_attn(const ec_kv* C, int n_seqs, int64_t n_rows, int max_new, int64_t max_len, const ec_kv_attn* at) {
     if (!C || !at) return EC_ERR_INVALID_ARG;
     if (n_seqs < 0 || n_rows < 0 || max_new < 0 || max_len < 0) return EC_ERR_SHAPE;
-    if (max_len > 0x7FFFFFF0) return EC_ERR_UNSUPPORTED;
+    if (max_len > kMaxLen) return EC_ERR_UNSUPPORTED;
     if (n_seqs > EC_KV_MAX_SEQS || max_new > (1 << 24) || at->n_q_heads > 65536) return EC_ERR_UNSUPPORTED;
     if (at->n_q_heads < 1 || at->n_q_heads % C->p.n_kv_heads) return EC_ERR_SHAPE;
     if (at->window < 0 || at->sinks < 0 || (at->sinks > 0 && at->window == 0)) return EC_ERR_INVALID_ARG;
@@ -1025,6 +1027,7 @@ extern "C" int ec_kv_attend_work_bytes(const ec_kv* C, int n_seqs, int64_t n_row
     } else sms = 152;
     *bytes = 0;
     if (n_seqs == 0 || max_new == 0) return EC_OK;
+    if (max_len == 0) max_len = kMaxLen;
     const ec_kv_attn at = within(*attn, max_len);
     for (int dtype : {EC_DTYPE_BF16, EC_DTYPE_FP32}) {
         size_t most = 0;
@@ -1041,7 +1044,7 @@ extern "C" int ec_kv_attend(const ec_kv* C, const ec_kv_attention* t, cudaStream
     int64_t max_len = t->max_len;
     if (max_len == 0) {
         max_len = t->seqs.table_stride * C->p.page_tokens;
-        if (max_len > 0x7FFFFFF0) max_len = 0x7FFFFFF0; /* lens are 32-bit */
+        if (max_len > kMaxLen) max_len = kMaxLen;
     }
     if ((rc = check_attn(C, t->seqs.n_seqs, t->n_rows, t->max_new, max_len, &t->attn)) != EC_OK) return rc;
     const ec_kv_attn at = within(t->attn, max_len);

@@ -34,3 +34,17 @@ def test_one_buffer_for_the_longest_chunk(ec):
             ec.kv_attend(c.cache, 0, c.seqs, q, outs[0], starts=starts_of(new), max_new=max(new), max_len=3000, work=work)
             ec.kv_attend(c.cache, 0, c.seqs, q, outs[1], starts=starts_of(new), max_new=max(new), max_len=3000)
             assert ec.status() == 0 and torch.equal(outs[0], outs[1]), new
+
+
+def test_buffers_sized_with_the_defaults(ec):
+    """Sizes asked for without a length are accepted by a call without one."""
+    lens = [9000, 3, 700, 5000]
+    c = Case(ec, lens, 8, 128, 64)
+    k, v = normal(36, sum(lens), 8, 128), normal(37, sum(lens), 8, 128)
+    c.fill(k, v)
+    work = torch.empty(ec.kv_attend_work_bytes(c.cache, 4, 4, 32), dtype=torch.uint8, device="cuda")
+    q = normal(38, 4, 32, 128)
+    a, b = torch.empty_like(q), torch.empty_like(q)
+    ec.kv_attend(c.cache, 0, c.seqs, q, a, work=work)
+    ec.kv_attend(c.cache, 0, c.seqs, q, b)
+    assert ec.status() == 0 and torch.equal(a, b)

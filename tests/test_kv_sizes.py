@@ -4,6 +4,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 INT_MAX = 2 ** 31 - 1
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -74,3 +75,25 @@ def test_a_buffer_for_larger_sizes_serves_smaller_ones(ec, heads, kvh, dim, wind
                 assert work[a] <= work[b], (a, b)
     for n, m, t in SIZES:  # fewer rows of the same bounds
         assert ec.kv_attend_work_bytes(cache, n, 1, heads, m, t, window, sinks) <= work[n, m, t]
+
+
+@pytest.mark.parametrize("max_new", [1, 5, 100])
+@pytest.mark.parametrize("window", [0, 600])
+def test_a_buffer_for_any_length(ec, cache, max_new, window):
+    """max_len 0 is any length, as in the call itself, and serves all."""
+    any_len = ec.kv_attend_work_bytes(cache, 4, 4 * max_new, 32, max_new, window=window)
+    for t in (1, 100, 8192, 500000, INT_MAX - 15):
+        assert ec.kv_attend_work_bytes(cache, 4, 4 * max_new, 32, max_new, t, window=window) <= any_len
+    assert any_len > 0
+
+
+def test_a_table_that_holds_more_than_a_sequence(ec):
+    """The binding's own buffer is sized for the tokens that the call takes from such a table."""
+    cache = ec.kv_cache(1, 100, 8, 128, 256, device=-1)
+
+    class Some:
+        n, packed, pages, device = 2, bytes(32), 1 << 24, -1
+    x = torch.zeros((2, 8, 128))
+    with pytest.raises(ec.EcError) as e:
+        ec.kv_attend(cache, 0, Some, x, x)
+    assert "work_bytes" not in str(e.value) and e.value.code == -1  # the library's answer: no pool
