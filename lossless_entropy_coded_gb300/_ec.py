@@ -173,6 +173,19 @@ def _stream_ptr(stream):
     return int(stream)
 
 
+def _work_buffer(nbytes: int, device, stream):
+    """A work buffer for one call on `stream`, allocated there: on the current stream its bytes
+    could still be in use by work queued before the call, or be handed to work queued after it
+    while the call runs."""
+    import torch
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _dev_ptr(t):
     return 0 if t is None else t.data_ptr()
 
@@ -365,8 +378,7 @@ def gemm(W: Matrix, x, y, batch: int, work=None, stream=None) -> None:
     """ec_gemm: y = x W^T for any batch (chunked decode + tensor-core GEMM).  work: a
     device tensor (its bytes are the buffer); None allocates one of gemm_work_bytes."""
     if work is None:
-        import torch
-        work = torch.empty(gemm_work_bytes(W, batch), dtype=torch.uint8, device=x.device)
+        work = _work_buffer(gemm_work_bytes(W, batch), x.device, stream)
     nbytes = work.numel() * work.element_size()
     _check(lib.ec_gemm(W.handle, _dev_ptr(x), _dev_ptr(y), batch, _dev_ptr(work), nbytes, _stream_ptr(stream)),
            "ec_gemm")
@@ -385,8 +397,7 @@ def gemm_group(Ws, xs, ys, batch: int, work=None, stream=None) -> None:
     the work buffer allows (None allocates gemm_group_work_bytes)."""
     n = len(Ws)
     if work is None:
-        import torch
-        work = torch.empty(gemm_group_work_bytes(Ws, batch), dtype=torch.uint8, device=ys[0].device)
+        work = _work_buffer(gemm_group_work_bytes(Ws, batch), ys[0].device, stream)
     hs = (ctypes.c_void_p * n)(*[W.handle.value for W in Ws])
     xp = (ctypes.c_void_p * n)(*[_dev_ptr(x) for x in xs])
     yp = (ctypes.c_void_p * n)(*[_dev_ptr(y) for y in ys])
@@ -601,10 +612,8 @@ def kv_attend(cache: KvCache, layer: int, seqs: KvSeqs, q, out, starts=None, max
                             or not lse.is_contiguous() or lse.numel() != n * heads):
         raise EcError(EC_ERR_INVALID_ARG, "ec_kv_attend: lse is a contiguous float32 tensor [rows, n_q_heads]")
     if work is None:
-        import torch
-        work = torch.empty(kv_attend_work_bytes(cache, seqs.n, n, heads, max_new,
-                                                max_len or min(seqs.pages * cache.params.page_tokens, _KV_MAX_LEN), window, sinks),
-                           dtype=torch.uint8, device=q.device)
+        most = max_len or min(seqs.pages * cache.params.page_tokens, _KV_MAX_LEN)
+        work = _work_buffer(kv_attend_work_bytes(cache, seqs.n, n, heads, max_new, most, window, sinks), q.device, stream)
     args = _ATTENTION.pack(_seqs(seqs, cache, "ec_kv_attend"), _int32_ptr(starts, cache, seqs.n + 1, "ec_kv_attend"), n, layer,
                            max_new, max_len, heads, window, sinks, scale, qr, orr,
                            0 if lse is None else _at(lse, cache, "ec_kv_attend"), _at(work, cache, "ec_kv_attend"), work.nbytes)
@@ -620,18 +629,15 @@ def kv_pages_work_bytes(cache: KvCache, n_from: int, n_to: int) -> int:
     return int(n.value)
 
 
-def _pages_work(cache, a: KvSeqs, b: KvSeqs, work):
-    if work is None:
-        import torch
-        work = torch.empty(kv_pages_work_bytes(cache, a.n, b.n), dtype=torch.uint8, device=a.lens.device)
-    return work
+def _pages_work(cache, a: KvSeqs, b: KvSeqs, work, stream):
+    return work if work is not None else _work_buffer(kv_pages_work_bytes(cache, a.n, b.n), a.lens.device, stream)
 
 
 def kv_fork(cache: KvCache, seqs: KvSeqs, refs, to: KvSeqs, refs_out, parents=None, grow=None, work=None,
             stream=None) -> None:
     """ec_kv_fork: sequences `to` continue seqs[parents] with room for `grow` more tokens."""
     n, what = cache.params.n_pages, "ec_kv_fork"
-    work = _pages_work(cache, seqs, to, work)
+    work = _pages_work(cache, seqs, to, work, stream)
     args = _PAGES.pack(_seqs(seqs, cache, what), _seqs(to, cache, what), _int32_ptr(refs, cache, n, what),
                        _int32_ptr(refs_out, cache, n, what), _int32_ptr(parents, cache, to.n, what),
                        _int32_ptr(grow, cache, to.n, what), 0, _at(work, cache, what), work.nbytes)
@@ -643,7 +649,7 @@ def kv_fork(cache: KvCache, seqs: KvSeqs, refs, to: KvSeqs, refs_out, parents=No
 def kv_compact(cache: KvCache, seqs: KvSeqs, refs, to: KvSeqs, refs_out, page_map=None, work=None, stream=None) -> None:
     """ec_kv_compact: the pages in use move to the lowest numbers; page_map: old number -> new."""
     n, what = cache.params.n_pages, "ec_kv_compact"
-    work = _pages_work(cache, seqs, to, work)
+    work = _pages_work(cache, seqs, to, work, stream)
     args = _PAGES.pack(_seqs(seqs, cache, what), _seqs(to, cache, what), _int32_ptr(refs, cache, n, what),
                        _int32_ptr(refs_out, cache, n, what), 0, 0, _int32_ptr(page_map, cache, n, what),
                        _at(work, cache, what), work.nbytes)

@@ -48,3 +48,36 @@ def test_buffers_sized_with_the_defaults(ec):
     ec.kv_attend(c.cache, 0, c.seqs, q, a, work=work)
     ec.kv_attend(c.cache, 0, c.seqs, q, b)
     assert ec.status() == 0 and torch.equal(a, b)
+
+
+def streams_with_memory():
+    return {s["stream"] for s in torch.cuda.memory_snapshot()}
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_calls_on_a_stream_of_their_own_allocate_there(ec, raw):
+    """Without a work buffer: neither the current stream's earlier work nor its later
+    allocations share bytes with the call."""
+    lens = [3000, 700]
+    c = Case(ec, lens, 2, 128, 64, spare=9)
+    c.fill(normal(39, sum(lens), 2, 128), normal(40, sum(lens), 2, 128))
+    q = normal(41, 2, 8, 128)
+    want = torch.empty_like(q)
+    ec.kv_attend(c.cache, 0, c.seqs, q, want)
+    refs = i32([sum(p in row for row in c.rows) for p in range(c.n_pages)])
+    to = [ec.kv_seqs(torch.empty_like(c.table), torch.empty_like(c.dlens)) for _ in range(2)]
+    refs_out = [torch.empty_like(refs) for _ in range(2)]
+    ec.kv_fork(c.cache, c.seqs, refs, to[0], refs_out[0])
+    out = torch.empty_like(q)
+    s = torch.cuda.Stream()
+    assert s.cuda_stream not in streams_with_memory()
+    s.wait_stream(torch.cuda.current_stream())
+    stream = s.cuda_stream if raw else s
+    ec.kv_attend(c.cache, 0, c.seqs, q, out, stream=stream)
+    ec.kv_fork(c.cache, c.seqs, refs, to[1], refs_out[1], stream=stream)
+    s.synchronize()
+    assert s.cuda_stream in streams_with_memory()
+    assert torch.equal(out, want) and torch.equal(to[0].table, to[1].table) and torch.equal(refs_out[0], refs_out[1])
+    ec.kv_attend(c.cache, 0, c.seqs, q, out, stream=0)  # the default stream by its handle
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and ec.status() == 0
