@@ -559,6 +559,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const __grid
     int64_t more = 0;
     if (tid < a.n_in) {
         const int64_t n = a.lens[tid];
+        if (n > in_cap) flag_corrupt(a.status);
         len_of[tid] = (int)(n < 0 ? 0 : n > in_cap ? in_cap : n);
         first[tid] = a.n_out;
     }
@@ -700,7 +701,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const __g
     }
     __syncthreads();
     if (tid == 0) *a.count = movers;
-    for (int s = tid; s < a.n_in; s += kPlanThreads) a.lens_out[s] = a.lens[s];
+    for (int s = tid; s < a.n_in; s += kPlanThreads) {
+        if (a.lens[s] > a.in_stride << a.P.page_shift) flag_corrupt(a.status);
+        a.lens_out[s] = a.lens[s];
+    }
     for (int s = tid >> 5; s < a.n_in; s += kPlanThreads / 32)
         for (int64_t col = tid & 31; col < a.out_stride; col += 32) {
             const int p = col < a.in_stride ? a.table[s * a.in_stride + col] : -1;

@@ -81,3 +81,19 @@ def test_calls_on_a_stream_of_their_own_allocate_there(ec, raw):
     ec.kv_attend(c.cache, 0, c.seqs, q, out, stream=0)  # the default stream by its handle
     torch.cuda.synchronize()
     assert torch.equal(out, want) and ec.status() == 0
+
+
+@pytest.mark.parametrize("op", ["fork", "compact"])
+def test_page_operations_flag_lengths_past_the_table(ec, op):
+    """More tokens than a row of the table holds are an inconsistency, as in the other calls."""
+    c = Case(ec, [40, 16], 1, 64, 16, spare=5)
+    c.table.copy_(i32([[0, 1, 2, 3], [4, 5, 6, 7]]))  # every place of a row names a page
+    refs = i32([1] * 8 + [0] * (c.n_pages - 8))
+    out = torch.empty_like(refs)
+    to = ec.kv_seqs(torch.empty_like(c.table), torch.empty_like(c.dlens))
+    call = ec.kv_fork if op == "fork" else ec.kv_compact
+    cap = c.table.shape[1] * 16
+    for n, code in ((16, 0), (cap, 0), (cap + 1, -5), (1 << 30, -5), (2 ** 31 - 1, -5), (-3, 0)):
+        c.dlens[1] = n
+        call(c.cache, c.seqs, refs, to, out)
+        assert ec.status() == code, n
