@@ -468,9 +468,9 @@ class KvCache:
 
 
 def _at(t, cache, what: str) -> int:
-    """The address of a tensor on the cache's device."""
-    if t.get_device() != cache.device:
-        raise EcError(EC_ERR_INVALID_ARG, what + ": tensors on the cache's device")
+    """The address of a tensor on the cache's device, whose bytes lie together."""
+    if t.get_device() != cache.device or not t.is_contiguous():
+        raise EcError(EC_ERR_INVALID_ARG, what + ": contiguous tensors on the cache's device")
     return t.data_ptr()
 
 

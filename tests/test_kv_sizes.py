@@ -97,3 +97,15 @@ def test_a_table_that_holds_more_than_a_sequence(ec):
     with pytest.raises(ec.EcError) as e:
         ec.kv_attend(cache, 0, Some, x, x)
     assert "work_bytes" not in str(e.value) and e.value.code == -1  # the library's answer: no pool
+
+
+def test_a_work_tensor_has_to_hold_its_bytes(ec, cache):
+    """An expanded or strided tensor has fewer bytes, or other ones, than its shape says."""
+    class Some:
+        n, packed, pages, device = 2, bytes(32), 3, -1
+    x, refs = torch.zeros((2, 8, 128)), torch.zeros(100, dtype=torch.int32)
+    for work in (torch.zeros(1, dtype=torch.uint8).expand(1 << 25), torch.zeros(1 << 10)[::2]):
+        for call in (lambda: ec.kv_attend(cache, 0, Some, x, x.clone(), work=work), lambda: ec.kv_fork(cache, Some, refs, Some, refs.clone(), work=work),
+                     lambda: ec.kv_compact(cache, Some, refs, Some, refs.clone(), work=work)):
+            with pytest.raises(ec.EcError, match="contiguous"):
+                call()
