@@ -317,8 +317,8 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
     for (int k = 0; k < S; ++k) fill();
 
     uint32_t count = 0; /* stages taken from the ring */
-    bool live = true;
-    while (x < x_end) {
+    bool live = true;   /* no wait has run out */
+    while (live && x < x_end) {
         /* (the segment lies in shared memory for its masked ends and for what follows the loop,
          * so that the loop need not keep it in registers) */
         auto look_up = [&](Seg& sg, int3& f) {
@@ -448,9 +448,10 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
 #pragma unroll 1
         for (; u < u1; u += 2) {
             const uint32_t st = count & (S - 1), buf = ring + st * (2 * UB);
-            if (live && !mbar_wait(bars + 8 * st, (count / S) & 1u)) {
+            if (!mbar_wait(bars + 8 * st, (count / S) & 1u)) {
                 live = false;
                 if (lane == 0) flag_corrupt(a.status);
+                break;
             }
             ++count;
 
@@ -755,6 +756,8 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
             }
         }
     }
+    if (!live) /* the copies in flight end before the shared memory is given back */
+        for (; count != p_count; ++count) mbar_wait(bars + 8 * (count & (S - 1)), (count / S) & 1u);
     __syncwarp();
     if (lds32(own + 60)) redo_wide<NB>(a, pre, info, (float*)(at_smem + warp * H::WARP_BYTES));
 

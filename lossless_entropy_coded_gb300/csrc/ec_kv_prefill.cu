@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
     static_assert(H::META % 16 == 0 && H::RAW % 16 == 0, "sections stay aligned");
     const uint32_t raw_full = bars, raw_empty = bars + 16, buf_full = bars + 32, buf_empty = buf_full + 8 * NBUF,
                    s_full = buf_empty + 8 * NBUF, p_full = s_full + 8 * NQ, o_done = p_full + 8 * NQ, q_full = o_done + 8 * NQ,
-                   meta_full = q_full + 8, tslot = meta_full + 8 * H::MS, wide = bars + 248;
+                   meta_full = q_full + 8, tslot = meta_full + 8 * H::MS, drained = bars + 240, wide = bars + 248;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(raw_full + 8 * i, 1);
@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
         }
         for (int i = 0; i < H::MS; ++i) mbar_init(meta_full + 8 * i, 1);
         mbar_init(q_full, 4 * NQ);
+        mbar_init(drained, 1);
         sts32(wide, 0u);
         mbar_fence_init();
     }
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
     }
     const int T = __shfl_sync(kAll, (J.u1 - J.u0 + UT - 1) / UT, 0);
     const int NA = __shfl_sync(kAll, min(NQ, (J.R - J.r0 + 127) / 128), 0); /* row tiles that hold rows */
-    bool live = true;
+    bool live = true; /* no wait of this warp has run out; its role ends when one has */
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (live && !mbar_wait(bar, parity)) {
             live = false;
@@ -375,6 +376,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             const uint32_t meta = meta_at + j % H::MS * H::META;
             wait(meta_full + 8 * (j % H::MS), (j / H::MS) & 1);
             wait(s_full + 8 * t, j & 1);
+            if (!live) break;
             tc_fence_after();
             const float f = fmaxf(rowfac * __uint_as_float((lds32(meta) - 13u) << 23), kTiny); /* > 0: a masked -inf stays one */
             const uint32_t flags = lds32(meta + 4);
@@ -543,6 +545,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                 const int buf = n % NBUF;
                 const uint32_t add = both_halves(28 - (int)lds32(meta));
                 wait(buf_empty + 8 * buf, ((n / NBUF) & 1) ^ 1u);
+                if (!live) break;
 #pragma unroll 1
                 for (int u = we; u < UT; u += 4) {
                     const uint32_t src = raw + u * UB;
@@ -578,6 +581,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             {
                 const int buf = n % NBUF;
                 wait(buf_empty + 8 * buf, ((n / NBUF) & 1) ^ 1u);
+                if (!live) break;
 #pragma unroll 1
                 for (int u = we; u < UT; u += 4) {
                     const uint32_t src = raw + u * UB;
@@ -664,17 +668,18 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             wait(buf_full, 0);
             tc_fence_after();
 #pragma unroll 1
-            for (int t = 0; t < NA; ++t) {
+            for (int t = 0; t < NA && live; ++t) {
                 scores(t, 0);
                 tc_commit(s_full + 8 * t);
             }
             tc_commit(buf_empty);
-            for (int j = 0; j < T; ++j) {
+            for (int j = 0; j < T && live; ++j) {
                 const int vn = 2 * j + 1, kn = 2 * j + 2, vb = vn % NBUF, kb = kn % NBUF;
                 wait(buf_full + 8 * vb, (vn / NBUF) & 1);
 #pragma unroll 1
                 for (int t = 0; t < NA; ++t) {
                     wait(p_full + 8 * t, j & 1);
+                    if (!live) break;
                     tc_fence_after();
                     values(t, vb, j);
                     tc_commit(o_done + 8 * t);
@@ -687,17 +692,22 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                         /* the scores take the weights' place: not before their product is done
                          * (products of other shapes and accumulators may overtake it) */
                         wait(o_done + 8 * t, j & 1);
+                        if (!live) break;
                         scores(t, kb);
                         tc_commit(s_full + 8 * t);
                         if (t == NA - 1) tc_commit(buf_empty + 8 * kb);
                     }
                 }
             }
+            /* nothing is in flight when the tensor memory is given back, whatever ran out */
+            tc_commit(drained);
+            mbar_wait(drained, 0);
         }
         __syncwarp();
     } else if (warp == 4 * NQ + H::EW + 1) {
         /* ---------------------------------------------------------------- copies */
-        for (int j = 0; j < T; ++j) {
+        int j = 0;
+        for (; j < T; ++j) {
             const int s = j % H::RS, ut = J.u0 + j * UT, have = min(UT, J.u1 - ut);
             int page = 0, unit = 0;
             if (lane < have) {
@@ -710,10 +720,12 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             }
             const uint8_t* src = page_ptr(a.P, page, J.h, unit & ((1 << (a.P.page_shift - 4)) - 1));
             wait(raw_empty + 8 * s, ((j / H::RS) & 1) ^ 1u);
+            if (!live) break;
             if (lane == 0) mbar_arrive_tx(raw_full + 8 * s, have * UB);
             __syncwarp();
             if (lane < have) bulk_g2s(raw_at + s * H::RAW + lane * UB, src, UB, raw_full + 8 * s);
         }
+        for (int i = max(0, j - H::RS); i < j; ++i) mbar_wait(raw_full + 8 * (i % H::RS), (i / H::RS) & 1); /* nor any copy */
     } else if (warp == 4 * NQ + H::EW + 2) {
         /* ---------------------------------------------------------------- references */
         constexpr int WU = 4 * NB;             /* words of scales per unit, keys' or values' */
@@ -727,6 +739,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             const int s = j % H::RS, ut = J.u0 + j * UT, have = min(UT, J.u1 - ut);
             const uint32_t raw = raw_at + s * H::RAW, meta = meta_at + j % H::MS * H::META;
             wait(raw_full + 8 * s, (j / H::RS) & 1);
+            if (!live) break;
             const int last = ut + have >= J.units ? min(kUnit, J.len - unit_of(ut + have - 1) * kUnit) : kUnit; /* tokens of the last unit */
             uint32_t kw[PER], vw[PER];
 #pragma unroll
