@@ -597,8 +597,8 @@ typedef struct {
 
 /* Sequences that continue others, for all layers at once: sequence i of `to` gets the
  * tokens of sequence parents[i] of `from` (parents device, [to.n_seqs], -1: an empty
- * sequence; NULL: i) and room for grow[i] >= 0 more (device; NULL: none); its len is
- * the parent's plus grow[i].  Whole pages are shared; a partly filled last page stays
+ * sequence without room, whatever grow[i]; NULL: i) and room for grow[i] >= 0 more (device;
+ * NULL: none); its len is the parent's plus grow[i].  Whole pages are shared; a partly filled last page stays
  * with the first child (lowest i), the others get copies of its used units.  Sequences
  * of `from` without a child are dropped.  New pages are the free ones of lowest number,
  * taken in the order of the sequences (a copied page first).  A sequence for which no

@@ -721,8 +721,8 @@ struct CopyArgs {
 
 /* A copy moves the first `units` units of every head of every layer of a page: runs of
  * units * 17 D contiguous bytes, one CTA per (copy, head) run at a time.  Bound by HBM: a
- * compaction that moves 0.2 GB takes 69 us with its plan (5.8 TB/s, 0.86 of the measured
- * copy rate), 64 samples of 6 prompts over 32 layers 22 us (112 MB, 5.0 TB/s). */
+ * compaction that moves 0.2 GB takes 68 to 74 us with its plan (5.4 to 5.9 TB/s, 0.81 to 0.88 of
+ * the measured copy rate), 64 samples of 6 prompts over 32 layers 22 to 23.5 us (112 MB, 5 TB/s). */
 constexpr int kCopyThreads = 256;
 __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_constant__ CopyArgs a) {
     grid_dep_launch();

@@ -11,16 +11,17 @@
  *
  * Bounds.  The floor is HBM: 4.25 bits per element of every visible key and value.  An SM
  * gets 45 bytes/ns of it, a unit (16 tokens, 2176 bytes at 128 channels) every 94 clocks;
- * the four schedulers then have 375 issue slots for it.  A unit takes about 275
+ * the four schedulers then have 375 issue slots for it.  A unit takes about 270
  * instructions, 140 of them on the integer pipe, which issues every second clock (the
  * expansion of E2M1 to FP16 alone is 64), so the integer pipe and the dependent chain of
  * a warp bound the kernel, not HBM.  Measured, 128 channels, 32 query over 8 key/value
- * heads: 400003 tokens 83.8 us (5.19 TB/s, 0.77 of the measured copy rate; 113 us with
+ * heads: 400003 tokens 83.4 us (5.22 TB/s, 0.78 of the measured copy rate; 113 us with
  * one unit per step and all segment state in registers); 64 sequences of 1 to 8192 tokens
- * 36.1 us for 92 MB (245 us with one CTA per tile and fixed chunks: most tiles are short,
+ * 36.0 us for 92 MB (245 us with one CTA per tile and fixed chunks: most tiles are short,
  * and their fixed cost, about that of 10 units, has to be shared out too).
- * mma.sync rather than tcgen05: the products have 8 columns, a tcgen05 tile 128 rows; the
- * legacy pipe is 28 % busy at the rate above.
+ * mma.sync, whose operands a warp expands in its own registers; the pipe is 28 % busy at the
+ * rate above.  tcgen05 with the tokens as its 128 rows and the query rows as columns would
+ * expand a tile once for all of a head's rows, in shared memory; it has not been tried.
  */
 #include "ec_kv_attn.h"
 
@@ -29,8 +30,11 @@ namespace kv {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 /* Work is counted in units of 16 tokens of one tile (the rows of one key/value head's
- * group, 8 at a time), plus kTileCost for a tile's queries and outputs
- * (6, 10, 14 and 20 took 39.3, 34.4, 36.5 and 35.9 us on the 64 ragged sequences). */
+ * group, 8 at a time), plus kTileCost for a tile's queries and outputs.  Measured (us, cost 6 /
+ * 10 / 14 / 20), 32 query over 8 key/value heads of 128 channels: 64 sequences of 1 to 8192
+ * tokens 30.7 / 27.1 / 28.8 / 28.4, with FP32 queries 42.3 / 35.9 / 37.3 / 36.8; 200 of 16 to 2000
+ * 43.0 / 39.4 / 41.8 / 44.9; 1000 of 1 to 300 62.9 / 62.5 / 63.1 / 66.9; 64 over 8: 16 of 500 to 30000
+ * 37.9 / 35.6 / 35.5 / 34.6; 16 over 16 of 64 channels, 100 of 64 to 4000 37.6 / 35.4 / 36.0 / 38.3. */
 constexpr int kTileCost = 10;
 
 /* The keys that a sequence's new rows see, in units: the sinks' units, then lo_u ..
@@ -142,16 +146,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t both_halves(int v) { return ((uint32_t)v & 0xFFFFu) * 0x10001u; }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *(const uint32_t*)&h;
 }
 
 /* Bits of the probabilities: p is held as 2^kBias p in FP16, the running reference of a

@@ -130,6 +130,18 @@ __device__ __forceinline__ float scale_value(int e) {
 /* 2^(127 - e), e in 1..253. */
 __device__ __forceinline__ float inv_scale(int e) { return __uint_as_float((uint32_t)(254 - e) << 23); }
 
+/* ------------------------------------------------------------ pairs of 16 bits */
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t both_halves(int v) { return ((uint32_t)v & 0xFFFFu) * 0x10001u; }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *(const uint32_t*)&h;
+}
+
 /* ------------------------------------------------------------ PTX helpers */
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -19,7 +19,7 @@
  *
  * Bounds.  The floor is the tensor pipe: 4 D operations per visible (query, token) pair.
  * Two prompts (2999 and 5003 new rows of 32 query over 8 key/value heads, 128 channels, up
- * to 13000 tokens): 1143 us, 1.15 PFLOP/s, 0.61 of the measured BF16 rate; tensor pipe 47 %
+ * to 13000 tokens): 1140 us, 1.16 PFLOP/s, 0.59 of the measured BF16 rate; tensor pipe 47 %
  * active over a whole launch.  What bounds it is the chain of one row tile: softmax of 128
  * tokens (about 1850 clocks), then its product and the next scores (1500), of which the
  * other row tile hides only its own share; shared memory carries the products' operands
@@ -155,16 +155,6 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-__device__ __forceinline__ uint32_t half_mul2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t both_halves(int v) { return ((uint32_t)v & 0xFFFFu) * 0x10001u; }
-__device__ __forceinline__ uint32_t half_pack(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *(const uint32_t*)&h;
 }
 
 /* (a f + c, b f + c) and acc + (a, b): the two-wide FP32 instructions. */
@@ -354,9 +344,9 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float y0 = x[2 * i] * s, y1 = x[2 * i + 1] * s;
-                    w[i] = half_pack(y0, y1);
+                    w[i] = pack_f16(y0, y1);
                     const float2 hi = __half22float2(*(const __half2*)&w[i]);
-                    lo[i] = half_pack(y0 - hi.x, y1 - hi.y);
+                    lo[i] = pack_f16(y0 - hi.x, y1 - hi.y);
                 }
                 const uint32_t at = q_at + t * QT * H::QBYTES + (d >> 6) * (128 * 128) + lr * 128 + ((((d >> 3) & 7) ^ (lr & 7)) << 4);
                 sts128(at, w[0], w[1], w[2], w[3]);
@@ -464,7 +454,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                     const float2 y = fma2(v[i], v[i + 1], f, off);
                     const float p0 = ex2(y.x), p1 = ex2(y.y);
                     acc = add2(acc, p0, p1);
-                    p[i / 2] = half_pack(p0, p1);
+                    p[i / 2] = pack_f16(p0, p1);
                 }
                 tc_st16(s_at + 16 * k, p);
             }
@@ -568,8 +558,8 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                                 if ((flags & 2u) && ((e2[r] >> (8 * bb)) & 0xFFu) == 255u) sc = 0x7E007E00u;
                                 uint32_t h4[4];
                                 e2m1x8_f16(ww[2 * bb + r], h4);
-                                sts128((bb ? odd : even) + i * (TN * 128) + r * 1024, half_mul2(h4[0], sc), half_mul2(h4[1], sc),
-                                       half_mul2(h4[2], sc), half_mul2(h4[3], sc));
+                                sts128((bb ? odd : even) + i * (TN * 128) + r * 1024, hmul2(h4[0], sc), hmul2(h4[1], sc),
+                                       hmul2(h4[2], sc), hmul2(h4[3], sc));
                             }
                     }
                 }
@@ -622,10 +612,10 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                             uint32_t h4[4]; /* byte r + 2 p: channel 8 r + g of them */
                             e2m1x8_f16(ww[i], h4);
                             const uint32_t o = (64 * i4 + 16 * i) * 128;
-                            sts32(at0 + o, half_mul2(h4[0], s0[i / 2]));
-                            sts32(at0 + o + 1024, half_mul2(h4[1], s0[i / 2]));
-                            sts32(at1 + o, half_mul2(h4[2], s1[i / 2]));
-                            sts32(at1 + o + 1024, half_mul2(h4[3], s1[i / 2]));
+                            sts32(at0 + o, hmul2(h4[0], s0[i / 2]));
+                            sts32(at0 + o + 1024, hmul2(h4[1], s0[i / 2]));
+                            sts32(at1 + o, hmul2(h4[2], s1[i / 2]));
+                            sts32(at1 + o + 1024, hmul2(h4[3], s1[i / 2]));
                         }
                     }
                 }
@@ -897,7 +887,8 @@ static int run_prefill(AttnArgs a, const PrefillPlan& p, cudaStream_t stream) {
     return rc;
 }
 
-/* Two row tiles per CTA where shared and tensor memory hold them: FP16 and BF16 queries of up to 128 channels. */
+/* Two row tiles per CTA for FP16 and BF16 queries of up to 128 channels.  (64 channels with FP32
+ * queries and 192 with 16-bit ones would fit shared and tensor memory too; not measured.) */
 static int row_tiles_per_cta(int nb, int dtype) { return nb <= 4 && dtype != EC_DTYPE_FP32 ? 2 : 1; }
 
 bool plan_prefill(const ec_kv* C, int sms, int n_seqs, int max_new, int64_t max_units, int group, int dtype, PrefillPlan* p) {
