@@ -558,7 +558,8 @@ int ec_kv_read(const ec_kv* C, const ec_kv_tokens* a, cudaStream_t stream);
  * max_new and max_len are upper bounds, over the sequences, of the new tokens and of
  * lens (0: what a table row can hold); work: device memory of the caller, 16-byte
  * aligned, of at least ec_kv_attend_work_bytes(); its contents need no clearing, and
- * two calls that may overlap need one each.  out: FP16, BF16 or FP32. */
+ * two calls that may overlap need one each.  out: FP16, BF16 or FP32; it may be q itself
+ * (one address, type and strides). */
 typedef struct {
     ec_kv_seqs seqs;
     const int32_t* starts;

@@ -156,7 +156,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 constexpr float kBias = 5.f;
 constexpr int kRefUp = 7, kRefDown = 8;
 /* A step whose scales span more than the two, or a reference that is more than kRefSpan from its
- * segment's first, sends the warp's work to redo_wide: the accumulators' FP32 range is far from
+ * segment's first, sends the rest of the warp's work to redo_wide: the accumulators' FP32 range is far from
  * its ends, and tokens that weigh little cannot drown those that count. */
 constexpr int kRefSpan = 16;
 
@@ -203,15 +203,17 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int row0, int h, in
     if (d == 0 && a.lse) a.lse[row * a.n_q_heads + head] = L == 0.f ? -INFINITY : (M - kBias + log2f(L)) * kLn2;
 }
 
-/* A warp's work again, row by row in FP32; `own`: the warp's shared memory. */
+/* A warp's work again, row by row in FP32, from the place whose lower half is `from`; `own`: the
+ * warp's shared memory. */
 template <int NB>
-__device__ __forceinline__ void redo_wide(const AttnArgs& a, const int64_t* pre, const int3* info, float* own) {
+__device__ __forceinline__ void redo_wide(const AttnArgs& a, const int64_t* pre, const int3* info, uint32_t from, float* own) {
     using H = Shape<NB>;
     constexpr int RB = H::RB, LD = H::LD;
     const int warp = threadIdx.x >> 5, W = blockDim.x >> 5;
     const int64_t X = pre[a.S.n_seqs], share = share_of(a, X, gridDim.x, W), x1 = min(X, (blockIdx.x + 1) * share);
     int64_t x = min(x1, blockIdx.x * share + warp * (share / W));
     const int64_t x_end = min(x1, x + share / W);
+    x += from - (uint32_t)x; /* a warp's places are fewer than 2^32 */
     while (x < x_end) {
         const Seg s = seg_at(a, pre, info, RB, x, x_end);
         x = s.next;
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
     if (lane == 0) {
         for (int s = 0; s < S; ++s) mbar_init(bars + 8 * s, 1);
         mbar_fence_init();
-        sts32(own + 60, 0u); /* not 0: redo_wide takes the warp's work */
+        sts32(own + 60, 0u); /* not 0: redo_wide takes the warp's work from the place in the word before */
         slot_tile[2 * warp] = slot_tile[2 * warp + 1] = -1;
     }
     grid_dep_launch();
@@ -327,6 +329,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
         {
             const Seg sg = seg_at(a, pre, info, RB, x, x_end);
             const int3 f = info[sg.b];
+            const uint32_t place = (uint32_t)x;
             x = sg.next;
             if (sg.u0 >= sg.u1) continue;
             __syncwarp();
@@ -334,7 +337,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
                 uint4* o = (uint4*)(at_smem + warp * H::WARP_BYTES + H::RING + H::KEEP * 4);
                 o[0] = make_uint4(sg.b, sg.h, sg.r0, sg.u0);
                 o[1] = make_uint4(sg.u1, sg.units, (uint32_t)sg.tile, (uint32_t)((uint64_t)sg.tile >> 32));
-                o[2] = make_uint4(f.x, f.y, f.z, 0);
+                o[2] = make_uint4(f.x, f.y, f.z, place);
             }
             __syncwarp();
             const Span sp = span_of(a, f.x, f.y);
@@ -619,7 +622,10 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
                         z1[v][k2] = __vmins2(__viaddmax_s16x2(__byte_perm(vw[v][k2], 0, 0x4342), add7, 0u), 0x00160016u) - 0x00070007u;
                     }
                 }
-                if (wide) sts32(own + 60, 1u);
+                if (wide && lds32(own + 60) == 0) {
+                    sts32(own + 56, lds32(own + 44));
+                    sts32(own + 60, 1u);
+                }
             }
 
             /* O^T: rows = channels, columns = query rows */
@@ -678,6 +684,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
             back[k] = ref > 0 ? __uint_as_float((uint32_t)ref << 23) : 0.f;
         }
         if (sg.u0 == 0 && sg.u1 == sg.units) {
+            if (lds32(own + 60)) continue; /* nothing is written over queries that are still to be read, should out be q */
             float inv[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -753,7 +760,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
     if (!live) /* the copies in flight end before the shared memory is given back */
         for (; count != p_count; ++count) mbar_wait(bars + 8 * (count & (S - 1)), (count / S) & 1u);
     __syncwarp();
-    if (lds32(own + 60)) redo_wide<NB>(a, pre, info, (float*)(at_smem + warp * H::WARP_BYTES));
+    if (lds32(own + 60)) redo_wide<NB>(a, pre, info, lds32(own + 56), (float*)(at_smem + warp * H::WARP_BYTES));
 
     /* join the warps' parts, tile by tile, in order: lane k holds slot k's tile; 8, 4, 2 or one
      * warps take a tile, a row at a time, so that most warps have one */

@@ -479,6 +479,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             wait(o_done + 8 * t, (T - 1) & 1);
             tc_fence_after();
         }
+        const bool redo = lds32(wide) != 0; /* nothing is written over queries that are still to be read, should out be q */
         const float inv = a.splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
         float* part = a.part + ((int64_t)blockIdx.x * NQ + t) * (128 * (D + 2));
 #pragma unroll 1
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             float x[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = nan ? __uint_as_float(0x7FC00000u) : __uint_as_float(v[i]) * back * inv;
-            if (!on) continue;
+            if (!on || redo) continue;
             if (a.splits > 1) {
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                 }
             }
         }
-        if (on) {
+        if (on && !redo) {
             if (a.splits > 1) {
                 part[128 * D + 32 * q4 + lane] = set || !(l == 0.f) ? m : -FLT_MAX;
                 part[128 * D + 128 + 32 * q4 + lane] = l;
@@ -807,13 +808,16 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(meta_full + 8 * (j % H::MS));
-            /* (nobody waits for this: ahead of the arrival it cost 29 us of 1146) */
+            /* (behind the arrival, where nobody waits for it: ahead of it this cost 29 us of 1146; but
+             * the last tile's waiters learn whether the rows are done again) */
+            if (lane == 0 && j + 1 < T) mbar_arrive(meta_full + 8 * (j % H::MS));
 #pragma unroll
             for (int q = 0; q < PER; ++q) kl = bytes_min(kl, kw[q]);
             kmost = max(kmost, kref);
         }
         if (far || half_min(kl) < kmost - 27) sts32(wide, 1u);
+        __syncwarp();
+        if (lane == 0 && T > 0) mbar_arrive(meta_full + 8 * ((T - 1) % H::MS));
     }
     tc_fence_before();
     __syncthreads();

@@ -216,3 +216,26 @@ def test_a_key_of_nan_spoils_rows_that_see_it(ec, qh):
     c.fill(k, v)
     out, _ = check(ec, c, k, v, [2], (u * 4 + 0.05 * normal(25, 2, qh, 128)))
     assert not torch.isnan(out[0]).any() and torch.isnan(out[1]).all()
+
+
+# ------------------------------------------------------------------ outputs in the queries' place
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("lens,new", [([700, 90, 5000], [3, 2, 2]), ([700, 90, 5000], [90, 70, 30]), ([400, 90, 130], [90, 70, 30]),
+                                      ([10, 40, 3, 17] * 250, [1] * 1000)])
+@pytest.mark.parametrize("loud", [0, 8, 60])
+def test_outputs_may_replace_the_queries(ec, lens, new, loud, dtype):
+    """The same bits as with an output of its own, also where rows are done again."""
+    kvh = 8 if len(lens) > 3 else 2
+    c = Case(ec, lens, kvh, 128, 32)
+    k, v = normal(60, sum(lens), kvh, 128), normal(61, sum(lens), kvh, 128)
+    v[2::67] *= 2.0 ** loud
+    c.fill(k, v)
+    q = normal(62, sum(new), 4 * kvh, 128).to(dtype)
+    want = torch.empty_like(q)
+    ec.kv_attend(c.cache, 0, c.seqs, q, want, starts=starts_of(new), max_new=max(new))
+    if len(lens) == 3:
+        check(ec, c, k, v, new, q, dtype)
+    for _ in range(5):
+        x = q.clone()
+        ec.kv_attend(c.cache, 0, c.seqs, x, x, starts=starts_of(new), max_new=max(new))
+        assert ec.status() == 0 and torch.equal(x, want)
