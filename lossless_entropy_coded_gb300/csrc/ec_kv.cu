@@ -168,11 +168,12 @@ __device__ __forceinline__ UnitJob unit_job(const IoArgs& a) {
     const int first = j.q.len - j.q.m; /* position of the first new token; < 0: rows without a token */
     const int f = first < 0 ? 0 : first;
     j.unit = f / kUnit + j.u;
-    j.tok0 = j.unit * kUnit;
+    const bool past = j.unit >= 1 << 27; /* of 2^31 tokens */
+    j.tok0 = past ? 0 : j.unit * kUnit;
     j.lo = f - j.tok0 > 0 ? f - j.tok0 : 0;
     j.hi = j.q.len - j.tok0 < kUnit ? j.q.len - j.tok0 : kUnit;
     j.row0 = j.q.row0 + (j.tok0 - first);
-    j.any = j.hi > j.lo && !(j.which == 0 ? !a.has_k : !a.has_v);
+    j.any = !past && j.hi > j.lo && !(j.which == 0 ? !a.has_k : !a.has_v);
     return j;
 }
 
@@ -401,8 +402,8 @@ __global__ void __launch_bounds__(kIoWarps * 32) kv_read_kernel(const __grid_con
     const int none = j.q.m - j.q.len;
     if (none > 0 && (j.which ? a.has_v : a.has_k)) { /* rows of tokens before the sequence's first: zeros, 16 at a time */
         const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int r0 = j.u * kUnit; r0 < none; r0 += a.units * kUnit)
-            for (int r = r0; r < min(none, r0 + kUnit); ++r)
+        for (int64_t r0 = j.u * kUnit; r0 < none; r0 += a.units * kUnit)
+            for (int64_t r = r0; r < min((int64_t)none, r0 + kUnit); ++r)
                 for (int d = 8 * lane; d < D; d += 256) store8(R, (j.q.row0 + r) * R.row + (int64_t)j.h * R.head + d, z);
     }
     if (!j.any) return;
@@ -574,6 +575,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const __grid
     __syncthreads();
     if (parent >= 0) atomicMin(&first[parent], tid);
     __syncthreads();
+    auto pages_of = [&](int len) { return (int)(((int64_t)len + T - 1) >> shift); };
     auto page_in = [&](int s, int k) {
         const int p = a.table[(int64_t)s * a.in_stride + k];
         return p < 0 || p >= N ? -1 : p;
@@ -597,7 +599,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const __grid
      * first add theirs (a first child takes its parent's place in every count) */
     for (int s = tid >> 5; s < a.n_in; s += kPlanThreads / 32)
         if (first[s] == a.n_out)
-            for (int k = lane; k < (len_of[s] + T - 1) >> shift; k += 32) {
+            for (int k = lane; k < pages_of(len_of[s]); k += 32) {
                 const int p = page_in(s, k);
                 if (p >= 0) atomicSub(&cnt[p], 1);
                 else flag_corrupt(a.status);

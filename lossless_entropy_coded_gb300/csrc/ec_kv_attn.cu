@@ -27,6 +27,7 @@
 
 namespace kv {
 
+constexpr int64_t kMaxLen = 0x7FFFFFF0; /* tokens of a sequence: lens are 32-bit, and a unit past them too */
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 /* Work is counted in units of 16 tokens of one tile (the rows of one key/value head's
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
                 const int pos_lo = first + min(sg.r0, R - 1) / a.group, pos_hi = first + min(sg.r0 + RB - 1, R - 1) / a.group;
                 int tok[2];
 #pragma unroll
-                for (int v = 0; v < 2; ++v) tok[v] = u + v < u1 ? (u + v < sp.sink_u ? u + v : u + v + skip) * kUnit : 0x7FFFFF00;
+                for (int v = 0; v < 2; ++v) tok[v] = u + v < u1 ? (u + v < sp.sink_u ? u + v : u + v + skip) * kUnit : (int)kMaxLen; /* past every token */
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int p = first + min(sg.r0 + 2 * c + j, R - 1) / a.group;
@@ -912,8 +913,6 @@ static void plan_shape(Plan* p, int sms, int64_t tiles, int64_t units) {
  * rows 81 / 118, 24 rows 109 / 119, 32 rows 137 / 118; 192 channels: 24 rows 78 / 107, 40
  * rows 118 / 107.  One sequence of 30000 and 128 channels, 40 rows: 41 / 42. */
 constexpr int64_t few_rows(int nb) { return nb == 2 ? 40 : nb == 4 ? 32 : 24; }
-
-constexpr int64_t kMaxLen = 0x7FFFFFF0; /* lens are 32-bit */
 
 /* The mask as the kernels take it: a window that hides none of max_len tokens is none, and there
  * are no more sinks than tokens, so that sums with either stay within 31 bits. */

@@ -2,8 +2,9 @@
 import pytest
 import torch
 
+import kv_ref as R
 from test_gpu_kv import FP32, Case, ec, i32, starts_of  # noqa: F401 (ec is a fixture)
-from test_gpu_kv_rows import check, normal
+from test_gpu_kv_rows import check, normal, row_bounds, stored
 
 pytestmark = pytest.mark.gpu
 INT_MAX = 2 ** 31 - 1
@@ -97,3 +98,33 @@ def test_page_operations_flag_lengths_past_the_table(ec, op):
         c.dlens[1] = n
         call(c.cache, c.seqs, refs, to, out)
         assert ec.status() == code, n
+
+
+def test_sequences_at_the_end_of_31_bits(ec):
+    """2^31 - 16 tokens (most of them in one page that the table names again and again): new
+    tokens, what a window sees of them, and the pages that a dropped sequence gives up."""
+    n, pages, new = 2 ** 31 - 16, 1 << 23, 40
+    cache = ec.kv_cache(1, 4, 1, 64, 256)
+    cache.pool.fill_(255)
+    table = torch.zeros((1, pages), dtype=torch.int32, device="cuda")
+    table[0, -1], table[0, -2] = 2, 1
+    seqs, starts = ec.kv_seqs(table, i32([n])), i32([0, new])
+    k, v = normal(42, new, 1, 64), normal(43, new, 1, 64)
+    ec.kv_append(cache, 0, seqs, k, v, starts=starts, max_new=100)
+    held = torch.empty((2, new, 1, 64), device="cuda")
+    ec.kv_read(cache, 0, seqs, held[0], held[1], starts=starts, max_new=100)
+    assert ec.status() == 0
+    assert torch.equal(held[0].double(), stored(k)) and torch.equal(held[1].double(), stored(v))
+    for qh in (2, 80):
+        q = normal(44, 3, qh, 64)
+        out = torch.empty_like(q)
+        ec.kv_attend(cache, 0, seqs, q, out, starts=i32([0, 3]), max_new=3, window=30)
+        r = R.attend(q.double(), stored(k), stored(v), new - 3, None, 30)
+        e, _ = row_bounds(r, q.double(), stored(k), stored(v), new - 3, None, 30, 0, FP32)
+        assert ec.status() == 0 and bool(((out.double() - r.out).abs() <= e).all())
+    refs, out = i32([pages - 2, 1, 1, 5]), torch.empty(4, dtype=torch.int32, device="cuda")
+    none = ec.kv_seqs(torch.empty((0, 4), dtype=torch.int32, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda"))
+    for tokens in (n, 2 ** 31 - 1):
+        seqs.lens.fill_(tokens)
+        ec.kv_fork(cache, seqs, refs, none, out, parents=torch.empty(0, dtype=torch.int32, device="cuda"))
+        assert ec.status() == 0 and out.tolist() == [0, 0, 0, 5], tokens
