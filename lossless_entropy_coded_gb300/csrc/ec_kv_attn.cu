@@ -540,7 +540,17 @@ __global__ void __launch_bounds__(Shape<NB>::W * 32, 1) kv_attn_kernel(const __g
                         o[i][j + 2] *= al;
                     }
                 }
-                weights();
+                if (__any_sync(kAll, weights())) {
+                    /* Scores of 2^22 and more: what rounds off the product of the largest one is more than
+                     * weights can bear, so the products are rounded as the reference was.  (A row of NaN
+                     * comes by as well.) */
+#pragma unroll
+                    for (int v = 0; v < 2; ++v)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) p[v][j] = ex2(__fadd_rn(__fmul_rn(s[v][j], fac[j & 1]), -m[j & 1]) + kBias);
+                    sum[0] = (p[0][0] + p[0][2]) + (p[1][0] + p[1][2]);
+                    sum[1] = (p[0][1] + p[0][3]) + (p[1][1] + p[1][3]);
+                }
             }
             /* their transposition into the second product's operand */
             uint32_t p0[2], p1[2];

@@ -91,7 +91,7 @@ __device__ __forceinline__ void wide_row(const AttnArgs& a, const RowJob& j, flo
         for (int r = 0; r < 2; ++r) {
             s[r] += __shfl_xor_sync(kAll, s[r], 1);
             s[r] += __shfl_xor_sync(kAll, s[r], 2);
-            s[r] = sees(tok + g + 8 * r) ? s[r] * f : -INFINITY;
+            s[r] = sees(tok + g + 8 * r) ? __fmul_rn(s[r], f) : -INFINITY;
         }
         float mx = fmaxf(s[0], s[1]);
 #pragma unroll

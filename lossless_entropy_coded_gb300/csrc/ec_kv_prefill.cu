@@ -12,7 +12,7 @@
  *           it) only when a tile's scales lie more than 2^13 above or 2^14 below.
  * Where a tile's value scales span more, or vref would go further than kVSpan from its
  * first, or a key's scale lies 2^-28 below the largest kref, the CTA's rows are done again in
- * FP32 at the end (wide_row).
+ * FP32 at the end (wide_row); and a warp's rows, where a score passes kMost.
  * S (FP32, in tensor memory) is read one row per thread, the weights 2^(s - m + 6) go
  * back as FP16 in S's place and are the tensor-memory operand of O += P V.  The row's
  * reference m moves, and O with it, only when a score passes it by 2^8.
@@ -39,6 +39,8 @@ namespace kv {
 
 constexpr float kPBias = 6.f, kPSlack = 8.f;
 constexpr int kVUp = 13, kVDown = 14, kVSpan = 16;
+/* A reference from which what rounds off a score's product may raise a weight twofold. */
+constexpr float kMost = 4194304.f;
 
 template <int NB, int NQ, int QT>
 struct PShape {
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
         for (int i = 0; i < H::MS; ++i) mbar_init(meta_full + 8 * i, 1);
         mbar_init(q_full, 4 * NQ);
         mbar_init(drained, 1);
-        sts32(wide, 0u);
+        sts32(wide, 0u); /* bit w: the rows of softmax warp w are done again */
         mbar_fence_init();
     }
     if (warp == 4 * NQ + H::EW) {
@@ -422,6 +424,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
                 /* references move: the accumulators follow once the products before are done */
                 const float nm = set ? fmaxf(m, mx) : mx > -INFINITY ? mx : 0.f, al = set ? ex2(m - nm) : 0.f;
                 set |= mx > -INFINITY;
+                if (fabsf(nm) > kMost) atomicOr((uint32_t*)__cvta_shared_to_generic(wide), 1u << warp);
                 if (j > 0) {
                     wait(o_done + 8 * t, (j - 1) & 1);
                     tc_fence_after();
@@ -479,7 +482,8 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             wait(o_done + 8 * t, (T - 1) & 1);
             tc_fence_after();
         }
-        const bool redo = lds32(wide) != 0; /* nothing is written over queries that are still to be read, should out be q */
+        __syncwarp();
+        const bool redo = lds32(wide) >> warp & 1u; /* nothing is written over queries that are still to be read, should out be q */
         const float inv = a.splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
         float* part = a.part + ((int64_t)blockIdx.x * NQ + t) * (128 * (D + 2));
 #pragma unroll 1
@@ -815,7 +819,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
             for (int q = 0; q < PER; ++q) kl = bytes_min(kl, kw[q]);
             kmost = max(kmost, kref);
         }
-        if (far || half_min(kl) < kmost - 27) sts32(wide, 1u);
+        if (far || half_min(kl) < kmost - 27) sts32(wide, ~0u);
         __syncwarp();
         if (lane == 0 && T > 0) mbar_arrive(meta_full + 8 * ((T - 1) % H::MS));
     }
@@ -828,6 +832,7 @@ __global__ void __launch_bounds__(PShape<NB, NQ, QT>::WARPS * 32, 1) kv_prefill_
     if (lds32(wide)) {
 #pragma unroll 1
         for (int i = warp; i < min(128 * NQ, J.R - J.r0); i += H::WARPS) {
+            if (!(lds32(wide) >> (i / 32) & 1u)) continue;
             const int t = (J.r0 + i) / J.group;
             const RowJob row{J.b, J.h, J.h * J.group + (J.r0 + i) % J.group, J.first + t, J.sink_u, J.lo_u, J.u0, J.u1, J.row0 + t};
             float* part = a.part + ((int64_t)blockIdx.x * NQ + i / 128) * (128 * (D + 2)) + 128 * D + i % 128;

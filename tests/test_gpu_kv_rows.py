@@ -239,3 +239,31 @@ def test_outputs_may_replace_the_queries(ec, lens, new, loud, dtype):
         x = q.clone()
         ec.kv_attend(c.cache, 0, c.seqs, x, x, starts=starts_of(new), max_new=max(new))
         assert ec.status() == 0 and torch.equal(x, want)
+
+
+# ------------------------------------------------------------------ large scores
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("qh,new", [(4, 1), (3, 20), (80, 20), (4, 650)])
+@pytest.mark.parametrize("power", [10, 18, 22, 26, 30, 40])
+def test_scores_of_any_size(ec, qh, new, power, dtype):
+    """One token that outweighs all others that a row sees is what the row gives, however large
+    the scores: 2^power times those of the other tests."""
+    n = 700
+    c = Case(ec, [n], 1, 128, 32)
+    u, a = normal(63, 128), 0.05 * normal(64, n)
+    a[100], a[690] = 1, 2
+    k = (u * a[:, None] * 2.0 ** power)[:, None].to(dtype)
+    v = normal(65, n, 1, 128)
+    v[690] *= 100   # a scale above the references of the tokens before
+    v = v.to(dtype)
+    c.fill(k, v)
+    q = (u * (0.5 + torch.rand((new, qh, 1), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda"))).to(dtype)
+    out = torch.empty((new, qh, 128), device="cuda")
+    ec.kv_attend(c.cache, 0, c.seqs, q, out, starts=starts_of([new]), max_new=new)
+    assert ec.status() == 0
+    vs, pos = stored(v), torch.arange(n - new, n, device="cuda")
+    for row in range(new):
+        if pos[row] >= 100:
+            want = vs[690 if pos[row] >= 690 else 100, 0]
+            # its weight is 1 but for FP16's 2^-11 and what 699 tokens of weight 0 (2^-22 each at most) leave
+            assert bool(((out[row].double() - want).abs() <= want.abs() * 2.0 ** -10 + 1e-12).all()), (row, (out[row].double() - want).abs().max())
