@@ -548,13 +548,14 @@ int ec_kv_read(const ec_kv* C, const ec_kv_tokens* a, cudaStream_t stream);
  * that the row sees; lse[row, j] (FP32 [n_rows, n_q_heads], may be NULL) the natural
  * logarithm of the sum of the exponentials.  Scores, sums and outputs are held in FP32;
  * products are those of the 4-bit values with FP16 parts of q (one for BF16 and FP16, two
- * for FP32) and with FP16 probabilities, good to 2^-11 of themselves and 2^-22 of the row's
- * largest (smaller ones may be lost from out; lse counts all).  Values whose scales FP16 does
- * not span (in a block of 32 channels, 2^15 within 32 tokens or 2^16 along a sequence), and
- * with many new rows keys that span 2^27, take FP32 products on the CUDA cores instead, some
- * ten times slower, with many new rows a hundred times.  Keys and values of 2^100 and more may
- * overflow the FP32 sums.  A row that sees nothing gives zeros and lse = -inf; a block of NaN
- * that a row sees makes its channels NaN.
+ * for FP32; elements below 2^-28 of their row's largest lose bits) and with FP16
+ * probabilities, good to 2^-11 of themselves and 2^-22 of the row's largest (smaller ones may
+ * be lost from out; lse counts all).  Values whose scales FP16 does not span (in a block of 32
+ * channels, 2^15 within 32 tokens or 2^16 along a sequence), and with many new rows keys that
+ * span 2^27 or scores of 2^22, take FP32 products on the CUDA cores instead, some ten times
+ * slower, with many new rows a hundred times.  Keys and values of 2^100 and more may overflow
+ * the FP32 sums.  A row that sees nothing gives zeros and lse = -inf; a block of NaN that a
+ * row sees makes its channels NaN.
  * max_new and max_len are upper bounds, over the sequences, of the new tokens and of
  * lens (0: what a table row can hold); work: device memory of the caller, 16-byte
  * aligned, of at least ec_kv_attend_work_bytes(); its contents need no clearing, and

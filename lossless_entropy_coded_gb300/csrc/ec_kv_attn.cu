@@ -15,9 +15,9 @@
  * instructions, 140 of them on the integer pipe, which issues every second clock (the
  * expansion of E2M1 to FP16 alone is 64), so the integer pipe and the dependent chain of
  * a warp bound the kernel, not HBM.  Measured, 128 channels, 32 query over 8 key/value
- * heads: 400003 tokens 83.4 us (5.22 TB/s, 0.78 of the measured copy rate; 113 us with
+ * heads: 400003 tokens 82.6 us (5.27 TB/s, 0.79 of the measured copy rate; 113 us with
  * one unit per step and all segment state in registers); 64 sequences of 1 to 8192 tokens
- * 36.0 us for 92 MB (245 us with one CTA per tile and fixed chunks: most tiles are short,
+ * 36.2 us for 92 MB (245 us with one CTA per tile and fixed chunks: most tiles are short,
  * and their fixed cost, about that of 10 units, has to be shared out too).
  * mma.sync, whose operands a warp expands in its own registers; the pipe is 28 % busy at the
  * rate above.  tcgen05 with the tokens as its 128 rows and the query rows as columns would

@@ -44,7 +44,7 @@ struct RowJob {
  * word what the formats put there: channels 32 b + 8 c + 0..7 of keys g and g + 8, channels
  * 16 i + 8 r + g of values 2c, 2c + 1, 2c + 8, 2c + 9.  Bound by its instructions: 2.2 us per 16
  * tokens and row for each of an SM's 16 warps (one token over 400003, 32 query over 8 key/value
- * heads of 128 channels, 822 us for 84), so only data that needs it comes here.
+ * heads of 128 channels, 822 us for 83), so only data that needs it comes here.
  *
  * dst: the unnormalised sums of weights 2^(s - m + bias) go there, m and the weights' sum to
  * *dst_m and *dst_l; NULL: the row's output and lse are written. */

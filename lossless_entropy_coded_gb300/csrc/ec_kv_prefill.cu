@@ -19,7 +19,7 @@
  *
  * Bounds.  The floor is the tensor pipe: 4 D operations per visible (query, token) pair.
  * Two prompts (2999 and 5003 new rows of 32 query over 8 key/value heads, 128 channels, up
- * to 13000 tokens): 1140 us, 1.16 PFLOP/s, 0.59 of the measured BF16 rate; tensor pipe 47 %
+ * to 13000 tokens): 1135 us, 1.16 PFLOP/s, 0.59 of the measured BF16 rate; tensor pipe 47 %
  * active over a whole launch.  What bounds it is the chain of one row tile: softmax of 128
  * tokens (about 1850 clocks), then its product and the next scores (1500), of which the
  * other row tile hides only its own share; shared memory carries the products' operands
